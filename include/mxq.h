@@ -58,14 +58,16 @@ typedef enum {
   MXQ_ERR_DTYPE = -5,  /* a dtype tag that the entry point does not accept         */
   MXQ_ERR_ARG = -6,    /* any other invalid argument (axis, non-finite alpha)      */
   MXQ_ERR_HIP = -7,    /* the HIP runtime reported an error when enqueuing          */
-  MXQ_ERR_SCRATCH = -8 /* mxq_gemm_ex_noalloc: more workspace than its static scratch */
+  MXQ_ERR_SCRATCH = -8 /* mxq_gemm_ex_noalloc: more workspace than its static scratch;
+                          mxq_moe_fp4: a workspace smaller than it needs            */
 } mxq_status;
 
 typedef enum {
   MXQ_F32 = 0,   /* IEEE binary32                                       */
   MXQ_BF16 = 1,  /* bfloat16 (upper half of binary32), stored as 2 bytes */
   MXQ_E4M3 = 2,  /* OCP FP8 E4M3 element code (forward operands)        */
-  MXQ_E5M2 = 3   /* OCP FP8 E5M2 element code (gradients)               */
+  MXQ_E5M2 = 3,  /* OCP FP8 E5M2 element code (gradients)               */
+  MXQ_E2M1 = 4   /* OCP FP4 E2M1 element code, two to a byte (the *_fp4 entry points) */
 } mxq_dtype;
 
 typedef enum {
@@ -360,6 +362,111 @@ int mxq_gemm_ex_noalloc(int64_t M, int64_t N, int64_t K,
  */
 int mxq_gemm_exact_plan(int64_t M, int64_t N, int64_t K, int cus, int* tile_n, int* ranges_per_tile,
                         int* split_tiles, int* whole_tiles, int64_t* workspace_bytes);
+
+/* ------------------------------------------------------------------------------ MXFP4
+ *
+ * The 4-bit format of the OCP Microscaling Formats (MX) Specification v1.0: 32 consecutive
+ * values along K share one E8M0 scale byte, each value is an E2M1 code (sign, two exponent
+ * bits of bias 1, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6; no infinity, no NaN).  Two
+ * codes share a byte, the even element in the low half, so a block is 16 bytes.
+ *
+ * Code arrays [L][ld_codes]: ld_codes in BYTES, >= 16 * nb and a multiple of 16, pointer 16-byte
+ * aligned.  Scale arrays [L][ld_scales], ld_scales >= nb, any alignment; nothing outside the
+ * L x nb scale bytes and L x 16 nb code bytes is read or written.
+ */
+
+/*
+ * mxq_quantize_fp4 -- mxq_quantize_rule for MXFP4.
+ * src, axis, rule as there.  Per block: amax; scale byte 127 if amax == 0, else e + 127 with
+ *   MXQ_SCALE_CEIL  e the smallest integer >= -127 with amax <= 6 * 2^e
+ *   MXQ_SCALE_OCP   e = max(-127, floor(log2 amax) - 2); values above 6 * 2^e saturate
+ * and codes RNE-satfinite(x * 2^-e), the sign copied (-0 and negative underflow give 8).
+ * Positions K .. Kp-1 of the last block get code 0.  A block holding NaN or Inf gets scale
+ * byte 255 and every code 7.  Bit-exact, whatever the launch configuration.
+ */
+int mxq_quantize_fp4(const void* src, int src_type, int64_t rows, int64_t cols, int64_t ld_src, int axis, int rule,
+                     uint8_t* codes, int64_t ld_codes, uint8_t* scales, int64_t ld_scales, void* stream);
+
+/*
+ * mxq_quantize_fp4_sr -- mxq_quantize_fp4 (ceil rule) with stochastically rounded codes, for
+ * gradients.  Random numbers and decision as mxq_quantize_sr: element n = line * Kp + k draws
+ * word n % 4 of Philox4x32-10(counter n / 4, key seed) and its top 24 bits r round up iff
+ * r < 2^24 * (|x/S| - l) / (u - l), decided exactly.
+ */
+int mxq_quantize_fp4_sr(const void* src, int src_type, int64_t rows, int64_t cols, int64_t ld_src, int axis,
+                        uint64_t seed, uint8_t* codes, int64_t ld_codes, uint8_t* scales, int64_t ld_scales,
+                        void* stream);
+
+/*
+ * mxq_quantize_fp4_dual -- both orientations from one read of src: bit for bit
+ * mxq_quantize_fp4(MXQ_ROWWISE) into row_* ([rows]) and (MXQ_COLWISE) into col_* ([cols]), both
+ * under the ceil rule.
+ */
+int mxq_quantize_fp4_dual(const void* src, int src_type, int64_t rows, int64_t cols, int64_t ld_src,
+                          uint8_t* row_codes, int64_t ld_row_codes, uint8_t* row_scales, int64_t ld_row_scales,
+                          uint8_t* col_codes, int64_t ld_col_codes, uint8_t* col_scales, int64_t ld_col_scales,
+                          void* stream);
+
+/*
+ * mxq_dequantize_fp4 -- dec(code) * 2^(s-127) as MXQ_F32 (exact; 2^128 and beyond are Inf) or
+ * MXQ_BF16 (rounded to nearest even), dst [L][ld_dst] of any element alignment.  Scale byte
+ * 255 gives NaN.
+ */
+int mxq_dequantize_fp4(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales, int64_t L,
+                       int64_t K, void* dst, int dst_type, int64_t ld_dst, void* stream);
+
+/*
+ * mxq_gemm_fp4 -- Y = act(alpha * (X W) + bias) with W in MXFP4.
+ *
+ * X        x_type MXQ_BF16: [M][ld_x] bf16 (ld_x >= K, in elements, any element alignment),
+ *          x_scales ignored.  x_type MXQ_E2M1: codes [M][ld_x] and x_scales [M][ld_xs].
+ * W        codes [N][ld_w] and scales [N][ld_ws]: column j of the K x N matrix is line j, as
+ *          for mxq_gemm.
+ * Result   FP32 sums of exact products.  With X in MXFP4 the scaled FP4 matrix cores take
+ *          codes and scales as they are; the sums inside a block are exact (E2M1 products are
+ *          multiples of 1/4 of at most 36).  With X in bf16 each code of W is decoded with its
+ *          scale to bf16, exactly for scale bytes 0 .. 252 (253 and 254 may overflow to Inf, 255
+ *          is NaN), and the bf16 matrix cores form exact products.  Codes at k >= K are
+ *          ignored.  The summation order is fixed for a shape and a device; it differs
+ *          between shapes.  Epilogue, bias, act, alpha, y as mxq_gemm_ex.
+ * The gradients of a linear layer are two such products: dX from dY quantized along its rows
+ * and W along its outputs, dW from dY quantized along its columns and X along the tokens.
+ * Limits   M, N < 2^31, K < 2^24, ld_w and ld_ws < 2^24.
+ */
+int mxq_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, int x_type, int64_t ld_x, const uint8_t* x_scales,
+                 int64_t ld_xs, const uint8_t* w_codes, int64_t ld_w, const uint8_t* w_scales, int64_t ld_ws,
+                 float alpha, const float* bias, int act, void* y, int y_type, int64_t ld_y, void* stream);
+
+/*
+ * mxq_moe_fp4 -- a mixture-of-experts layer for a few tokens, from the router's logits on.
+ *
+ *   p = softmax(logits[t]);  the k greatest logits choose the token's experts (ties to the
+ *   lower index);  share = p, divided by the sum of the k shares if renormalize
+ *   y[t] = sum over the chosen e of share * W2_e (silu(W1_e x[t]) * (W3_e x[t]))
+ *
+ * x        [T][ld_x] bf16; logits [T][ld_logits] FP32.
+ * w13      codes [E][2I][ld_w13] along H (rows 0 .. I-1 of an expert are W1, the gate, rows
+ *          I .. 2I-1 are W3), scales [E][2I][ld_s13]; expert_w13 and expert_s13 are the bytes
+ *          from one expert to the next (expert_w13 a multiple of 16).
+ * w2       codes [E][H][ld_w2] along I, scales [E][H][ld_s2]; expert_w2, expert_s2 likewise.
+ * y        [T][ld_y] of y_type.
+ * An expert whose logit is -inf is never taken, also when fewer than k are left; a token with
+ * no expert left gets y = 0.  A NaN logit orders above every number and makes the token's
+ * shares NaN.
+ * Products exact, sums in FP32; the hidden values are carried as 2 (y_type MXQ_BF16) or 3
+ * (MXQ_F32) bf16 terms, 16 or 24 bits.  The result does not depend on how workgroups are
+ * scheduled.
+ * workspace  256-byte aligned, at least the bytes that mxq_moe_fp4_workspace gives
+ *          (MXQ_ERR_SCRATCH otherwise); it holds nothing between calls.
+ * Limits   T <= 1024, E <= 1024, 1 <= k <= E, H and I < 2^24, (I + 128) * ld_w13 < 2^32.
+ */
+int mxq_moe_fp4_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int y_type, int64_t* bytes);
+int mxq_moe_fp4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int renormalize, const void* x, int64_t ld_x,
+                const float* logits, int64_t ld_logits, const uint8_t* w13_codes, int64_t ld_w13,
+                int64_t expert_w13, const uint8_t* w13_scales, int64_t ld_s13, int64_t expert_s13,
+                const uint8_t* w2_codes, int64_t ld_w2, int64_t expert_w2, const uint8_t* w2_scales, int64_t ld_s2,
+                int64_t expert_s2, void* y, int y_type, int64_t ld_y, void* workspace, int64_t workspace_bytes,
+                void* stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* mxq_status_string(int status);

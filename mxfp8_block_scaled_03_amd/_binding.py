@@ -7,7 +7,7 @@ import os
 PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(PKG, "libmxq.so")
 
-MXQ_F32, MXQ_BF16, MXQ_E4M3, MXQ_E5M2 = 0, 1, 2, 3
+MXQ_F32, MXQ_BF16, MXQ_E4M3, MXQ_E5M2, MXQ_E2M1 = 0, 1, 2, 3, 4
 MXQ_ROWWISE, MXQ_COLWISE = 0, 1
 MXQ_ACC_FP8_MFMA, MXQ_ACC_FP32 = 0, 1
 MXQ_ACT_NONE, MXQ_ACT_SILU = 0, 1
@@ -71,6 +71,22 @@ def lib():
         L.mxq_gemm_exact_plan.restype = ci
         ip = ctypes.POINTER(ci)
         L.mxq_gemm_exact_plan.argtypes = [i64, i64, i64, ci, ip, ip, ip, ip, ctypes.POINTER(i64)]
+        L.mxq_quantize_fp4.restype = ci
+        L.mxq_quantize_fp4.argtypes = [vp, ci, i64, i64, i64, ci, ci, vp, i64, vp, i64, vp]
+        L.mxq_quantize_fp4_sr.restype = ci
+        L.mxq_quantize_fp4_sr.argtypes = [vp, ci, i64, i64, i64, ci, ctypes.c_uint64, vp, i64, vp, i64, vp]
+        L.mxq_quantize_fp4_dual.restype = ci
+        L.mxq_quantize_fp4_dual.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+        L.mxq_dequantize_fp4.restype = ci
+        L.mxq_dequantize_fp4.argtypes = [vp, i64, vp, i64, i64, i64, vp, ci, i64, vp]
+        L.mxq_gemm_fp4.restype = ci
+        L.mxq_gemm_fp4.argtypes = [i64, i64, i64, vp, ci, i64, vp, i64, vp, i64, vp, i64, ctypes.c_float, vp, ci, vp,
+                                   ci, i64, vp]
+        L.mxq_moe_fp4_workspace.restype = ci
+        L.mxq_moe_fp4_workspace.argtypes = [i64, i64, i64, i64, i64, ci, ctypes.POINTER(i64)]
+        L.mxq_moe_fp4.restype = ci
+        L.mxq_moe_fp4.argtypes = [i64, i64, i64, i64, i64, ci, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, i64,
+                                  i64, vp, i64, i64, vp, ci, i64, vp, i64, vp]
         _lib = L
     return _lib
 
@@ -151,6 +167,49 @@ def mxq_gemm_exact_plan(M: int, N: int, K: int, cus: int) -> dict:
                                      ctypes.byref(wh), ctypes.byref(wb)), "mxq_gemm_exact_plan")
     return {"tile_n": tn.value, "ranges_per_tile": ks.value, "split_tiles": sp.value, "whole_tiles": wh.value,
             "workspace_bytes": wb.value}
+
+
+def mxq_quantize_fp4(src, src_type, rows, cols, ld_src, axis, rule, codes, ld_codes, scales, ld_scales,
+                     stream=None) -> int:
+    return lib().mxq_quantize_fp4(src, src_type, rows, cols, ld_src, axis, rule, codes, ld_codes, scales, ld_scales,
+                                  stream)
+
+
+def mxq_quantize_fp4_sr(src, src_type, rows, cols, ld_src, axis, seed, codes, ld_codes, scales, ld_scales,
+                        stream=None) -> int:
+    return lib().mxq_quantize_fp4_sr(src, src_type, rows, cols, ld_src, axis, seed, codes, ld_codes, scales, ld_scales,
+                                     stream)
+
+
+def mxq_quantize_fp4_dual(src, src_type, rows, cols, ld_src, row_codes, ld_row_codes, row_scales, ld_row_scales,
+                          col_codes, ld_col_codes, col_scales, ld_col_scales, stream=None) -> int:
+    return lib().mxq_quantize_fp4_dual(src, src_type, rows, cols, ld_src, row_codes, ld_row_codes, row_scales,
+                                       ld_row_scales, col_codes, ld_col_codes, col_scales, ld_col_scales, stream)
+
+
+def mxq_dequantize_fp4(codes, ld_codes, scales, ld_scales, L, K, dst, dst_type, ld_dst, stream=None) -> int:
+    return lib().mxq_dequantize_fp4(codes, ld_codes, scales, ld_scales, L, K, dst, dst_type, ld_dst, stream)
+
+
+def mxq_gemm_fp4(M, N, K, x, x_type, ld_x, x_scales, ld_xs, w_codes, ld_w, w_scales, ld_ws, alpha, bias, act, y,
+                 y_type, ld_y, stream=None) -> int:
+    return lib().mxq_gemm_fp4(M, N, K, x, x_type, ld_x, x_scales, ld_xs, w_codes, ld_w, w_scales, ld_ws, alpha, bias,
+                              act, y, y_type, ld_y, stream)
+
+
+def mxq_moe_fp4_workspace(T, H, I, E, k, y_type) -> int:
+    """Bytes of workspace that mxq_moe_fp4 needs (host logic only); raises MxqError."""
+    n = ctypes.c_int64()
+    _check(lib().mxq_moe_fp4_workspace(T, H, I, E, k, y_type, ctypes.byref(n)), "mxq_moe_fp4_workspace")
+    return n.value
+
+
+def mxq_moe_fp4(T, H, I, E, k, renormalize, x, ld_x, logits, ld_logits, w13_codes, ld_w13, expert_w13, w13_scales,
+                ld_s13, expert_s13, w2_codes, ld_w2, expert_w2, w2_scales, ld_s2, expert_s2, y, y_type, ld_y,
+                workspace, workspace_bytes, stream=None) -> int:
+    return lib().mxq_moe_fp4(T, H, I, E, k, renormalize, x, ld_x, logits, ld_logits, w13_codes, ld_w13, expert_w13,
+                             w13_scales, ld_s13, expert_s13, w2_codes, ld_w2, expert_w2, w2_scales, ld_s2, expert_s2,
+                             y, y_type, ld_y, workspace, workspace_bytes, stream)
 
 
 # ----------------------------------------------------------------- torch conveniences

@@ -41,12 +41,12 @@ const char* mxq_status_string(int status) {
     case MXQ_ERR_DTYPE: return "MXQ_ERR_DTYPE: dtype tag not accepted here";
     case MXQ_ERR_ARG: return "MXQ_ERR_ARG: invalid argument";
     case MXQ_ERR_HIP: return "MXQ_ERR_HIP: HIP runtime error while enqueuing";
-    case MXQ_ERR_SCRATCH: return "MXQ_ERR_SCRATCH: the problem needs more workspace than the static scratch holds";
+    case MXQ_ERR_SCRATCH: return "MXQ_ERR_SCRATCH: the problem needs more workspace than there is";
     default: return "unknown mxq status";
   }
 }
 
-int mxq_version(void) { return 102; }
+int mxq_version(void) { return 103; }
 
 int mxq_gemm_exact_plan(int64_t M, int64_t N, int64_t K, int cus, int* tile_n, int* ranges_per_tile,
                         int* split_tiles, int* whole_tiles, int64_t* workspace_bytes) {

@@ -93,4 +93,47 @@ hipError_t launch_gemm(int64_t M, int64_t N, int64_t K,
                        const GemmEpilogue& ep, int exact, void* workspace, int64_t workspace_bytes, bool may_alloc,
                        hipStream_t stream);
 
+// ---- MXFP4 (quantize_fp4.hip, gemm_fp4.hip, moe_fp4.hip).  Code rows hold 16 bytes per block;
+// ld_codes is in bytes.
+
+// One orientation: RNE codes under `rule`, or stochastically rounded ones (sr; ceil rule).
+hipError_t launch_quant4(const void* src, int src_bf16, int64_t rows, int64_t cols, int64_t ld_src, bool colwise,
+                         int rule, bool sr, uint64_t seed, uint8_t* codes, int64_t ld_codes, uint8_t* scales,
+                         int64_t ld_scales, hipStream_t stream);
+hipError_t launch_quant4_dual(const void* src, int src_bf16, int64_t rows, int64_t cols, int64_t ld_src, uint8_t* rcodes,
+                              int64_t ld_rc, uint8_t* rscales, int64_t ld_rs, uint8_t* ccodes, int64_t ld_cc,
+                              uint8_t* cscales, int64_t ld_cs, hipStream_t stream);
+hipError_t launch_dequant4(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales, int64_t L,
+                           int64_t K, void* dst, int dst_bf16, int64_t ld_dst, hipStream_t stream);
+
+// X in bf16 (ld_x in elements, xs null) or MXFP4 (ld_x in bytes), W in MXFP4.
+hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool x_fp4, int64_t ld_x, const uint8_t* xs,
+                           int64_t ld_xs, const uint8_t* wc, int64_t ld_w, const uint8_t* ws, int64_t ld_ws,
+                           const GemmEpilogue& ep, hipStream_t stream);
+
+// A mixture-of-experts layer; ld_ are row pitches and st_ expert pitches, in bytes for codes
+// and scales, in elements for x, logits and y.
+struct MoeFp4 {
+  int64_t T, H, I, E, k;
+  bool renorm;
+  const void* x;
+  int64_t ld_x;
+  const float* logits;
+  int64_t ld_logits;
+  const uint8_t* w13;
+  int64_t ld_w13, st_w13;
+  const uint8_t* s13;
+  int64_t ld_s13, st_s13;
+  const uint8_t* w2;
+  int64_t ld_w2, st_w2;
+  const uint8_t* s2;
+  int64_t ld_s2, st_s2;
+  void* y;
+  int64_t ld_y;
+  bool y_bf16;
+  void* workspace;
+};
+int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16);
+hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t stream);
+
 }  // namespace mxq

@@ -1,0 +1,374 @@
+"""GPU parity of the MXFP4 operators with the 64-bit reference (fp4_reference): codes and
+scales byte for byte, products and the expert layer within the reference's derived bounds."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_reference as ref
+import mxfp8_block_scaled_03_amd as mxq
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def data(rng, rows, cols, dtype, spread=20):
+    """Rows of very different sizes, signed zeros, exact ties."""
+    x = rng.standard_normal((rows, cols)) * np.exp2(rng.integers(-spread, spread + 1, (rows, 1)))
+    x.flat[::7] = np.copysign(0.0, rng.standard_normal(x.flat[::7].size))
+    x.flat[3::11] = rng.integers(-24, 25, x.flat[3::11].size) * 0.25
+    return torch.from_numpy(x.astype(np.float32)).to(dtype)
+
+
+def check_bytes(got, want, what):
+    got, want = got.cpu().numpy(), np.asarray(want)
+    assert got.shape == want.shape, what
+    if not np.array_equal(got, want):
+        at = np.argwhere(got != want)[0].tolist()
+        raise AssertionError("%s: at %s 0x%02x, expected 0x%02x" % (what, at, got[tuple(at)], want[tuple(at)]))
+
+
+SHAPES = [(1, 1), (3, 5), (7, 31), (5, 32), (4, 33), (16, 64), (9, 100), (130, 72), (33, 513), (129, 257), (260, 40)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("axis", ["row", "col"])
+@pytest.mark.parametrize("how", ["ceil", "ocp", "sr"])
+def test_quantize(dtype, axis, how):
+    rng = np.random.default_rng(10)
+    for rows, cols in SHAPES:
+        say("quantize_fp4 %s %s %s %dx%d" % (dtype, axis, how, rows, cols))
+        x = data(rng, rows, cols, dtype)
+        lines = f64(x) if axis == "row" else f64(x).T
+        seed = 0xFEDCBA9876543210 + rows
+        want = ref.quantize(lines, "ocp" if how == "ocp" else "ceil", seed if how == "sr" else None)
+        L, nb = want[1].shape
+        # outputs wider than needed, rows of the source padded: nothing else is touched
+        codes = torch.full((L, 16 * nb + 16), 0xCD, dtype=torch.uint8, device=DEV)
+        scales = torch.full((L, nb + 3), 0xCD, dtype=torch.uint8, device=DEV)
+        wide = torch.full((rows, cols + 3), 99.0, dtype=dtype, device=DEV)
+        wide[:, :cols] = x.to(DEV)
+        call = (lambda y, **k: mxq.quantize_fp4_sr(y, seed, axis, **k)) if how == "sr" else \
+            (lambda y, **k: mxq.quantize_fp4(y, axis, rule=how, **k))
+        call(wide[:, :cols], codes=codes, scales=scales)
+        assert (codes[:, 16 * nb:] == 0xCD).all() and (scales[:, nb:] == 0xCD).all()
+        check_bytes(scales[:, :nb], want[1], "scales")
+        check_bytes(codes[:, :16 * nb], want[0], "codes")
+        c, s = call(x.to(DEV))
+        check_bytes(s, want[1], "scales, dense")
+        check_bytes(c, want[0], "codes, dense")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_quantize_extremes(dtype):
+    """Blocks of zeros, subnormals, the largest values, infinities and NaN; scale byte 0."""
+    rng = np.random.default_rng(11)
+    x = np.zeros((12, 64), np.float32)
+    x[1] = rng.standard_normal(64) * 1e-39
+    x[2] = rng.standard_normal(64) * 2.0 ** -127
+    x[3] = 3.3e38 * rng.uniform(-1, 1, 64)
+    x[4, 5], x[5, 6], x[6, 40] = np.inf, -np.inf, np.nan
+    x[7] = np.copysign(0, rng.standard_normal(64))
+    x[8, 0], x[8, 1:] = 6e30, 1e-30
+    x[9] = 2.0 ** -149
+    x[10] = 6.0 * 2.0 ** rng.integers(-140, 120, 64)
+    x[11] = np.repeat([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], 8)
+    t = torch.from_numpy(x).to(dtype)
+    for axis in ("row", "col"):
+        lines = f64(t) if axis == "row" else f64(t).T
+        for how in ("ceil", "ocp"):
+            got = mxq.quantize_fp4(t.to(DEV), axis, rule=how)
+            want = ref.quantize(lines, how)
+            check_bytes(got[1], want[1], "%s %s scales" % (axis, how))
+            check_bytes(got[0], want[0], "%s %s codes" % (axis, how))
+        got, want = mxq.quantize_fp4_sr(t.to(DEV), 5, axis), ref.quantize(lines, "ceil", 5)
+        check_bytes(got[1], want[1], axis + " sr scales")
+        check_bytes(got[0], want[0], axis + " sr codes")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_quantize_dual(dtype):
+    rng = np.random.default_rng(12)
+    for rows, cols in SHAPES + [(300, 1000), (1030, 264)]:
+        say("quantize_fp4_dual %s %dx%d" % (dtype, rows, cols))
+        x = data(rng, rows, cols, dtype).to(DEV)
+        rc, rs, cc, cs = mxq.quantize_fp4_dual(x)
+        for got, want in zip((rc, rs, cc, cs), mxq.quantize_fp4(x, "row") + mxq.quantize_fp4(x, "col")):
+            assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_dequantize(dtype):
+    rng = np.random.default_rng(13)
+    for L, K in [(1, 1), (3, 7), (5, 32), (4, 33), (9, 100), (2, 2048), (65, 515), (256, 32)]:
+        codes = rng.integers(0, 256, (L, 16 * ref.blocks(K)), dtype=np.uint8)
+        scales = rng.integers(0, 256, (L, ref.blocks(K)), dtype=np.uint8)
+        got = mxq.dequantize_fp4(torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV), K, out_dtype=dtype)
+        with np.errstate(over="ignore"):
+            want = torch.from_numpy(ref.values(codes, scales, K).astype(np.float32)).to(dtype)
+        got = got.cpu()
+        nan = torch.isnan(want)
+        assert torch.equal(torch.isnan(got), nan)
+        assert torch.equal(got[~nan], want[~nan]) and torch.equal(torch.signbit(got[~nan]), torch.signbit(want[~nan]))
+
+
+# ------------------------------------------------------------------------------- products
+
+def operand(rng, rows, K, pad=0, std=1.0):
+    """Codes and scales on the GPU (rows wider by `pad` blocks of garbage) and their values."""
+    x = rng.standard_normal((rows, K)) * std
+    x.flat[::97] *= 50
+    codes, scales = ref.quantize(x.astype(np.float32).astype(np.float64)) if rows * K < 40000 else fast_codes(rng, rows, K)
+    nb = scales.shape[1]
+    v = ref.values(codes, scales, K)
+    c = np.full((rows, 16 * (nb + pad)), 0x5D, np.uint8)
+    s = np.full((rows, nb + pad), 255, np.uint8)
+    c[:, :16 * nb], s[:, :nb] = codes, scales
+    return torch.from_numpy(c).to(DEV)[:, :16 * nb], torch.from_numpy(s).to(DEV)[:, :nb], v
+
+
+def fast_codes(rng, rows, K):
+    return (rng.integers(0, 256, (rows, 16 * ref.blocks(K)), dtype=np.uint8),
+            rng.integers(118, 128, (rows, ref.blocks(K)), dtype=np.uint8))
+
+
+def bf16_operand(rng, rows, K, pad=0):
+    x = torch.from_numpy(rng.standard_normal((rows, K)).astype(np.float32)).to(BF16)
+    wide = torch.full((rows, K + pad), float("nan"), dtype=BF16, device=DEV)
+    wide[:, :K] = x.to(DEV)
+    return wide[:, :K], None, f64(x)
+
+
+def check_product(y, want, bound, what):
+    got = f64(y)
+    assert np.isfinite(got).all(), what
+    err = np.abs(got - want)
+    assert (err <= bound).all(), "%s: off by %.3g, bound %.3g, at %s" % (
+        what, err.flat[np.argmax(err - bound)], bound.flat[np.argmax(err - bound)], np.argwhere(err > bound)[0].tolist())
+
+
+PRODUCTS = [(1, 1, 1), (1, 16, 32), (2, 5, 33), (3, 17, 127), (1, 64, 128), (16, 40, 129), (17, 33, 300), (15, 130, 1000),
+            (40, 70, 257), (64, 64, 1024), (65, 65, 1025), (130, 200, 511), (1, 300, 4096), (257, 129, 640), (300, 520, 384)]
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp4"])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_gemm(xt, out):
+    rng = np.random.default_rng(20)
+    for n, (M, N, K) in enumerate(PRODUCTS):
+        pad = n % 3
+        x, xs, xv = operand(rng, M, K, pad) if xt == "fp4" else bf16_operand(rng, M, K, pad)
+        w, ws, wv = operand(rng, N, K, pad, 0.1)
+        bias = torch.from_numpy(rng.standard_normal(N).astype(np.float32)).to(DEV) if n % 2 else None
+        alpha, act = (0.75 if n % 5 == 1 else 1.0), ("silu" if n % 3 == 2 else None)
+        say("gemm_fp4 %s %s %dx%dx%d" % (xt, out, M, N, K))
+        wide = torch.full((M, N + pad), 7.0, dtype=out, device=DEV)
+        y = mxq.gemm_fp4(x, xs, w, ws, K, alpha=alpha, bias=bias, act=act, out=wide[:, :N])
+        want, bound = ref.product(xv, wv, alpha, None if bias is None else f64(bias), act, out == BF16)
+        check_product(y, want, bound, "%dx%dx%d" % (M, N, K))
+        assert (wide[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp4"])
+@pytest.mark.parametrize("M,N,K", [(512, 768, 512), (700, 1030, 289), (1030, 1100, 1000), (2100, 64, 160), (64, 2100, 4001)])
+def test_gemm_large(xt, M, N, K):
+    rng = np.random.default_rng(21)
+    x, xs, xv = operand(rng, M, K) if xt == "fp4" else bf16_operand(rng, M, K)
+    w, ws, wv = operand(rng, N, K)
+    y = mxq.gemm_fp4(x, xs, w, ws, K, out_dtype=F32)
+    check_product(y, *ref.product(xv, wv), "%dx%dx%d" % (M, N, K))
+    assert torch.equal(y, mxq.gemm_fp4(x, xs, w, ws, K, out_dtype=F32))
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp4"])
+def test_gemm_empty_and_special(xt):
+    rng = np.random.default_rng(22)
+    x, xs, xv = operand(rng, 5, 96) if xt == "fp4" else bf16_operand(rng, 5, 96)
+    w, ws, wv = operand(rng, 33, 96)
+    bias = torch.arange(33, dtype=F32, device=DEV)
+    none = None if xs is None else xs[:, :0]
+    y = mxq.gemm_fp4(x[:, :0], none, w[:, :0], ws[:, :0], 0, bias=bias, out_dtype=F32)
+    assert torch.equal(y, bias.expand(5, 33))
+    assert mxq.gemm_fp4(x[:0], None if xs is None else xs[:0], w, ws, 96).shape == (0, 33)
+    assert mxq.gemm_fp4(x, xs, w[:0], ws[:0], 96).shape == (5, 0)
+    # a NaN scale byte reaches its row and column only
+    ws2 = ws.clone()
+    ws2[7, 1] = 255
+    y = f64(mxq.gemm_fp4(x, xs, w, ws2, 96, out_dtype=F32))
+    assert np.isnan(y[:, 7]).all() and np.isfinite(np.delete(y, 7, 1)).all()
+    if xs is not None:
+        xs2 = xs.clone()
+        xs2[2, 2] = 255
+        y = f64(mxq.gemm_fp4(x, xs2, w, ws, 96, out_dtype=F32))
+        assert np.isnan(y[2]).all() and np.isfinite(np.delete(y, 2, 0)).all()
+    # the smallest scales: 2^-127 against large ones, products in FP32's normal range
+    wz = torch.zeros_like(ws)
+    big = torch.full((5, 96), 2.0 ** 100, dtype=BF16, device=DEV)
+    if xs is None:
+        y, want = mxq.gemm_fp4(big, None, w, wz, 96, out_dtype=F32), ref.product(
+            np.full((5, 96), 2.0 ** 100), ref.values(w.cpu().numpy(), np.zeros((33, 3), np.uint8), 96))
+    else:
+        xb = torch.full_like(xs, 227)
+        y, want = mxq.gemm_fp4(x, xb, w, wz, 96, out_dtype=F32), ref.product(
+            ref.values(x.cpu().numpy(), np.full((5, 3), 227, np.uint8), 96),
+            ref.values(w.cpu().numpy(), np.zeros((33, 3), np.uint8), 96))
+    check_product(y, *want, "smallest scales")
+
+
+def test_gemm_infinite_input():
+    rng = np.random.default_rng(23)
+    x, _, _ = bf16_operand(rng, 4, 64)
+    w = torch.full((16, 32), 0x22, dtype=torch.uint8, device=DEV)          # all ones
+    ws = torch.full((16, 2), 127, dtype=torch.uint8, device=DEV)
+    x[1, 3], x[2, 60] = float("inf"), float("nan")
+    y = mxq.gemm_fp4(x, None, w, ws, 64, out_dtype=F32)
+    assert torch.isinf(y[1]).all() and torch.isnan(y[2]).all() and torch.isfinite(y[[0, 3]]).all()
+
+
+def test_linear_gradients():
+    """dX and dW of a linear layer against float64 products of the same quantized values, and
+    the mean of many stochastic roundings against the unquantized gradient."""
+    rng = np.random.default_rng(24)
+    M, N, K = 96, 160, 64
+    dy = torch.from_numpy((rng.standard_normal((M, N)) * 1e-3).astype(np.float32)).to(BF16)
+    w, ws, wv = operand(rng, K, N)
+    xt, xts, xv = operand(rng, K, M)
+    r, rs = mxq.quantize_fp4_sr(dy.to(DEV), 3, "row")
+    c, cs = mxq.quantize_fp4_sr(dy.to(DEV), 4, "col")
+    rv = ref.values(r.cpu().numpy(), rs.cpu().numpy(), N)
+    cv = ref.values(c.cpu().numpy(), cs.cpu().numpy(), M)
+    check_product(mxq.gemm_fp4(r, rs, w, ws, N, out_dtype=BF16), *ref.product(rv, wv, bf16=True), "dx")
+    check_product(mxq.gemm_fp4(c, cs, xt, xts, M, out_dtype=F32), *ref.product(cv, xv), "dw")
+    total, n = torch.zeros((M, K), dtype=torch.float64, device=DEV), 400
+    for seed in range(n):
+        r, rs = mxq.quantize_fp4_sr(dy.to(DEV), seed, "row")
+        total += mxq.gemm_fp4(r, rs, w, ws, N, out_dtype=F32)
+    # a rounding's variance is at most (step / 2)^2 with a step of at most 2 S, S <= amax / 3
+    step = 2 * np.abs(f64(dy)).reshape(M, -1, 32).max(-1) / 3
+    var = (np.repeat(step, 32, 1) / 2) ** 2 @ (wv ** 2).T / n
+    off = np.abs(total.cpu().numpy() / n - f64(dy) @ wv.T)
+    assert (off <= 6 * np.sqrt(var) + 1e-9).all()
+
+
+# -------------------------------------------------------------------------------- experts
+
+def experts(rng, E, H, I):
+    w = [operand(rng, E * r, c, 0, c ** -0.5) for r, c in ((2 * I, H), (H, I))]
+    out = []
+    for (codes, scales, v), rows in zip(w, (2 * I, H)):
+        pitch = (scales.shape[1] + 15) // 16 * 16
+        s = torch.full((E, rows, pitch), 255, dtype=torch.uint8, device=DEV)
+        s[..., :scales.shape[1]] = scales.view(E, rows, -1)
+        out += [codes.reshape(E, rows, -1).contiguous(), s[..., :scales.shape[1]], v.reshape(E, rows, -1)]
+    return out
+
+
+def run_experts(rng, T, H, I, E, k, renorm, out, logits=None):
+    w13, s13, v13, w2, s2, v2 = experts(rng, E, H, I)
+    x, _, xv = bf16_operand(rng, T, H, 3)
+    lg = rng.standard_normal((T, E)) * 1.5 if logits is None else np.asarray(logits, np.float64)
+    lg = lg.astype(np.float32)
+    y = mxq.moe_fp4(x, torch.from_numpy(lg).to(DEV), w13, s13, w2, s2, k, renormalize=renorm, out_dtype=out)
+    want, bound = ref.moe(xv, lg.astype(np.float64), v13, v2, k, renorm, out == BF16)
+    check_product(y, want, bound, "T%d H%d I%d E%d k%d" % (T, H, I, E, k))
+    return y
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,H,I,E,k", [
+    (1, 32, 16, 1, 1), (1, 64, 40, 8, 2), (1, 256, 136, 70, 5), (2, 100, 30, 4, 4), (5, 130, 65, 16, 3), (7, 200, 104, 60, 6),
+    (16, 64, 32, 8, 2), (17, 96, 48, 3, 2), (40, 64, 24, 4, 3), (64, 128, 64, 16, 4), (70, 33, 129, 2, 1), (3, 64, 24, 130, 2)])
+def test_experts(out, renorm, T, H, I, E, k):
+    say("moe_fp4 T%d H%d I%d E%d k%d %s" % (T, H, I, E, k, out))
+    run_experts(np.random.default_rng(30), T, H, I, E, k, renorm, out)
+
+
+def test_experts_ties_and_masks():
+    """Equal logits (ties to the lower index), -inf and the lowest float, rows with fewer than k
+    experts or none, one expert for everybody."""
+    rng = np.random.default_rng(31)
+    low = np.finfo(np.float32).min
+    lg = np.zeros((8, 6))
+    lg[1] = [1, 2, 2, 2, 0, 2]
+    lg[2] = [-np.inf, 0, -np.inf, -np.inf, 1, -np.inf]
+    lg[3] = -np.inf
+    lg[4] = low
+    lg[5] = [low, low, 3, low, low, low]
+    lg[6] = [-0.0, 0.0, -0.0, -1, -1, -1]
+    lg[7] = [-np.inf, -np.inf, 5, -np.inf, -np.inf, -np.inf]
+    for renorm in (True, False):
+        for out in (F32, BF16):
+            y = run_experts(rng, 8, 96, 40, 6, 3, renorm, out, lg)
+            assert (y[3] == 0).all()
+    run_experts(rng, 40, 64, 32, 6, 2, True, F32, np.tile([0, 9, 0, 0, 8, 0], (40, 1)))
+    run_experts(rng, 1, 64, 32, 9, 2, True, F32, [[-np.inf] * 8 + [0.0]])
+
+
+def test_experts_nan_logits():
+    """A NaN logit makes its own token NaN and no other."""
+    rng = np.random.default_rng(32)
+    w13, s13, _, w2, s2, _ = experts(rng, 4, 64, 32)
+    x, _, _ = bf16_operand(rng, 3, 64)
+    lg = torch.zeros((3, 4), device=DEV)
+    lg[1, 2] = float("nan")
+    y = mxq.moe_fp4(x, lg, w13, s13, w2, s2, 2, out_dtype=F32)
+    assert torch.isnan(y[1]).all() and torch.isfinite(y[[0, 2]]).all()
+
+
+def test_experts_strided_weights_and_output():
+    """Experts that are slices of wider arrays, logits with a pitch, a preallocated output."""
+    rng = np.random.default_rng(33)
+    E, T, H, I, k = 5, 6, 96, 72, 2
+    w13, s13, v13, w2, s2, v2 = experts(rng, E, H, I)
+
+    def embed(t, rows, cols):
+        big = torch.full((E, t.shape[1] + rows, t.shape[2] + cols), 0x7F, dtype=torch.uint8, device=DEV)
+        big[:, :t.shape[1], :t.shape[2]] = t
+        return big[:, :t.shape[1], :t.shape[2]]
+    x, _, xv = bf16_operand(rng, T, H)
+    lg = torch.from_numpy(rng.standard_normal((T, E + 4)).astype(np.float32)).to(DEV)[:, 2:2 + E]
+    out = torch.full((T, H + 5), 3.0, dtype=BF16, device=DEV)
+    y = mxq.moe_fp4(x, lg, embed(w13, 3, 16), embed(s13, 1, 3), embed(w2, 2, 32), embed(s2, 4, 1), k, out=out[:, :H])
+    want, bound = ref.moe(xv, f64(lg), v13, v2, k, True, True)
+    check_product(y, want, bound, "strided")
+    assert (out[:, H:] == 3.0).all()
+
+
+def test_other_stream_and_graph():
+    """The operators on a side stream, and captured into a graph that is replayed on new inputs
+    with eager work between the replays."""
+    rng = np.random.default_rng(34)
+    w13, s13, _, w2, s2, _ = experts(rng, 8, 128, 64)
+    x = torch.from_numpy(rng.standard_normal((4, 128)).astype(np.float32)).to(BF16).to(DEV)
+    lg = torch.from_numpy(rng.standard_normal((4, 8)).astype(np.float32)).to(DEV)
+
+    def step(x, lg):
+        c, s = mxq.quantize_fp4(x)
+        return (mxq.moe_fp4(x, lg, w13, s13, w2, s2, 2), mxq.gemm_fp4(x, None, w13[0], s13[0], 128),
+                mxq.gemm_fp4(c, s, w13[1], s13[1], 128), mxq.dequantize_fp4(c, s, 128), *mxq.quantize_fp4_dual(x))
+
+    want = step(x, lg)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step(x, lg)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    gx, gl = x.clone(), lg.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(gx, gl)
+    for r in range(4):
+        gx.copy_(torch.roll(x, r, 0) * (r + 1))
+        gl.copy_(torch.roll(lg, r, 1))
+        want = step(gx, gl)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want)), r
