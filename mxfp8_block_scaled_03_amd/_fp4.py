@@ -3,32 +3,63 @@ mixture-of-experts layer (the ``mxq_*_fp4`` entry points of include/mxq.h).  Arg
 and marshalling only, like ``_binding``; every call raises if the library is missing."""
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
-from ._binding import (_ACT, _AXIS, _RULE, MXQ_BF16, MXQ_COLWISE, MXQ_E2M1, MXQ_F32, MXQ_ROWWISE, MxqError, _ld,
-                       _req_2d, _req_cuda, _req_wide, lib)
+from ._binding import (_ACT, _AXIS, _RULE, MXQ_BF16, MXQ_COLWISE, MXQ_E2M1, MXQ_F32, MxqError, _req_2d,
+                       _req_wide, lib, mxq_moe_fp4_workspace)
 
 _WIDE = {torch.float32: MXQ_F32, torch.bfloat16: MXQ_BF16}
+_U8 = torch.uint8
+_stream = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
+_entry = {}
 
 
-def _call(name: str, device, *args):
-    """The library's entry point `name` on torch's current stream of `device`."""
-    fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+def _call(name: str, device: int, *args):
+    """The library's entry point `name` on torch's current stream of the device."""
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(lib(), name)
+    if device == _current():
+        status = fn(*args, _stream(device))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+            status = fn(*args, _stream(device))
     if status != 0:
         raise MxqError(status, name)
 
 
-def _same_device(first, *named):
+# These calls are short, so the checks are made in one pass over each tensor: what _req_2d
+# rejects is found with few attribute reads, and the message is left to _req_2d.
+
+def _lines(t, name: str, dtype, rows, cols: int) -> int:
+    """Checks rows of at least `cols` elements, `rows` of them at least; the row pitch."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 2:
+        _req_2d(t, name, dtype)
+    r, c = t.shape
+    pitch, step = t.stride()
+    if c < cols or (rows is not None and r < rows) or (r > 1 and c > 0 and (step != 1 or pitch < c)):
+        _req_2d(t, name, dtype, rows, cols)
+    return pitch if r > 0 and pitch >= c else max(c, 1)
+
+
+def _on_one_device(first, *named) -> int:
+    """The index of the device that holds `first` and every other tensor."""
+    device = first.get_device()
     for name, t in named:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != device and device >= 0:
+            if t.get_device() < 0:
+                raise ValueError("%s must be a CUDA (HIP device) tensor, got device %s" % (name, t.device))
             raise ValueError("%s is on %s, expected %s" % (name, t.device, first.device))
+    if device < 0:
+        raise ValueError("expected CUDA (HIP device) tensors, got device %s" % first.device)
+    return device
+
+
+def _wide(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype not in _WIDE:
+        _req_wide(t, name)
+    return _lines(t, name, t.dtype, None, 0)
 
 
 def _blocks(k: int) -> int:
@@ -39,22 +70,31 @@ def _code_array(lines: int, k: int, device):
     """Empty codes [lines][16 * blocks] and scales [lines][blocks], the scale rows padded to 16
     bytes (the layout that the product reads fastest)."""
     nb = _blocks(k)
-    return (torch.empty((lines, 16 * nb), dtype=torch.uint8, device=device),
-            torch.empty((lines, (nb + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :nb])
+    pitch = (nb + 15) // 16 * 16
+    return (torch.empty((lines, 16 * nb), dtype=_U8, device=device),
+            torch.empty_strided((lines, nb), (pitch, 1), dtype=_U8, device=device))
 
 
-def _outputs(x, lines: int, k: int, codes, scales):
-    nb = _blocks(k)
-    if codes is not None:
-        _req_2d(codes, "codes", torch.uint8, lines, 16 * nb)
-    if scales is not None:
-        _req_2d(scales, "scales", torch.uint8, lines, nb)
-    _req_cuda(("x", x), ("codes", codes), ("scales", scales))
-    _same_device(x, ("codes", codes), ("scales", scales))
+def _orient(x, axis, codes, scales):
+    """What the one-orientation quantizers share: pitch of x, axis tag, device, outputs."""
+    ld = _wide(x, "x")
+    if axis not in _AXIS:
+        raise ValueError("axis must be 'row' or 'col'")
+    ax = _AXIS[axis]
+    L, K = x.shape
+    if ax == MXQ_COLWISE:
+        L, K = K, L
+    nb = _blocks(K)
+    ld_c = None if codes is None else _lines(codes, "codes", _U8, L, 16 * nb)
+    ld_s = None if scales is None else _lines(scales, "scales", _U8, L, nb)
+    device = _on_one_device(x, ("codes", codes), ("scales", scales))
     if codes is None or scales is None:
-        c, s = _code_array(lines, k, x.device)
-        codes, scales = c if codes is None else codes, s if scales is None else scales
-    return codes, scales
+        c, s = _code_array(L, K, x.device)
+        if codes is None:
+            codes, ld_c = c, max(16 * nb, 1)
+        if scales is None:
+            scales, ld_s = s, max((nb + 15) // 16 * 16, 1)
+    return ld, ax, device, codes, ld_c, scales, ld_s
 
 
 def quantize_fp4(x, axis="row", codes=None, scales=None, rule: str = "ceil"):
@@ -66,45 +106,33 @@ def quantize_fp4(x, axis="row", codes=None, scales=None, rule: str = "ceil"):
     scales are E8M0 bytes.  rule "ceil" (no code saturates) or "ocp" (the MX specification's
     floor(log2 amax) - 2), see mxq_quantize_fp4.  Preallocated outputs may be wider.
     """
-    _req_wide(x, "x")
-    if axis not in _AXIS:
-        raise ValueError("axis must be 'row' or 'col'")
     if rule not in _RULE:
         raise ValueError("rule must be 'ceil' or 'ocp'")
-    rows, cols = x.shape
-    ax = _AXIS[axis]
-    L, K = (rows, cols) if ax == MXQ_ROWWISE else (cols, rows)
-    codes, scales = _outputs(x, L, K, codes, scales)
-    _call("mxq_quantize_fp4", x.device, x.data_ptr(), _WIDE[x.dtype], rows, cols, _ld(x), ax, _RULE[rule],
-          codes.data_ptr(), _ld(codes), scales.data_ptr(), _ld(scales))
+    ld, ax, device, codes, ld_c, scales, ld_s = _orient(x, axis, codes, scales)
+    _call("mxq_quantize_fp4", device, x.data_ptr(), _WIDE[x.dtype], x.shape[0], x.shape[1], ld, ax, _RULE[rule],
+          codes.data_ptr(), ld_c, scales.data_ptr(), ld_s)
     return codes, scales
 
 
 def quantize_fp4_sr(x, seed: int, axis="row", codes=None, scales=None):
     """quantize_fp4() with stochastically rounded codes (Philox4x32-10 keyed by `seed`, see
     mxq_quantize_fp4_sr): for gradients."""
-    _req_wide(x, "x")
-    if axis not in _AXIS:
-        raise ValueError("axis must be 'row' or 'col'")
-    rows, cols = x.shape
-    ax = _AXIS[axis]
-    L, K = (rows, cols) if ax == MXQ_ROWWISE else (cols, rows)
-    codes, scales = _outputs(x, L, K, codes, scales)
-    _call("mxq_quantize_fp4_sr", x.device, x.data_ptr(), _WIDE[x.dtype], rows, cols, _ld(x), ax,
-          int(seed) & (2 ** 64 - 1), codes.data_ptr(), _ld(codes), scales.data_ptr(), _ld(scales))
+    ld, ax, device, codes, ld_c, scales, ld_s = _orient(x, axis, codes, scales)
+    _call("mxq_quantize_fp4_sr", device, x.data_ptr(), _WIDE[x.dtype], x.shape[0], x.shape[1], ld, ax,
+          int(seed) & (2 ** 64 - 1), codes.data_ptr(), ld_c, scales.data_ptr(), ld_s)
     return codes, scales
 
 
 def quantize_fp4_dual(x):
     """Both orientations of a 2-D bf16/fp32 CUDA tensor from one read of it: (row_codes,
     row_scales, col_codes, col_scales), as quantize_fp4(x, "row") and quantize_fp4(x, "col")."""
-    _req_wide(x, "x")
-    _req_cuda(("x", x))
+    ld = _wide(x, "x")
+    device = _on_one_device(x)
     rows, cols = x.shape
     rc, rs = _code_array(rows, cols, x.device)
     cc, cs = _code_array(cols, rows, x.device)
-    _call("mxq_quantize_fp4_dual", x.device, x.data_ptr(), _WIDE[x.dtype], rows, cols, _ld(x), rc.data_ptr(), _ld(rc),
-          rs.data_ptr(), _ld(rs), cc.data_ptr(), _ld(cc), cs.data_ptr(), _ld(cs))
+    _call("mxq_quantize_fp4_dual", device, x.data_ptr(), _WIDE[x.dtype], rows, cols, ld, rc.data_ptr(), rc.stride(0),
+          rs.data_ptr(), rs.stride(0), cc.data_ptr(), cc.stride(0), cs.data_ptr(), cs.stride(0))
     return rc, rs, cc, cs
 
 
@@ -115,14 +143,14 @@ def dequantize_fp4(codes, scales, K: int, out_dtype=None):
         raise ValueError("out_dtype must be float32 or bfloat16")
     if K < 0:
         raise ValueError("K must be >= 0")
-    _req_2d(codes, "codes", torch.uint8, None, 16 * _blocks(K))
+    nb = _blocks(K)
+    ld_c = _lines(codes, "codes", _U8, None, 16 * nb)
     L = codes.shape[0]
-    _req_2d(scales, "scales", torch.uint8, L, _blocks(K))
-    _req_cuda(("codes", codes), ("scales", scales))
-    _same_device(codes, ("scales", scales))
+    ld_s = _lines(scales, "scales", _U8, L, nb)
+    device = _on_one_device(codes, ("scales", scales))
     dst = torch.empty((L, K), dtype=out_dtype, device=codes.device)
-    _call("mxq_dequantize_fp4", codes.device, codes.data_ptr(), _ld(codes), scales.data_ptr(), _ld(scales), L, K,
-          dst.data_ptr(), _WIDE[out_dtype], max(K, 1))
+    _call("mxq_dequantize_fp4", device, codes.data_ptr(), ld_c, scales.data_ptr(), ld_s, L, K, dst.data_ptr(),
+          _WIDE[out_dtype], max(K, 1))
     return dst
 
 
@@ -136,48 +164,52 @@ def gemm_fp4(x, x_scales, w_codes, w_scales, K: int, alpha: float = 1.0, bias=No
     if K < 0:
         raise ValueError("K must be >= 0")
     nb = _blocks(K)
-    _req_2d(w_codes, "w_codes", torch.uint8, None, 16 * nb)
+    ld_w = _lines(w_codes, "w_codes", _U8, None, 16 * nb)
     N = w_codes.shape[0]
-    _req_2d(w_scales, "w_scales", torch.uint8, N, nb)
+    ld_ws = _lines(w_scales, "w_scales", _U8, N, nb)
     if x_scales is None:
-        _req_2d(x, "x", torch.bfloat16)
+        ld_x = _lines(x, "x", torch.bfloat16, None, K)
+        M = x.shape[0]
         if x.shape[1] != K:
             raise ValueError("x has %d columns, expected K = %d" % (x.shape[1], K))
-        M = x.shape[0]
+        x_type, xs_ptr, ld_xs = MXQ_BF16, None, 0
     else:
-        _req_2d(x, "x", torch.uint8, None, 16 * nb)
+        ld_x = _lines(x, "x", _U8, None, 16 * nb)
         M = x.shape[0]
-        _req_2d(x_scales, "x_scales", torch.uint8, M, nb)
+        ld_xs = _lines(x_scales, "x_scales", _U8, M, nb)
+        x_type, xs_ptr = MXQ_E2M1, x_scales.data_ptr()
     if bias is not None and (not isinstance(bias, torch.Tensor) or bias.dtype != torch.float32 or bias.dim() != 1
                              or bias.shape[0] != N or (N > 1 and bias.stride(0) != 1)):
         raise ValueError("bias must be a contiguous 1-D float32 tensor of N = %d elements" % N)
     if act not in _ACT:
         raise ValueError("act must be None or 'silu'")
     if out is not None:
-        _req_wide(out, "out")
+        ld_y = _wide(out, "out")
         if tuple(out.shape) != (M, N):
             raise ValueError("out must have shape (M, N) = (%d, %d), got %s" % (M, N, tuple(out.shape)))
     elif out_dtype is not None and out_dtype not in _WIDE:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    _req_cuda(("x", x), ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("bias", bias),
-              ("out", out))
-    _same_device(x, ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("bias", bias), ("out", out))
+    device = _on_one_device(x, ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("bias", bias),
+                            ("out", out))
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=x.device)
-    _call("mxq_gemm_fp4", x.device, M, N, K, x.data_ptr(), MXQ_BF16 if x_scales is None else MXQ_E2M1, _ld(x),
-          None if x_scales is None else x_scales.data_ptr(), 0 if x_scales is None else _ld(x_scales),
-          w_codes.data_ptr(), _ld(w_codes), w_scales.data_ptr(), _ld(w_scales), float(alpha),
-          None if bias is None else bias.data_ptr(), _ACT[act], out.data_ptr(), _WIDE[out.dtype], _ld(out))
+        ld_y = max(N, 1)
+    _call("mxq_gemm_fp4", device, M, N, K, x.data_ptr(), x_type, ld_x, xs_ptr, ld_xs, w_codes.data_ptr(), ld_w,
+          w_scales.data_ptr(), ld_ws, alpha, None if bias is None else bias.data_ptr(), _ACT[act], out.data_ptr(),
+          _WIDE[out.dtype], ld_y)
     return out
 
 
-def _req_expert(t, name: str, experts: int, rows: int, cols: int):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.dim() != 3:
+def _expert(t, name: str, experts: int, rows: int, cols: int):
+    """Checks a stack of code or scale rows; the expert and row pitches."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _U8 or t.dim() != 3:
         raise ValueError("%s must be a 3-D uint8 tensor" % name)
-    if t.shape[0] != experts or t.shape[1] != rows or t.shape[2] < cols:
-        raise ValueError("%s must have shape (%d, %d, >= %d), got %s" % (name, experts, rows, cols, tuple(t.shape)))
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    shape, stride = t.shape, t.stride()
+    if shape[0] != experts or shape[1] != rows or shape[2] < cols:
+        raise ValueError("%s must have shape (%d, %d, >= %d), got %s" % (name, experts, rows, cols, tuple(shape)))
+    if shape[2] > 1 and stride[2] != 1:
         raise ValueError("%s must have unit stride along its last dimension" % name)
+    return stride[0], stride[1]
 
 
 def moe_fp4(x, logits, w13_codes, w13_scales, w2_codes, w2_scales, k: int, renormalize: bool = True, out_dtype=None,
@@ -190,41 +222,35 @@ def moe_fp4(x, logits, w13_codes, w13_scales, w2_codes, w2_scales, k: int, renor
     renormalize: the k shares sum to 1.  Returns [T][H] in out_dtype (bf16 by default, or fp32).
     See mxq_moe_fp4 for ties, masked experts and precision.
     """
-    _req_2d(x, "x", torch.bfloat16)
-    _req_2d(logits, "logits", torch.float32)
-    (T, H), E = x.shape, logits.shape[1]
-    if logits.shape[0] != T:
-        raise ValueError("logits has %d rows, expected T = %d" % (logits.shape[0], T))
+    ld_x = _lines(x, "x", torch.bfloat16, None, 0)
+    ld_l = _lines(logits, "logits", torch.float32, None, 0)
+    (T, H), (rows, E) = x.shape, logits.shape
+    if rows != T:
+        raise ValueError("logits has %d rows, expected T = %d" % (rows, T))
     if not isinstance(w13_codes, torch.Tensor) or w13_codes.dim() != 3 or w13_codes.shape[1] % 2:
         raise ValueError("w13_codes must be a 3-D tensor with an even number of rows")
     I = w13_codes.shape[1] // 2
     if not 1 <= k <= E:
         raise ValueError("k must be between 1 and E = %d" % E)
-    _req_expert(w13_codes, "w13_codes", E, 2 * I, 16 * _blocks(H))
-    _req_expert(w13_scales, "w13_scales", E, 2 * I, _blocks(H))
-    _req_expert(w2_codes, "w2_codes", E, H, 16 * _blocks(I))
-    _req_expert(w2_scales, "w2_scales", E, H, _blocks(I))
+    e13, l13 = _expert(w13_codes, "w13_codes", E, 2 * I, 16 * _blocks(H))
+    es13, ls13 = _expert(w13_scales, "w13_scales", E, 2 * I, _blocks(H))
+    e2, l2 = _expert(w2_codes, "w2_codes", E, H, 16 * _blocks(I))
+    es2, ls2 = _expert(w2_scales, "w2_scales", E, H, _blocks(I))
     if out is not None:
-        _req_wide(out, "out")
+        ld_y = _wide(out, "out")
         if tuple(out.shape) != (T, H):
             raise ValueError("out must have shape (T, H) = (%d, %d), got %s" % (T, H, tuple(out.shape)))
     elif out_dtype is not None and out_dtype not in _WIDE:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    named = (("logits", logits), ("w13_codes", w13_codes), ("w13_scales", w13_scales), ("w2_codes", w2_codes),
-             ("w2_scales", w2_scales), ("out", out))
-    _req_cuda(("x", x), *named)
-    _same_device(x, *named)
+    device = _on_one_device(x, ("logits", logits), ("w13_codes", w13_codes), ("w13_scales", w13_scales),
+                            ("w2_codes", w2_codes), ("w2_scales", w2_scales), ("out", out))
     if out is None:
         out = torch.empty((T, H), dtype=out_dtype or torch.bfloat16, device=x.device)
+        ld_y = max(H, 1)
     y_type = _WIDE[out.dtype]
-    need = ctypes.c_int64()
-    status = lib().mxq_moe_fp4_workspace(T, H, I, E, k, y_type, ctypes.byref(need))
-    if status != 0:
-        raise MxqError(status, "mxq_moe_fp4_workspace")
-    workspace = torch.empty((max(need.value, 1),), dtype=torch.uint8, device=x.device)
-    _call("mxq_moe_fp4", x.device, T, H, I, E, k, 1 if renormalize else 0, x.data_ptr(), _ld(x), logits.data_ptr(),
-          _ld(logits), w13_codes.data_ptr(), w13_codes.stride(1), w13_codes.stride(0), w13_scales.data_ptr(),
-          w13_scales.stride(1), w13_scales.stride(0), w2_codes.data_ptr(), w2_codes.stride(1), w2_codes.stride(0),
-          w2_scales.data_ptr(), w2_scales.stride(1), w2_scales.stride(0), out.data_ptr(), y_type, _ld(out),
-          workspace.data_ptr(), need.value)
+    need = mxq_moe_fp4_workspace(T, H, I, E, k, y_type)
+    workspace = torch.empty((need,), dtype=_U8, device=x.device)
+    _call("mxq_moe_fp4", device, T, H, I, E, k, 1 if renormalize else 0, x.data_ptr(), ld_x, logits.data_ptr(), ld_l,
+          w13_codes.data_ptr(), l13, e13, w13_scales.data_ptr(), ls13, es13, w2_codes.data_ptr(), l2, e2,
+          w2_scales.data_ptr(), ls2, es2, out.data_ptr(), y_type, ld_y, workspace.data_ptr(), need)
     return out

@@ -114,7 +114,8 @@ int mxq_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, int x_type, int
   const int64_t nb = blocks_of(K);
   if (!y || (K > 0 && (!x || !w_codes || !w_scales || (x_fp4 && !x_scales)))) return MXQ_ERR_NULL;
   if (K > 0) {
-    if (ld_w >= kMaxK || ld_ws >= kMaxK || ld_x >= kMaxDim || ld_xs >= kMaxDim) return MXQ_ERR_LD;
+    if (ld_w >= kMaxK || ld_ws >= kMaxK || ld_x >= (x_fp4 ? kMaxK : kMaxDim) || ld_xs >= (x_fp4 ? kMaxK : INT64_MAX))
+      return MXQ_ERR_LD;
     int st = check_codes(w_codes, N, ld_w, w_scales, ld_ws, nb);
     if (st == MXQ_OK && x_fp4) st = check_codes(x, M, ld_x, x_scales, ld_xs, nb);
     if (st != MXQ_OK) return st;

@@ -1,12 +1,9 @@
 // gemm_fp4.hip -- Y = act(alpha * (X W) + bias) with W in MXFP4 and X in bf16 or MXFP4, for
-// gfx950.  Exact products, FP32 sums (see fp4_mma.hpp).
-#include "fp4_mma.hpp"
+// gfx950: the choice of kernel, and the kernel of few rows or tiles (fp4_stream.hpp).
+#include "fp4_stream.hpp"
 
 namespace mxq {
 namespace {
-
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
 
 struct Fp4Args {
   int M, N, K, tiles_m, tiles_n;
@@ -18,6 +15,8 @@ struct Fp4Args {
   int64_t ld_w;
   const uint8_t* ws;
   int64_t ld_ws;
+  bool x_pieces;                       // X rows are whole 16-byte pieces
+  bool xs_words, ws_words;             // scale rows are whole 4-byte words
 };
 
 __device__ __forceinline__ void store4(const GemmEpilogue& ep, int64_t row, int col, int N, v4f v) {
@@ -49,82 +48,102 @@ __device__ __forceinline__ void store4(const GemmEpilogue& ep, int64_t row, int 
   }
 }
 
-// A workgroup computes 16 * MT rows x 16 * NT columns of Y, its eight waves taking the units
-// of K in turn; their sums meet in LDS and are added in wave order.  Consecutive workgroups
-// of an XCD take the row tiles of one column tile, which read the same part of W.
-template <int XT, int MT, int NT, int D>
-__global__ __launch_bounds__(kThreads) void k_gemm4_rows(const Fp4Args a, const GemmEpilogue ep) {
-  extern __shared__ __align__(16) float part[];
-  const int t = xcd_order(blockIdx.x, a.tiles_m * a.tiles_n);
-  const int m0 = (t % a.tiles_m) * 16 * MT, n0 = (t / a.tiles_m) * 16 * NT;
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+// A workgroup computes 16 * MT rows x 16 * NTW columns of Y.  Consecutive workgroups of an XCD
+// take the row tiles of one column tile, which read the same part of W.
+template <bool XFP4, int MT, int NTW>
+__global__ __launch_bounds__(kThreads, 2) void k_gemm4_stream(const Fp4Args a, const GemmEpilogue ep) {
+  const int wg = xcd_order(blockIdx.x, a.tiles_m * a.tiles_n);
+  const int m0 = (wg % a.tiles_m) * 16 * MT, n0 = (wg / a.tiles_m) * 16 * NTW;
+  const int lane = threadIdx.x & 63, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  Rows<MT, NT> r;
-  r.w = a.w + (int64_t)n0 * a.ld_w;
-  r.ws = a.ws + (int64_t)n0 * a.ld_ws;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {                       // rows past the end read the last one again
-    const int row = min(16 * n + i, a.N - 1 - n0);
-    r.wo[n] = (uint32_t)(row * a.ld_w) + 16u * g;
-    r.so[n] = (uint32_t)(row * a.ld_ws) + (uint32_t)g;
-  }
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int64_t row = min(m0 + 16 * m + i, a.M - 1);
-    r.x[m] = a.x + row * a.ld_x;
-    r.xs[m] = XT == kXFp4 ? a.xs + row * a.ld_xs : nullptr;
-  }
-  v4f acc[MT][NT];
+  const int nb = (a.K + 31) / 32;
+  const Lines w = lines_of(a.w + n0 * a.ld_w, a.ld_w, a.ws + n0 * a.ld_ws, a.ld_ws, min(16 * NTW, a.N - n0), nb, a.ws_words);
+  const ItemOffsets wo = item_offsets(w.ld_c, w.ld_s, lane);
+  auto issue = [&](int t, int c, uint32_t lds) { issue_item(w, wo, t, c, lds); };
+  auto scales_of = [&](int t, int c, uint32_t slot) { return item_scales(w, slot, t, c, nb, lane); };
+  const uint32_t ring = (uint32_t)wave * kWaveLds, lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)smem + ring;
+  v4f acc[MT][NTW];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[m][n] = {0.0f, 0.0f, 0.0f, 0.0f};
-  sum_units<XT, MT, NT, D>(r, wave, kWaves, g, a.K, acc);
-  store_part<MT, NT>(part, wave, lane, acc);
+    for (int n = 0; n < NTW; ++n) acc[m][n] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (XFP4) {
+    const Lines xl = lines_of(a.x + m0 * a.ld_x, a.ld_x, a.xs + m0 * a.ld_xs, a.ld_xs, min(16 * MT, a.M - m0), nb, a.xs_words);
+    const ItemOffsets xo = item_offsets(xl.ld_c, xl.ld_s, lane);
+    stream<XFp4<MT>, MT, NTW>(a.K, wave, lane, a.ws_words, issue, [&](XFp4<MT>& x, int c, auto first) {
+      static_assert(MT <= kRing, "X tiles pass through the ring");
+#pragma unroll
+      for (int m = 0; m < MT; ++m) issue_item(xl, xo, m, c, lds0 + m * kSlot);
+      wait_vm<0>();
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          x.f[u][m] = item_codes(ring + m * kSlot, lane, u);
+          if (kChunk * (c + 1) > a.K) x.f[u][m] = keep_codes(x.f[u][m], a.K - kChunk * c - 32 * (4 * (lane >> 4) + u));
+        }
+        x.s[m] = item_scales(xl, ring + m * kSlot, m, c, nb, lane);
+      }
+      reads_done();
+      first();
+    }, scales_of, acc);
+  } else {
+    const uint8_t* row[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) row[m] = a.x + min((int64_t)m0 + 16 * m + i, (int64_t)a.M - 1) * a.ld_x;
+    stream<XWide<MT, 1>, MT, NTW>(a.K, wave, lane, a.ws_words, issue, [&](XWide<MT, 1>& x, int c, auto first) {
+      const int left = a.K - kChunk * c;
+      if (a.M - m0 <= 4 || left < kChunk || !a.x_pieces) {
+        first();
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          x.load_direct(m, row[m] + 2 * kChunk * (int64_t)c, m0 + 16 * m + i < a.M, left, lane);
+      } else {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          stage_rows((uint64_t)(uintptr_t)row[m], min(16, a.M - m0 - 16 * m), c, lds0, lane);
+          wait_vm<0>();
+          asm volatile("" ::: "memory");
+          x.read_staged(m, ring, lane);
+          reads_done();
+        }
+        first();
+      }
+    }, scales_of, acc);
+  }
   __syncthreads();
-  for (int q = threadIdx.x; q < 16 * MT * 4 * NT; q += kThreads) {
-    const int m = q / (4 * NT), n = 4 * (q % (4 * NT));
-    if (m0 + m < a.M && n0 + n < a.N)
-      store4(ep, m0 + m, n0 + n, a.N, sum_part<MT, NT>(part, kWaves, m, n));
+  store_part<MT, NTW>(wave, lane, acc);
+  __syncthreads();
+  for (int q = threadIdx.x; q < 16 * MT * 4 * NTW; q += kThreads) {
+    const int m = q / (4 * NTW), n = 4 * (q % (4 * NTW));
+    if (m0 + m < a.M && n0 + n < a.N) store4(ep, m0 + m, n0 + n, a.N, sum_part<MT, NTW>(m, n));
   }
 }
 
-template <int XT, int MT, int NT, int D>
-hipError_t launch_rows(Fp4Args a, const GemmEpilogue& ep, hipStream_t st) {
+template <bool XFP4, int MT, int NTW>
+hipError_t launch_stream(Fp4Args a, const GemmEpilogue& ep, hipStream_t st) {
+  static bool set[64] = {false};
   a.tiles_m = (a.M + 16 * MT - 1) / (16 * MT);
-  a.tiles_n = (a.N + 16 * NT - 1) / (16 * NT);
+  a.tiles_n = (a.N + 16 * NTW - 1) / (16 * NTW);
   if ((int64_t)a.tiles_m * a.tiles_n > 0x7FFFFFFF) return hipErrorInvalidValue;
-  constexpr int lds = kWaves * part_wave<MT, NT>() * 4;
-  auto kern = k_gemm4_rows<XT, MT, NT, D>;
-  if (lds > 65536) {
-    static bool set[64] = {false};
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
-    if (!set[dev]) {
-      const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-      if (e != hipSuccess) return e;
-      set[dev] = true;
-    }
-  }
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(kThreads), lds, st, a, ep);
+  auto kern = k_gemm4_stream<XFP4, MT, NTW>;
+  const hipError_t e = allow_lds(kern, stream_lds<MT, NTW>(), set);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(kThreads), (stream_lds<MT, NTW>()), st, a, ep);
   return hipGetLastError();
 }
 
 // Columns per workgroup: as many as still give every CU a workgroup.
-template <int XT, int MT>
+template <bool XFP4, int MT>
 hipError_t launch_m(const Fp4Args& a, const GemmEpilogue& ep, hipStream_t st) {
   const int64_t tm = (a.M + 16 * MT - 1) / (16 * MT);
   const int64_t cus = device_cu_count();
-  if (tm * ((a.N + 63) / 64) >= cus) return launch_rows<XT, MT, 4, 2>(a, ep, st);
-  if (tm * ((a.N + 31) / 32) >= cus) return launch_rows<XT, MT, 2, 2>(a, ep, st);
-  return launch_rows<XT, MT, 1, MT == 1 ? 4 : 2>(a, ep, st);
-}
-
-template <int XT>
-hipError_t launch_x(const Fp4Args& a, const GemmEpilogue& ep, hipStream_t st) {
-  if (a.M <= 16) return launch_m<XT, 1>(a, ep, st);
-  if (a.M <= 32) return launch_m<XT, 2>(a, ep, st);
-  return launch_m<XT, 4>(a, ep, st);
+  if constexpr (MT == 1)
+    if (tm * ((a.N + 127) / 128) >= cus) return launch_stream<XFP4, MT, 8>(a, ep, st);
+  if (tm * ((a.N + 63) / 64) >= cus) return launch_stream<XFP4, MT, 4>(a, ep, st);
+  if (tm * ((a.N + 31) / 32) >= cus) return launch_stream<XFP4, MT, 2>(a, ep, st);
+  return launch_stream<XFP4, MT, 1>(a, ep, st);
 }
 
 }  // namespace
@@ -132,6 +151,12 @@ hipError_t launch_x(const Fp4Args& a, const GemmEpilogue& ep, hipStream_t st) {
 hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool x_fp4, int64_t ld_x, const uint8_t* xs,
                            int64_t ld_xs, const uint8_t* wc, int64_t ld_w, const uint8_t* ws, int64_t ld_ws,
                            const GemmEpilogue& ep, hipStream_t st) {
+  auto whole = [](const void* p, int64_t ld, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0 && ld % n == 0; };
+  // 256 x 256 tiles once they fill half the CUs: 2048 x 4096 x 4096 takes 31 us so and 47 as a stream,
+  // 1024 x 4096 x 4096 (64 tiles) 30 and 23
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  if (x_fp4 && K > 0 && 2 * tiles >= device_cu_count() && whole(xs, ld_xs, 16) && whole(ws, ld_ws, 16))
+    return launch_gemm_fp4_tile(M, N, K, (const uint8_t*)x, ld_x, xs, ld_xs, wc, ld_w, ws, ld_ws, ep, st);
   Fp4Args a{};
   a.M = (int)M;
   a.N = (int)N;
@@ -144,7 +169,11 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool 
   a.ld_w = ld_w;
   a.ws = ws;
   a.ld_ws = ld_ws;
-  return x_fp4 ? launch_x<kXFp4>(a, ep, st) : launch_x<kXBf16>(a, ep, st);
+  a.x_pieces = whole(x, a.ld_x, 16);
+  a.xs_words = whole(xs, ld_xs, 4);
+  a.ws_words = whole(ws, ld_ws, 4);
+  if (x_fp4) return M <= 16 ? launch_m<true, 1>(a, ep, st) : M <= 32 ? launch_m<true, 2>(a, ep, st) : launch_m<true, 4>(a, ep, st);
+  return M <= 16 ? launch_m<false, 1>(a, ep, st) : launch_m<false, 2>(a, ep, st);
 }
 
 }  // namespace mxq

@@ -111,6 +111,11 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool 
                            int64_t ld_xs, const uint8_t* wc, int64_t ld_w, const uint8_t* ws, int64_t ld_ws,
                            const GemmEpilogue& ep, hipStream_t stream);
 
+// The 256 x 256 tile kernel behind it: X and W in MXFP4, scale rows 16-byte aligned, ld_x < 2^24.
+hipError_t launch_gemm_fp4_tile(int64_t M, int64_t N, int64_t K, const uint8_t* xc, int64_t ld_x, const uint8_t* xs,
+                                int64_t ld_xs, const uint8_t* wc, int64_t ld_w, const uint8_t* ws, int64_t ld_ws,
+                                const GemmEpilogue& ep, hipStream_t stream);
+
 // A mixture-of-experts layer; ld_ are row pitches and st_ expert pitches, in bytes for codes
 // and scales, in elements for x, logits and y.
 struct MoeFp4 {

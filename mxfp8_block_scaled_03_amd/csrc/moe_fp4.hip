@@ -5,22 +5,20 @@
 //   h = share * silu(x W1_e) * (x W3_e)      (gate rows [0, I) and up rows [I, 2I) of w13[e])
 //   y = sum over the token's experts, in the order of their rank, of h W2_e
 //
-// Three launches: k_moe_up (routing, gate and up products, h), k_moe_down (down products, one
-// partial row per token and expert), k_moe_sum (the sum of a token's rows).  The weights of
-// every expert that a token chose are read once and bound the time; everything else is kept
-// out of their way: each workgroup of k_moe_up works out the tokens of its own expert (one
-// ballot per token), h goes to memory in the fragment order that k_moe_down reads, and
-// experts that nobody chose end their workgroups at once.
+// Four launches: k_moe_route (ranks and shares, one wave a token), k_moe_up (gate and up
+// products, h), k_moe_down (down products, one partial row per token and expert), k_moe_sum
+// (the sum of a token's rows).  The weights of every expert that a token chose are read once
+// and bound the time (fp4_stream.hpp); everything else is kept out of their way: a workgroup
+// finds the tokens of its expert with one ballot, h goes to memory in the fragment order that
+// k_moe_down reads, and the workgroups of experts that nobody chose end at once.
 //
 // An expert with logit -inf is never taken: its share is zero, and a token whose logits are
 // all -inf gets y = 0.  NaN logits order above +inf; their shares are NaN, as softmax's.
-#include "fp4_mma.hpp"
+#include "fp4_stream.hpp"
 
 namespace mxq {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
 constexpr uint32_t kMasked = 0x007FFFFFu;   // order key of -inf
 
 struct MoeArgs {
@@ -30,12 +28,16 @@ struct MoeArgs {
   int tiles;                           // column tiles of a launch
   const uint8_t* x;
   int64_t ld_x;                        // bytes
+  bool x_pieces;                       // X rows are whole 16-byte pieces
+  bool s13_words, s2_words;            // scale rows are whole 4-byte words
   const float* logits;
   int64_t ld_logits;
   const uint8_t *w13, *s13, *w2, *s2;
   int64_t ld_w13, st_w13, ld_s13, st_s13, ld_w2, st_w2, ld_s2, st_s2;   // rows and experts, bytes
-  int* table;                          // [slots][2 + T]: expert, tokens, rows t * k + rank
-  uint8_t* h;                          // [slots][mt_cap][units][terms][4][64][16 bytes]
+  int* chosen;                         // [T][k]: expert, or -1
+  float* share;                        // [T][k]
+  int16_t* rank;                       // [E][T]: rank of the expert for the token, or -1
+  uint8_t* h;                          // [slots][mt_cap][chunks][4][terms][4][64][16 bytes]
   float* part;                         // [T * k][H]
   void* y;
   int64_t ld_y;
@@ -49,19 +51,8 @@ __device__ __forceinline__ uint32_t order_key(float l) {
   return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-// How many logits of the row come before expert e (the whole wave calls).
-__device__ __forceinline__ int rank_of(const float* row, int E, int e, uint32_t ke, int lane) {
-  int n = 0;
-  for (int j0 = 0; j0 < E; j0 += 64) {
-    const int j = j0 + lane;
-    const uint32_t kj = j < E ? order_key(row[j]) : 0u;
-    n += __popcll(__ballot(j < E && (kj > ke || (kj == ke && j < e))));
-  }
-  return n;
-}
-
-// The rank of the lane's own expert j (key kj) in the row.
-__device__ __forceinline__ int rank_of_lane(const float* row, int E, int j, uint32_t kj, int lane) {
+// The rank of the lane's own expert j (key kj) in the row: how many come before it.
+__device__ __forceinline__ int rank_of(const float* row, int E, int j, uint32_t kj, int lane) {
   int n = 0;
   for (int i0 = 0; i0 < E; i0 += 64) {
     const uint32_t ki = i0 + lane < E ? order_key(row[i0 + lane]) : 0u;
@@ -86,25 +77,64 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-// The share of expert e of a row that chose it: exp(l_e - max) over the sum of the chosen
-// experts' exponentials (renorm) or of all.
-__device__ __forceinline__ float share_of(const float* row, const MoeArgs& a, int e, int lane) {
-  float top = -__builtin_inff(), s = 0.0f;
+// ---- routing: a wave a token.  share = exp(l - max) over the sum of the chosen experts'
+// exponentials (renorm) or of all.
+__global__ __launch_bounds__(kThreads) void k_moe_route(const MoeArgs a) {
+  const int t = blockIdx.x * kWaves + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (t >= a.T) return;                                  // the whole wave
+  const float* row = a.logits + t * a.ld_logits;
+  float top = -__builtin_inff();
   bool nan = false;
   for (int j = lane; j < a.E; j += 64) {
-    top = fmaxf(top, row[j]);
-    nan |= row[j] != row[j];
+    const float l = row[j];
+    top = fmaxf(top, l);
+    nan |= l != l;
   }
-  top = wave_max(top);
-  if (__any(nan)) return __builtin_nanf("");
+  top = __any(nan) ? __builtin_nanf("") : wave_max(top);
+  float sum = 0.0f;
   for (int j0 = 0; j0 < a.E; j0 += 64) {
     const int j = j0 + lane;
     const float l = j < a.E ? row[j] : -__builtin_inff();
-    bool in = j < a.E;
-    if (a.renorm) in &= rank_of_lane(row, a.E, j, order_key(l), lane) < a.k;
-    s += in ? expf(l - top) : 0.0f;
+    const uint32_t kj = order_key(l);
+    const int r = rank_of(row, a.E, j, kj, lane);
+    const bool in = j < a.E && r < a.k;
+    const float p = expf(l - top);
+    if (a.renorm ? in : j < a.E) sum += p;
+    if (j < a.E) a.rank[(int64_t)j * a.T + t] = (int16_t)(in && kj != kMasked ? r : -1);
+    if (in) {
+      a.chosen[t * a.k + r] = kj != kMasked ? j : -1;
+      a.share[t * a.k + r] = p;                          // divided below, by the same lane
+    }
   }
-  return expf(row[e] - top) / wave_sum(s);
+  sum = wave_sum(sum);
+  for (int j0 = 0; j0 < a.E; j0 += 64) {
+    const int j = j0 + lane;
+    const int r = j < a.E ? a.rank[(int64_t)j * a.T + t] : -1;
+    if (r >= 0) a.share[t * a.k + r] /= sum;
+  }
+}
+
+// The expert of a slot and its tokens, in order: s_row[m] = t * k + rank.  Returns their number,
+// 0 where there is nothing to do: no token, or (by_token) an earlier token's slot has the
+// expert already.  Ends with a barrier.
+__device__ __forceinline__ int slot_tokens(const MoeArgs& a, int slot, int* s_row, int* s_cnt, int& e) {
+  e = a.by_token ? a.chosen[slot] : slot;
+  const int lane = threadIdx.x & 63;
+  if (threadIdx.x < 64) {
+    int cnt = 0;
+    if (e >= 0)
+      for (int t0 = 0; t0 < a.T; t0 += 64) {
+        const int t = t0 + lane;
+        const int r = t < a.T ? a.rank[(int64_t)e * a.T + t] : -1;
+        const uint64_t b = __ballot(r >= 0);
+        if (r >= 0) s_row[cnt + __popcll(b & ((1ull << lane) - 1))] = t * a.k + r;
+        cnt += __popcll(b);
+      }
+    if (lane == 0) *s_cnt = cnt;
+  }
+  __syncthreads();
+  const int cnt = *s_cnt;
+  return cnt > 0 && a.by_token && s_row[0] != slot ? 0 : cnt;
 }
 
 // Rounds v to `TERMS` bf16 terms whose sum is v to 8 * TERMS bits.
@@ -118,120 +148,97 @@ __device__ __forceinline__ void split_bf16(float v, uint32_t out[TERMS]) {
   }
 }
 
-// ---- gate and up products.  A workgroup: one slot, 8 * NT columns of I (16 * NT rows of w13).
-template <int MT, int NT, int TERMS>
-__global__ __launch_bounds__(kThreads) void k_moe_up(const MoeArgs a) {
-  constexpr int IC = 8 * NT;
-  extern __shared__ __align__(16) float part[];
-  __shared__ int s_e, s_cnt;
-  __shared__ int16_t s_rank[1024], s_tok[1024];
-  __shared__ float s_share[1024];
+// Byte offset in a 16-row tile of h of the 16 bytes that hold row m's elements k .. k+7, term 0.
+template <int TERMS>
+__device__ __forceinline__ int64_t h_offset(int m, int k) {
+  const int c = k / kChunk, b = (k % kChunk) / 32;       // block b = 4 g + u of the chunk
+  return ((int64_t)(4 * c + b % 4) * TERMS * 4 + (k % 32) / 8) * 1024 + (16 * (b / 4) + m) * 16;
+}
+
+// ---- gate and up products.  A workgroup: one slot, 8 * NTW columns of I: row tiles
+// 0 .. NTW/2-1 of its 16 * NTW rows of w13 are gate rows, the others the up rows.
+template <int MT, int NTW, int TERMS>
+__global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
+  constexpr int IC = 8 * NTW, NG = NTW / 2;
+  int* s_row = reinterpret_cast<int*>(smem + stream_lds<MT, NTW>());
+  __shared__ int s_cnt;
   const int slot = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // ---- the slot's expert and tokens
-  int e = slot, t0 = 0;
-  if (a.by_token) {
-    t0 = slot / a.k;
-    const int r0 = slot % a.k;
-    const float* row = a.logits + t0 * a.ld_logits;
-    if (threadIdx.x == 0) s_e = -1;
-    __syncthreads();
-    for (int j0 = 64 * wave; j0 < a.E; j0 += kThreads) {
-      const int j = j0 + lane;
-      const uint32_t kj = j < a.E ? order_key(row[j]) : 0u;
-      const int n = rank_of_lane(row, a.E, j, kj, lane);
-      if (j < a.E && n == r0 && kj != kMasked) s_e = j;          // ranks are distinct: one lane
-    }
-    __syncthreads();
-    e = s_e;
-  }
-  if (e >= 0)
-    for (int t = wave; t < a.T; t += kWaves) {
-      const float* row = a.logits + t * a.ld_logits;
-      const uint32_t ke = order_key(row[e]);
-      const int n = rank_of(row, a.E, e, ke, lane);
-      const bool in = n < a.k && ke != kMasked;
-      const float s = in ? share_of(row, a, e, lane) : 0.0f;
-      if (lane == 0) {
-        s_rank[t] = (int16_t)(in ? n : -1);
-        s_share[t] = s;
-      }
-    }
-  __syncthreads();
-  if (wave == 0) {
-    int cnt = 0;
-    if (e >= 0)
-      for (int j0 = 0; j0 < a.T; j0 += 64) {
-        const bool in = j0 + lane < a.T && s_rank[j0 + lane] >= 0;
-        const uint64_t b = __ballot(in);
-        if (in) s_tok[cnt + __popcll(b & ((1ull << lane) - 1))] = (int16_t)(j0 + lane);
-        cnt += __popcll(b);
-      }
-    // by_token: an earlier token's slot has the expert already
-    if (a.by_token && cnt > 0 && s_tok[0] != t0) cnt = 0;
-    if (lane == 0) s_cnt = cnt;
-    if (tile == 0) {
-      int* tab = a.table + (int64_t)slot * (2 + a.T);
-      if (lane == 0) {
-        tab[0] = e;
-        tab[1] = cnt;
-      }
-      for (int m = lane; m < cnt; m += 64) tab[2 + m] = s_tok[m] * a.k + s_rank[s_tok[m]];
-    }
-  }
-  __syncthreads();
-  const int cnt = s_cnt;
+  int e;
+  const int cnt = slot_tokens(a, slot, s_row, &s_cnt, e);
   if (cnt == 0) return;
-  // ---- the product
-  const int i0 = tile * IC;
-  const int units = (a.I + kUnit - 1) / kUnit;
-  Rows<MT, NT> r;
-  r.w = a.w13 + e * a.st_w13 + i0 * a.ld_w13;
-  r.ws = a.s13 + e * a.st_s13 + i0 * a.ld_s13;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {                       // columns past I read the last one again
-    const int64_t row = min(16 * (n % (NT / 2)) + i, a.I - 1 - i0) + (n < NT / 2 ? 0 : a.I);
-    r.wo[n] = (uint32_t)(row * a.ld_w13) + 16u * g;
-    r.so[n] = (uint32_t)(row * a.ld_s13) + (uint32_t)g;
-  }
+  const int i0 = tile * IC, nb = (a.H + 31) / 32;
+  const int rows = min(IC, a.I - i0);
+  const uint8_t* w = a.w13 + e * a.st_w13 + i0 * a.ld_w13;
+  const uint8_t* s = a.s13 + e * a.st_s13 + i0 * a.ld_s13;
+  const Lines gate = lines_of(w, a.ld_w13, s, a.ld_s13, rows, nb, a.s13_words);
+  const Lines up = lines_of(w + a.I * a.ld_w13, a.ld_w13, s + a.I * a.ld_s13, a.ld_s13, rows, nb, a.s13_words);
+  const ItemOffsets wo = item_offsets(gate.ld_c, gate.ld_s, lane);
+  const uint32_t ring = (uint32_t)wave * kWaveLds, lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)smem + ring;
+  const int chunks = (a.I + kChunk - 1) / kChunk;
   for (int m0 = 0; m0 < cnt; m0 += 16 * MT) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      r.x[m] = a.x + s_tok[min(m0 + 16 * m + i, cnt - 1)] * a.ld_x;
-      r.xs[m] = nullptr;
-    }
-    v4f acc[MT][NT];
+    if (m0 > 0) __syncthreads();
+    v4f acc[MT][NTW];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n] = {0.0f, 0.0f, 0.0f, 0.0f};
-    sum_units<kXBf16, MT, NT, 2>(r, wave, kWaves, g, a.H, acc);
-    if (m0 > 0) __syncthreads();
-    store_part<MT, NT>(part, wave, lane, acc);
+      for (int n = 0; n < NTW; ++n) acc[m][n] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint8_t* row[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) row[m] = a.x + (int64_t)(s_row[min(m0 + 16 * m + i, cnt - 1)] / a.k) * a.ld_x;
+    stream<XWide<MT, 1>, MT, NTW>(
+        a.H, wave, lane, a.s13_words,
+        [&](int t, int c, uint32_t lds) {
+          if (t < NG) issue_item(gate, wo, t, c, lds);
+          else issue_item(up, wo, t - NG, c, lds);
+        },
+        [&](XWide<MT, 1>& x, int c, auto first) {
+          const int left = a.H - kChunk * c;
+          if (cnt - m0 <= 4 || left < kChunk || !a.x_pieces) {
+            first();
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+              x.load_direct(m, row[m] + 2 * kChunk * (int64_t)c, m0 + 16 * m + i < cnt, left, lane);
+          } else {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              stage_rows((uint64_t)(uintptr_t)row[m], min(16, cnt - m0 - 16 * m), c, lds0, lane);
+              wait_vm<0>();
+              asm volatile("" ::: "memory");
+              x.read_staged(m, ring, lane);
+              reads_done();
+            }
+            first();
+          }
+        },
+        [&](int t, int c, uint32_t slot_at) {
+          return t < NG ? item_scales(gate, slot_at, t, c, nb, lane) : item_scales(up, slot_at, t - NG, c, nb, lane);
+        },
+        acc);
+    __syncthreads();
+    store_part<MT, NTW>(wave, lane, acc);
     __syncthreads();
     for (int q = threadIdx.x; q < 16 * MT * (IC / 8); q += kThreads) {
       const int m = q / (IC / 8), c = 8 * (q % (IC / 8));
       if (m0 + m >= cnt || i0 + c >= a.I) continue;
-      const float share = s_share[s_tok[m0 + m]];
+      const float share = a.share[s_row[m0 + m]];
       uint32_t o[TERMS][4];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const v4f gt = sum_part<MT, NT>(part, kWaves, m, c + 4 * hf);
-        const v4f up = sum_part<MT, NT>(part, kWaves, m, IC + c + 4 * hf);
+        const v4f gt = sum_part<MT, NTW>(m, c + 4 * hf), u = sum_part<MT, NTW>(m, IC + c + 4 * hf);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           uint32_t b0[TERMS], b1[TERMS];
           const int col = i0 + c + 4 * hf + 2 * p;     // zeros past I
-          split_bf16<TERMS>(col < a.I ? share * (silu(gt[2 * p]) * up[2 * p]) : 0.0f, b0);
-          split_bf16<TERMS>(col + 1 < a.I ? share * (silu(gt[2 * p + 1]) * up[2 * p + 1]) : 0.0f, b1);
+          split_bf16<TERMS>(col < a.I ? share * (silu(gt[2 * p]) * u[2 * p]) : 0.0f, b0);
+          split_bf16<TERMS>(col + 1 < a.I ? share * (silu(gt[2 * p + 1]) * u[2 * p + 1]) : 0.0f, b1);
 #pragma unroll
           for (int t = 0; t < TERMS; ++t) o[t][2 * hf + p] = b0[t] | (b1[t] << 16);
         }
       }
-      const int k = i0 + c, mt = (m0 + m) / 16;
-      uint8_t* dst = a.h + (((int64_t)slot * a.mt_cap + mt) * units + k / kUnit) * (TERMS * 4096) +
-                     ((k % 32) / 8) * 1024 + (16 * ((k % kUnit) / 32) + m % 16) * 16;
+      const int mt = (m0 + m) / 16;
+      uint8_t* dst = a.h + ((int64_t)slot * a.mt_cap + mt) * chunks * (TERMS * 16384) + h_offset<TERMS>(m % 16, i0 + c);
 #pragma unroll
       for (int t = 0; t < TERMS; ++t)
         *reinterpret_cast<uint4*>(dst + 4096 * t) = make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
@@ -239,98 +246,53 @@ __global__ __launch_bounds__(kThreads) void k_moe_up(const MoeArgs a) {
   }
 }
 
-// ---- down products.  A workgroup: one slot, 16 * NT columns of H; h comes in fragment order.
-template <int MT, int NT, int TERMS>
-struct HUnit {
-  v4i w[NT];
-  uint32_t ws[NT];
-  v4i x[MT][TERMS][4];
-};
-
-template <int MT, int NT, int TERMS>
-__global__ __launch_bounds__(kThreads) void k_moe_down(const MoeArgs a) {
-  extern __shared__ __align__(16) float part[];
+// ---- down products.  A workgroup: one slot, 16 * NTW columns of H; h comes in fragment order.
+template <int NTW, int TERMS>
+__global__ __launch_bounds__(kThreads, TERMS == 2 ? 2 : 1) void k_moe_down(const MoeArgs a) {
+  int* s_row = reinterpret_cast<int*>(smem + stream_lds<1, NTW>());
+  __shared__ int s_cnt;
   const int slot = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
-  const int* tab = a.table + (int64_t)slot * (2 + a.T);
-  const int e = tab[0], cnt = tab[1];
-  if (cnt == 0) return;
-  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = 16 * NT * tile;
-  const int units = (a.I + kUnit - 1) / kUnit;
-  const uint8_t* w = a.w2 + e * a.st_w2 + (int64_t)n0 * a.ld_w2;
-  const uint8_t* ws = a.s2 + e * a.st_s2 + (int64_t)n0 * a.ld_s2;
-  uint32_t wo[NT], so[NT];
+  int e;
+  const int cnt = slot_tokens(a, slot, s_row, &s_cnt, e);
+  if (cnt == 0) return;
+  const int n0 = 16 * NTW * tile, nb = (a.I + 31) / 32;
+  const Lines w = lines_of(a.w2 + e * a.st_w2 + n0 * a.ld_w2, a.ld_w2, a.s2 + e * a.st_s2 + n0 * a.ld_s2, a.ld_s2,
+                           min(16 * NTW, a.H - n0), nb, a.s2_words);
+  const ItemOffsets wo = item_offsets(w.ld_c, w.ld_s, lane);
+  const int chunks = (a.I + kChunk - 1) / kChunk;
+  for (int m0 = 0; m0 < cnt; m0 += 16) {
+    if (m0 > 0) __syncthreads();
+    const uint8_t* h = a.h + ((int64_t)slot * a.mt_cap + m0 / 16) * chunks * (TERMS * 16384) + 16 * lane;
+    v4f acc[1][NTW];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int row = min(16 * n + i, a.H - 1 - n0);
-    wo[n] = (uint32_t)(row * a.ld_w2) + 16u * g;
-    so[n] = (uint32_t)(row * a.ld_s2) + (uint32_t)g;
-  }
-  const int mtiles = (cnt + 15) / 16;
-  for (int mt0 = 0; mt0 < mtiles; mt0 += MT) {
-    const uint8_t* hx[MT];
+    for (int n = 0; n < NTW; ++n) acc[0][n] = {0.0f, 0.0f, 0.0f, 0.0f};
+    stream<XWide<1, TERMS>, 1, NTW>(
+        a.I, wave, lane, a.s2_words, [&](int t, int c, uint32_t lds) { issue_item(w, wo, t, c, lds); },
+        [&](XWide<1, TERMS>& x, int c, auto first) {
+          first();
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      hx[m] = a.h + ((int64_t)slot * a.mt_cap + min(mt0 + m, mtiles - 1)) * units * (TERMS * 4096);
-    auto load = [&](HUnit<MT, NT, TERMS>& t, int u) {
-      // codes past I are zeroed, and so are the blocks past the end, under scale 1
-      const int left = a.I - kUnit * u - 32 * g;
-      const v4i zero = {0, 0, 0, 0};
+          for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        t.w[n] = zero;
-        t.ws[n] = 127u;
-        if (left > 0) {
-          t.w[n] = *reinterpret_cast<const v4i*>(w + (wo[n] + 64u * (uint32_t)u));
-          t.ws[n] = ws[so[n] + 4u * (uint32_t)u];
-        }
-        if (left < 32) t.w[n] = keep_codes(t.w[n], left);
-      }
+            for (int p = 0; p < TERMS; ++p)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int p = 0; p < TERMS; ++p)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            t.x[m][p][j] = zero;                       // h has nothing at k >= I
-            if (8 * j < left)
-              t.x[m][p][j] = *reinterpret_cast<const v4i*>(hx[m] + ((int64_t)u * TERMS + p) * 4096 + 1024 * j + 16 * lane);
-          }
-    };
-    v4f acc[MT][NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n] = {0.0f, 0.0f, 0.0f, 0.0f};
-    HUnit<MT, NT, TERMS> t;
-    for (int u = wave; u < units; u += kWaves) {
-      load(t, u);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float s = e8m0_to_f32(t.ws[n]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t d[4];
-          fp4::decode8_bf16((uint32_t)t.w[n][j], s, d);
-          const v4i dv = {(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int p = TERMS - 1; p >= 0; --p)
-              acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  __builtin_bit_cast(v8bf, dv), __builtin_bit_cast(v8bf, t.x[m][p][j]), acc[m][n], 0, 0, 0);
-        }
-      }
-    }
-    if (mt0 > 0) __syncthreads();
-    store_part<MT, NT>(part, wave, lane, acc);
+              for (int j = 0; j < 4; ++j) {
+                const int k = kChunk * c + 32 * (4 * (lane >> 4) + u) + 8 * j;
+                v4i v = {0, 0, 0, 0};                  // h has nothing at k >= I
+                if (k < a.I) v = *reinterpret_cast<const v4i*>(h + (((int64_t)4 * c + u) * TERMS + p) * 4096 + 1024 * j);
+                x.f[u][j][0][p] = v;
+              }
+        },
+        [&](int t, int c, uint32_t slot_at) { return item_scales(w, slot_at, t, c, nb, lane); }, acc);
     __syncthreads();
-    for (int q = threadIdx.x; q < 16 * MT * 4 * NT; q += kThreads) {
-      const int m = 16 * mt0 + q / (4 * NT), n = 4 * (q % (4 * NT));
-      if (m >= cnt || n0 + n >= a.H) continue;
-      const v4f v = sum_part<MT, NT>(part, kWaves, q / (4 * NT), n);
-      float* p = a.part + (int64_t)tab[2 + m] * a.H + n0 + n;
+    store_part<1, NTW>(wave, lane, acc);
+    __syncthreads();
+    for (int q = threadIdx.x; q < 16 * 4 * NTW; q += kThreads) {
+      const int m = q / (4 * NTW), n = 4 * (q % (4 * NTW));
+      if (m0 + m >= cnt || n0 + n >= a.H) continue;
+      const v4f v = sum_part<1, NTW>(m, n);
+      float* p = a.part + (int64_t)s_row[m0 + m] * a.H + n0 + n;
 #pragma unroll
       for (int x = 0; x < 4; ++x)
         if (n0 + n + x < a.H) p[x] = v[x];
@@ -338,67 +300,60 @@ __global__ __launch_bounds__(kThreads) void k_moe_down(const MoeArgs a) {
   }
 }
 
-// ---- y[t] = sum of the token's rows, in the order of rank; masked experts come last and
+// ---- y[t] = sum of the token's rows, in the order of rank; masked experts, which come last,
 // have none.
 __global__ __launch_bounds__(256) void k_moe_sum(const MoeArgs a) {
   const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
-  const int lane = threadIdx.x & 63;
-  int valid = 0;
-  for (int j0 = 0; j0 < a.E; j0 += 64)
-    valid += __popcll(__ballot(j0 + lane < a.E && order_key(a.logits[t * a.ld_logits + j0 + lane]) != kMasked));
-  if (valid > a.k) valid = a.k;
   if (n >= a.H) return;
   float s = 0.0f;
-  for (int r = 0; r < valid; ++r) s += a.part[((int64_t)t * a.k + r) * a.H + n];
+  for (int r = 0; r < a.k && a.chosen[t * a.k + r] >= 0; ++r) s += a.part[((int64_t)t * a.k + r) * a.H + n];
   if (a.y_bf16)
     reinterpret_cast<uint16_t*>(a.y)[t * a.ld_y + n] = (uint16_t)f32_to_bf16_rne(s);
   else
     reinterpret_cast<float*>(a.y)[t * a.ld_y + n] = s;
 }
 
-template <typename K>
-hipError_t launch_lds(K kern, bool* set, unsigned grid, int lds, const MoeArgs& a, hipStream_t st) {
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
-  if (lds > 49152 && !set[dev]) {
-    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (e != hipSuccess) return e;
-    set[dev] = true;
-  }
-  hipLaunchKernelGGL(kern, dim3(grid), dim3(kThreads), lds, st, a);
+template <int MT, int NTW, int TERMS>
+hipError_t launch_up(MoeArgs a, hipStream_t st) {
+  static bool set[64] = {false};
+  a.tiles = (a.I + 8 * NTW - 1) / (8 * NTW);
+  if ((int64_t)a.slots * a.tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+  auto kern = k_moe_up<MT, NTW, TERMS>;
+  const hipError_t e = allow_lds(kern, stream_lds<MT, NTW>() + 4 * 1024, set);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.slots * a.tiles)), dim3(kThreads), (stream_lds<MT, NTW>() + 4 * a.T), st, a);
   return hipGetLastError();
 }
 
-template <int MT, int NT, int TERMS>
-hipError_t launch_up(MoeArgs a, hipStream_t st) {
-  static bool set[64] = {false};
-  a.tiles = (a.I + 8 * NT - 1) / (8 * NT);
-  if ((int64_t)a.slots * a.tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-  return launch_lds(k_moe_up<MT, NT, TERMS>, set, (unsigned)(a.slots * a.tiles), kWaves * part_wave<MT, NT>() * 4, a, st);
-}
-
-template <int MT, int NT, int TERMS>
+template <int NTW, int TERMS>
 hipError_t launch_down(MoeArgs a, hipStream_t st) {
   static bool set[64] = {false};
-  a.tiles = (a.H + 16 * NT - 1) / (16 * NT);
+  a.tiles = (a.H + 16 * NTW - 1) / (16 * NTW);
   if ((int64_t)a.slots * a.tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-  return launch_lds(k_moe_down<MT, NT, TERMS>, set, (unsigned)(a.slots * a.tiles), kWaves * part_wave<MT, NT>() * 4, a,
-                    st);
+  auto kern = k_moe_down<NTW, TERMS>;
+  const hipError_t e = allow_lds(kern, stream_lds<1, NTW>() + 4 * 1024, set);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.slots * a.tiles)), dim3(kThreads), (stream_lds<1, NTW>() + 4 * a.T), st, a);
+  return hipGetLastError();
 }
 
-// Column tiles as wide as still give every CU a workgroup (a slot's expert may be unused, so
+// Column tiles as wide as still give every CU two workgroups (a slot's expert may be unused, so
 // the count is an upper bound).
 template <int MT, int TERMS>
 hipError_t launch_all(const MoeArgs& a, hipStream_t st) {
   const int64_t cus = device_cu_count();
-  hipError_t e = (int64_t)a.slots * ((a.I + 31) / 32) >= cus ? launch_up<MT, 4, TERMS>(a, st) : launch_up<MT, 2, TERMS>(a, st);
+  hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if ((int64_t)a.slots * ((a.H + 63) / 64) >= 2 * cus)
-    e = launch_down<MT, 4, TERMS>(a, st);
-  else if ((int64_t)a.slots * ((a.H + 31) / 32) >= cus)
-    e = launch_down<MT, 2, TERMS>(a, st);
+  if ((int64_t)a.slots * ((a.I + 63) / 64) >= 2 * cus)
+    e = launch_up<MT, 8, TERMS>(a, st);
   else
-    e = launch_down<MT, 1, TERMS>(a, st);
+    e = (int64_t)a.slots * ((a.I + 31) / 32) >= 2 * cus ? launch_up<MT, 4, TERMS>(a, st) : launch_up<MT, 2, TERMS>(a, st);
+  if (e != hipSuccess) return e;
+  if ((int64_t)a.slots * ((a.H + 127) / 128) >= 2 * cus)
+    e = launch_down<8, TERMS>(a, st);
+  else
+    e = (int64_t)a.slots * ((a.H + 63) / 64) >= 2 * cus ? launch_down<4, TERMS>(a, st) : launch_down<2, TERMS>(a, st);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), dim3(256), 0, st, a);
   return hipGetLastError();
@@ -407,16 +362,18 @@ hipError_t launch_all(const MoeArgs& a, hipStream_t st) {
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Slots: one per expert, or, where the tokens can choose fewer, one per token and rank.
-void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int terms, MoeArgs* a, int64_t off[3],
+void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int terms, MoeArgs* a, int64_t off[5],
                 int64_t* total) {
   a->by_token = T * k < E;
   a->slots = (int)(a->by_token ? T * k : E);
   a->mt_cap = (int)((T + 15) / 16);
-  const int64_t units = (I + kUnit - 1) / kUnit;
+  const int64_t chunks = (I + kChunk - 1) / kChunk;
   off[0] = 0;
-  off[1] = up256((int64_t)a->slots * (2 + T) * 4);
-  off[2] = off[1] + (int64_t)a->slots * a->mt_cap * units * terms * 4096;
-  *total = off[2] + up256(T * k * H * 4);
+  off[1] = up256(T * k * 4);
+  off[2] = off[1] + up256(T * k * 4);
+  off[3] = off[2] + up256(E * T * 2);
+  off[4] = off[3] + (int64_t)a->slots * a->mt_cap * chunks * terms * 16384;
+  *total = off[4] + up256(T * k * H * 4);
 }
 
 int terms_of(bool y_bf16) { return y_bf16 ? 2 : 3; }
@@ -425,14 +382,14 @@ int terms_of(bool y_bf16) { return y_bf16 ? 2 : 3; }
 
 int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16) {
   MoeArgs a{};
-  int64_t off[3], total;
+  int64_t off[5], total;
   moe_layout(T, H, I, E, k, terms_of(y_bf16), &a, off, &total);
   return total;
 }
 
 hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   MoeArgs a{};
-  int64_t off[3], total;
+  int64_t off[5], total;
   moe_layout(p.T, p.H, p.I, p.E, p.k, terms_of(p.y_bf16), &a, off, &total);
   a.T = (int)p.T;
   a.H = (int)p.H;
@@ -456,9 +413,15 @@ hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   a.s2 = p.s2;
   a.ld_s2 = p.ld_s2;
   a.st_s2 = p.st_s2;
-  a.table = (int*)((uint8_t*)p.workspace + off[0]);
-  a.h = (uint8_t*)p.workspace + off[1];
-  a.part = (float*)((uint8_t*)p.workspace + off[2]);
+  uint8_t* ws = (uint8_t*)p.workspace;
+  a.chosen = (int*)(ws + off[0]);
+  a.share = (float*)(ws + off[1]);
+  a.rank = (int16_t*)(ws + off[2]);
+  a.h = ws + off[3];
+  a.part = (float*)(ws + off[4]);
+  a.x_pieces = (uintptr_t)p.x % 16 == 0 && a.ld_x % 16 == 0;
+  a.s13_words = (uintptr_t)p.s13 % 4 == 0 && p.ld_s13 % 4 == 0 && p.st_s13 % 4 == 0;
+  a.s2_words = (uintptr_t)p.s2 % 4 == 0 && p.ld_s2 % 4 == 0 && p.st_s2 % 4 == 0;
   a.y = p.y;
   a.ld_y = p.ld_y;
   a.y_bf16 = p.y_bf16;
