@@ -148,6 +148,29 @@ __device__ __forceinline__ v4f mma_bf16(v4i w, v4i x, v4f acc) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, x), acc, 0, 0, 0);
 }
 
+// Eight 16-bit elements without the first n (0 .. 7), zeros behind.
+__device__ __forceinline__ v4i drop_low(v4i v, int n) {
+  uint32_t d[4] = {(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
+  if (n & 4) {
+    d[0] = d[2];
+    d[1] = d[3];
+    d[2] = d[3] = 0;
+  }
+  if (n & 2) {
+    d[0] = d[1];
+    d[1] = d[2];
+    d[2] = d[3];
+    d[3] = 0;
+  }
+  if (n & 1) {
+    d[0] = __builtin_amdgcn_alignbit(d[1], d[0], 16);
+    d[1] = __builtin_amdgcn_alignbit(d[2], d[1], 16);
+    d[2] = __builtin_amdgcn_alignbit(d[3], d[2], 16);
+    d[3] >>= 16;
+  }
+  return v4i{(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
+}
+
 // ---- X fragments of a chunk.
 
 // bf16 rows, TERMS = 1; or the sum of TERMS bf16 values (the expert layer's hidden values).
@@ -172,8 +195,9 @@ struct XWide {
     }
   }
 
-  // Straight from memory: row pointers by lane, rows of the tile in use, elements of the chunk.
-  __device__ __forceinline__ void load_direct(int m, const uint8_t* row, bool live, int left, int lane) {
+  // Straight from memory: the lane's row at the chunk, whether it is one, the elements left in it
+  // and the row's length.  A piece that the row's end cuts is read from the last 8 elements.
+  __device__ __forceinline__ void load_direct(int m, const uint8_t* row, bool live, int left, int K, int lane) {
     const int g = lane >> 4;
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -181,15 +205,23 @@ struct XWide {
       for (int j = 0; j < 4; ++j) {
         const int k = 32 * (4 * g + u) + 8 * j;
         v4i v = {0, 0, 0, 0};
-        if (live && k + 8 <= left) {
-          __builtin_memcpy(&v, row + 2 * k, 16);
-        } else if (live && k < left) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (k + e < left) v[e >> 1] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(row)[k + e] << (16 * (e & 1)));
-        }
+        if (live && k < left && K >= 8) __builtin_memcpy(&v, row + 2 * min(k, left - 8), 16);
         f[u][j][m][0] = v;
       }
+    if (left < kChunk) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = 32 * (4 * g + u) + 8 * j, cut = k < left ? max(k + 8 - left, 0) : 0;
+          f[u][j][m][0] = drop_low(f[u][j][m][0], cut);
+        }
+    }
+    if (K < 8 && g == 0 && live) {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < K) f[0][0][m][0][e >> 1] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << (16 * (e & 1)));
+    }
   }
 
   // From 16 rows of 1 KiB in LDS, 16-byte piece p of row r at p ^ r.
@@ -229,29 +261,51 @@ __device__ __forceinline__ void stage_rows(uint64_t row, int rows, int c, uint32
   }
 }
 
-// ---- the stream.  tile_of(t, c, lds) starts the DMA of row tile t's item; load_x(x, c, first)
-// brings the chunk's X fragments, calling first() as soon as the ring is its own no more;
-// scales_of(t, c, slot) gives a tile's scale dword.  acc[m][t] holds row tile m, tile t.
+// ---- the stream.  A wave's run of items [it0, it1), item c * NTW + t being row tile t of chunk c.
+struct Run {
+  int it0, it1;
+};
+
+template <int NTW>
+__device__ __forceinline__ Run run_of(int K, int wave) {
+  const int items = ((K + kChunk - 1) / kChunk) * NTW;
+  return Run{items * wave / kWaves, items * (wave + 1) / kWaves};
+}
+
+// Starts the DMA of up to a ring's worth of items from `it` on, those before `end`.
+template <int NTW, typename Issue>
+__device__ __forceinline__ void fill_ring(int it, int end, uint32_t lds0, Issue issue) {
+#pragma unroll
+  for (int n = 0; n < kRing; ++n)
+    if (it + n < end) issue((it + n) % NTW, (it + n) / NTW, lds0 + n * kSlot);
+}
+
+// issue(t, c, lds) starts an item's DMA; load_x(x, c) brings a chunk's X fragments;
+// scales_of(t, c, slot) gives an item's scale dword.  acc[m][t] sums row tile m of X, t of W.
+// through: load_x leaves the ring alone, so items of the next chunk are in flight already when
+// a chunk ends, and the caller has filled the ring for the first one; otherwise X passes
+// through the ring and every chunk starts with it empty.
 template <typename X, int MT, int NTW, typename Issue, typename Load, typename Scales>
-__device__ __forceinline__ void stream(int K, int wave, int lane, bool s_words, Issue issue, Load load_x, Scales scales_of,
-                                       v4f acc[MT][NTW]) {
+__device__ __forceinline__ void stream(Run run, int wave, int lane, bool s_words, bool through, Issue issue, Load load_x,
+                                       Scales scales_of, v4f acc[MT][NTW]) {
   const uint32_t ring = (uint32_t)wave * kWaveLds;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)smem + ring;
-  const int items = ((K + kChunk - 1) / kChunk) * NTW;
-  const int it0 = items * wave / kWaves, it1 = items * (wave + 1) / kWaves;
-  for (int c = it0 / NTW; c * NTW < it1; ++c) {
-    const int lo = max(it0 - c * NTW, 0), hi = min(it1 - c * NTW, NTW);
+  int n = 0;                                             // the slot of the next item
+  for (int c = run.it0 / NTW; c * NTW < run.it1; ++c) {
+    const int lo = max(run.it0 - c * NTW, 0), hi = min(run.it1 - c * NTW, NTW);
+    const int end = through ? run.it1 : c * NTW + hi;    // items that may be in flight
     X x;
-    load_x(x, c, [&]() {
-#pragma unroll
-      for (int n = 0; n < kRing; ++n)
-        if (lo + n < hi) issue(lo + n, c, lds0 + n * kSlot);
-    });
+    load_x(x, c);
+    if (!through) {
+      fill_ring<NTW>(c * NTW + lo, end, lds0, issue);
+      n = 0;
+    }
 #pragma unroll
     for (int t = 0; t < NTW; ++t) {
       if (t < lo || t >= hi) continue;
+      const int it = c * NTW + t;
       // in flight behind this item: up to three more
-      const int after = hi - 1 - t;
+      const int after = end - 1 - it;
       if (!s_words || after == 0)
         wait_vm<0>();
       else if (after == 1)
@@ -261,13 +315,14 @@ __device__ __forceinline__ void stream(int K, int wave, int lane, bool s_words, 
       else
         wait_vm<15>();
       asm volatile("" ::: "memory");
-      const uint32_t n = (uint32_t)(t - lo) % kRing, slot = ring + n * kSlot;
+      const uint32_t slot = ring + n * kSlot;
       v4i w[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) w[u] = item_codes(slot, lane, u);
       const uint32_t ws = scales_of(t, c, slot);
       reads_done();
-      if (t + kRing < hi) issue(t + kRing, c, lds0 + n * kSlot);
+      if (it + kRing < end) issue((it + kRing) % NTW, (it + kRing) / NTW, lds0 + n * kSlot);
+      n = (n + 1) % kRing;
       x.mma(w, ws, &acc[0][t], NTW);
     }
   }

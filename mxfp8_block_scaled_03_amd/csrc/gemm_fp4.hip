@@ -67,10 +67,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm4_stream(const Fp4Args a, c
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NTW; ++n) acc[m][n] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const Run run = run_of<NTW>(a.K, wave);
   if constexpr (XFP4) {
     const Lines xl = lines_of(a.x + m0 * a.ld_x, a.ld_x, a.xs + m0 * a.ld_xs, a.ld_xs, min(16 * MT, a.M - m0), nb, a.xs_words);
     const ItemOffsets xo = item_offsets(xl.ld_c, xl.ld_s, lane);
-    stream<XFp4<MT>, MT, NTW>(a.K, wave, lane, a.ws_words, issue, [&](XFp4<MT>& x, int c, auto first) {
+    stream<XFp4<MT>, MT, NTW>(run, wave, lane, a.ws_words, false, issue, [&](XFp4<MT>& x, int c) {
       static_assert(MT <= kRing, "X tiles pass through the ring");
 #pragma unroll
       for (int m = 0; m < MT; ++m) issue_item(xl, xo, m, c, lds0 + m * kSlot);
@@ -86,19 +87,20 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm4_stream(const Fp4Args a, c
         x.s[m] = item_scales(xl, ring + m * kSlot, m, c, nb, lane);
       }
       reads_done();
-      first();
     }, scales_of, acc);
   } else {
     const uint8_t* row[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) row[m] = a.x + min((int64_t)m0 + 16 * m + i, (int64_t)a.M - 1) * a.ld_x;
-    stream<XWide<MT, 1>, MT, NTW>(a.K, wave, lane, a.ws_words, issue, [&](XWide<MT, 1>& x, int c, auto first) {
+    // few rows come straight into registers; more pass through the ring a chunk at a time
+    const bool through = a.M - m0 <= 4 || !a.x_pieces;
+    if (through) fill_ring<NTW>(run.it0, run.it1, lds0, issue);
+    stream<XWide<MT, 1>, MT, NTW>(run, wave, lane, a.ws_words, through, issue, [&](XWide<MT, 1>& x, int c) {
       const int left = a.K - kChunk * c;
-      if (a.M - m0 <= 4 || left < kChunk || !a.x_pieces) {
-        first();
+      if (through || left < kChunk) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          x.load_direct(m, row[m] + 2 * kChunk * (int64_t)c, m0 + 16 * m + i < a.M, left, lane);
+          x.load_direct(m, row[m] + 2 * kChunk * (int64_t)c, m0 + 16 * m + i < a.M, left, a.K, lane);
       } else {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -108,7 +110,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm4_stream(const Fp4Args a, c
           x.read_staged(m, ring, lane);
           reads_done();
         }
-        first();
       }
     }, scales_of, acc);
   }

@@ -114,22 +114,23 @@ __global__ __launch_bounds__(kThreads) void k_moe_route(const MoeArgs a) {
   }
 }
 
-// The expert of a slot and its tokens, in order: s_row[m] = t * k + rank.  Returns their number,
-// 0 where there is nothing to do: no token, or (by_token) an earlier token's slot has the
-// expert already.  Ends with a barrier.
-__device__ __forceinline__ int slot_tokens(const MoeArgs& a, int slot, int* s_row, int* s_cnt, int& e) {
-  e = a.by_token ? a.chosen[slot] : slot;
+// The expert of a slot, or -1.
+__device__ __forceinline__ int slot_expert(const MoeArgs& a, int slot) { return a.by_token ? a.chosen[slot] : slot; }
+
+// The tokens of a slot's expert e, in order: s_row[m] = t * k + rank.  Returns their number, 0
+// where there is nothing to do: no token, or (by_token) an earlier token's slot has the expert
+// already.  Holds a barrier.
+__device__ __forceinline__ int slot_tokens(const MoeArgs& a, int slot, int e, int* s_row, int* s_cnt) {
   const int lane = threadIdx.x & 63;
   if (threadIdx.x < 64) {
     int cnt = 0;
-    if (e >= 0)
-      for (int t0 = 0; t0 < a.T; t0 += 64) {
-        const int t = t0 + lane;
-        const int r = t < a.T ? a.rank[(int64_t)e * a.T + t] : -1;
-        const uint64_t b = __ballot(r >= 0);
-        if (r >= 0) s_row[cnt + __popcll(b & ((1ull << lane) - 1))] = t * a.k + r;
-        cnt += __popcll(b);
-      }
+    for (int t0 = 0; t0 < a.T; t0 += 64) {
+      const int t = t0 + lane;
+      const int r = t < a.T ? a.rank[(int64_t)e * a.T + t] : -1;
+      const uint64_t b = __ballot(r >= 0);
+      if (r >= 0) s_row[cnt + __popcll(b & ((1ull << lane) - 1))] = t * a.k + r;
+      cnt += __popcll(b);
+    }
     if (lane == 0) *s_cnt = cnt;
   }
   __syncthreads();
@@ -157,17 +158,17 @@ __device__ __forceinline__ int64_t h_offset(int m, int k) {
 
 // ---- gate and up products.  A workgroup: one slot, 8 * NTW columns of I: row tiles
 // 0 .. NTW/2-1 of its 16 * NTW rows of w13 are gate rows, the others the up rows.
-template <int MT, int NTW, int TERMS>
+template <int NTW, int TERMS>
 __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
   constexpr int IC = 8 * NTW, NG = NTW / 2;
-  int* s_row = reinterpret_cast<int*>(smem + stream_lds<MT, NTW>());
+  int* s_row = reinterpret_cast<int*>(smem + stream_lds<1, NTW>());
   __shared__ int s_cnt;
-  const int slot = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
+  const int wg = xcd_order(blockIdx.x, a.slots * a.tiles);
+  const int slot = wg / a.tiles, tile = wg % a.tiles;
   const int lane = threadIdx.x & 63, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int e;
-  const int cnt = slot_tokens(a, slot, s_row, &s_cnt, e);
-  if (cnt == 0) return;
+  const int e = slot_expert(a, slot);
+  if (e < 0) return;
   const int i0 = tile * IC, nb = (a.H + 31) / 32;
   const int rows = min(IC, a.I - i0);
   const uint8_t* w = a.w13 + e * a.st_w13 + i0 * a.ld_w13;
@@ -177,39 +178,41 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
   const ItemOffsets wo = item_offsets(gate.ld_c, gate.ld_s, lane);
   const uint32_t ring = (uint32_t)wave * kWaveLds, lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)smem + ring;
   const int chunks = (a.I + kChunk - 1) / kChunk;
-  for (int m0 = 0; m0 < cnt; m0 += 16 * MT) {
-    if (m0 > 0) __syncthreads();
-    v4f acc[MT][NTW];
+  const Run run = run_of<NTW>(a.H, wave);
+  auto issue = [&](int t, int c, uint32_t lds) {
+    if (t < NG) issue_item(gate, wo, t, c, lds);
+    else issue_item(up, wo, t - NG, c, lds);
+  };
+  // few tokens come straight into registers, and the first weights are on their way while they
+  // are looked up; more pass through the ring a chunk at a time
+  const bool through = a.T <= 4 || a.T * a.k <= 2 * a.E || !a.x_pieces;
+  if (through) fill_ring<NTW>(run.it0, run.it1, lds0, issue);
+  const int cnt = slot_tokens(a, slot, e, s_row, &s_cnt);
+  if (cnt == 0) {
+    wait_vm<0>();
+    return;
+  }
+  for (int m0 = 0; m0 < cnt; m0 += 16) {
+    if (m0 > 0) {
+      __syncthreads();
+      if (through) fill_ring<NTW>(run.it0, run.it1, lds0, issue);
+    }
+    v4f acc[1][NTW];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NTW; ++n) acc[m][n] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const uint8_t* row[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) row[m] = a.x + (int64_t)(s_row[min(m0 + 16 * m + i, cnt - 1)] / a.k) * a.ld_x;
-    stream<XWide<MT, 1>, MT, NTW>(
-        a.H, wave, lane, a.s13_words,
-        [&](int t, int c, uint32_t lds) {
-          if (t < NG) issue_item(gate, wo, t, c, lds);
-          else issue_item(up, wo, t - NG, c, lds);
-        },
-        [&](XWide<MT, 1>& x, int c, auto first) {
+    for (int n = 0; n < NTW; ++n) acc[0][n] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint8_t* row = a.x + (int64_t)(s_row[min(m0 + i, cnt - 1)] / a.k) * a.ld_x;
+    stream<XWide<1, 1>, 1, NTW>(
+        run, wave, lane, a.s13_words, through, issue,
+        [&](XWide<1, 1>& x, int c) {
           const int left = a.H - kChunk * c;
-          if (cnt - m0 <= 4 || left < kChunk || !a.x_pieces) {
-            first();
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-              x.load_direct(m, row[m] + 2 * kChunk * (int64_t)c, m0 + 16 * m + i < cnt, left, lane);
+          if (through || left < kChunk) {
+            x.load_direct(0, row + 2 * kChunk * (int64_t)c, m0 + i < cnt, left, a.H, lane);
           } else {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              stage_rows((uint64_t)(uintptr_t)row[m], min(16, cnt - m0 - 16 * m), c, lds0, lane);
-              wait_vm<0>();
-              asm volatile("" ::: "memory");
-              x.read_staged(m, ring, lane);
-              reads_done();
-            }
-            first();
+            stage_rows((uint64_t)(uintptr_t)row, min(16, cnt - m0), c, lds0, lane);
+            wait_vm<0>();
+            asm volatile("" ::: "memory");
+            x.read_staged(0, ring, lane);
+            reads_done();
           }
         },
         [&](int t, int c, uint32_t slot_at) {
@@ -217,16 +220,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
         },
         acc);
     __syncthreads();
-    store_part<MT, NTW>(wave, lane, acc);
+    store_part<1, NTW>(wave, lane, acc);
     __syncthreads();
-    for (int q = threadIdx.x; q < 16 * MT * (IC / 8); q += kThreads) {
+    for (int q = threadIdx.x; q < 16 * (IC / 8); q += kThreads) {
       const int m = q / (IC / 8), c = 8 * (q % (IC / 8));
       if (m0 + m >= cnt || i0 + c >= a.I) continue;
       const float share = a.share[s_row[m0 + m]];
       uint32_t o[TERMS][4];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const v4f gt = sum_part<MT, NTW>(m, c + 4 * hf), u = sum_part<MT, NTW>(m, IC + c + 4 * hf);
+        const v4f gt = sum_part<1, NTW>(m, c + 4 * hf), u = sum_part<1, NTW>(m, IC + c + 4 * hf);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           uint32_t b0[TERMS], b1[TERMS];
@@ -237,8 +240,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
           for (int t = 0; t < TERMS; ++t) o[t][2 * hf + p] = b0[t] | (b1[t] << 16);
         }
       }
-      const int mt = (m0 + m) / 16;
-      uint8_t* dst = a.h + ((int64_t)slot * a.mt_cap + mt) * chunks * (TERMS * 16384) + h_offset<TERMS>(m % 16, i0 + c);
+      const int mt = m0 / 16;
+      uint8_t* dst = a.h + ((int64_t)slot * a.mt_cap + mt) * chunks * (TERMS * 16384) + h_offset<TERMS>(m, i0 + c);
 #pragma unroll
       for (int t = 0; t < TERMS; ++t)
         *reinterpret_cast<uint4*>(dst + 4096 * t) = make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
@@ -251,36 +254,49 @@ template <int NTW, int TERMS>
 __global__ __launch_bounds__(kThreads, TERMS == 2 ? 2 : 1) void k_moe_down(const MoeArgs a) {
   int* s_row = reinterpret_cast<int*>(smem + stream_lds<1, NTW>());
   __shared__ int s_cnt;
-  const int slot = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
-  const int lane = threadIdx.x & 63;
+  const int wg = xcd_order(blockIdx.x, a.slots * a.tiles);
+  const int slot = wg / a.tiles, tile = wg % a.tiles;
+  const int lane = threadIdx.x & 63, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int e;
-  const int cnt = slot_tokens(a, slot, s_row, &s_cnt, e);
-  if (cnt == 0) return;
+  const int e = slot_expert(a, slot);
+  if (e < 0) return;
   const int n0 = 16 * NTW * tile, nb = (a.I + 31) / 32;
   const Lines w = lines_of(a.w2 + e * a.st_w2 + n0 * a.ld_w2, a.ld_w2, a.s2 + e * a.st_s2 + n0 * a.ld_s2, a.ld_s2,
                            min(16 * NTW, a.H - n0), nb, a.s2_words);
   const ItemOffsets wo = item_offsets(w.ld_c, w.ld_s, lane);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)smem + (uint32_t)wave * kWaveLds;
   const int chunks = (a.I + kChunk - 1) / kChunk;
+  const Run run = run_of<NTW>(a.I, wave);
+  auto issue = [&](int t, int c, uint32_t lds) { issue_item(w, wo, t, c, lds); };
+  fill_ring<NTW>(run.it0, run.it1, lds0, issue);
+  const int cnt = slot_tokens(a, slot, e, s_row, &s_cnt);
+  if (cnt == 0) {
+    wait_vm<0>();
+    return;
+  }
   for (int m0 = 0; m0 < cnt; m0 += 16) {
-    if (m0 > 0) __syncthreads();
+    if (m0 > 0) {
+      __syncthreads();
+      fill_ring<NTW>(run.it0, run.it1, lds0, issue);
+    }
     const uint8_t* h = a.h + ((int64_t)slot * a.mt_cap + m0 / 16) * chunks * (TERMS * 16384) + 16 * lane;
     v4f acc[1][NTW];
 #pragma unroll
     for (int n = 0; n < NTW; ++n) acc[0][n] = {0.0f, 0.0f, 0.0f, 0.0f};
     stream<XWide<1, TERMS>, 1, NTW>(
-        a.I, wave, lane, a.s2_words, [&](int t, int c, uint32_t lds) { issue_item(w, wo, t, c, lds); },
-        [&](XWide<1, TERMS>& x, int c, auto first) {
-          first();
+        run, wave, lane, a.s2_words, true, issue,
+        [&](XWide<1, TERMS>& x, int c) {
 #pragma unroll
           for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int p = 0; p < TERMS; ++p)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
+                // rows past the last token and elements past I have nothing in h
                 const int k = kChunk * c + 32 * (4 * (lane >> 4) + u) + 8 * j;
-                v4i v = {0, 0, 0, 0};                  // h has nothing at k >= I
-                if (k < a.I) v = *reinterpret_cast<const v4i*>(h + (((int64_t)4 * c + u) * TERMS + p) * 4096 + 1024 * j);
+                v4i v = {0, 0, 0, 0};
+                if (k < a.I && m0 + i < cnt)
+                  v = *reinterpret_cast<const v4i*>(h + (((int64_t)4 * c + u) * TERMS + p) * 4096 + 1024 * j);
                 x.f[u][j][0][p] = v;
               }
         },
@@ -313,15 +329,15 @@ __global__ __launch_bounds__(256) void k_moe_sum(const MoeArgs a) {
     reinterpret_cast<float*>(a.y)[t * a.ld_y + n] = s;
 }
 
-template <int MT, int NTW, int TERMS>
+template <int NTW, int TERMS>
 hipError_t launch_up(MoeArgs a, hipStream_t st) {
   static bool set[64] = {false};
   a.tiles = (a.I + 8 * NTW - 1) / (8 * NTW);
   if ((int64_t)a.slots * a.tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = k_moe_up<MT, NTW, TERMS>;
-  const hipError_t e = allow_lds(kern, stream_lds<MT, NTW>() + 4 * 1024, set);
+  auto kern = k_moe_up<NTW, TERMS>;
+  const hipError_t e = allow_lds(kern, stream_lds<1, NTW>() + 4 * 1024, set);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.slots * a.tiles)), dim3(kThreads), (stream_lds<MT, NTW>() + 4 * a.T), st, a);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.slots * a.tiles)), dim3(kThreads), (stream_lds<1, NTW>() + 4 * a.T), st, a);
   return hipGetLastError();
 }
 
@@ -339,16 +355,16 @@ hipError_t launch_down(MoeArgs a, hipStream_t st) {
 
 // Column tiles as wide as still give every CU two workgroups (a slot's expert may be unused, so
 // the count is an upper bound).
-template <int MT, int TERMS>
+template <int TERMS>
 hipError_t launch_all(const MoeArgs& a, hipStream_t st) {
   const int64_t cus = device_cu_count();
   hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if ((int64_t)a.slots * ((a.I + 63) / 64) >= 2 * cus)
-    e = launch_up<MT, 8, TERMS>(a, st);
+    e = launch_up<8, TERMS>(a, st);
   else
-    e = (int64_t)a.slots * ((a.I + 31) / 32) >= 2 * cus ? launch_up<MT, 4, TERMS>(a, st) : launch_up<MT, 2, TERMS>(a, st);
+    e = (int64_t)a.slots * ((a.I + 31) / 32) >= 2 * cus ? launch_up<4, TERMS>(a, st) : launch_up<2, TERMS>(a, st);
   if (e != hipSuccess) return e;
   if ((int64_t)a.slots * ((a.H + 127) / 128) >= 2 * cus)
     e = launch_down<8, TERMS>(a, st);
@@ -425,10 +441,7 @@ hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   a.y = p.y;
   a.ld_y = p.ld_y;
   a.y_bf16 = p.y_bf16;
-  // rows that an expert can expect: 32-row tiles once its share of the tokens passes 16
-  const bool wide = p.T > 16 && p.T * p.k > 12 * p.E;
-  if (p.y_bf16) return wide ? launch_all<2, 2>(a, st) : launch_all<1, 2>(a, st);
-  return wide ? launch_all<2, 3>(a, st) : launch_all<1, 3>(a, st);
+  return p.y_bf16 ? launch_all<2>(a, st) : launch_all<3>(a, st);
 }
 
 }  // namespace mxq
