@@ -14,42 +14,12 @@
 //
 // An expert with logit -inf is never taken: its share is zero, and a token whose logits are
 // all -inf gets y = 0.  NaN logits order above +inf; their shares are NaN, as softmax's.
-#include "fp4_stream.hpp"
+#include <math.h>
+
+#include "moe_fp4.hpp"
 
 namespace mxq {
 namespace {
-
-constexpr uint32_t kMasked = 0x007FFFFFu;   // order key of -inf
-
-struct MoeArgs {
-  int T, H, I, E, k, renorm;
-  int slots, by_token;                 // by_token: slot = (token, rank), else slot = expert
-  int mt_cap;                          // 16-row tiles that a slot's part of h holds
-  int tiles;                           // column tiles of a launch
-  const uint8_t* x;
-  int64_t ld_x;                        // bytes
-  bool x_pieces;                       // X rows are whole 16-byte pieces
-  bool s13_words, s2_words;            // scale rows are whole 4-byte words
-  const float* logits;
-  int64_t ld_logits;
-  const uint8_t *w13, *s13, *w2, *s2;
-  int64_t ld_w13, st_w13, ld_s13, st_s13, ld_w2, st_w2, ld_s2, st_s2;   // rows and experts, bytes
-  int* chosen;                         // [T][k]: expert, or -1
-  float* share;                        // [T][k]
-  int16_t* rank;                       // [E][T]: rank of the expert for the token, or -1
-  uint8_t* h;                          // [slots][mt_cap][chunks][4][terms][4][64][16 bytes]
-  float* part;                         // [T * k][H]
-  void* y;
-  int64_t ld_y;
-  int y_bf16;
-};
-
-// Order key of a logit: greater for greater values, equal for -0 and +0, NaN above +inf.
-__device__ __forceinline__ uint32_t order_key(float l) {
-  if (l != l) return 0xFFFFFFFFu;
-  const uint32_t b = __float_as_uint(l + 0.0f);
-  return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
-}
 
 // The rank of the lane's own expert j (key kj) in the row: how many come before it.
 __device__ __forceinline__ int rank_of(const float* row, int E, int j, uint32_t kj, int lane) {
@@ -138,24 +108,6 @@ __device__ __forceinline__ int slot_tokens(const MoeArgs& a, int slot, int e, in
   return cnt > 0 && a.by_token && s_row[0] != slot ? 0 : cnt;
 }
 
-// Rounds v to `TERMS` bf16 terms whose sum is v to 8 * TERMS bits.
-template <int TERMS>
-__device__ __forceinline__ void split_bf16(float v, uint32_t out[TERMS]) {
-#pragma unroll
-  for (int t = 0; t < TERMS; ++t) {
-    const uint32_t b = f32_to_bf16_rne(v);
-    out[t] = b;
-    v = (b & 0x7F80u) == 0x7F80u ? 0.0f : v - __uint_as_float(b << 16);
-  }
-}
-
-// Byte offset in a 16-row tile of h of the 16 bytes that hold row m's elements k .. k+7, term 0.
-template <int TERMS>
-__device__ __forceinline__ int64_t h_offset(int m, int k) {
-  const int c = k / kChunk, b = (k % kChunk) / 32;       // block b = 4 g + u of the chunk
-  return ((int64_t)(4 * c + b % 4) * TERMS * 4 + (k % 32) / 8) * 1024 + (16 * (b / 4) + m) * 16;
-}
-
 // ---- gate and up products.  A workgroup: one slot, 8 * NTW columns of I: row tiles
 // 0 .. NTW/2-1 of its 16 * NTW rows of w13 are gate rows, the others the up rows.
 template <int NTW, int TERMS>
@@ -234,8 +186,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
         for (int p = 0; p < 2; ++p) {
           uint32_t b0[TERMS], b1[TERMS];
           const int col = i0 + c + 4 * hf + 2 * p;     // zeros past I
-          split_bf16<TERMS>(col < a.I ? share * (silu(gt[2 * p]) * u[2 * p]) : 0.0f, b0);
-          split_bf16<TERMS>(col + 1 < a.I ? share * (silu(gt[2 * p + 1]) * u[2 * p + 1]) : 0.0f, b1);
+          split_bf16<TERMS>(col < a.I ? gated(share, gt[2 * p], u[2 * p]) : 0.0f, b0);
+          split_bf16<TERMS>(col + 1 < a.I ? gated(share, gt[2 * p + 1], u[2 * p + 1]) : 0.0f, b1);
 #pragma unroll
           for (int t = 0; t < TERMS; ++t) o[t][2 * hf + p] = b0[t] | (b1[t] << 16);
         }
@@ -322,7 +274,8 @@ __global__ __launch_bounds__(256) void k_moe_sum(const MoeArgs a) {
   const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
   if (n >= a.H) return;
   float s = 0.0f;
-  for (int r = 0; r < a.k && a.chosen[t * a.k + r] >= 0; ++r) s += a.part[((int64_t)t * a.k + r) * a.H + n];
+  for (int r = 0; r < a.k && a.chosen[t * a.k + r] >= 0; ++r)
+    for (int p = 0; p < a.parts; ++p) s += a.part[(((int64_t)t * a.k + r) * a.parts + p) * a.H + n];
   if (a.y_bf16)
     reinterpret_cast<uint16_t*>(a.y)[t * a.ld_y + n] = (uint16_t)f32_to_bf16_rne(s);
   else
@@ -353,32 +306,76 @@ hipError_t launch_down(MoeArgs a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Experts that some token chooses, if the choices were independent.
+double active_experts(int64_t T, int64_t E, int64_t k) { return E * (1.0 - pow(1.0 - (double)k / E, (double)T)); }
+
+// K ranges of the wide down product: the fewest, up to 8, whose works come out even enough over
+// the workgroups (a range costs a partial row per token and expert).
+int down_parts(int64_t works, int64_t chunks, int64_t cus) {
+  int best = 1;
+  double eff = 0.0;
+  for (int p = 1; p <= 8 && p <= chunks; p *= 2) {
+    const double n = (double)works * p, rounds = ceil(n / cus), e = n / (rounds * cus) - 0.02 * p;
+    if (e > eff + 0.01) {
+      eff = e;
+      best = p;
+    }
+  }
+  return best;
+}
+
+struct Plan {
+  bool up_wide, down_wide;
+  int parts;
+};
+
+// The wide kernels keep one workgroup per CU busy with a queue of works (128 columns of I or 256 of H
+// of one expert); below about two works a CU the finer workgroups of this file are better.
+Plan plan_of(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16) {
+  const int64_t cus = device_cu_count();
+  const double experts = active_experts(T, E, k);
+  const int64_t chunks = (I + kChunk - 1) / kChunk;
+  Plan p{};
+  p.up_wide = experts * ((I + 127) / 128) >= 1.9 * cus;
+  const int64_t works = (int64_t)(experts * ((H + 255) / 256));
+  p.parts = y_bf16 ? down_parts(works, chunks, cus) : 1;
+  p.down_wide = y_bf16 && (double)works * p.parts >= 1.9 * cus;
+  if (!p.down_wide) p.parts = 1;
+  return p;
+}
+
 // Column tiles as wide as still give every CU two workgroups (a slot's expert may be unused, so
 // the count is an upper bound).
 template <int TERMS>
-hipError_t launch_all(const MoeArgs& a, hipStream_t st) {
+hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
   const int64_t cus = device_cu_count();
   hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if ((int64_t)a.slots * ((a.I + 63) / 64) >= 2 * cus)
+  if (plan.up_wide && a.x_pieces && a.H % 8 == 0 && a.s13_words)
+    e = launch_moe_up_wide<TERMS>(a, st);
+  else if ((int64_t)a.slots * ((a.I + 63) / 64) >= 2 * cus)
     e = launch_up<8, TERMS>(a, st);
   else
     e = (int64_t)a.slots * ((a.I + 31) / 32) >= 2 * cus ? launch_up<4, TERMS>(a, st) : launch_up<2, TERMS>(a, st);
   if (e != hipSuccess) return e;
-  if ((int64_t)a.slots * ((a.H + 127) / 128) >= 2 * cus)
-    e = launch_down<8, TERMS>(a, st);
+  MoeArgs d = a;
+  d.parts = plan.down_wide && a.s2_words ? plan.parts : 1;
+  if (plan.down_wide && a.s2_words)
+    e = launch_moe_down_wide(d, st);
+  else if ((int64_t)a.slots * ((a.H + 127) / 128) >= 2 * cus)
+    e = launch_down<8, TERMS>(d, st);
   else
-    e = (int64_t)a.slots * ((a.H + 63) / 64) >= 2 * cus ? launch_down<4, TERMS>(a, st) : launch_down<2, TERMS>(a, st);
+    e = (int64_t)a.slots * ((a.H + 63) / 64) >= 2 * cus ? launch_down<4, TERMS>(d, st) : launch_down<2, TERMS>(d, st);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), dim3(256), 0, st, d);
   return hipGetLastError();
 }
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Slots: one per expert, or, where the tokens can choose fewer, one per token and rank.
-void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int terms, MoeArgs* a, int64_t off[5],
+void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int terms, int parts, MoeArgs* a, int64_t off[5],
                 int64_t* total) {
   a->by_token = T * k < E;
   a->slots = (int)(a->by_token ? T * k : E);
@@ -389,7 +386,7 @@ void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int terms
   off[2] = off[1] + up256(T * k * 4);
   off[3] = off[2] + up256(E * T * 2);
   off[4] = off[3] + (int64_t)a->slots * a->mt_cap * chunks * terms * 16384;
-  *total = off[4] + up256(T * k * H * 4);
+  *total = off[4] + up256(T * k * parts * H * 4);
 }
 
 int terms_of(bool y_bf16) { return y_bf16 ? 2 : 3; }
@@ -399,14 +396,15 @@ int terms_of(bool y_bf16) { return y_bf16 ? 2 : 3; }
 int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16) {
   MoeArgs a{};
   int64_t off[5], total;
-  moe_layout(T, H, I, E, k, terms_of(y_bf16), &a, off, &total);
+  moe_layout(T, H, I, E, k, terms_of(y_bf16), plan_of(T, H, I, E, k, y_bf16).parts, &a, off, &total);
   return total;
 }
 
 hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   MoeArgs a{};
   int64_t off[5], total;
-  moe_layout(p.T, p.H, p.I, p.E, p.k, terms_of(p.y_bf16), &a, off, &total);
+  const Plan plan = plan_of(p.T, p.H, p.I, p.E, p.k, p.y_bf16);
+  moe_layout(p.T, p.H, p.I, p.E, p.k, terms_of(p.y_bf16), plan.parts, &a, off, &total);
   a.T = (int)p.T;
   a.H = (int)p.H;
   a.I = (int)p.I;
@@ -441,7 +439,7 @@ hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   a.y = p.y;
   a.ld_y = p.ld_y;
   a.y_bf16 = p.y_bf16;
-  return p.y_bf16 ? launch_all<2>(a, st) : launch_all<3>(a, st);
+  return p.y_bf16 ? launch_all<2>(a, plan, st) : launch_all<3>(a, plan, st);
 }
 
 }  // namespace mxq

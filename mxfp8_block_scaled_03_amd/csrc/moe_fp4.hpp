@@ -1,0 +1,72 @@
+// moe_fp4.hpp -- what the kernels of the expert layer share: their arguments, the order of
+// logits, and the layout of the hidden values.
+#pragma once
+#include "fp4_stream.hpp"
+
+namespace mxq {
+
+constexpr uint32_t kMasked = 0x007FFFFFu;   // order key of -inf
+
+struct MoeArgs {
+  int T, H, I, E, k, renorm;
+  int slots, by_token;                 // by_token: slot = (token, rank), else slot = expert
+  int mt_cap;                          // 16-row tiles that a slot's part of h holds
+  int tiles;                           // column tiles of a launch
+  const uint8_t* x;
+  int64_t ld_x;                        // bytes
+  bool x_pieces;                       // X rows are whole 16-byte pieces
+  bool s13_words, s2_words;            // scale rows are whole 4-byte words
+  const float* logits;
+  int64_t ld_logits;
+  const uint8_t *w13, *s13, *w2, *s2;
+  int64_t ld_w13, st_w13, ld_s13, st_s13, ld_w2, st_w2, ld_s2, st_s2;   // rows and experts, bytes
+  int* chosen;                         // [T][k]: expert, or -1
+  float* share;                        // [T][k]
+  int16_t* rank;                       // [E][T]: rank of the expert for the token, or -1
+  uint8_t* h;                          // [slots][mt_cap][chunks][4][terms][4][64][16 bytes]
+  int parts;                           // K ranges of the down product
+  float* part;                         // [T * k][parts][H]
+  void* y;
+  int64_t ld_y;
+  int y_bf16;
+};
+
+namespace {
+
+// Order key of a logit: greater for greater values, equal for -0 and +0, NaN above +inf.
+__device__ __forceinline__ uint32_t order_key(float l) {
+  if (l != l) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(l + 0.0f);
+  return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+// Rounds v to `TERMS` bf16 terms whose sum is v to 8 * TERMS bits.
+template <int TERMS>
+__device__ __forceinline__ void split_bf16(float v, uint32_t out[TERMS]) {
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) {
+    const uint32_t b = f32_to_bf16_rne(v);
+    out[t] = b;
+    v = (b & 0x7F80u) == 0x7F80u ? 0.0f : v - __uint_as_float(b << 16);
+  }
+}
+
+// Byte offset in a 16-row tile of h of the 16 bytes that hold row m's elements k .. k+7, term 0.
+template <int TERMS>
+__device__ __forceinline__ int64_t h_offset(int m, int k) {
+  const int c = k / kChunk, b = (k % kChunk) / 32;       // block b = 4 g + u of the chunk
+  return ((int64_t)(4 * c + b % 4) * TERMS * 4 + (k % 32) / 8) * 1024 + (16 * (b / 4) + m) * 16;
+}
+
+// Share times the gated value of one hidden element, SiLU in fp32.
+__device__ __forceinline__ float gated(float share, float gate, float up) { return share * (silu(gate) * up); }
+
+}  // namespace
+
+// The kernels of many workgroups' worth of weights (moe_fp4_wide.hip): rows of X in whole 16-byte
+// pieces and H a multiple of 8, scale rows in whole words.  up fills h, down fills part.
+template <int TERMS>
+hipError_t launch_moe_up_wide(const MoeArgs& a, hipStream_t st);
+hipError_t launch_moe_down_wide(const MoeArgs& a, hipStream_t st);
+
+}  // namespace mxq

@@ -1,0 +1,450 @@
+// moe_fp4_wide.hip -- the expert layer's gate, up and down products where there are weights for
+// every CU to stream for long: one persistent workgroup per CU over an equal run of works.
+//
+// A work is 16 tokens of one expert x 128 columns of I (up: 16 gate and 16 up rows of w13 for
+// each of eight waves) or 256 columns of H (down: 32 rows of w2 a wave), over all of K or one
+// range of it.  A wave owns its columns, so nothing is added across waves: its weights move as
+// in fp4_stream.hpp (items of 16 rows x 512 elements, LDS DMA into a ring of its own, three
+// slots) without a pause from chunk to chunk and from work to work, because the DMA runs three
+// items ahead of the products through the whole run.  X is shared: the workgroup stages it by
+// DMA, a stage or two ahead, and meets at one barrier per stage.
+//
+// Every stage issues the same number of loads (those past the run's end, and rows of X that no
+// token has, go through an empty descriptor), so the waits are constants; an item's wait counts
+// the loads issued after it.  Against the finer workgroups of moe_fp4.hip, whose fixed costs
+// (looking up tokens, filling the ring, adding the waves' sums) come at the same time on every
+// CU: gate and up of 64 tokens over 64 experts of 4096 x 2048 (570 MB) 135 us before.
+#include "moe_fp4.hpp"
+
+namespace mxq {
+namespace {
+namespace wide {
+
+constexpr int kW = 8;                        // waves
+constexpr int kT = 64 * kW;
+constexpr int kRingW = 3;
+constexpr int kRingBytes = kW * kRingW * kSlot;
+constexpr int kStage = 16384;                // bytes of X per stage
+constexpr int kUpStages = 2, kDownStages = 3;
+
+// The run of works of this workgroup, and where a work lies: s_end[s] is the number of works of
+// slots 0 .. s.  A slot's works: its 16-token tiles, of each its K ranges, of each its columns.
+struct Works {
+  const int* s_end;
+  int tiles, parts;
+};
+
+struct Pos {
+  int w, slot, m, part, tile;
+};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ void seek(Pos& p, const Works& q, int w) {
+  p.w = w;
+  while (uniform(q.s_end[p.slot]) <= w) ++p.slot;
+  const int i = w - (p.slot > 0 ? uniform(q.s_end[p.slot - 1]) : 0);
+  const int per = q.tiles * q.parts;
+  p.m = i / per;
+  p.part = (i % per) / q.tiles;
+  p.tile = i % q.tiles;
+}
+
+__device__ __forceinline__ int expert_of(const MoeArgs& a, int slot) { return a.by_token ? uniform(a.chosen[slot]) : slot; }
+
+// The wave's lanes 0 .. 15: t * k + rank + 1 of the expert's tokens 16 m .. 16 m + 15, 0 past the
+// last; other lanes: anything.
+__device__ __forceinline__ int rows_of(const MoeArgs& a, int e, int m, int lane) {
+  int got = 0, before = 0;
+  for (int t0 = 0; t0 < a.T; t0 += 64) {
+    const int t = t0 + lane;
+    const int r = t < a.T ? a.rank[(int64_t)e * a.T + t] : -1;
+    const uint64_t b = __ballot(r >= 0);
+    const int at = before + __popcll(b & ((1ull << lane) - 1)) - 16 * m;
+    const bool mine = r >= 0 && at >= 0 && at < 16;
+    got |= __builtin_amdgcn_ds_permute(4 * (mine ? at : 63), mine ? t * a.k + r + 1 : 0);
+    before += __popcll(b);
+  }
+  return got;
+}
+
+// Counts every slot's works into s_end (all waves; barriers inside) and returns the total.
+__device__ __forceinline__ int count_works(const MoeArgs& a, int per, int* s_end, int lane, int wave) {
+  for (int s = wave; s < a.slots; s += kW) {
+    const int e = expert_of(a, s);
+    int cnt = 0, first = -1;
+    if (e >= 0)
+      for (int t0 = 0; t0 < a.T; t0 += 64) {
+        const int r = t0 + lane < a.T ? a.rank[(int64_t)e * a.T + t0 + lane] : -1;
+        const uint64_t b = __ballot(r >= 0);
+        if (b != 0 && first < 0) {
+          const int l = __ffsll((unsigned long long)b) - 1;
+          first = (t0 + l) * a.k + __builtin_amdgcn_readlane(r, l);
+        }
+        cnt += __popcll(b);
+      }
+    if (a.by_token && first != s) cnt = 0;               // an earlier token's slot has the expert
+    if (lane == 0) s_end[s] = (cnt + 15) / 16 * per;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    int base = 0;
+    for (int s0 = 0; s0 < a.slots; s0 += 64) {
+      int v = s0 + lane < a.slots ? s_end[s0 + lane] : 0;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+      }
+      if (s0 + lane < a.slots) s_end[s0 + lane] = base + v;
+      base += __shfl(v, 63);
+    }
+  }
+  __syncthreads();
+  return uniform(s_end[a.slots - 1]);
+}
+
+// The next item's DMA of a wave: items t = 0, 1 of chunk c of work p.
+struct Feed {
+  Pos p;
+  int c, c1, t, n;                           // next item, end of the work's chunks, ring slot
+  bool live;
+  Lines l[2];
+};
+
+template <int SLOTS>
+__device__ __forceinline__ void feed_next(Feed& f) {
+  f.n = f.n + 1 == SLOTS ? 0 : f.n + 1;
+}
+
+// The last loads of the wave that LDS reads of this stage have to see are there, and the wave's
+// reads of the stage before are done: then all waves meet.
+__device__ __forceinline__ void meet() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  lds_barrier();
+}
+
+template <int N>
+__device__ __forceinline__ void landed() {
+  wait_vm<N>();
+  asm volatile("" ::: "memory");
+}
+
+// ---- gate and up.
+template <int TERMS>
+__global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
+  int* s_end = reinterpret_cast<int*>(smem + kRingBytes + kUpStages * kStage);
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int total = count_works(a, a.tiles, s_end, lane, wave);
+  const int wg = xcd_order(blockIdx.x, gridDim.x);
+  const int w0 = (int)((int64_t)total * wg / gridDim.x), w1 = (int)((int64_t)total * (wg + 1) / gridDim.x);
+  if (w0 >= w1) return;
+  const Works works{s_end, a.tiles, 1};
+  const int nb = (a.H + 31) / 32, chunks = (a.H + kChunk - 1) / kChunk, h_chunks = (a.I + kChunk - 1) / kChunk;
+  const uint32_t ring = (uint32_t)wave * (kRingW * kSlot);
+  const uint32_t lds = (uint32_t)(uintptr_t)(lds_ptr_t)smem;
+  const ItemOffsets wo = item_offsets((uint32_t)a.ld_w13, (uint32_t)a.ld_s13, lane);
+
+  Feed f;
+  auto feed_work = [&](int w) {
+    f.live = w < w1;
+    f.c = 0;
+    f.t = 0;
+    if (!f.live) return;
+    seek(f.p, works, w);
+    const int e = expert_of(a, f.p.slot), i0 = 128 * f.p.tile + 16 * wave;
+    const int rows = min(16, a.I - i0);
+    const uint8_t* c = a.w13 + e * a.st_w13 + (int64_t)i0 * a.ld_w13;
+    const uint8_t* s = a.s13 + e * a.st_s13 + (int64_t)i0 * a.ld_s13;
+    f.l[0] = lines_of(c, a.ld_w13, s, a.ld_s13, rows, nb, true);
+    f.l[1] = lines_of(c + a.I * a.ld_w13, a.ld_w13, s + a.I * a.ld_s13, a.ld_s13, rows, nb, true);
+    if (rows <= 0) f.l[0].c_bytes = f.l[0].s_bytes = f.l[1].c_bytes = f.l[1].s_bytes = 0;
+  };
+  auto feed = [&]() {
+    Lines l = f.l[0];
+    if (f.t == 1) l = f.l[1];
+    if (!f.live) l.c_bytes = l.s_bytes = 0;
+    issue_item(l, wo, 0, f.c, lds + ring + f.n * kSlot);
+    feed_next<kRingW>(f);
+    f.t ^= 1;
+    if (f.t == 0 && ++f.c == chunks) feed_work(f.p.w + 1);
+  };
+  // X: this wave's two rows of the next stage
+  Pos xp{0, 0, 0, 0, 0};
+  int xc = -1, xn = 0, xrows = 0;
+  bool xlive = true;
+  auto stage = [&]() {
+    if (xc < 0 || ++xc == chunks) {
+      const int w = xc < 0 ? w0 : xp.w + 1, slot = xc < 0 ? -1 : xp.slot, m = xp.m;
+      xlive = w < w1;
+      xc = 0;
+      if (xlive) {
+        seek(xp, works, w);
+        if (xp.slot != slot || xp.m != m) xrows = rows_of(a, expert_of(a, xp.slot), xp.m, lane);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = 2 * wave + r, id = __builtin_amdgcn_readlane(xrows, row);
+      const int left = xlive && id > 0 ? min(2 * (a.H - kChunk * xc), 1024) : 0;
+      const uint64_t at = (uint64_t)(uintptr_t)a.x + (uint64_t)((id > 0 ? id - 1 : 0) / a.k) * (uint64_t)a.ld_x + 1024u * (uint64_t)xc;
+      dma16(lds + kRingBytes + xn * kStage + 1024 * row, 16u * (uint32_t)(lane ^ row), rsrc_of(at, (uint32_t)left));
+    }
+    xn ^= 1;
+  };
+
+  f.p = Pos{0, 0, 0, 0, 0};
+  f.n = 0;
+  feed_work(w0);
+  stage();
+  feed();
+  feed();
+  feed();
+  landed<0>();
+  meet();
+  Pos p{0, 0, 0, 0, 0};
+  int xbuf = 0, slot = 0;                                // stage and ring slot of the products
+  for (int w = w0; w < w1; ++w) {
+    seek(p, works, w);
+    const int rows = xrows;
+    v4f acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    for (int c = 0; c < chunks; ++c) {
+      XWide<1, 1> x;
+      x.read_staged(0, kRingBytes + xbuf * kStage, lane);
+      xbuf ^= 1;
+      stage();
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        // behind the item: two items, the stages of this chunk and the one before (t = 0), or
+        // two items and this chunk's stage
+        if (t == 0) landed<14>();
+        else landed<12>();
+        const uint32_t at = ring + slot * kSlot;
+        slot = slot + 1 == kRingW ? 0 : slot + 1;
+        v4i wf[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) wf[u] = item_codes(at, lane, u);
+        uint32_t ws = *reinterpret_cast<const uint32_t*>(smem + at + 4096 + 16 * i + 4 * g);
+        if (16 * c + 16 > nb) ws = keep_scales(ws, nb - 16 * c - 4 * g);
+        reads_done();
+        feed();
+        x.mma(wf, ws, &acc[t], 1);
+      }
+      landed<10>();
+      meet();
+    }
+    // lane (i, g): columns 4g .. 4g+3 of the wave's 16, token row i
+    const int id = __shfl(rows, i), col = 128 * p.tile + 16 * wave + 4 * g;
+    if (id > 0 && (col & ~7) < a.I) {
+      const float share = a.share[id - 1];
+      uint32_t o[TERMS][2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t b0[TERMS], b1[TERMS];
+        split_bf16<TERMS>(col + 2 * q < a.I ? gated(share, acc[0][2 * q], acc[1][2 * q]) : 0.0f, b0);
+        split_bf16<TERMS>(col + 2 * q + 1 < a.I ? gated(share, acc[0][2 * q + 1], acc[1][2 * q + 1]) : 0.0f, b1);
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) o[t][q] = b0[t] | (b1[t] << 16);
+      }
+      uint8_t* dst = a.h + ((int64_t)p.slot * a.mt_cap + p.m) * h_chunks * (TERMS * 16384) + h_offset<TERMS>(i, col & ~7) +
+                     2 * (col & 4);
+#pragma unroll
+      for (int t = 0; t < TERMS; ++t) *reinterpret_cast<uint2*>(dst + 4096 * t) = make_uint2(o[t][0], o[t][1]);
+    }
+  }
+  landed<0>();                                           // no load may land after the workgroup
+}
+
+// ---- down, h in two terms.  A stage is half a chunk of h (steps 0, 1 or 2, 3): 16 KiB, in the
+// order in which it lies in memory.
+__global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
+  constexpr int TERMS = 2;
+  int* s_end = reinterpret_cast<int*>(smem + kRingBytes + kDownStages * kStage);
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int total = count_works(a, a.tiles * a.parts, s_end, lane, wave);
+  const int wg = xcd_order(blockIdx.x, gridDim.x);
+  const int w0 = (int)((int64_t)total * wg / gridDim.x), w1 = (int)((int64_t)total * (wg + 1) / gridDim.x);
+  if (w0 >= w1) return;
+  const Works works{s_end, a.tiles, a.parts};
+  const int nb = (a.I + 31) / 32, chunks = (a.I + kChunk - 1) / kChunk;
+  const uint32_t ring = (uint32_t)wave * (kRingW * kSlot);
+  const uint32_t lds = (uint32_t)(uintptr_t)(lds_ptr_t)smem;
+  const ItemOffsets wo = item_offsets((uint32_t)a.ld_w2, (uint32_t)a.ld_s2, lane);
+
+  Feed f;
+  auto feed_work = [&](int w) {
+    f.live = w < w1;
+    f.c = f.t = 0;
+    f.c1 = 1;
+    if (!f.live) return;
+    seek(f.p, works, w);
+    f.c = chunks * f.p.part / a.parts;
+    f.c1 = chunks * (f.p.part + 1) / a.parts;
+    const int e = expert_of(a, f.p.slot);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int n0 = 256 * f.p.tile + 32 * wave + 16 * t, rows = min(16, a.H - n0);
+      f.l[t] = lines_of(a.w2 + e * a.st_w2 + (int64_t)n0 * a.ld_w2, a.ld_w2, a.s2 + e * a.st_s2 + (int64_t)n0 * a.ld_s2,
+                        a.ld_s2, rows, nb, true);
+      if (rows <= 0) f.l[t].c_bytes = f.l[t].s_bytes = 0;
+    }
+  };
+  auto feed = [&]() {
+    Lines l = f.l[0];
+    if (f.t == 1) l = f.l[1];
+    if (!f.live) l.c_bytes = l.s_bytes = 0;
+    issue_item(l, wo, 0, f.c, lds + ring + f.n * kSlot);
+    feed_next<kRingW>(f);
+    f.t ^= 1;
+    if (f.t == 0 && ++f.c == f.c1) feed_work(f.live ? f.p.w + 1 : w1);
+  };
+  Pos xp{0, 0, 0, 0, 0};
+  int xs = 0, xs1 = 0, xn = 0, xw = w0 - 1;              // next stage of the work, its end, buffer, work
+  uint64_t xat = 0;
+  auto stage = [&]() {
+    if (xs == xs1 && xw < w1) {
+      if (++xw < w1) {
+        seek(xp, works, xw);
+        xs = 2 * (chunks * xp.part / a.parts);
+        xs1 = 2 * (chunks * (xp.part + 1) / a.parts);
+        xat = (uint64_t)(uintptr_t)a.h + ((uint64_t)xp.slot * a.mt_cap + xp.m) * (uint64_t)chunks * (TERMS * 16384);
+      }
+    }
+    const v4i rs = rsrc_of(xat + (uint64_t)xs * kStage, xw < w1 ? (uint32_t)kStage : 0u);
+    const uint32_t to = lds + kRingBytes + xn * kStage;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) dma16(to + 2048 * wave + 1024 * r, (uint32_t)(2048 * wave + 1024 * r + 16 * lane), rs);
+    if (xw < w1) ++xs;
+    xn = xn + 1 == kDownStages ? 0 : xn + 1;
+  };
+
+  f.p = Pos{0, 0, 0, 0, 0};
+  f.n = 0;
+  feed_work(w0);
+  stage();
+  stage();
+  feed();
+  feed();
+  feed();
+  landed<0>();
+  meet();
+  Pos p{0, 0, 0, 0, 0};
+  int xbuf = 0, slot = 0, rows = 0, old_slot = -1, old_m = 0;
+  for (int w = w0; w < w1; ++w) {
+    seek(p, works, w);
+    if (p.slot != old_slot || p.m != old_m) rows = rows_of(a, expert_of(a, p.slot), p.m, lane);
+    old_slot = p.slot;
+    old_m = p.m;
+    v4f acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    const int c1 = chunks * (p.part + 1) / a.parts;
+    for (int c = chunks * p.part / a.parts; c < c1; ++c) {
+      v4i wf[2][4];
+      uint32_t ws[2];
+#pragma unroll
+      for (int hs = 0; hs < 2; ++hs) {
+        v4i x[2][TERMS][4];
+        const uint32_t from = kRingBytes + xbuf * kStage + 16 * lane;
+        xbuf = xbuf + 1 == kDownStages ? 0 : xbuf + 1;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int q = 0; q < TERMS; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[u][q][j] = lds16(from, ((u * TERMS + q) * 4 + j) * 1024);
+        if (kChunk * (c + 1) > a.I) {                    // h has nothing at k >= I
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (kChunk * c + 32 * (4 * g + 2 * hs + u) + 8 * j >= a.I) {
+#pragma unroll
+                for (int q = 0; q < TERMS; ++q) x[u][q][j] = v4i{0, 0, 0, 0};
+              }
+        }
+        stage();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (hs == 0) {
+            // behind the item: two items and four stages (t = 0), or two items and two stages
+            if (t == 0) landed<18>();
+            else landed<14>();
+            const uint32_t at = ring + slot * kSlot;
+            slot = slot + 1 == kRingW ? 0 : slot + 1;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) wf[t][u] = item_codes(at, lane, u);
+            ws[t] = *reinterpret_cast<const uint32_t*>(smem + at + 4096 + 16 * i + 4 * g);
+            if (16 * c + 16 > nb) ws[t] = keep_scales(ws[t], nb - 16 * c - 4 * g);
+            reads_done();
+            feed();
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float s = e8m0_to_f32((ws[t] >> (8 * (2 * hs + u))) & 255u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t d[4];
+              fp4::decode8_bf16((uint32_t)wf[t][2 * hs + u][j], s, d);
+              const v4i dv = {(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
+#pragma unroll
+              for (int q = TERMS - 1; q >= 0; --q) acc[t] = mma_bf16(dv, x[u][q][j], acc[t]);
+            }
+          }
+        }
+        // the next stage: behind it one stage and two items
+        landed<12>();
+        meet();
+      }
+    }
+    const int id = __shfl(rows, i);
+    if (id > 0) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int n = 256 * p.tile + 32 * wave + 16 * t + 4 * g;
+        float* to = a.part + ((int64_t)(id - 1) * a.parts + p.part) * a.H + n;
+        if (n + 4 <= a.H) {
+          __builtin_memcpy(to, &acc[t], 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < a.H) to[e] = acc[t][e];
+        }
+      }
+    }
+  }
+  landed<0>();
+}
+
+}  // namespace wide
+}  // namespace
+
+template <int TERMS>
+hipError_t launch_moe_up_wide(const MoeArgs& args, hipStream_t st) {
+  static bool set[64] = {false};
+  MoeArgs a = args;
+  a.tiles = (a.I + 127) / 128;
+  auto kern = wide::k_moe_up_wide<TERMS>;
+  constexpr int lds = wide::kRingBytes + wide::kUpStages * wide::kStage;
+  const hipError_t e = allow_lds(kern, lds + 4 * 1024, set);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)device_cu_count()), dim3(wide::kT), lds + 4 * a.slots, st, a);
+  return hipGetLastError();
+}
+
+template hipError_t launch_moe_up_wide<2>(const MoeArgs&, hipStream_t);
+template hipError_t launch_moe_up_wide<3>(const MoeArgs&, hipStream_t);
+
+hipError_t launch_moe_down_wide(const MoeArgs& args, hipStream_t st) {
+  static bool set[64] = {false};
+  MoeArgs a = args;
+  a.tiles = (a.H + 255) / 256;
+  auto kern = wide::k_moe_down_wide;
+  constexpr int lds = wide::kRingBytes + wide::kDownStages * wide::kStage;
+  const hipError_t e = allow_lds(kern, lds + 4 * 1024, set);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)device_cu_count()), dim3(wide::kT), lds + 4 * a.slots, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace mxq

@@ -290,6 +290,25 @@ def test_experts(out, renorm, T, H, I, E, k):
     run_experts(np.random.default_rng(30), T, H, I, E, k, renorm, out)
 
 
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("T,H,I,E,k", [(200, 72, 120, 512, 8), (40, 1032, 1100, 64, 8), (150, 520, 520, 64, 8)])
+def test_experts_many(out, T, H, I, E, k):
+    """Sizes whose weights occupy every CU for long: the persistent kernels, several tiles of
+    tokens, ragged columns, K of several chunks."""
+    say("moe_fp4 T%d H%d I%d E%d k%d %s" % (T, H, I, E, k, out))
+    run_experts(np.random.default_rng(35), T, H, I, E, k, True, out)
+
+
+def test_experts_many_with_unused_experts():
+    """Most experts unused, one overloaded, tokens without any."""
+    rng = np.random.default_rng(36)
+    lg = rng.standard_normal((130, 256)).astype(np.float32)
+    lg[:, 200] = 9.0
+    lg[5] = -np.inf
+    lg[::3, 100:190] = -np.inf
+    run_experts(rng, 130, 64, 300, 256, 4, False, BF16, lg)
+
+
 def test_experts_ties_and_masks():
     """Equal logits (ties to the lower index), -inf and the lowest float, rows with fewer than k
     experts or none, one expert for everybody."""
