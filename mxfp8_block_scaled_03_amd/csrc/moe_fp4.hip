@@ -352,7 +352,7 @@ hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
   hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (plan.up_wide && a.x_pieces && a.H % 8 == 0 && a.s13_words)
+  if (plan.up_wide && a.x_pieces && a.H % 8 == 0 && a.s13_pieces)
     e = launch_moe_up_wide<TERMS>(a, st);
   else if ((int64_t)a.slots * ((a.I + 63) / 64) >= 2 * cus)
     e = launch_up<8, TERMS>(a, st);
@@ -360,8 +360,8 @@ hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
     e = (int64_t)a.slots * ((a.I + 31) / 32) >= 2 * cus ? launch_up<4, TERMS>(a, st) : launch_up<2, TERMS>(a, st);
   if (e != hipSuccess) return e;
   MoeArgs d = a;
-  d.parts = plan.down_wide && a.s2_words ? plan.parts : 1;
-  if (plan.down_wide && a.s2_words)
+  d.parts = plan.down_wide && a.s2_pieces ? plan.parts : 1;
+  if (plan.down_wide && a.s2_pieces)
     e = launch_moe_down_wide(d, st);
   else if ((int64_t)a.slots * ((a.H + 127) / 128) >= 2 * cus)
     e = launch_down<8, TERMS>(d, st);
@@ -436,6 +436,8 @@ hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   a.x_pieces = (uintptr_t)p.x % 16 == 0 && a.ld_x % 16 == 0;
   a.s13_words = (uintptr_t)p.s13 % 4 == 0 && p.ld_s13 % 4 == 0 && p.st_s13 % 4 == 0;
   a.s2_words = (uintptr_t)p.s2 % 4 == 0 && p.ld_s2 % 4 == 0 && p.st_s2 % 4 == 0;
+  a.s13_pieces = (uintptr_t)p.s13 % 16 == 0 && p.ld_s13 % 16 == 0 && p.st_s13 % 16 == 0;
+  a.s2_pieces = (uintptr_t)p.s2 % 16 == 0 && p.ld_s2 % 16 == 0 && p.st_s2 % 16 == 0;
   a.y = p.y;
   a.ld_y = p.ld_y;
   a.y_bf16 = p.y_bf16;

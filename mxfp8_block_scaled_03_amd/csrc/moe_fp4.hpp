@@ -16,6 +16,7 @@ struct MoeArgs {
   int64_t ld_x;                        // bytes
   bool x_pieces;                       // X rows are whole 16-byte pieces
   bool s13_words, s2_words;            // scale rows are whole 4-byte words
+  bool s13_pieces, s2_pieces;          // and 16-byte aligned
   const float* logits;
   int64_t ld_logits;
   const uint8_t *w13, *s13, *w2, *s2;
@@ -64,7 +65,7 @@ __device__ __forceinline__ float gated(float share, float gate, float up) { retu
 }  // namespace
 
 // The kernels of many workgroups' worth of weights (moe_fp4_wide.hip): rows of X in whole 16-byte
-// pieces and H a multiple of 8, scale rows in whole words.  up fills h, down fills part.
+// pieces and H a multiple of 8, scale rows 16-byte aligned.  up fills h, down fills part.
 template <int TERMS>
 hipError_t launch_moe_up_wide(const MoeArgs& a, hipStream_t st);
 hipError_t launch_moe_down_wide(const MoeArgs& a, hipStream_t st);

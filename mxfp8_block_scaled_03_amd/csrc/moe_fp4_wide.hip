@@ -9,9 +9,13 @@
 // items ahead of the products through the whole run.  X is shared: the workgroup stages it by
 // DMA, a stage or two ahead, and meets at one barrier per stage.
 //
-// Every stage issues the same number of loads (those past the run's end, and rows of X that no
-// token has, go through an empty descriptor), so the waits are constants; an item's wait counts
-// the loads issued after it.  Against the finer workgroups of moe_fp4.hip, whose fixed costs
+// Scale bytes come for several chunks at a time (GROUP: 4 or 2; 64 or 32 bytes of a row), since 16
+// bytes of a row per chunk would fetch each of its memory lines anew every time: 120 us with a
+// fetch per chunk.  They are read into registers when the group begins.
+//
+// Every stage issues at least the same number of loads (those past the run's end, and rows of X
+// that no token has, go through an empty descriptor), so the waits are constants: an item's
+// wait counts the loads that are sure to be issued after it.  Against the finer workgroups of moe_fp4.hip, whose fixed costs
 // (looking up tokens, filling the ring, adding the waves' sums) come at the same time on every
 // CU: gate and up of 64 tokens over 64 experts of 4096 x 2048 (570 MB) 135 us before.
 #include "moe_fp4.hpp"
@@ -23,9 +27,13 @@ namespace wide {
 constexpr int kW = 8;                        // waves
 constexpr int kT = 64 * kW;
 constexpr int kRingW = 3;
-constexpr int kRingBytes = kW * kRingW * kSlot;
+constexpr int kCodes = 4096;                 // bytes of an item's codes
+constexpr int kRingBytes = kW * kRingW * kCodes;
 constexpr int kStage = 16384;                // bytes of X per stage
-constexpr int kUpStages = 2, kDownStages = 3;
+constexpr int kDownStages = 3;
+// LDS of the two kernels: ring, X stages, scales, works
+constexpr int kUpX = kRingBytes, kUpScales = kUpX + 2 * kStage, kUpLds = kUpScales + kW * 2048;
+constexpr int kDownX = kRingBytes, kDownScales = kDownX + kDownStages * kStage, kDownLds = kDownScales + kW * 1024;
 
 // The run of works of this workgroup, and where a work lies: s_end[s] is the number of works of
 // slots 0 .. s.  A slot's works: its 16-token tiles, of each its K ranges, of each its columns.
@@ -104,17 +112,55 @@ __device__ __forceinline__ int count_works(const MoeArgs& a, int per, int* s_end
   return uniform(s_end[a.slots - 1]);
 }
 
-// The next item's DMA of a wave: items t = 0, 1 of chunk c of work p.
+// The next item of a wave: row tile t = 0, 1 of chunk c of work p, into slot n.
 struct Feed {
   Pos p;
-  int c, c1, t, n;                           // next item, end of the work's chunks, ring slot
+  int c, c1, t, n;
   bool live;
-  Lines l[2];
+  uint64_t at[2];                            // the tiles' codes
+  uint32_t bytes[2];
 };
 
-template <int SLOTS>
-__device__ __forceinline__ void feed_next(Feed& f) {
-  f.n = f.n + 1 == SLOTS ? 0 : f.n + 1;
+__device__ __forceinline__ void issue_codes(const Feed& f, const ItemOffsets& o, uint32_t ring) {
+  const uint32_t off = 256u * (uint32_t)f.c, bytes = f.t == 0 ? f.bytes[0] : f.bytes[1];
+  const v4i r = rsrc_of((f.t == 0 ? f.at[0] : f.at[1]) + off, f.live && off < bytes ? bytes - off : 0u);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) dma16(ring + f.n * kCodes + 1024 * d, o.c[d], r);
+}
+
+// Bytes from a tile's first row to its last block; 0 without rows.
+__device__ __forceinline__ uint32_t code_bytes(int rows, int64_t ld, int nb) {
+  return rows > 0 ? (uint32_t)((rows - 1) * ld + 16 * nb) : 0u;
+}
+
+// Scales of a group of chunks for both tiles of a wave: GROUP 4: two loads of 16 rows x 64 bytes;
+// GROUP 2: one of 32 rows x 32 bytes (the second tile `step` bytes behind the first).  Row r of
+// tile t lies at (16 t + r) * 16 * GROUP.
+template <int GROUP>
+__device__ __forceinline__ void issue_scales(const uint8_t* base, int64_t ld, int64_t step, int rows0, int rows1, int nb, int c,
+                                             uint32_t lds, int lane) {
+  constexpr int PIECES = GROUP;              // 16-byte pieces of a row
+  const uint32_t nb4 = (uint32_t)(nb + 3) & ~3u, off = 16u * (uint32_t)c;
+#pragma unroll
+  for (int t = 0; t < (GROUP == 4 ? 2 : 1); ++t) {
+    const int r = lane / PIECES;             // 0 .. 15, or 0 .. 31 over both tiles
+    const uint32_t voff = (uint32_t)((r & 15) * ld) + (r >= 16 ? (uint32_t)step : 0u) + 16u * (uint32_t)(lane % PIECES);
+    const int rows = GROUP == 4 ? (t == 0 ? rows0 : rows1) : (rows1 > 0 ? rows1 : rows0);
+    uint32_t bytes = rows > 0 ? (uint32_t)((rows - 1) * ld) + nb4 + (GROUP == 2 && rows1 > 0 ? (uint32_t)step : 0u) : 0u;
+    bytes = off < bytes ? bytes - off : 0u;
+    dma16(lds + 1024 * t, voff, rsrc_of((uint64_t)(uintptr_t)base + (uint64_t)(t * step) + off, bytes));
+  }
+}
+
+// The scale dwords of row i, blocks 4g .. 4g+3 of the group's chunks.
+template <int GROUP>
+__device__ __forceinline__ void read_scales(uint32_t s[2][GROUP], uint32_t at, int lane) {
+  const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int c = 0; c < GROUP; ++c)
+      s[t][c] = *reinterpret_cast<const uint32_t*>(smem + at + (16 * t + i) * (16 * GROUP) + 16 * c + 4 * g);
 }
 
 // The last loads of the wave that LDS reads of this stage have to see are there, and the wave's
@@ -133,7 +179,8 @@ __device__ __forceinline__ void landed() {
 // ---- gate and up.
 template <int TERMS>
 __global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
-  int* s_end = reinterpret_cast<int*>(smem + kRingBytes + kUpStages * kStage);
+  constexpr int GROUP = 4;
+  int* s_end = reinterpret_cast<int*>(smem + kUpLds);
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = uniform(threadIdx.x >> 6);
   const int total = count_works(a, a.tiles, s_end, lane, wave);
@@ -142,7 +189,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
   if (w0 >= w1) return;
   const Works works{s_end, a.tiles, 1};
   const int nb = (a.H + 31) / 32, chunks = (a.H + kChunk - 1) / kChunk, h_chunks = (a.I + kChunk - 1) / kChunk;
-  const uint32_t ring = (uint32_t)wave * (kRingW * kSlot);
+  const uint32_t ring = (uint32_t)wave * (kRingW * kCodes), my_scales = kUpScales + (uint32_t)wave * 2048;
   const uint32_t lds = (uint32_t)(uintptr_t)(lds_ptr_t)smem;
   const ItemOffsets wo = item_offsets((uint32_t)a.ld_w13, (uint32_t)a.ld_s13, lane);
 
@@ -154,21 +201,29 @@ __global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
     if (!f.live) return;
     seek(f.p, works, w);
     const int e = expert_of(a, f.p.slot), i0 = 128 * f.p.tile + 16 * wave;
-    const int rows = min(16, a.I - i0);
-    const uint8_t* c = a.w13 + e * a.st_w13 + (int64_t)i0 * a.ld_w13;
-    const uint8_t* s = a.s13 + e * a.st_s13 + (int64_t)i0 * a.ld_s13;
-    f.l[0] = lines_of(c, a.ld_w13, s, a.ld_s13, rows, nb, true);
-    f.l[1] = lines_of(c + a.I * a.ld_w13, a.ld_w13, s + a.I * a.ld_s13, a.ld_s13, rows, nb, true);
-    if (rows <= 0) f.l[0].c_bytes = f.l[0].s_bytes = f.l[1].c_bytes = f.l[1].s_bytes = 0;
+    f.at[0] = (uint64_t)(uintptr_t)(a.w13 + e * a.st_w13 + (int64_t)i0 * a.ld_w13);
+    f.at[1] = f.at[0] + (uint64_t)(a.I * a.ld_w13);
+    f.bytes[0] = f.bytes[1] = code_bytes(min(16, a.I - i0), a.ld_w13, nb);
   };
   auto feed = [&]() {
-    Lines l = f.l[0];
-    if (f.t == 1) l = f.l[1];
-    if (!f.live) l.c_bytes = l.s_bytes = 0;
-    issue_item(l, wo, 0, f.c, lds + ring + f.n * kSlot);
-    feed_next<kRingW>(f);
+    issue_codes(f, wo, lds + ring);
+    f.n = f.n + 1 == kRingW ? 0 : f.n + 1;
     f.t ^= 1;
     if (f.t == 0 && ++f.c == chunks) feed_work(f.p.w + 1);
+  };
+  // scales of the next group
+  Pos sp{0, 0, 0, 0, 0};
+  int sc = 0, sw = w0 - 1;
+  auto scales = [&]() {
+    if (sw < w0 || sc >= chunks) {
+      sc = 0;
+      if (++sw >= w1) return;
+      seek(sp, works, sw);
+    }
+    const int e = expert_of(a, sp.slot), i0 = 128 * sp.tile + 16 * wave, rows = min(16, a.I - i0);
+    issue_scales<GROUP>(a.s13 + e * a.st_s13 + (int64_t)i0 * a.ld_s13, a.ld_s13, a.I * a.ld_s13, rows, rows, nb, sc,
+                        lds + my_scales, lane);
+    sc += GROUP;
   };
   // X: this wave's two rows of the next stage
   Pos xp{0, 0, 0, 0, 0};
@@ -189,7 +244,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
       const int row = 2 * wave + r, id = __builtin_amdgcn_readlane(xrows, row);
       const int left = xlive && id > 0 ? min(2 * (a.H - kChunk * xc), 1024) : 0;
       const uint64_t at = (uint64_t)(uintptr_t)a.x + (uint64_t)((id > 0 ? id - 1 : 0) / a.k) * (uint64_t)a.ld_x + 1024u * (uint64_t)xc;
-      dma16(lds + kRingBytes + xn * kStage + 1024 * row, 16u * (uint32_t)(lane ^ row), rsrc_of(at, (uint32_t)left));
+      dma16(lds + kUpX + xn * kStage + 1024 * row, 16u * (uint32_t)(lane ^ row), rsrc_of(at, (uint32_t)left));
     }
     xn ^= 1;
   };
@@ -197,6 +252,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
   f.p = Pos{0, 0, 0, 0, 0};
   f.n = 0;
   feed_work(w0);
+  scales();
   stage();
   feed();
   feed();
@@ -205,33 +261,42 @@ __global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
   meet();
   Pos p{0, 0, 0, 0, 0};
   int xbuf = 0, slot = 0;                                // stage and ring slot of the products
+  uint32_t sg[2][GROUP];
   for (int w = w0; w < w1; ++w) {
     seek(p, works, w);
     const int rows = xrows;
     v4f acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
     for (int c = 0; c < chunks; ++c) {
       XWide<1, 1> x;
-      x.read_staged(0, kRingBytes + xbuf * kStage, lane);
+      x.read_staged(0, kUpX + xbuf * kStage, lane);
       xbuf ^= 1;
+      if (c % GROUP == 0) {
+        read_scales<GROUP>(sg, my_scales, lane);
+        reads_done();
+        scales();
+      }
       stage();
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        // behind the item: two items, the stages of this chunk and the one before (t = 0), or
+        // behind the item: two items and the stages of this chunk and the one before (t = 0), or
         // two items and this chunk's stage
-        if (t == 0) landed<14>();
-        else landed<12>();
-        const uint32_t at = ring + slot * kSlot;
+        if (t == 0) landed<12>();
+        else landed<10>();
+        const uint32_t at = ring + slot * kCodes;
         slot = slot + 1 == kRingW ? 0 : slot + 1;
         v4i wf[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) wf[u] = item_codes(at, lane, u);
-        uint32_t ws = *reinterpret_cast<const uint32_t*>(smem + at + 4096 + 16 * i + 4 * g);
+        uint32_t ws = sg[t][0];
+        sg[t][0] = sg[t][1];
+        sg[t][1] = sg[t][2];
+        sg[t][2] = sg[t][3];
         if (16 * c + 16 > nb) ws = keep_scales(ws, nb - 16 * c - 4 * g);
         reads_done();
         feed();
         x.mma(wf, ws, &acc[t], 1);
       }
-      landed<10>();
+      landed<8>();                                       // this chunk's stage, behind it two items
       meet();
     }
     // lane (i, g): columns 4g .. 4g+3 of the wave's 16, token row i
@@ -259,8 +324,8 @@ __global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
 // ---- down, h in two terms.  A stage is half a chunk of h (steps 0, 1 or 2, 3): 16 KiB, in the
 // order in which it lies in memory.
 __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
-  constexpr int TERMS = 2;
-  int* s_end = reinterpret_cast<int*>(smem + kRingBytes + kDownStages * kStage);
+  constexpr int TERMS = 2, GROUP = 2;
+  int* s_end = reinterpret_cast<int*>(smem + kDownLds);
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = uniform(threadIdx.x >> 6);
   const int total = count_works(a, a.tiles * a.parts, s_end, lane, wave);
@@ -269,7 +334,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
   if (w0 >= w1) return;
   const Works works{s_end, a.tiles, a.parts};
   const int nb = (a.I + 31) / 32, chunks = (a.I + kChunk - 1) / kChunk;
-  const uint32_t ring = (uint32_t)wave * (kRingW * kSlot);
+  const uint32_t ring = (uint32_t)wave * (kRingW * kCodes), my_scales = kDownScales + (uint32_t)wave * 1024;
   const uint32_t lds = (uint32_t)(uintptr_t)(lds_ptr_t)smem;
   const ItemOffsets wo = item_offsets((uint32_t)a.ld_w2, (uint32_t)a.ld_s2, lane);
 
@@ -282,23 +347,31 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
     seek(f.p, works, w);
     f.c = chunks * f.p.part / a.parts;
     f.c1 = chunks * (f.p.part + 1) / a.parts;
-    const int e = expert_of(a, f.p.slot);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int n0 = 256 * f.p.tile + 32 * wave + 16 * t, rows = min(16, a.H - n0);
-      f.l[t] = lines_of(a.w2 + e * a.st_w2 + (int64_t)n0 * a.ld_w2, a.ld_w2, a.s2 + e * a.st_s2 + (int64_t)n0 * a.ld_s2,
-                        a.ld_s2, rows, nb, true);
-      if (rows <= 0) f.l[t].c_bytes = f.l[t].s_bytes = 0;
-    }
+    const int n0 = 256 * f.p.tile + 32 * wave;
+    f.at[0] = (uint64_t)(uintptr_t)(a.w2 + expert_of(a, f.p.slot) * a.st_w2 + (int64_t)n0 * a.ld_w2);
+    f.at[1] = f.at[0] + (uint64_t)(16 * a.ld_w2);
+    f.bytes[0] = code_bytes(min(16, a.H - n0), a.ld_w2, nb);
+    f.bytes[1] = code_bytes(min(16, a.H - n0 - 16), a.ld_w2, nb);
   };
   auto feed = [&]() {
-    Lines l = f.l[0];
-    if (f.t == 1) l = f.l[1];
-    if (!f.live) l.c_bytes = l.s_bytes = 0;
-    issue_item(l, wo, 0, f.c, lds + ring + f.n * kSlot);
-    feed_next<kRingW>(f);
+    issue_codes(f, wo, lds + ring);
+    f.n = f.n + 1 == kRingW ? 0 : f.n + 1;
     f.t ^= 1;
     if (f.t == 0 && ++f.c == f.c1) feed_work(f.live ? f.p.w + 1 : w1);
+  };
+  Pos sp{0, 0, 0, 0, 0};
+  int sc = 0, sc1 = 0, sw = w0 - 1;
+  auto scales = [&]() {
+    if (sc >= sc1) {
+      if (++sw >= w1) return;
+      seek(sp, works, sw);
+      sc = chunks * sp.part / a.parts;
+      sc1 = chunks * (sp.part + 1) / a.parts;
+    }
+    const int n0 = 256 * sp.tile + 32 * wave;
+    issue_scales<GROUP>(a.s2 + expert_of(a, sp.slot) * a.st_s2 + (int64_t)n0 * a.ld_s2, a.ld_s2, 16 * a.ld_s2,
+                        min(16, a.H - n0), min(16, a.H - n0 - 16), nb, sc, lds + my_scales, lane);
+    sc += GROUP;
   };
   Pos xp{0, 0, 0, 0, 0};
   int xs = 0, xs1 = 0, xn = 0, xw = w0 - 1;              // next stage of the work, its end, buffer, work
@@ -313,7 +386,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
       }
     }
     const v4i rs = rsrc_of(xat + (uint64_t)xs * kStage, xw < w1 ? (uint32_t)kStage : 0u);
-    const uint32_t to = lds + kRingBytes + xn * kStage;
+    const uint32_t to = lds + kDownX + xn * kStage;
 #pragma unroll
     for (int r = 0; r < 2; ++r) dma16(to + 2048 * wave + 1024 * r, (uint32_t)(2048 * wave + 1024 * r + 16 * lane), rs);
     if (xw < w1) ++xs;
@@ -323,6 +396,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
   f.p = Pos{0, 0, 0, 0, 0};
   f.n = 0;
   feed_work(w0);
+  scales();
   stage();
   stage();
   feed();
@@ -332,20 +406,22 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
   meet();
   Pos p{0, 0, 0, 0, 0};
   int xbuf = 0, slot = 0, rows = 0, old_slot = -1, old_m = 0;
+  uint32_t sg[2][GROUP];
   for (int w = w0; w < w1; ++w) {
     seek(p, works, w);
     if (p.slot != old_slot || p.m != old_m) rows = rows_of(a, expert_of(a, p.slot), p.m, lane);
     old_slot = p.slot;
     old_m = p.m;
     v4f acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-    const int c1 = chunks * (p.part + 1) / a.parts;
-    for (int c = chunks * p.part / a.parts; c < c1; ++c) {
+    const int c0 = chunks * p.part / a.parts, c1 = chunks * (p.part + 1) / a.parts;
+    for (int c = c0; c < c1; ++c) {
       v4i wf[2][4];
       uint32_t ws[2];
+      const bool begins = (c - c0) % GROUP == 0;
 #pragma unroll
       for (int hs = 0; hs < 2; ++hs) {
         v4i x[2][TERMS][4];
-        const uint32_t from = kRingBytes + xbuf * kStage + 16 * lane;
+        const uint32_t from = kDownX + xbuf * kStage + 16 * lane;
         xbuf = xbuf + 1 == kDownStages ? 0 : xbuf + 1;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -363,18 +439,24 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
                 for (int q = 0; q < TERMS; ++q) x[u][q][j] = v4i{0, 0, 0, 0};
               }
         }
+        if (hs == 0 && begins) {
+          read_scales<GROUP>(sg, my_scales, lane);
+          reads_done();
+          scales();
+        }
         stage();
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (hs == 0) {
             // behind the item: two items and four stages (t = 0), or two items and two stages
-            if (t == 0) landed<18>();
-            else landed<14>();
-            const uint32_t at = ring + slot * kSlot;
+            if (t == 0) landed<16>();
+            else landed<12>();
+            const uint32_t at = ring + slot * kCodes;
             slot = slot + 1 == kRingW ? 0 : slot + 1;
 #pragma unroll
             for (int u = 0; u < 4; ++u) wf[t][u] = item_codes(at, lane, u);
-            ws[t] = *reinterpret_cast<const uint32_t*>(smem + at + 4096 + 16 * i + 4 * g);
+            ws[t] = sg[t][0];
+            sg[t][0] = sg[t][1];
             if (16 * c + 16 > nb) ws[t] = keep_scales(ws[t], nb - 16 * c - 4 * g);
             reads_done();
             feed();
@@ -393,7 +475,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
           }
         }
         // the next stage: behind it one stage and two items
-        landed<12>();
+        landed<10>();
         meet();
       }
     }
@@ -425,7 +507,7 @@ hipError_t launch_moe_up_wide(const MoeArgs& args, hipStream_t st) {
   MoeArgs a = args;
   a.tiles = (a.I + 127) / 128;
   auto kern = wide::k_moe_up_wide<TERMS>;
-  constexpr int lds = wide::kRingBytes + wide::kUpStages * wide::kStage;
+  constexpr int lds = wide::kUpLds;
   const hipError_t e = allow_lds(kern, lds + 4 * 1024, set);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)device_cu_count()), dim3(wide::kT), lds + 4 * a.slots, st, a);
@@ -440,7 +522,7 @@ hipError_t launch_moe_down_wide(const MoeArgs& args, hipStream_t st) {
   MoeArgs a = args;
   a.tiles = (a.H + 255) / 256;
   auto kern = wide::k_moe_down_wide;
-  constexpr int lds = wide::kRingBytes + wide::kDownStages * wide::kStage;
+  constexpr int lds = wide::kDownLds;
   const hipError_t e = allow_lds(kern, lds + 4 * 1024, set);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)device_cu_count()), dim3(wide::kT), lds + 4 * a.slots, st, a);
