@@ -69,12 +69,15 @@ __device__ __forceinline__ uint32_t keep_scales(uint32_t s, int n) {
   return (s & m) | (0x7F7F7F7Fu & ~m);
 }
 
-// Consecutive rows of codes and scales (uniform).
+// Consecutive rows of codes and scales (uniform).  Row tiles from `first` on lie `far_c` and
+// `far_s` bytes further (the up rows behind the gate rows of an expert).
 struct Lines {
   uint64_t c, s;
   uint32_t c_bytes, s_bytes;
   uint32_t ld_c, ld_s;
   bool s_words;                              // scale rows are whole 4-byte words
+  int first;
+  uint64_t far_c, far_s;
 };
 
 __device__ __forceinline__ Lines lines_of(const uint8_t* c, int64_t ld_c, const uint8_t* s, int64_t ld_s, int rows,
@@ -87,6 +90,8 @@ __device__ __forceinline__ Lines lines_of(const uint8_t* c, int64_t ld_c, const 
   l.c_bytes = (uint32_t)((int64_t)(rows - 1) * ld_c + 16 * nb);
   l.s_bytes = (uint32_t)((int64_t)(rows - 1) * ld_s + ((nb + 3) & ~3));
   l.s_words = s_words;
+  l.first = 1 << 30;
+  l.far_c = l.far_s = 0;
   return l;
 }
 
@@ -109,11 +114,13 @@ __device__ __forceinline__ ItemOffsets item_offsets(uint32_t ld_c, uint32_t ld_s
 // Rows 16 t .. 16 t + 15, chunk c, into the slot at `lds`: five loads, or four where scales are
 // not read by words.  What lies past the last row's end reads as zero.
 __device__ __forceinline__ void issue_item(const Lines& l, const ItemOffsets& o, int t, int c, uint32_t lds) {
-  const uint32_t oc = 16u * t * l.ld_c + 256u * c, os = 16u * t * l.ld_s + 16u * c;
-  const v4i rc = rsrc_of(l.c + oc, oc < l.c_bytes ? l.c_bytes - oc : 0u);
+  const bool far = t >= l.first;
+  const uint32_t n = (uint32_t)(far ? t - l.first : t);
+  const uint32_t oc = 16u * n * l.ld_c + 256u * c, os = 16u * n * l.ld_s + 16u * c;
+  const v4i rc = rsrc_of(l.c + (far ? l.far_c : 0) + oc, oc < l.c_bytes ? l.c_bytes - oc : 0u);
 #pragma unroll
   for (int d = 0; d < 4; ++d) dma16(lds + 1024 * d, o.c[d], rc);
-  if (l.s_words) dma4(lds + 4096, o.s, rsrc_of(l.s + os, os < l.s_bytes ? l.s_bytes - os : 0u));
+  if (l.s_words) dma4(lds + 4096, o.s, rsrc_of(l.s + (far ? l.far_s : 0) + os, os < l.s_bytes ? l.s_bytes - os : 0u));
 }
 
 // Step u's fragment of the item in the slot at byte `slot` of LDS.
@@ -130,10 +137,12 @@ __device__ __forceinline__ uint32_t item_scales(const Lines& l, uint32_t slot, i
   if (l.s_words) {
     s = *reinterpret_cast<const uint32_t*>(smem + slot + 4096 + 16 * i + 4 * g);
   } else {
-    const uint64_t at = (uint64_t)(16 * t + i) * l.ld_s + 16 * c + 4 * g;
+    const bool far = t >= l.first;
+    const uint64_t at = (uint64_t)(16 * (far ? t - l.first : t) + i) * l.ld_s + 16 * c + 4 * g;
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(l.s + (far ? l.far_s : 0));
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (u < left && at + u < l.s_bytes) s |= (uint32_t)reinterpret_cast<const uint8_t*>(l.s)[at + u] << (8 * u);
+      if (u < left && at + u < l.s_bytes) s |= (uint32_t)p[at + u] << (8 * u);
   }
   return 16 * c + 16 > nb ? keep_scales(s, left) : s;
 }
@@ -173,10 +182,52 @@ __device__ __forceinline__ v4i drop_low(v4i v, int n) {
 
 // ---- X fragments of a chunk.
 
-// bf16 rows, TERMS = 1; or the sum of TERMS bf16 values (the expert layer's hidden values).
-template <int MT, int TERMS>
+// What the fragments hold of an element: bf16 (rows of X); the sum of two bf16 (planes 0, 1); or
+// fp32 (plane p: elements 4p .. 4p+3), which is cut into three bf16 that add up to it exactly:
+// its 24 significant bits, eight at a time.
+enum : int { kOne = 1, kTwo = 2, kF32 = 3 };
+
+// Planes of 16 bytes per 8 elements.
+constexpr int planes_of(int kind) { return kind == kOne ? 1 : 2; }
+
+// The three terms of eight fp32 values, each as eight bf16.
+__device__ __forceinline__ void cut_f32(const v4i p[2], v4i term[3]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t t[3][2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float v = __uint_as_float((uint32_t)p[q >> 1][2 * (q & 1) + e]);
+#pragma unroll
+      for (int n = 0; n < 3; ++n) {
+        t[n][e] = __float_as_uint(v) & 0xFFFF0000u;
+        v -= __uint_as_float(t[n][e]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 3; ++n) term[n][q] = (int)__builtin_amdgcn_perm(t[n][1], t[n][0], 0x07060302u);
+  }
+}
+
+template <int MT, int KIND>
 struct XWide {
-  v4i f[4][4][MT][TERMS];                    // step, MFMA, row tile, term
+  v4i f[4][4][MT][planes_of(KIND)];          // step, MFMA, row tile, plane
+
+  // The terms of a fragment, the smallest last.
+  static constexpr int kTerms = KIND;
+  __device__ __forceinline__ void terms(int u, int j, int m, v4i t[KIND]) const {
+    if (KIND == kF32) {
+      // cut anew for every use: kept, the terms of a chunk would take 192 registers
+      v4i p[2] = {f[u][j][m][0], f[u][j][m][planes_of(KIND) - 1]}, c[3];
+      asm volatile("" : "+v"(p[0]), "+v"(p[1]));
+      cut_f32(p, c);
+#pragma unroll
+      for (int n = 0; n < KIND; ++n) t[n] = c[n];
+    } else {
+#pragma unroll
+      for (int n = 0; n < KIND; ++n) t[n] = f[u][j][m][n < planes_of(KIND) ? n : 0];
+    }
+  }
 
   __device__ __forceinline__ void mma(const v4i w[4], uint32_t ws, v4f* acc, int stride) const {
 #pragma unroll
@@ -188,9 +239,12 @@ struct XWide {
         fp4::decode8_bf16((uint32_t)w[u][j], s, d);
         const v4i dv = {(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m) {
+          v4i t[KIND];
+          terms(u, j, m, t);
 #pragma unroll
-          for (int p = TERMS - 1; p >= 0; --p) acc[m * stride] = mma_bf16(dv, f[u][j][m][p], acc[m * stride]);
+          for (int p = KIND - 1; p >= 0; --p) acc[m * stride] = mma_bf16(dv, t[p], acc[m * stride]);
+        }
       }
     }
   }
@@ -272,12 +326,13 @@ __device__ __forceinline__ Run run_of(int K, int wave) {
   return Run{items * wave / kWaves, items * (wave + 1) / kWaves};
 }
 
-// Starts the DMA of up to a ring's worth of items from `it` on, those before `end`.
+// Starts the DMA of up to a ring's worth of items from `it` on, those before `end`.  A loop: what a
+// workgroup runs but once is paid for in instruction fetches.
 template <int NTW, typename Issue>
 __device__ __forceinline__ void fill_ring(int it, int end, uint32_t lds0, Issue issue) {
-#pragma unroll
-  for (int n = 0; n < kRing; ++n)
-    if (it + n < end) issue((it + n) % NTW, (it + n) / NTW, lds0 + n * kSlot);
+#pragma unroll 1
+  for (int n = 0; n < min(kRing, end - it); ++n)
+    issue((int)((uint32_t)(it + n) % NTW), (int)((uint32_t)(it + n) / NTW), lds0 + n * kSlot);
 }
 
 // issue(t, c, lds) starts an item's DMA; load_x(x, c) brings a chunk's X fragments;
@@ -321,7 +376,7 @@ __device__ __forceinline__ void stream(Run run, int wave, int lane, bool s_words
       for (int u = 0; u < 4; ++u) w[u] = item_codes(slot, lane, u);
       const uint32_t ws = scales_of(t, c, slot);
       reads_done();
-      if (it + kRing < end) issue((it + kRing) % NTW, (it + kRing) / NTW, lds0 + n * kSlot);
+      if (it + kRing < end) issue((int)((uint32_t)(it + kRing) % NTW), (int)((uint32_t)(it + kRing) / NTW), lds0 + n * kSlot);
       n = (n + 1) % kRing;
       x.mma(w, ws, &acc[0][t], NTW);
     }

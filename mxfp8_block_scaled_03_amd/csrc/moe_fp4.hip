@@ -61,7 +61,9 @@ __global__ __launch_bounds__(kThreads) void k_moe_route(const MoeArgs a) {
     nan |= l != l;
   }
   top = __any(nan) ? __builtin_nanf("") : wave_max(top);
-  float sum = 0.0f;
+  // the first 64 experts stay in registers until the sum is known, further ones are looked at again
+  float sum = 0.0f, p0 = 0.0f;
+  int r0 = -1;
   for (int j0 = 0; j0 < a.E; j0 += 64) {
     const int j = j0 + lane;
     const float l = j < a.E ? row[j] : -__builtin_inff();
@@ -70,18 +72,27 @@ __global__ __launch_bounds__(kThreads) void k_moe_route(const MoeArgs a) {
     const bool in = j < a.E && r < a.k;
     const float p = expf(l - top);
     if (a.renorm ? in : j < a.E) sum += p;
-    if (j < a.E) a.rank[(int64_t)j * a.T + t] = (int16_t)(in && kj != kMasked ? r : -1);
-    if (in) {
-      a.chosen[t * a.k + r] = kj != kMasked ? j : -1;
-      a.share[t * a.k + r] = p;                          // divided below, by the same lane
+    const int mine = in && kj != kMasked ? r : -1;
+    if (j < a.E) a.rank[(int64_t)j * a.T + t] = (int16_t)mine;
+    if (in) a.chosen[t * a.k + r] = mine >= 0 ? j : -1;
+    if (j0 == 0) {
+      p0 = p;
+      r0 = mine;
     }
   }
   sum = wave_sum(sum);
-  for (int j0 = 0; j0 < a.E; j0 += 64) {
+  if (r0 >= 0) a.share[t * a.k + r0] = p0 / sum;
+  for (int j0 = 64; j0 < a.E; j0 += 64) {
     const int j = j0 + lane;
     const int r = j < a.E ? a.rank[(int64_t)j * a.T + t] : -1;
-    if (r >= 0) a.share[t * a.k + r] /= sum;
+    if (r >= 0) a.share[t * a.k + r] = expf(row[j] - top) / sum;
   }
+}
+
+// The work of a workgroup: neighbours on one XCD where every slot has some; dealt round where many
+// slots may have none, whose XCDs would be left idle.
+__device__ __forceinline__ int work_of(const MoeArgs& a) {
+  return a.by_token ? (int)blockIdx.x : xcd_order(blockIdx.x, a.slots * a.tiles);
 }
 
 // The expert of a slot, or -1.
@@ -110,12 +121,12 @@ __device__ __forceinline__ int slot_tokens(const MoeArgs& a, int slot, int e, in
 
 // ---- gate and up products.  A workgroup: one slot, 8 * NTW columns of I: row tiles
 // 0 .. NTW/2-1 of its 16 * NTW rows of w13 are gate rows, the others the up rows.
-template <int NTW, int TERMS>
+template <int NTW, int KIND>
 __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
   constexpr int IC = 8 * NTW, NG = NTW / 2;
   int* s_row = reinterpret_cast<int*>(smem + stream_lds<1, NTW>());
   __shared__ int s_cnt;
-  const int wg = xcd_order(blockIdx.x, a.slots * a.tiles);
+  const int wg = work_of(a);
   const int slot = wg / a.tiles, tile = wg % a.tiles;
   const int lane = threadIdx.x & 63, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -125,16 +136,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
   const int rows = min(IC, a.I - i0);
   const uint8_t* w = a.w13 + e * a.st_w13 + i0 * a.ld_w13;
   const uint8_t* s = a.s13 + e * a.st_s13 + i0 * a.ld_s13;
-  const Lines gate = lines_of(w, a.ld_w13, s, a.ld_s13, rows, nb, a.s13_words);
-  const Lines up = lines_of(w + a.I * a.ld_w13, a.ld_w13, s + a.I * a.ld_s13, a.ld_s13, rows, nb, a.s13_words);
-  const ItemOffsets wo = item_offsets(gate.ld_c, gate.ld_s, lane);
+  Lines l = lines_of(w, a.ld_w13, s, a.ld_s13, rows, nb, a.s13_words);
+  l.first = NG;
+  l.far_c = (uint64_t)(a.I * a.ld_w13);
+  l.far_s = (uint64_t)(a.I * a.ld_s13);
+  const ItemOffsets wo = item_offsets(l.ld_c, l.ld_s, lane);
   const uint32_t ring = (uint32_t)wave * kWaveLds, lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)smem + ring;
   const int chunks = (a.I + kChunk - 1) / kChunk;
   const Run run = run_of<NTW>(a.H, wave);
-  auto issue = [&](int t, int c, uint32_t lds) {
-    if (t < NG) issue_item(gate, wo, t, c, lds);
-    else issue_item(up, wo, t - NG, c, lds);
-  };
+  auto issue = [&](int t, int c, uint32_t lds) { issue_item(l, wo, t, c, lds); };
   // few tokens come straight into registers, and the first weights are on their way while they
   // are looked up; more pass through the ring a chunk at a time
   const bool through = a.T <= 4 || a.T * a.k <= 2 * a.E || !a.x_pieces;
@@ -167,10 +177,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
             reads_done();
           }
         },
-        [&](int t, int c, uint32_t slot_at) {
-          return t < NG ? item_scales(gate, slot_at, t, c, nb, lane) : item_scales(up, slot_at, t - NG, c, nb, lane);
-        },
-        acc);
+        [&](int t, int c, uint32_t slot_at) { return item_scales(l, slot_at, t, c, nb, lane); }, acc);
     __syncthreads();
     store_part<1, NTW>(wave, lane, acc);
     __syncthreads();
@@ -178,35 +185,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
       const int m = q / (IC / 8), c = 8 * (q % (IC / 8));
       if (m0 + m >= cnt || i0 + c >= a.I) continue;
       const float share = a.share[s_row[m0 + m]];
-      uint32_t o[TERMS][4];
+      const int k = i0 + c;
+      uint8_t* dst = a.h + (((int64_t)slot * a.mt_cap + m0 / 16) * chunks) * kHiddenChunk + h_offset(m, k);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const v4f gt = sum_part<1, NTW>(m, c + 4 * hf), u = sum_part<1, NTW>(m, IC + c + 4 * hf);
+        float v[4];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          uint32_t b0[TERMS], b1[TERMS];
-          const int col = i0 + c + 4 * hf + 2 * p;     // zeros past I
-          split_bf16<TERMS>(col < a.I ? gated(share, gt[2 * p], u[2 * p]) : 0.0f, b0);
-          split_bf16<TERMS>(col + 1 < a.I ? gated(share, gt[2 * p + 1], u[2 * p + 1]) : 0.0f, b1);
-#pragma unroll
-          for (int t = 0; t < TERMS; ++t) o[t][2 * hf + p] = b0[t] | (b1[t] << 16);
-        }
+        for (int p = 0; p < 4; ++p) v[p] = k + 4 * hf + p < a.I ? gated(share, gt[p], u[p]) : 0.0f;   // zeros past I
+        store_hidden<KIND>(dst, hf, v);
       }
-      const int mt = m0 / 16;
-      uint8_t* dst = a.h + ((int64_t)slot * a.mt_cap + mt) * chunks * (TERMS * 16384) + h_offset<TERMS>(m, i0 + c);
-#pragma unroll
-      for (int t = 0; t < TERMS; ++t)
-        *reinterpret_cast<uint4*>(dst + 4096 * t) = make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
     }
   }
 }
 
 // ---- down products.  A workgroup: one slot, 16 * NTW columns of H; h comes in fragment order.
-template <int NTW, int TERMS>
-__global__ __launch_bounds__(kThreads, TERMS == 2 ? 2 : 1) void k_moe_down(const MoeArgs a) {
+template <int NTW, int KIND>
+__global__ __launch_bounds__(kThreads, 2) void k_moe_down(const MoeArgs a) {
   int* s_row = reinterpret_cast<int*>(smem + stream_lds<1, NTW>());
   __shared__ int s_cnt;
-  const int wg = xcd_order(blockIdx.x, a.slots * a.tiles);
+  const int wg = work_of(a);
   const int slot = wg / a.tiles, tile = wg % a.tiles;
   const int lane = threadIdx.x & 63, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -231,24 +229,24 @@ __global__ __launch_bounds__(kThreads, TERMS == 2 ? 2 : 1) void k_moe_down(const
       __syncthreads();
       fill_ring<NTW>(run.it0, run.it1, lds0, issue);
     }
-    const uint8_t* h = a.h + ((int64_t)slot * a.mt_cap + m0 / 16) * chunks * (TERMS * 16384) + 16 * lane;
+    const uint8_t* h = a.h + ((int64_t)slot * a.mt_cap + m0 / 16) * chunks * kHiddenChunk + 16 * lane;
     v4f acc[1][NTW];
 #pragma unroll
     for (int n = 0; n < NTW; ++n) acc[0][n] = {0.0f, 0.0f, 0.0f, 0.0f};
-    stream<XWide<1, TERMS>, 1, NTW>(
+    stream<XWide<1, KIND>, 1, NTW>(
         run, wave, lane, a.s2_words, true, issue,
-        [&](XWide<1, TERMS>& x, int c) {
+        [&](XWide<1, KIND>& x, int c) {
 #pragma unroll
           for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int p = 0; p < TERMS; ++p)
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 // rows past the last token and elements past I have nothing in h
                 const int k = kChunk * c + 32 * (4 * (lane >> 4) + u) + 8 * j;
                 v4i v = {0, 0, 0, 0};
                 if (k < a.I && m0 + i < cnt)
-                  v = *reinterpret_cast<const v4i*>(h + (((int64_t)4 * c + u) * TERMS + p) * 4096 + 1024 * j);
+                  v = *reinterpret_cast<const v4i*>(h + (((int64_t)4 * c + u) * 2 + p) * 4096 + 1024 * j);
                 x.f[u][j][0][p] = v;
               }
         },
@@ -282,24 +280,24 @@ __global__ __launch_bounds__(256) void k_moe_sum(const MoeArgs a) {
     reinterpret_cast<float*>(a.y)[t * a.ld_y + n] = s;
 }
 
-template <int NTW, int TERMS>
+template <int NTW, int KIND>
 hipError_t launch_up(MoeArgs a, hipStream_t st) {
   static bool set[64] = {false};
   a.tiles = (a.I + 8 * NTW - 1) / (8 * NTW);
   if ((int64_t)a.slots * a.tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = k_moe_up<NTW, TERMS>;
+  auto kern = k_moe_up<NTW, KIND>;
   const hipError_t e = allow_lds(kern, stream_lds<1, NTW>() + 4 * 1024, set);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)(a.slots * a.tiles)), dim3(kThreads), (stream_lds<1, NTW>() + 4 * a.T), st, a);
   return hipGetLastError();
 }
 
-template <int NTW, int TERMS>
+template <int NTW, int KIND>
 hipError_t launch_down(MoeArgs a, hipStream_t st) {
   static bool set[64] = {false};
   a.tiles = (a.H + 16 * NTW - 1) / (16 * NTW);
   if ((int64_t)a.slots * a.tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = k_moe_down<NTW, TERMS>;
+  auto kern = k_moe_down<NTW, KIND>;
   const hipError_t e = allow_lds(kern, stream_lds<1, NTW>() + 4 * 1024, set);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)(a.slots * a.tiles)), dim3(kThreads), (stream_lds<1, NTW>() + 4 * a.T), st, a);
@@ -331,42 +329,55 @@ struct Plan {
 
 // The wide kernels keep one workgroup per CU busy with a queue of works (128 columns of I or 256 of H
 // of one expert); below about two works a CU the finer workgroups of this file are better.
-Plan plan_of(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16) {
+Plan plan_of(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
   const int64_t cus = device_cu_count();
   const double experts = active_experts(T, E, k);
   const int64_t chunks = (I + kChunk - 1) / kChunk;
   Plan p{};
   p.up_wide = experts * ((I + 127) / 128) >= 1.9 * cus;
   const int64_t works = (int64_t)(experts * ((H + 255) / 256));
-  p.parts = y_bf16 ? down_parts(works, chunks, cus) : 1;
-  p.down_wide = y_bf16 && (double)works * p.parts >= 1.9 * cus;
+  p.parts = down_parts(works, chunks, cus);
+  p.down_wide = (double)works * p.parts >= 1.9 * cus;
   if (!p.down_wide) p.parts = 1;
   return p;
 }
 
-// Column tiles as wide as still give every CU two workgroups (a slot's expert may be unused, so
-// the count is an upper bound).
-template <int TERMS>
+// Row tiles of a workgroup over `n` columns of one expert: the fewest rounds of workgroups (two a CU)
+// times what one takes, its row tiles and a fixed cost worth about three of them (lookups, filling
+// the ring, adding up).
+int row_tiles(double experts, int64_t n, int columns_per_tile, int64_t cus) {
+  int best = 8;
+  double least = 1e30;
+  for (int t = 8; t >= 2; t /= 2) {
+    const double cost = ceil(experts * ceil((double)n / (columns_per_tile * t)) / (2.0 * cus)) * (t + 3);
+    if (cost < least) {
+      least = cost;
+      best = t;
+    }
+  }
+  return best;
+}
+
+template <int KIND>
 hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
   const int64_t cus = device_cu_count();
+  const double experts = active_experts(a.T, a.E, a.k);
   hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  const int nu = row_tiles(experts, a.I, 8, cus), nd = row_tiles(experts, a.H, 16, cus);
   if (plan.up_wide && a.x_pieces && a.H % 8 == 0 && a.s13_pieces)
-    e = launch_moe_up_wide<TERMS>(a, st);
-  else if ((int64_t)a.slots * ((a.I + 63) / 64) >= 2 * cus)
-    e = launch_up<8, TERMS>(a, st);
+    e = launch_moe_up_wide<KIND>(a, st);
   else
-    e = (int64_t)a.slots * ((a.I + 31) / 32) >= 2 * cus ? launch_up<4, TERMS>(a, st) : launch_up<2, TERMS>(a, st);
+    e = nu == 8 ? launch_up<8, KIND>(a, st) : nu == 4 ? launch_up<4, KIND>(a, st) : launch_up<2, KIND>(a, st);
   if (e != hipSuccess) return e;
   MoeArgs d = a;
-  d.parts = plan.down_wide && a.s2_pieces ? plan.parts : 1;
-  if (plan.down_wide && a.s2_pieces)
-    e = launch_moe_down_wide(d, st);
-  else if ((int64_t)a.slots * ((a.H + 127) / 128) >= 2 * cus)
-    e = launch_down<8, TERMS>(d, st);
+  const bool wide = plan.down_wide && a.s2_pieces;
+  d.parts = wide ? plan.parts : 1;
+  if (wide)
+    e = launch_moe_down_wide<KIND>(d, st);
   else
-    e = (int64_t)a.slots * ((a.H + 63) / 64) >= 2 * cus ? launch_down<4, TERMS>(d, st) : launch_down<2, TERMS>(d, st);
+    e = nd == 8 ? launch_down<8, KIND>(d, st) : nd == 4 ? launch_down<4, KIND>(d, st) : launch_down<2, KIND>(d, st);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), dim3(256), 0, st, d);
   return hipGetLastError();
@@ -375,7 +386,7 @@ hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Slots: one per expert, or, where the tokens can choose fewer, one per token and rank.
-void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int terms, int parts, MoeArgs* a, int64_t off[5],
+void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int parts, MoeArgs* a, int64_t off[5],
                 int64_t* total) {
   a->by_token = T * k < E;
   a->slots = (int)(a->by_token ? T * k : E);
@@ -385,26 +396,24 @@ void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int terms
   off[1] = up256(T * k * 4);
   off[2] = off[1] + up256(T * k * 4);
   off[3] = off[2] + up256(E * T * 2);
-  off[4] = off[3] + (int64_t)a->slots * a->mt_cap * chunks * terms * 16384;
+  off[4] = off[3] + (int64_t)a->slots * a->mt_cap * chunks * kHiddenChunk;
   *total = off[4] + up256(T * k * parts * H * 4);
 }
 
-int terms_of(bool y_bf16) { return y_bf16 ? 2 : 3; }
-
 }  // namespace
 
-int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16) {
+int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
   MoeArgs a{};
   int64_t off[5], total;
-  moe_layout(T, H, I, E, k, terms_of(y_bf16), plan_of(T, H, I, E, k, y_bf16).parts, &a, off, &total);
+  moe_layout(T, H, I, E, k, plan_of(T, H, I, E, k).parts, &a, off, &total);
   return total;
 }
 
 hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   MoeArgs a{};
   int64_t off[5], total;
-  const Plan plan = plan_of(p.T, p.H, p.I, p.E, p.k, p.y_bf16);
-  moe_layout(p.T, p.H, p.I, p.E, p.k, terms_of(p.y_bf16), plan.parts, &a, off, &total);
+  const Plan plan = plan_of(p.T, p.H, p.I, p.E, p.k);
+  moe_layout(p.T, p.H, p.I, p.E, p.k, plan.parts, &a, off, &total);
   a.T = (int)p.T;
   a.H = (int)p.H;
   a.I = (int)p.I;
@@ -441,7 +450,7 @@ hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   a.y = p.y;
   a.ld_y = p.ld_y;
   a.y_bf16 = p.y_bf16;
-  return p.y_bf16 ? launch_all<2>(a, plan, st) : launch_all<3>(a, plan, st);
+  return p.y_bf16 ? launch_all<kTwo>(a, plan, st) : launch_all<kF32>(a, plan, st);
 }
 
 }  // namespace mxq

@@ -177,7 +177,7 @@ __device__ __forceinline__ void landed() {
 }
 
 // ---- gate and up.
-template <int TERMS>
+template <int KIND>
 __global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
   constexpr int GROUP = 4;
   int* s_end = reinterpret_cast<int*>(smem + kUpLds);
@@ -303,28 +303,20 @@ __global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
     const int id = __shfl(rows, i), col = 128 * p.tile + 16 * wave + 4 * g;
     if (id > 0 && (col & ~7) < a.I) {
       const float share = a.share[id - 1];
-      uint32_t o[TERMS][2];
+      float v[4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t b0[TERMS], b1[TERMS];
-        split_bf16<TERMS>(col + 2 * q < a.I ? gated(share, acc[0][2 * q], acc[1][2 * q]) : 0.0f, b0);
-        split_bf16<TERMS>(col + 2 * q + 1 < a.I ? gated(share, acc[0][2 * q + 1], acc[1][2 * q + 1]) : 0.0f, b1);
-#pragma unroll
-        for (int t = 0; t < TERMS; ++t) o[t][q] = b0[t] | (b1[t] << 16);
-      }
-      uint8_t* dst = a.h + ((int64_t)p.slot * a.mt_cap + p.m) * h_chunks * (TERMS * 16384) + h_offset<TERMS>(i, col & ~7) +
-                     2 * (col & 4);
-#pragma unroll
-      for (int t = 0; t < TERMS; ++t) *reinterpret_cast<uint2*>(dst + 4096 * t) = make_uint2(o[t][0], o[t][1]);
+      for (int q = 0; q < 4; ++q) v[q] = col + q < a.I ? gated(share, acc[0][q], acc[1][q]) : 0.0f;
+      store_hidden<KIND>(a.h + ((int64_t)p.slot * a.mt_cap + p.m) * h_chunks * kHiddenChunk + h_offset(i, col & ~7), (col >> 2) & 1, v);
     }
   }
   landed<0>();                                           // no load may land after the workgroup
 }
 
-// ---- down, h in two terms.  A stage is half a chunk of h (steps 0, 1 or 2, 3): 16 KiB, in the
+// ---- down.  A stage is half a chunk of h (steps 0, 1 or 2, 3): 16 KiB, in the
 // order in which it lies in memory.
+template <int KIND>
 __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
-  constexpr int TERMS = 2, GROUP = 2;
+  constexpr int GROUP = 2;
   int* s_end = reinterpret_cast<int*>(smem + kDownLds);
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = uniform(threadIdx.x >> 6);
@@ -382,7 +374,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
         seek(xp, works, xw);
         xs = 2 * (chunks * xp.part / a.parts);
         xs1 = 2 * (chunks * (xp.part + 1) / a.parts);
-        xat = (uint64_t)(uintptr_t)a.h + ((uint64_t)xp.slot * a.mt_cap + xp.m) * (uint64_t)chunks * (TERMS * 16384);
+        xat = (uint64_t)(uintptr_t)a.h + ((uint64_t)xp.slot * a.mt_cap + xp.m) * (uint64_t)chunks * kHiddenChunk;
       }
     }
     const v4i rs = rsrc_of(xat + (uint64_t)xs * kStage, xw < w1 ? (uint32_t)kStage : 0u);
@@ -420,15 +412,15 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
       const bool begins = (c - c0) % GROUP == 0;
 #pragma unroll
       for (int hs = 0; hs < 2; ++hs) {
-        v4i x[2][TERMS][4];
+        v4i x[2][4][2];
         const uint32_t from = kDownX + xbuf * kStage + 16 * lane;
         xbuf = xbuf + 1 == kDownStages ? 0 : xbuf + 1;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int q = 0; q < TERMS; ++q)
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[u][q][j] = lds16(from, ((u * TERMS + q) * 4 + j) * 1024);
+            for (int j = 0; j < 4; ++j) x[u][j][q] = lds16(from, ((u * 2 + q) * 4 + j) * 1024);
         if (kChunk * (c + 1) > a.I) {                    // h has nothing at k >= I
 #pragma unroll
           for (int u = 0; u < 2; ++u)
@@ -436,7 +428,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
             for (int j = 0; j < 4; ++j)
               if (kChunk * c + 32 * (4 * g + 2 * hs + u) + 8 * j >= a.I) {
 #pragma unroll
-                for (int q = 0; q < TERMS; ++q) x[u][q][j] = v4i{0, 0, 0, 0};
+                for (int q = 0; q < 2; ++q) x[u][j][q] = v4i{0, 0, 0, 0};
               }
         }
         if (hs == 0 && begins) {
@@ -469,8 +461,15 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
               uint32_t d[4];
               fp4::decode8_bf16((uint32_t)wf[t][2 * hs + u][j], s, d);
               const v4i dv = {(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
+              if (KIND == kF32) {
+                v4i c3[3];
+                cut_f32(x[u][j], c3);
 #pragma unroll
-              for (int q = TERMS - 1; q >= 0; --q) acc[t] = mma_bf16(dv, x[u][q][j], acc[t]);
+                for (int q = 2; q >= 0; --q) acc[t] = mma_bf16(dv, c3[q], acc[t]);
+              } else {
+#pragma unroll
+                for (int q = 1; q >= 0; --q) acc[t] = mma_bf16(dv, x[u][j][q], acc[t]);
+              }
             }
           }
         }
@@ -501,12 +500,12 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
 }  // namespace wide
 }  // namespace
 
-template <int TERMS>
+template <int KIND>
 hipError_t launch_moe_up_wide(const MoeArgs& args, hipStream_t st) {
   static bool set[64] = {false};
   MoeArgs a = args;
   a.tiles = (a.I + 127) / 128;
-  auto kern = wide::k_moe_up_wide<TERMS>;
+  auto kern = wide::k_moe_up_wide<KIND>;
   constexpr int lds = wide::kUpLds;
   const hipError_t e = allow_lds(kern, lds + 4 * 1024, set);
   if (e != hipSuccess) return e;
@@ -514,19 +513,23 @@ hipError_t launch_moe_up_wide(const MoeArgs& args, hipStream_t st) {
   return hipGetLastError();
 }
 
-template hipError_t launch_moe_up_wide<2>(const MoeArgs&, hipStream_t);
-template hipError_t launch_moe_up_wide<3>(const MoeArgs&, hipStream_t);
+template hipError_t launch_moe_up_wide<kTwo>(const MoeArgs&, hipStream_t);
+template hipError_t launch_moe_up_wide<kF32>(const MoeArgs&, hipStream_t);
 
+template <int KIND>
 hipError_t launch_moe_down_wide(const MoeArgs& args, hipStream_t st) {
   static bool set[64] = {false};
   MoeArgs a = args;
   a.tiles = (a.H + 255) / 256;
-  auto kern = wide::k_moe_down_wide;
+  auto kern = wide::k_moe_down_wide<KIND>;
   constexpr int lds = wide::kDownLds;
   const hipError_t e = allow_lds(kern, lds + 4 * 1024, set);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)device_cu_count()), dim3(wide::kT), lds + 4 * a.slots, st, a);
   return hipGetLastError();
 }
+
+template hipError_t launch_moe_down_wide<kTwo>(const MoeArgs&, hipStream_t);
+template hipError_t launch_moe_down_wide<kF32>(const MoeArgs&, hipStream_t);
 
 }  // namespace mxq
