@@ -147,7 +147,7 @@ int mxq_moe_fp4_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k,
   if (T < 0 || T > kMaxMoeTokens || H < 0 || H >= kMaxK || I < 0 || I >= kMaxK || E < 1 || E > kMaxExperts)
     return MXQ_ERR_SHAPE;
   if (k < 1 || k > E) return MXQ_ERR_ARG;
-  *bytes = T == 0 || H == 0 ? 0 : mxq::moe_fp4_workspace_bytes(T, H, I, E, k);
+  *bytes = T == 0 || H == 0 ? 0 : mxq::moe_fp4_workspace_bytes(T, H, I, E, k, y_type == MXQ_BF16);
   return MXQ_OK;
 }
 

@@ -138,7 +138,7 @@ struct MoeFp4 {
   bool y_bf16;
   void* workspace;
 };
-int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k);
+int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16);
 hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t stream);
 
 }  // namespace mxq

@@ -307,73 +307,63 @@ hipError_t launch_down(MoeArgs a, hipStream_t st) {
 // Experts that some token chooses, if the choices were independent.
 double active_experts(int64_t T, int64_t E, int64_t k) { return E * (1.0 - pow(1.0 - (double)k / E, (double)T)); }
 
-// K ranges of the wide down product: the fewest, up to 8, whose works come out even enough over
-// the workgroups (a range costs a partial row per token and expert).
-int down_parts(int64_t works, int64_t chunks, int64_t cus) {
-  int best = 1;
-  double eff = 0.0;
-  for (int p = 1; p <= 8 && p <= chunks; p *= 2) {
-    const double n = (double)works * p, rounds = ceil(n / cus), e = n / (rounds * cus) - 0.02 * p;
-    if (e > eff + 0.01) {
-      eff = e;
-      best = p;
-    }
+// How a product over `experts` matrices of `rows` x `K` runs: by the workgroups of this file, `tiles`
+// row tiles each, or by the persistent ones of moe_fp4_wide.hip with K in `parts` ranges.  The
+// estimates, in us, are fits to runs on 256 CUs:
+//   this file  rounds of two workgroups a CU, each 6 us and, per row tile and chunk, 0.33 us going up
+//              and 0.4 down (1.2 where h is cut from fp32), or the weights at 4.3 TB/s
+//   persistent rounds of one work a CU, 3.5 us a chunk and 8 us going up, 4.3 (9.2) a chunk and 6 us
+//              down, 0.3 us more for every range after the first, or the weights at 5.2 TB/s
+// Measured, this file's against the persistent ones': up 133 and 122 us (64 tokens, 64 experts of
+// 4096 x 2048), 80 and 71 (16, 8 of 5120 x 8192); down 74 and 76, 58 and 46; 46 and 34 (7 tokens, 60
+// experts of 2000 x 1064, y in fp32).
+struct Way {
+  bool wide;
+  int tiles, parts;
+  double us;
+};
+
+Way way_of(double experts, int64_t rows, int64_t K, bool up, bool f32) {
+  const double cus = device_cu_count(), mb = experts * rows * K * 17 / 32 * 1e-6;
+  const int64_t chunks = (K + kChunk - 1) / kChunk;
+  Way best{false, 8, 1, 1e30};
+  for (int t = 8; t >= 2; t /= 2) {
+    const double rounds = ceil(experts * ceil((double)rows / (16 * t)) / (2 * cus));
+    const double us = fmax(rounds * (6 + (up ? 0.33 : f32 ? 1.2 : 0.4) * t * chunks), mb / 4.3);
+    if (us < best.us) best = Way{false, t, 1, us};
+  }
+  const double works = experts * ceil((double)rows / 256);
+  for (int p = 1; p <= (up ? 1 : 8) && p <= chunks; p *= 2) {
+    const double chunk = up ? 3.5 : f32 ? 9.2 : 4.3;
+    const double us = fmax(ceil(works * p / cus) * ((chunks + p - 1) / p) * chunk, mb / 5.2) + (up ? 8 : 6) + 0.3 * (p - 1);
+    if (us < best.us) best = Way{true, 8, p, us};
   }
   return best;
 }
 
 struct Plan {
-  bool up_wide, down_wide;
-  int parts;
+  Way up, down;
 };
 
-// The wide kernels keep one workgroup per CU busy with a queue of works (128 columns of I or 256 of H
-// of one expert); below about two works a CU the finer workgroups of this file are better.
-Plan plan_of(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
-  const int64_t cus = device_cu_count();
+Plan plan_of(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool f32) {
   const double experts = active_experts(T, E, k);
-  const int64_t chunks = (I + kChunk - 1) / kChunk;
-  Plan p{};
-  p.up_wide = experts * ((I + 127) / 128) >= 1.9 * cus;
-  const int64_t works = (int64_t)(experts * ((H + 255) / 256));
-  p.parts = down_parts(works, chunks, cus);
-  p.down_wide = (double)works * p.parts >= 1.9 * cus;
-  if (!p.down_wide) p.parts = 1;
-  return p;
-}
-
-// Row tiles of a workgroup over `n` columns of one expert: the fewest rounds of workgroups (two a CU)
-// times what one takes, its row tiles and a fixed cost worth about three of them (lookups, filling
-// the ring, adding up).
-int row_tiles(double experts, int64_t n, int columns_per_tile, int64_t cus) {
-  int best = 8;
-  double least = 1e30;
-  for (int t = 8; t >= 2; t /= 2) {
-    const double cost = ceil(experts * ceil((double)n / (columns_per_tile * t)) / (2.0 * cus)) * (t + 3);
-    if (cost < least) {
-      least = cost;
-      best = t;
-    }
-  }
-  return best;
+  return Plan{way_of(experts, 2 * I, H, true, f32), way_of(experts, H, I, false, f32)};
 }
 
 template <int KIND>
 hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
-  const int64_t cus = device_cu_count();
-  const double experts = active_experts(a.T, a.E, a.k);
   hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int nu = row_tiles(experts, a.I, 8, cus), nd = row_tiles(experts, a.H, 16, cus);
-  if (plan.up_wide && a.x_pieces && a.H % 8 == 0 && a.s13_pieces)
+  const int nu = plan.up.tiles, nd = plan.down.tiles;
+  if (plan.up.wide && a.x_pieces && a.H % 8 == 0 && a.s13_pieces)
     e = launch_moe_up_wide<KIND>(a, st);
   else
     e = nu == 8 ? launch_up<8, KIND>(a, st) : nu == 4 ? launch_up<4, KIND>(a, st) : launch_up<2, KIND>(a, st);
   if (e != hipSuccess) return e;
   MoeArgs d = a;
-  const bool wide = plan.down_wide && a.s2_pieces;
-  d.parts = wide ? plan.parts : 1;
+  const bool wide = plan.down.wide && a.s2_pieces;
+  d.parts = wide ? plan.down.parts : 1;
   if (wide)
     e = launch_moe_down_wide<KIND>(d, st);
   else
@@ -402,18 +392,18 @@ void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int parts
 
 }  // namespace
 
-int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
+int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16) {
   MoeArgs a{};
   int64_t off[5], total;
-  moe_layout(T, H, I, E, k, plan_of(T, H, I, E, k).parts, &a, off, &total);
+  moe_layout(T, H, I, E, k, plan_of(T, H, I, E, k, !y_bf16).down.parts, &a, off, &total);
   return total;
 }
 
 hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   MoeArgs a{};
   int64_t off[5], total;
-  const Plan plan = plan_of(p.T, p.H, p.I, p.E, p.k);
-  moe_layout(p.T, p.H, p.I, p.E, p.k, plan.parts, &a, off, &total);
+  const Plan plan = plan_of(p.T, p.H, p.I, p.E, p.k, !p.y_bf16);
+  moe_layout(p.T, p.H, p.I, p.E, p.k, plan.down.parts, &a, off, &total);
   a.T = (int)p.T;
   a.H = (int)p.H;
   a.I = (int)p.I;

