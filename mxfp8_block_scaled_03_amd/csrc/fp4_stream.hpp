@@ -383,15 +383,143 @@ __device__ __forceinline__ void stream(Run run, int wave, int lane, bool s_words
   }
 }
 
+// The stream with X in bf16 staged in a place of its own behind the ring (16 KiB a wave, so one
+// workgroup a CU): while a chunk's items are multiplied, the next chunk's are on their way and so
+// is its first 16-row tile of X.  X is asked for before the items that need it.
+//   DMA        rows of whole 16-byte pieces: 16 loads a tile, and an item's scales in whole words
+//              (five loads), so what is behind X can be counted
+//   otherwise  through registers, row by row (1 KiB a load), any alignment and length
+// 16 x 4096 x 4096 takes 5.3 us so, and 8.0 with fragment-shaped loads straight into registers.
+constexpr int kStagedLds = kWaveLds + 16384;
+
+// The rows of a 16-row tile of X: `row` is the lane's (i), K its length.
+template <bool DMA, int MT>
+struct XStage {
+  const uint8_t* row[MT];
+  int K, lane;
+  uint32_t at;                               // this wave's place in LDS
+  v4i raw[DMA ? 1 : 16];                     // the tile on its way, row r's piece of the lane
+
+  __device__ __forceinline__ const uint8_t* row_of(int m, int r) const {
+    const uint64_t p = (uint64_t)(uintptr_t)row[m];
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)p, r);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(p >> 32), r);
+    return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
+  }
+
+  template <int M>
+  __device__ __forceinline__ void ask(int c) {
+    const int left = min(K - kChunk * c, kChunk);
+    if (DMA) {
+#pragma unroll 1
+      for (int r = 0; r < 16; ++r)
+        dma16((uint32_t)(uintptr_t)(lds_ptr_t)smem + at + 1024 * r, 16u * (uint32_t)(lane ^ r),
+              rsrc_of((uint64_t)(uintptr_t)row_of(M, r) + 1024u * (uint64_t)c, 2u * (uint32_t)left));
+    } else {
+      const int k = 8 * lane;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const uint8_t* p = row_of(M, r) + 1024 * (int64_t)c;
+        v4i v = {0, 0, 0, 0};
+        // the piece that the row's end cuts is read from the last 8 elements
+        if (k < left && K >= 8) __builtin_memcpy(&v, p + 2 * min(k, left - 8), 16);
+        if (K < 8 && lane == 0) {
+#pragma unroll
+          for (int e = 0; e < 7; ++e)
+            if (e < K) v[e >> 1] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1)));
+        }
+        raw[DMA ? 0 : r] = v;
+      }
+    }
+  }
+
+  template <int M, typename X>
+  __device__ __forceinline__ void take(X& x, int c) {
+    if (!DMA) {
+      const int left = K - kChunk * c, k = 8 * lane;
+      const int cut = K >= 8 && k < left ? max(k + 8 - left, 0) : 0;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        v4i v = raw[DMA ? 0 : r];
+        if (left < kChunk) v = drop_low(v, cut);
+        *reinterpret_cast<v4i*>(smem + at + 1024 * r + 16 * (lane ^ r)) = v;
+      }
+      wait_vm<0>();                          // with the tile, everything asked for before it
+      reads_done();
+    }
+    x.read_staged(M, at, lane);
+    reads_done();
+  }
+};
+
+template <bool DMA, int MT, int NTW, typename Issue, typename Scales>
+__device__ __forceinline__ void stream_staged(Run run, int wave, int lane, XStage<DMA, MT>& xs, Issue issue, Scales scales_of,
+                                              v4f acc[MT][NTW]) {
+  static_assert(NTW <= kRing && MT <= 2, "a chunk's items are in flight together");
+  const uint32_t ring = (uint32_t)wave * kStagedLds;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)smem + ring;
+  if (run.it0 >= run.it1) return;
+  int n = 0;                                             // slot of the next item
+  xs.template ask<0>(run.it0 / NTW);
+  fill_ring<NTW>(run.it0, run.it1, lds0, issue);
+  int behind = min(kRing, run.it1 - run.it0);            // items asked for after the tile of X
+  for (int c = run.it0 / NTW; c * NTW < run.it1; ++c) {
+    const int lo = max(run.it0 - c * NTW, 0), hi = min(run.it1 - c * NTW, NTW);
+    XWide<MT, 1> x;
+    if (DMA) {
+      if (behind >= 4) wait_vm<20>();
+      else if (behind == 3) wait_vm<15>();
+      else if (behind == 2) wait_vm<10>();
+      else if (behind == 1) wait_vm<5>();
+      else wait_vm<0>();
+      asm volatile("" ::: "memory");
+    }
+    xs.template take<0>(x, c);
+    if constexpr (MT == 2) {
+      xs.template ask<1>(c);
+      if (DMA) {
+        wait_vm<0>();
+        asm volatile("" ::: "memory");
+      }
+      xs.template take<1>(x, c);
+    }
+    const bool next = (c + 1) * NTW < run.it1;
+    if (next) xs.template ask<0>(c + 1);
+    behind = 0;
+    if (DMA && MT == 1) {                                // this chunk's items, asked for before
+      if (next) wait_vm<16>();
+      else wait_vm<0>();
+      asm volatile("" ::: "memory");
+    }
+#pragma unroll
+    for (int t = 0; t < NTW; ++t) {
+      if (t < lo || t >= hi) continue;
+      const int it = c * NTW + t;
+      const uint32_t slot = ring + n * kSlot;
+      v4i w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] = item_codes(slot, lane, u);
+      const uint32_t ws = scales_of(t, c, slot);
+      reads_done();
+      if (it + kRing < run.it1) {
+        issue((int)((uint32_t)(it + kRing) % NTW), (int)((uint32_t)(it + kRing) / NTW), lds0 + n * kSlot);
+        ++behind;
+      }
+      n = (n + 1) % kRing;
+      x.mma(w, ws, &acc[0][t], NTW);
+    }
+  }
+}
+
 // The waves' sums side by side in LDS: wave w's value of X row m, W row n is at [w][m][n], rows
 // of 16 * NTW + 4 floats.
 template <int NTW>
 constexpr int part_row() { return 16 * NTW + 4; }
 template <int MT, int NTW>
 constexpr int part_wave() { return 16 * MT * part_row<NTW>(); }
-template <int MT, int NTW>
+template <int MT, int NTW, int WAVE_LDS = kWaveLds>
 constexpr int stream_lds() {
-  return kWaves * part_wave<MT, NTW>() * 4 > kWaves * kWaveLds ? kWaves * part_wave<MT, NTW>() * 4 : kWaves * kWaveLds;
+  return part_wave<MT, NTW>() * 4 > WAVE_LDS ? kWaves * part_wave<MT, NTW>() * 4 : kWaves * WAVE_LDS;
 }
 
 template <int MT, int NTW>

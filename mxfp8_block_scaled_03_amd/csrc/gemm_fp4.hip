@@ -50,8 +50,11 @@ __device__ __forceinline__ void store4(const GemmEpilogue& ep, int64_t row, int 
 
 // A workgroup computes 16 * MT rows x 16 * NTW columns of Y.  Consecutive workgroups of an XCD
 // take the row tiles of one column tile, which read the same part of W.
-template <bool XFP4, int MT, int NTW>
-__global__ __launch_bounds__(kThreads, 2) void k_gemm4_stream(const Fp4Args a, const GemmEpilogue ep) {
+// How X comes: in MXFP4 through the ring, in bf16 staged by DMA or through registers.
+enum : int { kFp4Ring = 0, kBf16Dma = 1, kBf16Regs = 2 };
+
+template <int WAY, int MT, int NTW>
+__global__ __launch_bounds__(kThreads, WAY == kFp4Ring ? 2 : 1) void k_gemm4_stream(const Fp4Args a, const GemmEpilogue ep) {
   const int wg = xcd_order(blockIdx.x, a.tiles_m * a.tiles_n);
   const int m0 = (wg % a.tiles_m) * 16 * MT, n0 = (wg / a.tiles_m) * 16 * NTW;
   const int lane = threadIdx.x & 63, i = lane & 15;
@@ -68,7 +71,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm4_stream(const Fp4Args a, c
 #pragma unroll
     for (int n = 0; n < NTW; ++n) acc[m][n] = {0.0f, 0.0f, 0.0f, 0.0f};
   const Run run = run_of<NTW>(a.K, wave);
-  if constexpr (XFP4) {
+  if constexpr (WAY == kFp4Ring) {
     const Lines xl = lines_of(a.x + m0 * a.ld_x, a.ld_x, a.xs + m0 * a.ld_xs, a.ld_xs, min(16 * MT, a.M - m0), nb, a.xs_words);
     const ItemOffsets xo = item_offsets(xl.ld_c, xl.ld_s, lane);
     stream<XFp4<MT>, MT, NTW>(run, wave, lane, a.ws_words, false, issue, [&](XFp4<MT>& x, int c) {
@@ -89,29 +92,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm4_stream(const Fp4Args a, c
       reads_done();
     }, scales_of, acc);
   } else {
-    const uint8_t* row[MT];
+    XStage<WAY == kBf16Dma, MT> xs;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) row[m] = a.x + min((int64_t)m0 + 16 * m + i, (int64_t)a.M - 1) * a.ld_x;
-    // few rows come straight into registers; more pass through the ring a chunk at a time
-    const bool through = a.M - m0 <= 4 || !a.x_pieces;
-    if (through) fill_ring<NTW>(run.it0, run.it1, lds0, issue);
-    stream<XWide<MT, 1>, MT, NTW>(run, wave, lane, a.ws_words, through, issue, [&](XWide<MT, 1>& x, int c) {
-      const int left = a.K - kChunk * c;
-      if (through || left < kChunk) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          x.load_direct(m, row[m] + 2 * kChunk * (int64_t)c, m0 + 16 * m + i < a.M, left, a.K, lane);
-      } else {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          stage_rows((uint64_t)(uintptr_t)row[m], min(16, a.M - m0 - 16 * m), c, lds0, lane);
-          wait_vm<0>();
-          asm volatile("" ::: "memory");
-          x.read_staged(m, ring, lane);
-          reads_done();
-        }
-      }
-    }, scales_of, acc);
+    for (int m = 0; m < MT; ++m) xs.row[m] = a.x + min((int64_t)m0 + 16 * m + i, (int64_t)a.M - 1) * a.ld_x;
+    xs.K = a.K;
+    xs.lane = lane;
+    xs.at = (uint32_t)wave * kStagedLds + kWaveLds;
+    stream_staged<WAY == kBf16Dma, MT, NTW>(run, wave, lane, xs, issue, scales_of, acc);
   }
   __syncthreads();
   store_part<MT, NTW>(wave, lane, acc);
@@ -122,29 +109,30 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm4_stream(const Fp4Args a, c
   }
 }
 
-template <bool XFP4, int MT, int NTW>
+template <int WAY, int MT, int NTW>
 hipError_t launch_stream(Fp4Args a, const GemmEpilogue& ep, hipStream_t st) {
   static bool set[64] = {false};
   a.tiles_m = (a.M + 16 * MT - 1) / (16 * MT);
   a.tiles_n = (a.N + 16 * NTW - 1) / (16 * NTW);
   if ((int64_t)a.tiles_m * a.tiles_n > 0x7FFFFFFF) return hipErrorInvalidValue;
-  auto kern = k_gemm4_stream<XFP4, MT, NTW>;
-  const hipError_t e = allow_lds(kern, stream_lds<MT, NTW>(), set);
+  auto kern = k_gemm4_stream<WAY, MT, NTW>;
+  constexpr int lds = stream_lds<MT, NTW, WAY == kFp4Ring ? kWaveLds : kStagedLds>();
+  const hipError_t e = allow_lds(kern, lds, set);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(kThreads), (stream_lds<MT, NTW>()), st, a, ep);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(kThreads), lds, st, a, ep);
   return hipGetLastError();
 }
 
 // Columns per workgroup: as many as still give every CU a workgroup.
-template <bool XFP4, int MT>
+template <int WAY, int MT>
 hipError_t launch_m(const Fp4Args& a, const GemmEpilogue& ep, hipStream_t st) {
   const int64_t tm = (a.M + 16 * MT - 1) / (16 * MT);
   const int64_t cus = device_cu_count();
-  if constexpr (MT == 1)
-    if (tm * ((a.N + 127) / 128) >= cus) return launch_stream<XFP4, MT, 8>(a, ep, st);
-  if (tm * ((a.N + 63) / 64) >= cus) return launch_stream<XFP4, MT, 4>(a, ep, st);
-  if (tm * ((a.N + 31) / 32) >= cus) return launch_stream<XFP4, MT, 2>(a, ep, st);
-  return launch_stream<XFP4, MT, 1>(a, ep, st);
+  if constexpr (MT == 1 && WAY == kFp4Ring)
+    if (tm * ((a.N + 127) / 128) >= cus) return launch_stream<WAY, MT, 8>(a, ep, st);
+  if (tm * ((a.N + 63) / 64) >= cus) return launch_stream<WAY, MT, 4>(a, ep, st);
+  if (tm * ((a.N + 31) / 32) >= cus) return launch_stream<WAY, MT, 2>(a, ep, st);
+  return launch_stream<WAY, MT, 1>(a, ep, st);
 }
 
 }  // namespace
@@ -173,8 +161,13 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool 
   a.x_pieces = whole(x, a.ld_x, 16);
   a.xs_words = whole(xs, ld_xs, 4);
   a.ws_words = whole(ws, ld_ws, 4);
-  if (x_fp4) return M <= 16 ? launch_m<true, 1>(a, ep, st) : M <= 32 ? launch_m<true, 2>(a, ep, st) : launch_m<true, 4>(a, ep, st);
-  return M <= 16 ? launch_m<false, 1>(a, ep, st) : launch_m<false, 2>(a, ep, st);
+  if (x_fp4) {
+    if (M <= 16) return launch_m<kFp4Ring, 1>(a, ep, st);
+    return M <= 32 ? launch_m<kFp4Ring, 2>(a, ep, st) : launch_m<kFp4Ring, 4>(a, ep, st);
+  }
+  // whole 16-byte pieces, the last one of a row included, and scales in whole words
+  if (a.x_pieces && K % 8 == 0 && a.ws_words) return M <= 16 ? launch_m<kBf16Dma, 1>(a, ep, st) : launch_m<kBf16Dma, 2>(a, ep, st);
+  return M <= 16 ? launch_m<kBf16Regs, 1>(a, ep, st) : launch_m<kBf16Regs, 2>(a, ep, st);
 }
 
 }  // namespace mxq
