@@ -87,21 +87,43 @@ __device__ __forceinline__ uint32_t encode8(const Chunk<SRC_BF16>& c, uint32_t s
 }
 
 // Stochastically rounded code of the value with fp32 pattern vb under a finite scale byte
-// (inv = 2^(127 - sb)) and the 24-bit random integer r: between the neighbours l <= |a| < u,
-// up iff r < 2^24 * (|a| - l) / (u - l).  With step = 0.5, 1, 2 below 2, below 4 and from 4,
-// q = |a| / step is exact, so are floor(q), the fraction and the fraction times 2^24 (a
-// product by a power of two), so the comparison decides exactly.  |a| can underflow fp32 only
-// where the threshold is below 1: there any positive number decides alike, so a nonzero
-// value is kept from becoming 0.  The ceil rule keeps |a| <= 6.
-__device__ __forceinline__ uint32_t encode_sr(uint32_t vb, float inv, uint32_t r) {
-  const uint32_t mag = vb & 0x7FFFFFFFu;
-  float a = __uint_as_float(mag) * inv;
-  a = mag != 0u ? __builtin_fmaxf(a, 0x1p-126f) : 0.0f;
-  const bool b2 = a >= 2.0f, b4 = a >= 4.0f;
-  const float q = a * (b4 ? 0.5f : b2 ? 1.0f : 2.0f);
-  const float f = __builtin_floorf(q);
-  const uint32_t up = (float)r < (q - f) * 0x1p24f ? 1u : 0u;
-  return ((uint32_t)f + (b4 ? 4u : b2 ? 2u : 0u) + up) | ((vb >> 28) & 8u);
+// (inv = 2^(127 - sb)) and the 24-bit random integer r, given as the word w whose top 24 bits it is:
+// between the neighbours l <= |a| < u, up iff r < 2^24 * (|a| - l) / (u - l).  With |a| = m * 2^x,
+// 1 <= m < 2, the step is 2^(max(x, 0) - 1), so q = |a| / step is exact, floor(q) + 2 max(x, 0) is
+// the lower code, and the fraction of q times 2^32 and r * 2^8 are exact too: the comparison decides
+// exactly.  |a| can underflow fp32 only where the threshold is below 1: there any positive
+// number decides alike, so a nonzero value is kept from becoming 0 (min(|v|, 2^-126) is 0 for
+// zero alone).  The ceil rule keeps |a| <= 6.
+__device__ __forceinline__ uint32_t encode_sr(uint32_t vb, float inv, uint32_t w) {
+  const float v = __builtin_fabsf(__uint_as_float(vb));
+  const float a = __builtin_fmaxf(v * inv, __builtin_fminf(v, 0x1p-126f));
+  const int x1 = max(__builtin_amdgcn_frexp_expf(a), 1);               // max(x, 0) + 1
+  const float q = __builtin_amdgcn_ldexpf(a, 2 - x1);
+  const uint32_t up = (float)(w & 0xFFFFFF00u) < __builtin_amdgcn_fractf(q) * 0x1p32f ? 1u : 0u;
+  return ((uint32_t)q + (uint32_t)(2 * x1 - 2) + up) | ((vb >> 28) & 8u);
+}
+
+// The random words of the 32 elements of a block, as mxblock::block_random24 before its shift; the
+// three-operand xor is one instruction.
+__device__ __forceinline__ void block_random(uint64_t block, uint64_t seed, uint32_t r[32]) {
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    const uint64_t ctr = block * 8u + (uint64_t)g;
+    uint32_t c[4] = {(uint32_t)ctr, (uint32_t)(ctr >> 32), 0u, 0u};
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+      const uint64_t p0 = (uint64_t)c[0] * 0xD2511F53u, p1 = (uint64_t)c[2] * 0xCD9E8D57u;
+      c[0] = (uint32_t)__builtin_amdgcn_bitop3_b32((int)(p1 >> 32), (int)c[1], (int)k0, 0x96);
+      c[1] = (uint32_t)p1;
+      c[2] = (uint32_t)__builtin_amdgcn_bitop3_b32((int)(p0 >> 32), (int)c[3], (int)k1, 0x96);
+      c[3] = (uint32_t)p0;
+      k0 += 0x9E3779B9u;
+      k1 += 0xBB67AE85u;
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) r[4 * g + w] = c[w];
+  }
 }
 
 // Eight codes of a dword times the scale s = e8m0_to_f32(byte), as eight bf16 values in four

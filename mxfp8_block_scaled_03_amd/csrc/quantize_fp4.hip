@@ -57,7 +57,7 @@ __device__ __forceinline__ uint4 encode32(const Chunk<SRC_BF16> c[4], uint32_t s
   uint32_t d[4];
   if (SR && sb != 255u) {
     uint32_t rnd[32];
-    mxblock::block_random24(block, seed, rnd);
+    block_random(block, seed, rnd);
     const float inv = inv_scale_of(sb);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
