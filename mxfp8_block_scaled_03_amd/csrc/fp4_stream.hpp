@@ -183,52 +183,13 @@ __device__ __forceinline__ v4i drop_low(v4i v, int n) {
 
 // ---- X fragments of a chunk.
 
-// What the fragments hold of an element: bf16 (rows of X); the sum of two bf16 (planes 0, 1); or
-// fp32 (plane p: elements 4p .. 4p+3), which is cut into three bf16 that add up to it exactly:
-// its 24 significant bits, eight at a time.
-enum : int { kOne = 1, kTwo = 2, kF32 = 3 };
-
-// Planes of 16 bytes per 8 elements.
-constexpr int planes_of(int kind) { return kind == kOne ? 1 : 2; }
-
-// The three terms of eight fp32 values, each as eight bf16.
-__device__ __forceinline__ void cut_f32(const v4i p[2], v4i term[3]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t t[3][2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float v = __uint_as_float((uint32_t)p[q >> 1][2 * (q & 1) + e]);
-#pragma unroll
-      for (int n = 0; n < 3; ++n) {
-        t[n][e] = __float_as_uint(v) & 0xFFFF0000u;
-        v -= __uint_as_float(t[n][e]);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < 3; ++n) term[n][q] = (int)__builtin_amdgcn_perm(t[n][1], t[n][0], 0x07060302u);
-  }
-}
+// What the fragments hold of an element: a bf16 (rows of X), or the two or three bf16 that add up to a
+// hidden value, 16 or all 24 of its significant bits, a plane of 16 bytes per 8 elements each.
+enum : int { kOne = 1, kTwo = 2, kThree = 3 };
 
 template <int MT, int KIND>
 struct XWide {
-  v4i f[4][4][MT][planes_of(KIND)];          // step, MFMA, row tile, plane
-
-  // The terms of a fragment, the smallest last.
-  static constexpr int kTerms = KIND;
-  __device__ __forceinline__ void terms(int u, int j, int m, v4i t[KIND]) const {
-    if (KIND == kF32) {
-      // cut anew for every use: kept, the terms of a chunk would take 192 registers
-      v4i p[2] = {f[u][j][m][0], f[u][j][m][planes_of(KIND) - 1]}, c[3];
-      asm volatile("" : "+v"(p[0]), "+v"(p[1]));
-      cut_f32(p, c);
-#pragma unroll
-      for (int n = 0; n < KIND; ++n) t[n] = c[n];
-    } else {
-#pragma unroll
-      for (int n = 0; n < KIND; ++n) t[n] = f[u][j][m][n < planes_of(KIND) ? n : 0];
-    }
-  }
+  v4i f[4][4][MT][KIND];                     // step, MFMA, row tile, plane: the smallest term last
 
   __device__ __forceinline__ void mma(const v4i w[4], uint32_t ws, v4f* acc, int stride) const {
 #pragma unroll
@@ -240,12 +201,9 @@ struct XWide {
         fp4::decode8_bf16((uint32_t)w[u][j], s, d);
         const v4i dv = {(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          v4i t[KIND];
-          terms(u, j, m, t);
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int p = KIND - 1; p >= 0; --p) acc[m * stride] = mma_bf16(dv, t[p], acc[m * stride]);
-        }
+          for (int p = KIND - 1; p >= 0; --p) acc[m * stride] = mma_bf16(dv, f[u][j][m][p], acc[m * stride]);
       }
     }
   }
@@ -286,22 +244,6 @@ struct XWide {
     for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[u][j][m][0] = lds16(lds + 1024u * i + 16u * ((16u * g + 4u * u + j) ^ i), 0);
-  }
-};
-
-template <int MT>
-struct XFp4 {
-  v4i f[4][MT];                              // step, row tile
-  uint32_t s[MT];
-
-  __device__ __forceinline__ void mma(const v4i w[4], uint32_t ws, v4f* acc, int stride) const {
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      acc[m * stride] = mma_fp4<0>(w[0], ws, f[0][m], s[m], acc[m * stride]);
-      acc[m * stride] = mma_fp4<1>(w[1], ws, f[1][m], s[m], acc[m * stride]);
-      acc[m * stride] = mma_fp4<2>(w[2], ws, f[2][m], s[m], acc[m * stride]);
-      acc[m * stride] = mma_fp4<3>(w[3], ws, f[3][m], s[m], acc[m * stride]);
-    }
   }
 };
 
@@ -384,143 +326,15 @@ __device__ __forceinline__ void stream(Run run, int wave, int lane, bool s_words
   }
 }
 
-// The stream with X in bf16 staged in a place of its own behind the ring (16 KiB a wave, so one
-// workgroup a CU): while a chunk's items are multiplied, the next chunk's are on their way and so
-// is its first 16-row tile of X.  X is asked for before the items that need it.
-//   DMA        rows of whole 16-byte pieces: 16 loads a tile, and an item's scales in whole words
-//              (five loads), so what is behind X can be counted
-//   otherwise  through registers, row by row (1 KiB a load), any alignment and length
-// 16 x 4096 x 4096 takes 5.3 us so, and 8.0 with fragment-shaped loads straight into registers.
-constexpr int kStagedLds = kWaveLds + 16384;
-
-// The rows of a 16-row tile of X: `row` is the lane's (i), K its length.
-template <bool DMA, int MT>
-struct XStage {
-  const uint8_t* row[MT];
-  int K, lane;
-  uint32_t at;                               // this wave's place in LDS
-  v4i raw[DMA ? 1 : 16];                     // the tile on its way, row r's piece of the lane
-
-  __device__ __forceinline__ const uint8_t* row_of(int m, int r) const {
-    const uint64_t p = (uint64_t)(uintptr_t)row[m];
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)p, r);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(p >> 32), r);
-    return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
-  }
-
-  template <int M>
-  __device__ __forceinline__ void ask(int c) {
-    const int left = min(K - kChunk * c, kChunk);
-    if (DMA) {
-#pragma unroll 1
-      for (int r = 0; r < 16; ++r)
-        dma16((uint32_t)(uintptr_t)(lds_ptr_t)smem + at + 1024 * r, 16u * (uint32_t)(lane ^ r),
-              rsrc_of((uint64_t)(uintptr_t)row_of(M, r) + 1024u * (uint64_t)c, 2u * (uint32_t)left));
-    } else {
-      const int k = 8 * lane;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const uint8_t* p = row_of(M, r) + 1024 * (int64_t)c;
-        v4i v = {0, 0, 0, 0};
-        // the piece that the row's end cuts is read from the last 8 elements
-        if (k < left && K >= 8) __builtin_memcpy(&v, p + 2 * min(k, left - 8), 16);
-        if (K < 8 && lane == 0) {
-#pragma unroll
-          for (int e = 0; e < 7; ++e)
-            if (e < K) v[e >> 1] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1)));
-        }
-        raw[DMA ? 0 : r] = v;
-      }
-    }
-  }
-
-  template <int M, typename X>
-  __device__ __forceinline__ void take(X& x, int c) {
-    if (!DMA) {
-      const int left = K - kChunk * c, k = 8 * lane;
-      const int cut = K >= 8 && k < left ? max(k + 8 - left, 0) : 0;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        v4i v = raw[DMA ? 0 : r];
-        if (left < kChunk) v = drop_low(v, cut);
-        *reinterpret_cast<v4i*>(smem + at + 1024 * r + 16 * (lane ^ r)) = v;
-      }
-      wait_vm<0>();                          // with the tile, everything asked for before it
-      reads_done();
-    }
-    x.read_staged(M, at, lane);
-    reads_done();
-  }
-};
-
-template <bool DMA, int MT, int NTW, typename Issue, typename Scales>
-__device__ __forceinline__ void stream_staged(Run run, int wave, int lane, XStage<DMA, MT>& xs, Issue issue, Scales scales_of,
-                                              v4f acc[MT][NTW]) {
-  static_assert(NTW <= kRing && MT <= 2, "a chunk's items are in flight together");
-  const uint32_t ring = (uint32_t)wave * kStagedLds;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)smem + ring;
-  if (run.it0 >= run.it1) return;
-  int n = 0;                                             // slot of the next item
-  xs.template ask<0>(run.it0 / NTW);
-  fill_ring<NTW>(run.it0, run.it1, lds0, issue);
-  int behind = min(kRing, run.it1 - run.it0);            // items asked for after the tile of X
-  for (int c = run.it0 / NTW; c * NTW < run.it1; ++c) {
-    const int lo = max(run.it0 - c * NTW, 0), hi = min(run.it1 - c * NTW, NTW);
-    XWide<MT, 1> x;
-    if (DMA) {
-      if (behind >= 4) wait_vm<20>();
-      else if (behind == 3) wait_vm<15>();
-      else if (behind == 2) wait_vm<10>();
-      else if (behind == 1) wait_vm<5>();
-      else wait_vm<0>();
-      asm volatile("" ::: "memory");
-    }
-    xs.template take<0>(x, c);
-    if constexpr (MT == 2) {
-      xs.template ask<1>(c);
-      if (DMA) {
-        wait_vm<0>();
-        asm volatile("" ::: "memory");
-      }
-      xs.template take<1>(x, c);
-    }
-    const bool next = (c + 1) * NTW < run.it1;
-    if (next) xs.template ask<0>(c + 1);
-    behind = 0;
-    if (DMA && MT == 1) {                                // this chunk's items, asked for before
-      if (next) wait_vm<16>();
-      else wait_vm<0>();
-      asm volatile("" ::: "memory");
-    }
-#pragma unroll
-    for (int t = 0; t < NTW; ++t) {
-      if (t < lo || t >= hi) continue;
-      const int it = c * NTW + t;
-      const uint32_t slot = ring + n * kSlot;
-      v4i w[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] = item_codes(slot, lane, u);
-      const uint32_t ws = scales_of(t, c, slot);
-      reads_done();
-      if (it + kRing < run.it1) {
-        issue((int)((uint32_t)(it + kRing) % NTW), (int)((uint32_t)(it + kRing) / NTW), lds0 + n * kSlot);
-        ++behind;
-      }
-      n = (n + 1) % kRing;
-      x.mma(w, ws, &acc[0][t], NTW);
-    }
-  }
-}
-
 // The waves' sums side by side in LDS: wave w's value of X row m, W row n is at [w][m][n], rows
 // of 16 * NTW + 4 floats.
 template <int NTW>
 constexpr int part_row() { return 16 * NTW + 4; }
 template <int MT, int NTW>
 constexpr int part_wave() { return 16 * MT * part_row<NTW>(); }
-template <int MT, int NTW, int WAVE_LDS = kWaveLds>
+template <int MT, int NTW>
 constexpr int stream_lds() {
-  return part_wave<MT, NTW>() * 4 > WAVE_LDS ? kWaves * part_wave<MT, NTW>() * 4 : kWaves * WAVE_LDS;
+  return part_wave<MT, NTW>() * 4 > kWaveLds ? kWaves * part_wave<MT, NTW>() * 4 : kWaves * kWaveLds;
 }
 
 template <int MT, int NTW>

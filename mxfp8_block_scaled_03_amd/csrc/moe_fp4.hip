@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
       if (m0 + m >= cnt || i0 + c >= a.I) continue;
       const float share = a.share[s_row[m0 + m]];
       const int k = i0 + c;
-      uint8_t* dst = a.h + (((int64_t)slot * a.mt_cap + m0 / 16) * chunks) * kHiddenChunk + h_offset(m, k);
+      uint8_t* dst = a.h + (((int64_t)slot * a.mt_cap + m0 / 16) * chunks) * hidden_chunk(KIND) + h_offset<KIND>(m, k);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const v4f gt = sum_part<1, NTW>(m, c + 4 * hf), u = sum_part<1, NTW>(m, IC + c + 4 * hf);
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_down(const MoeArgs a) {
       __syncthreads();
       fill_ring<NTW>(run.it0, run.it1, lds0, issue);
     }
-    const uint8_t* h = a.h + ((int64_t)slot * a.mt_cap + m0 / 16) * chunks * kHiddenChunk + 16 * lane;
+    const uint8_t* h = a.h + ((int64_t)slot * a.mt_cap + m0 / 16) * chunks * hidden_chunk(KIND) + 16 * lane;
     v4f acc[1][NTW];
 #pragma unroll
     for (int n = 0; n < NTW; ++n) acc[0][n] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -239,14 +239,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_down(const MoeArgs a) {
 #pragma unroll
           for (int u = 0; u < 4; ++u)
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+            for (int p = 0; p < KIND; ++p)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 // rows past the last token and elements past I have nothing in h
                 const int k = kChunk * c + 32 * (4 * (lane >> 4) + u) + 8 * j;
                 v4i v = {0, 0, 0, 0};
                 if (k < a.I && m0 + i < cnt)
-                  v = *reinterpret_cast<const v4i*>(h + (((int64_t)4 * c + u) * 2 + p) * 4096 + 1024 * j);
+                  v = *reinterpret_cast<const v4i*>(h + (((int64_t)4 * c + u) * KIND + p) * 4096 + 1024 * j);
                 x.f[u][j][0][p] = v;
               }
         },
@@ -311,12 +311,13 @@ double active_experts(int64_t T, int64_t E, int64_t k) { return E * (1.0 - pow(1
 // row tiles each, or by the persistent ones of moe_fp4_wide.hip with K in `parts` ranges.  The
 // estimates, in us, are fits to runs on 256 CUs:
 //   this file  rounds of two workgroups a CU, each 6 us and, per row tile and chunk, 0.33 us going up
-//              and 0.4 down (1.2 where h is cut from fp32), or the weights at 4.3 TB/s
-//   persistent rounds of one work a CU, 3.5 us a chunk and 8 us going up, 4.3 (9.2) a chunk and 6 us
-//              down, 0.3 us more for every range after the first, or the weights at 5.2 TB/s
+//              and 0.4 down (0.6 for three terms of h), or the weights at 4.3 TB/s
+//   persistent rounds of one work a CU, 3.5 us a chunk and 8 us going up, 4.3 a chunk and 6 us down (5
+//              and 12 for three terms), 0.3 us more for every range after the first, or the weights at
+//              5.2 TB/s
 // Measured, this file's against the persistent ones': up 133 and 122 us (64 tokens, 64 experts of
-// 4096 x 2048), 80 and 71 (16, 8 of 5120 x 8192); down 74 and 76, 58 and 46; 46 and 34 (7 tokens, 60
-// experts of 2000 x 1064, y in fp32).
+// 4096 x 2048), 80 and 71 (16, 8 of 5120 x 8192); down 74 and 76, 58 and 46; with y in fp32 10.8 and
+// 18.4 (30 tokens, 32 experts of 1000 x 500).
 struct Way {
   bool wide;
   int tiles, parts;
@@ -327,15 +328,15 @@ Way way_of(double experts, int64_t rows, int64_t K, bool up, bool f32) {
   const double cus = device_cu_count(), mb = experts * rows * K * 17 / 32 * 1e-6;
   const int64_t chunks = (K + kChunk - 1) / kChunk;
   Way best{false, 8, 1, 1e30};
-  for (int t = 8; t >= 2; t /= 2) {
+  for (int t = f32 && !up ? 2 : 8; t >= 2; t /= 2) {   // three terms of h leave registers for two row tiles
     const double rounds = ceil(experts * ceil((double)rows / (16 * t)) / (2 * cus));
-    const double us = fmax(rounds * (6 + (up ? 0.33 : f32 ? 1.2 : 0.4) * t * chunks), mb / 4.3);
+    const double us = fmax(rounds * (6 + (up ? 0.33 : f32 ? 0.6 : 0.4) * t * chunks), mb / 4.3);
     if (us < best.us) best = Way{false, t, 1, us};
   }
   const double works = experts * ceil((double)rows / 256);
   for (int p = 1; p <= (up ? 1 : 8) && p <= chunks; p *= 2) {
-    const double chunk = up ? 3.5 : f32 ? 9.2 : 4.3;
-    const double us = fmax(ceil(works * p / cus) * ((chunks + p - 1) / p) * chunk, mb / 5.2) + (up ? 8 : 6) + 0.3 * (p - 1);
+    const double chunk = up ? 3.5 : f32 ? 5.0 : 4.3;
+    const double us = fmax(ceil(works * p / cus) * ((chunks + p - 1) / p) * chunk, mb / 5.2) + (up ? 8 : f32 ? 12 : 6) + 0.3 * (p - 1);
     if (us < best.us) best = Way{true, 8, p, us};
   }
   return best;
@@ -367,7 +368,8 @@ hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
   if (wide)
     e = launch_moe_down_wide<KIND>(d, st);
   else
-    e = nd == 8 ? launch_down<8, KIND>(d, st) : nd == 4 ? launch_down<4, KIND>(d, st) : launch_down<2, KIND>(d, st);
+    e = KIND == kTwo && nd == 8 ? launch_down<8, kTwo>(d, st)
+        : KIND == kTwo && nd == 4 ? launch_down<4, kTwo>(d, st) : launch_down<2, KIND>(d, st);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), dim3(256), 0, st, d);
   return hipGetLastError();
@@ -376,7 +378,7 @@ hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Slots: one per expert, or, where the tokens can choose fewer, one per token and rank.
-void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int parts, MoeArgs* a, int64_t off[5],
+void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int kind, int parts, MoeArgs* a, int64_t off[5],
                 int64_t* total) {
   a->by_token = T * k < E;
   a->slots = (int)(a->by_token ? T * k : E);
@@ -386,7 +388,7 @@ void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int parts
   off[1] = up256(T * k * 4);
   off[2] = off[1] + up256(T * k * 4);
   off[3] = off[2] + up256(E * T * 2);
-  off[4] = off[3] + (int64_t)a->slots * a->mt_cap * chunks * kHiddenChunk;
+  off[4] = off[3] + (int64_t)a->slots * a->mt_cap * chunks * hidden_chunk(kind);
   *total = off[4] + up256(T * k * parts * H * 4);
 }
 
@@ -395,7 +397,7 @@ void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int parts
 int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16) {
   MoeArgs a{};
   int64_t off[5], total;
-  moe_layout(T, H, I, E, k, plan_of(T, H, I, E, k, !y_bf16).down.parts, &a, off, &total);
+  moe_layout(T, H, I, E, k, y_bf16 ? kTwo : kThree, plan_of(T, H, I, E, k, !y_bf16).down.parts, &a, off, &total);
   return total;
 }
 
@@ -403,7 +405,7 @@ hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   MoeArgs a{};
   int64_t off[5], total;
   const Plan plan = plan_of(p.T, p.H, p.I, p.E, p.k, !p.y_bf16);
-  moe_layout(p.T, p.H, p.I, p.E, p.k, plan.down.parts, &a, off, &total);
+  moe_layout(p.T, p.H, p.I, p.E, p.k, p.y_bf16 ? kTwo : kThree, plan.down.parts, &a, off, &total);
   a.T = (int)p.T;
   a.H = (int)p.H;
   a.I = (int)p.I;
@@ -440,7 +442,7 @@ hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   a.y = p.y;
   a.ld_y = p.ld_y;
   a.y_bf16 = p.y_bf16;
-  return p.y_bf16 ? launch_all<kTwo>(a, plan, st) : launch_all<kF32>(a, plan, st);
+  return p.y_bf16 ? launch_all<kTwo>(a, plan, st) : launch_all<kThree>(a, plan, st);
 }
 
 }  // namespace mxq

@@ -24,7 +24,7 @@ struct MoeArgs {
   int* chosen;                         // [T][k]: expert, or -1
   float* share;                        // [T][k]
   int16_t* rank;                       // [E][T]: rank of the expert for the token, or -1
-  uint8_t* h;                          // [slots][mt_cap][chunks][4][2][4][64][16 bytes]
+  uint8_t* h;                          // [slots][mt_cap][chunks][4 steps][planes][4][64][16 bytes]
   int parts;                           // K ranges of the down product
   float* part;                         // [T * k][parts][H]
   void* y;
@@ -41,35 +41,37 @@ __device__ __forceinline__ uint32_t order_key(float l) {
   return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-// The hidden values go from one product to the next in the second one's fragment order and in 32
-// bits each, two planes of 16 bytes per 8 elements (XWide): as two bf16 terms, 16 bits, where y is bf16
-// (its own rounding is 2^-8), or as fp32.  kHiddenChunk: bytes of 16 rows x one chunk.
-constexpr int kHiddenChunk = 32768;
+// The hidden values go from one product to the next in the second one's fragment order, as bf16 terms
+// that the matrix cores take as they are, a plane of 16 bytes per 8 elements each (XWide): two terms,
+// 16 bits, where y is bf16 (its own rounding is 2^-8), or three, all 24 bits, where it is fp32 (cut
+// from fp32 in the down product instead, once per wave and use, they took 34 us against 27: 7 tokens,
+// 60 experts of 2000 x 1064).  Bytes of 16 rows x one chunk:
+constexpr int hidden_chunk(int kind) { return 16384 * kind; }
 
 // Byte offset in a 16-row tile of h of the 16 bytes of plane 0 that hold row m's elements k .. k+7.
+template <int KIND>
 __device__ __forceinline__ int64_t h_offset(int m, int k) {
   const int c = k / kChunk, b = (k % kChunk) / 32;       // block b = 4 g + u of the chunk
-  return ((int64_t)(4 * c + b % 4) * 8 + (k % 32) / 8) * 1024 + (16 * (b / 4) + m) * 16;
+  return ((int64_t)(4 * c + b % 4) * (4 * KIND) + (k % 32) / 8) * 1024 + (16 * (b / 4) + m) * 16;
 }
 
-// Four hidden values, elements 4 half .. 4 half + 3 of the eight at `to` (plane 0).
+// Four hidden values, elements 4 half .. 4 half + 3 of the eight at `to` (plane 0).  The terms are
+// rounded to nearest, so each is exact to 2^-9 of the one before; an infinity has no further term.
 template <int KIND>
 __device__ __forceinline__ void store_hidden(uint8_t* to, int half, const float v[4]) {
-  if (KIND == kF32) {
-    *reinterpret_cast<uint4*>(to + 4096 * half) =
-        make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-  } else {
-    uint32_t t[2][4];
+  uint32_t t[KIND][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      t[0][e] = f32_to_bf16_rne(v[e]);
-      const bool inf = (t[0][e] & 0x7F80u) == 0x7F80u;
-      t[1][e] = inf ? 0u : f32_to_bf16_rne(v[e] - __uint_as_float(t[0][e] << 16));
+  for (int e = 0; e < 4; ++e) {
+    float rest = v[e];
+#pragma unroll
+    for (int p = 0; p < KIND; ++p) {
+      t[p][e] = f32_to_bf16_rne(rest);
+      rest = (t[p][e] & 0x7F80u) == 0x7F80u ? 0.0f : rest - __uint_as_float(t[p][e] << 16);
     }
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-      *reinterpret_cast<uint2*>(to + 4096 * p + 8 * half) = make_uint2(t[p][0] | (t[p][1] << 16), t[p][2] | (t[p][3] << 16));
   }
+#pragma unroll
+  for (int p = 0; p < KIND; ++p)
+    *reinterpret_cast<uint2*>(to + 4096 * p + 8 * half) = make_uint2(t[p][0] | (t[p][1] << 16), t[p][2] | (t[p][3] << 16));
 }
 
 // Share times the gated value of one hidden element, SiLU in fp32.

@@ -26,14 +26,19 @@ namespace wide {
 
 constexpr int kW = 8;                        // waves
 constexpr int kT = 64 * kW;
-constexpr int kRingW = 3;
+constexpr int kRingW = 3;                    // slots going up, and down with hidden values of two terms
 constexpr int kCodes = 4096;                 // bytes of an item's codes
-constexpr int kRingBytes = kW * kRingW * kCodes;
-constexpr int kStage = 16384;                // bytes of X per stage
+constexpr int kStage = 16384;                // bytes of X per stage going up
 constexpr int kDownStages = 3;
-// LDS of the two kernels: ring, X stages, scales, works
-constexpr int kUpX = kRingBytes, kUpScales = kUpX + 2 * kStage, kUpLds = kUpScales + kW * 2048;
-constexpr int kDownX = kRingBytes, kDownScales = kDownX + kDownStages * kStage, kDownLds = kDownScales + kW * 1024;
+// LDS of the two kernels: ring, X stages, scales, works.  A stage going down is half a chunk of h; three
+// terms leave room for two slots of the ring.
+constexpr int ring_slots(int kind) { return kind == kThree ? 2 : kRingW; }
+constexpr int down_stage(int kind) { return hidden_chunk(kind) / 2; }
+constexpr int kUpX = kW * kRingW * kCodes, kUpScales = kUpX + 2 * kStage, kUpLds = kUpScales + kW * 2048;
+constexpr int down_x(int kind) { return kW * ring_slots(kind) * kCodes; }
+constexpr int down_scales(int kind) { return down_x(kind) + kDownStages * down_stage(kind); }
+constexpr int down_lds(int kind) { return down_scales(kind) + kW * 1024; }
+static_assert(down_lds(kTwo) + 4096 <= 160 * 1024 && down_lds(kThree) + 4096 <= 160 * 1024, "LDS of a CU");
 
 // The run of works of this workgroup, and where a work lies: s_end[s] is the number of works of
 // slots 0 .. s.  A slot's works: its 16-token tiles, of each its K ranges, of each its columns.
@@ -306,18 +311,18 @@ __global__ __launch_bounds__(kT, 1) void k_moe_up_wide(const MoeArgs a) {
       float v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = col + q < a.I ? gated(share, acc[0][q], acc[1][q]) : 0.0f;
-      store_hidden<KIND>(a.h + ((int64_t)p.slot * a.mt_cap + p.m) * h_chunks * kHiddenChunk + h_offset(i, col & ~7), (col >> 2) & 1, v);
+      store_hidden<KIND>(a.h + ((int64_t)p.slot * a.mt_cap + p.m) * h_chunks * hidden_chunk(KIND) + h_offset<KIND>(i, col & ~7), (col >> 2) & 1, v);
     }
   }
   landed<0>();                                           // no load may land after the workgroup
 }
 
-// ---- down.  A stage is half a chunk of h (steps 0, 1 or 2, 3): 16 KiB, in the
-// order in which it lies in memory.
+// ---- down.  A stage is half a chunk of h (steps 0, 1 or 2, 3) in the order in which it lies in
+// memory.
 template <int KIND>
 __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
-  constexpr int GROUP = 2;
-  int* s_end = reinterpret_cast<int*>(smem + kDownLds);
+  constexpr int GROUP = 2, RING = ring_slots(KIND), STAGE = down_stage(KIND), LOADS = STAGE / (1024 * kW);   // a wave's loads a stage
+  int* s_end = reinterpret_cast<int*>(smem + down_lds(KIND));
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = uniform(threadIdx.x >> 6);
   const int total = count_works(a, a.tiles * a.parts, s_end, lane, wave);
@@ -326,7 +331,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
   if (w0 >= w1) return;
   const Works works{s_end, a.tiles, a.parts};
   const int nb = (a.I + 31) / 32, chunks = (a.I + kChunk - 1) / kChunk;
-  const uint32_t ring = (uint32_t)wave * (kRingW * kCodes), my_scales = kDownScales + (uint32_t)wave * 1024;
+  const uint32_t ring = (uint32_t)wave * (RING * kCodes), my_scales = down_scales(KIND) + (uint32_t)wave * 1024;
   const uint32_t lds = (uint32_t)(uintptr_t)(lds_ptr_t)smem;
   const ItemOffsets wo = item_offsets((uint32_t)a.ld_w2, (uint32_t)a.ld_s2, lane);
 
@@ -347,7 +352,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
   };
   auto feed = [&]() {
     issue_codes(f, wo, lds + ring);
-    f.n = f.n + 1 == kRingW ? 0 : f.n + 1;
+    f.n = f.n + 1 == RING ? 0 : f.n + 1;
     f.t ^= 1;
     if (f.t == 0 && ++f.c == f.c1) feed_work(f.live ? f.p.w + 1 : w1);
   };
@@ -374,13 +379,13 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
         seek(xp, works, xw);
         xs = 2 * (chunks * xp.part / a.parts);
         xs1 = 2 * (chunks * (xp.part + 1) / a.parts);
-        xat = (uint64_t)(uintptr_t)a.h + ((uint64_t)xp.slot * a.mt_cap + xp.m) * (uint64_t)chunks * kHiddenChunk;
+        xat = (uint64_t)(uintptr_t)a.h + ((uint64_t)xp.slot * a.mt_cap + xp.m) * (uint64_t)chunks * hidden_chunk(KIND);
       }
     }
-    const v4i rs = rsrc_of(xat + (uint64_t)xs * kStage, xw < w1 ? (uint32_t)kStage : 0u);
-    const uint32_t to = lds + kDownX + xn * kStage;
+    const v4i rs = rsrc_of(xat + (uint64_t)xs * STAGE, xw < w1 ? (uint32_t)STAGE : 0u);
+    const uint32_t to = lds + down_x(KIND) + xn * STAGE;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) dma16(to + 2048 * wave + 1024 * r, (uint32_t)(2048 * wave + 1024 * r + 16 * lane), rs);
+    for (int r = 0; r < LOADS; ++r) dma16(to + 1024 * (LOADS * wave + r), (uint32_t)(1024 * (LOADS * wave + r) + 16 * lane), rs);
     if (xw < w1) ++xs;
     xn = xn + 1 == kDownStages ? 0 : xn + 1;
   };
@@ -391,9 +396,8 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
   scales();
   stage();
   stage();
-  feed();
-  feed();
-  feed();
+#pragma unroll
+  for (int r = 0; r < RING; ++r) feed();
   landed<0>();
   meet();
   Pos p{0, 0, 0, 0, 0};
@@ -412,15 +416,15 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
       const bool begins = (c - c0) % GROUP == 0;
 #pragma unroll
       for (int hs = 0; hs < 2; ++hs) {
-        v4i x[2][4][2];
-        const uint32_t from = kDownX + xbuf * kStage + 16 * lane;
+        v4i x[2][4][KIND];
+        const uint32_t from = down_x(KIND) + xbuf * STAGE + 16 * lane;
         xbuf = xbuf + 1 == kDownStages ? 0 : xbuf + 1;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < KIND; ++q)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[u][j][q] = lds16(from, ((u * 2 + q) * 4 + j) * 1024);
+            for (int j = 0; j < 4; ++j) x[u][j][q] = lds16(from, ((u * KIND + q) * 4 + j) * 1024);
         if (kChunk * (c + 1) > a.I) {                    // h has nothing at k >= I
 #pragma unroll
           for (int u = 0; u < 2; ++u)
@@ -428,7 +432,7 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
             for (int j = 0; j < 4; ++j)
               if (kChunk * c + 32 * (4 * g + 2 * hs + u) + 8 * j >= a.I) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) x[u][j][q] = v4i{0, 0, 0, 0};
+                for (int q = 0; q < KIND; ++q) x[u][j][q] = v4i{0, 0, 0, 0};
               }
         }
         if (hs == 0 && begins) {
@@ -440,11 +444,13 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (hs == 0) {
-            // behind the item: two items and four stages (t = 0), or two items and two stages
-            if (t == 0) landed<16>();
-            else landed<12>();
+            // behind the item, with three slots: two items and four stages (t = 0), or two items and
+            // two stages; with two slots: one item and two stages
+            if (RING == 2) landed<4 + 2 * LOADS>();
+            else if (t == 0) landed<8 + 4 * LOADS>();
+            else landed<8 + 2 * LOADS>();
             const uint32_t at = ring + slot * kCodes;
-            slot = slot + 1 == kRingW ? 0 : slot + 1;
+            slot = slot + 1 == RING ? 0 : slot + 1;
 #pragma unroll
             for (int u = 0; u < 4; ++u) wf[t][u] = item_codes(at, lane, u);
             ws[t] = sg[t][0];
@@ -461,20 +467,13 @@ __global__ __launch_bounds__(kT, 1) void k_moe_down_wide(const MoeArgs a) {
               uint32_t d[4];
               fp4::decode8_bf16((uint32_t)wf[t][2 * hs + u][j], s, d);
               const v4i dv = {(int)d[0], (int)d[1], (int)d[2], (int)d[3]};
-              if (KIND == kF32) {
-                v4i c3[3];
-                cut_f32(x[u][j], c3);
 #pragma unroll
-                for (int q = 2; q >= 0; --q) acc[t] = mma_bf16(dv, c3[q], acc[t]);
-              } else {
-#pragma unroll
-                for (int q = 1; q >= 0; --q) acc[t] = mma_bf16(dv, x[u][j][q], acc[t]);
-              }
+              for (int q = KIND - 1; q >= 0; --q) acc[t] = mma_bf16(dv, x[u][j][q], acc[t]);
             }
           }
         }
         // the next stage: behind it one stage and two items
-        landed<10>();
+        landed<8 + LOADS>();
         meet();
       }
     }
@@ -514,7 +513,7 @@ hipError_t launch_moe_up_wide(const MoeArgs& args, hipStream_t st) {
 }
 
 template hipError_t launch_moe_up_wide<kTwo>(const MoeArgs&, hipStream_t);
-template hipError_t launch_moe_up_wide<kF32>(const MoeArgs&, hipStream_t);
+template hipError_t launch_moe_up_wide<kThree>(const MoeArgs&, hipStream_t);
 
 template <int KIND>
 hipError_t launch_moe_down_wide(const MoeArgs& args, hipStream_t st) {
@@ -522,7 +521,7 @@ hipError_t launch_moe_down_wide(const MoeArgs& args, hipStream_t st) {
   MoeArgs a = args;
   a.tiles = (a.H + 255) / 256;
   auto kern = wide::k_moe_down_wide<KIND>;
-  constexpr int lds = wide::kDownLds;
+  constexpr int lds = wide::down_lds(KIND);
   const hipError_t e = allow_lds(kern, lds + 4 * 1024, set);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)device_cu_count()), dim3(wide::kT), lds + 4 * a.slots, st, a);
@@ -530,6 +529,6 @@ hipError_t launch_moe_down_wide(const MoeArgs& args, hipStream_t st) {
 }
 
 template hipError_t launch_moe_down_wide<kTwo>(const MoeArgs&, hipStream_t);
-template hipError_t launch_moe_down_wide<kF32>(const MoeArgs&, hipStream_t);
+template hipError_t launch_moe_down_wide<kThree>(const MoeArgs&, hipStream_t);
 
 }  // namespace mxq
