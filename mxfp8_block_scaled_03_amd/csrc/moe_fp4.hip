@@ -5,12 +5,13 @@
 //   h = share * silu(x W1_e) * (x W3_e)      (gate rows [0, I) and up rows [I, 2I) of w13[e])
 //   y = sum over the token's experts, in the order of their rank, of h W2_e
 //
-// Four launches: k_moe_route (ranks and shares, one wave a token), k_moe_up (gate and up
-// products, h), k_moe_down (down products, one partial row per token and expert), k_moe_sum
-// (the sum of a token's rows).  The weights of every expert that a token chose are read once
-// and bound the time (fp4_stream.hpp); everything else is kept out of their way: a workgroup
-// finds the tokens of its expert with one ballot, h goes to memory in the fragment order that
-// k_moe_down reads, and the workgroups of experts that nobody chose end at once.
+// Where hardly an expert has two tokens: two launches (moe_fp4_few.hip).  Otherwise four:
+// k_moe_route (ranks and shares, one wave a token), k_moe_up (gate and up products, h),
+// k_moe_down (down products, one partial row per token and expert), k_moe_sum (the sum of a
+// token's rows).  The weights of every expert that a token chose are read once and bound the
+// time (fp4_stream.hpp); everything else is kept out of their way: a workgroup finds the tokens
+// of its expert with one ballot, h goes to memory in the fragment order that k_moe_down reads, and
+// the workgroups of experts that nobody chose end at once.
 //
 // An expert with logit -inf is never taken: its share is zero, and a token whose logits are
 // all -inf gets y = 0.  NaN logits order above +inf; their shares are NaN, as softmax's.
@@ -342,17 +343,26 @@ Way way_of(double experts, int64_t rows, int64_t K, bool up, bool f32) {
   return best;
 }
 
+// The two launches of moe_fp4_few.hip read an expert's weights once for every token that chose it, the
+// four here and in moe_fp4_wide.hip once, but these cost 12 us of routing, adding up and launching, and the
+// estimates above are low for few tokens.  Measured, two launches' kernels against four: 23 and 38 us (1
+// token, 4 of 64 experts of 4096 x 2048), 83 and 131 (8 tokens), 160 and 212 (16); 47 and 70 (7, 6 of 60,
+// 2000 x 1064, y in fp32); 12 and 24 (2, 2 of 32, 1000 x 700).
 struct Plan {
   Way up, down;
+  bool few;
 };
 
 Plan plan_of(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool f32) {
   const double experts = active_experts(T, E, k);
-  return Plan{way_of(experts, 2 * I, H, true, f32), way_of(experts, H, I, false, f32)};
+  Plan p{way_of(experts, 2 * I, H, true, f32), way_of(experts, H, I, false, f32), false};
+  p.few = moe_few_us(T, H, I, E, k) < 1.2 * (p.up.us + p.down.us) + 12;
+  return p;
 }
 
 template <int KIND>
 hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
+  if (plan.few) return launch_moe_few(a, st);
   hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -397,7 +407,9 @@ void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int kind,
 int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16) {
   MoeArgs a{};
   int64_t off[5], total;
-  moe_layout(T, H, I, E, k, y_bf16 ? kTwo : kThree, plan_of(T, H, I, E, k, !y_bf16).down.parts, &a, off, &total);
+  const Plan plan = plan_of(T, H, I, E, k, !y_bf16);
+  if (plan.few) return moe_few_bytes(T, I, k);
+  moe_layout(T, H, I, E, k, y_bf16 ? kTwo : kThree, plan.down.parts, &a, off, &total);
   return total;
 }
 
@@ -432,7 +444,7 @@ hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   a.chosen = (int*)(ws + off[0]);
   a.share = (float*)(ws + off[1]);
   a.rank = (int16_t*)(ws + off[2]);
-  a.h = ws + off[3];
+  a.h = plan.few ? ws : ws + off[3];
   a.part = (float*)(ws + off[4]);
   a.x_pieces = (uintptr_t)p.x % 16 == 0 && a.ld_x % 16 == 0;
   a.s13_words = (uintptr_t)p.s13 % 4 == 0 && p.ld_s13 % 4 == 0 && p.st_s13 % 4 == 0;

@@ -11,7 +11,7 @@ struct MoeArgs {
   int T, H, I, E, k, renorm;
   int slots, by_token;                 // by_token: slot = (token, rank), else slot = expert
   int mt_cap;                          // 16-row tiles that a slot's part of h holds
-  int tiles;                           // column tiles of a launch
+  int tiles, per;                      // column tiles of a launch; column groups of a wave (moe_fp4_few.hip)
   const uint8_t* x;
   int64_t ld_x;                        // bytes
   bool x_pieces;                       // X rows are whole 16-byte pieces
@@ -85,5 +85,11 @@ template <int KIND>
 hipError_t launch_moe_up_wide(const MoeArgs& a, hipStream_t st);
 template <int KIND>
 hipError_t launch_moe_down_wide(const MoeArgs& a, hipStream_t st);
+
+// The layer where hardly an expert has two tokens (moe_fp4_few.hip): from the logits to y, with h as its
+// only workspace.  The estimate of its time is without bound where it does not take the sizes.
+double moe_few_us(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k);
+int64_t moe_few_bytes(int64_t T, int64_t I, int64_t k);
+hipError_t launch_moe_few(const MoeArgs& a, hipStream_t st);
 
 }  // namespace mxq

@@ -330,6 +330,51 @@ def test_experts_ties_and_masks():
     run_experts(rng, 1, 64, 32, 9, 2, True, F32, [[-np.inf] * 8 + [0.0]])
 
 
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,H,I,k", [(1, 100, 40, 3), (3, 33, 129, 2), (17, 64, 24, 4), (33, 130, 65, 2), (70, 96, 200, 1),
+                                     (64, 520, 136, 4), (5, 1030, 33, 8)])
+def test_experts_of_many(out, renorm, T, H, I, k):
+    """More experts than one wave of logits takes: the kernels with a launch for routing, at small
+    odd sizes."""
+    say("moe_fp4 T%d H%d I%d k%d of 264 %s" % (T, H, I, k, out))
+    run_experts(np.random.default_rng(37), T, H, I, 264, k, renorm, out)
+
+
+@pytest.mark.parametrize("masked", [0, 260])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_experts_special_logits(masked, out):
+    """Ties, -inf, the lowest float, rows with nothing left, +inf and NaN, also among many masked experts
+    (the other kernels); masked ones stand in front, so that ties are decided far from index 0."""
+    rng = np.random.default_rng(38)
+    low = np.finfo(np.float32).min
+    lg = np.zeros((7, 6), np.float32)
+    lg[1] = [1, 2, 2, 2, 0, 2]
+    lg[2] = [-np.inf, 0, -np.inf, -np.inf, 1, -np.inf]
+    lg[3] = -np.inf
+    lg[4] = low
+    lg[5] = [-0.0, 0.0, -0.0, -1, -1, -1]
+    lg = np.concatenate([np.full((7, masked), -np.inf, np.float32), lg], 1)
+    for renorm in (True, False):
+        y = run_experts(rng, 7, 72, 40, 6 + masked, 3, renorm, out, lg)
+        assert (y[3] == 0).all()
+    w13, s13, _, w2, s2, _ = experts(rng, 6 + masked, 72, 40)
+    x, _, _ = bf16_operand(rng, 7, 72)
+    bad = torch.from_numpy(lg).to(DEV)
+    bad[0, masked + 2], bad[6, masked + 4] = float("nan"), float("inf")
+    y = mxq.moe_fp4(x, bad, w13, s13, w2, s2, 3, out_dtype=out)
+    assert torch.isnan(y[[0, 6]]).all() and torch.isfinite(y[1:6]).all()
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 4096, 264, 8, 2), (2, 2080, 2100, 5, 3), (1, 9000, 40, 4, 1), (3, 70, 4200, 6, 2),
+                                       (1, 40, 72, 256, 9), (6, 2000, 1064, 10, 1)])
+def test_experts_of_few_tokens(out, T, H, I, E, k):
+    """Rows of several 2048-element segments, in both products, and waves with several row groups."""
+    say("moe_fp4 T%d H%d I%d E%d k%d %s" % (T, H, I, E, k, out))
+    run_experts(np.random.default_rng(39), T, H, I, E, k, True, out)
+
+
 def test_experts_nan_logits():
     """A NaN logit makes its own token NaN and no other."""
     rng = np.random.default_rng(32)
