@@ -3,6 +3,8 @@ mixture-of-experts layer (the ``mxq_*_fp4`` entry points of include/mxq.h).  Arg
 and marshalling only, like ``_binding``; every call raises if the library is missing."""
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from ._binding import (_ACT, _AXIS, _RULE, MXQ_BF16, MXQ_COLWISE, MXQ_E2M1, MXQ_F32, MxqError, _req_2d,
@@ -15,7 +17,7 @@ _current = torch._C._cuda_getDevice
 _entry = {}
 
 
-def _call(name: str, device: int, *args):
+def _call(name: str, device: int, args: tuple) -> None:
     """The library's entry point `name` on torch's current stream of the device."""
     fn = _entry.get(name)
     if fn is None:
@@ -29,28 +31,33 @@ def _call(name: str, device: int, *args):
         raise MxqError(status, name)
 
 
-# These calls are short, so the checks are made in one pass over each tensor: what _req_2d
-# rejects is found with few attribute reads, and the message is left to _req_2d.
+# These calls are short, so the checks read few attributes, once each: what is wrong is found here, and
+# _req_2d says what it is.  (torch.empty_strided is the quickest of torch's allocating calls.)
+_empty = torch.empty_strided
+
 
 def _lines(t, name: str, dtype, rows, cols: int) -> int:
     """Checks rows of at least `cols` elements, `rows` of them at least; the row pitch."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 2:
-        _req_2d(t, name, dtype)
-    r, c = t.shape
-    pitch, step = t.stride()
-    if c < cols or (rows is not None and r < rows) or (r > 1 and c > 0 and (step != 1 or pitch < c)):
+    try:
+        r, c = t.shape
+        pitch, step = t.stride()
+        good = t.dtype is dtype and c >= cols and (rows is None or r >= rows)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good or (step != 1 and c > 1 and r > 0) or (pitch < c and r > 1):
         _req_2d(t, name, dtype, rows, cols)
+        raise ValueError("%s must have unit stride along its last dimension" % name)
     return pitch if r > 0 and pitch >= c else max(c, 1)
 
 
-def _on_one_device(first, *named) -> int:
+def _on_one_device(first, others: tuple, names: tuple) -> int:
     """The index of the device that holds `first` and every other tensor."""
     device = first.get_device()
-    for name, t in named:
+    for i, t in enumerate(others):
         if t is not None and t.get_device() != device and device >= 0:
             if t.get_device() < 0:
-                raise ValueError("%s must be a CUDA (HIP device) tensor, got device %s" % (name, t.device))
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, first.device))
+                raise ValueError("%s must be a CUDA (HIP device) tensor, got device %s" % (names[i], t.device))
+            raise ValueError("%s is on %s, expected %s" % (names[i], t.device, first.device))
     if device < 0:
         raise ValueError("expected CUDA (HIP device) tensors, got device %s" % first.device)
     return device
@@ -62,17 +69,13 @@ def _wide(t, name: str) -> int:
     return _lines(t, name, t.dtype, None, 0)
 
 
-def _blocks(k: int) -> int:
-    return (k + 31) // 32
-
-
 def _code_array(lines: int, k: int, device):
-    """Empty codes [lines][16 * blocks] and scales [lines][blocks], the scale rows padded to 16
-    bytes (the layout that the product reads fastest)."""
-    nb = _blocks(k)
-    pitch = (nb + 15) // 16 * 16
-    return (torch.empty((lines, 16 * nb), dtype=_U8, device=device),
-            torch.empty_strided((lines, nb), (pitch, 1), dtype=_U8, device=device))
+    """Empty codes [lines][16 * blocks] and scales [lines][blocks] and their pitches, the scale rows
+    padded to 16 bytes (the layout that the product reads fastest)."""
+    nb = (k + 31) // 32
+    wide, pitch = max(16 * nb, 1), max((nb + 15) // 16 * 16, 1)
+    return (_empty((lines, 16 * nb), (wide, 1), dtype=_U8, device=device), wide,
+            _empty((lines, nb), (pitch, 1), dtype=_U8, device=device), pitch)
 
 
 def _orient(x, axis, codes, scales):
@@ -84,16 +87,16 @@ def _orient(x, axis, codes, scales):
     L, K = x.shape
     if ax == MXQ_COLWISE:
         L, K = K, L
-    nb = _blocks(K)
+    nb = (K + 31) // 32
     ld_c = None if codes is None else _lines(codes, "codes", _U8, L, 16 * nb)
     ld_s = None if scales is None else _lines(scales, "scales", _U8, L, nb)
-    device = _on_one_device(x, ("codes", codes), ("scales", scales))
+    device = _on_one_device(x, (codes, scales), ("codes", "scales"))
     if codes is None or scales is None:
-        c, s = _code_array(L, K, x.device)
+        c, pitch_c, s, pitch_s = _code_array(L, K, x.device)
         if codes is None:
-            codes, ld_c = c, max(16 * nb, 1)
+            codes, ld_c = c, pitch_c
         if scales is None:
-            scales, ld_s = s, max((nb + 15) // 16 * 16, 1)
+            scales, ld_s = s, pitch_s
     return ld, ax, device, codes, ld_c, scales, ld_s
 
 
@@ -109,8 +112,9 @@ def quantize_fp4(x, axis="row", codes=None, scales=None, rule: str = "ceil"):
     if rule not in _RULE:
         raise ValueError("rule must be 'ceil' or 'ocp'")
     ld, ax, device, codes, ld_c, scales, ld_s = _orient(x, axis, codes, scales)
-    _call("mxq_quantize_fp4", device, x.data_ptr(), _WIDE[x.dtype], x.shape[0], x.shape[1], ld, ax, _RULE[rule],
-          codes.data_ptr(), ld_c, scales.data_ptr(), ld_s)
+    rows, cols = x.shape
+    _call("mxq_quantize_fp4", device, (x.data_ptr(), _WIDE[x.dtype], rows, cols, ld, ax, _RULE[rule],
+                                       codes.data_ptr(), ld_c, scales.data_ptr(), ld_s))
     return codes, scales
 
 
@@ -118,8 +122,9 @@ def quantize_fp4_sr(x, seed: int, axis="row", codes=None, scales=None):
     """quantize_fp4() with stochastically rounded codes (Philox4x32-10 keyed by `seed`, see
     mxq_quantize_fp4_sr): for gradients."""
     ld, ax, device, codes, ld_c, scales, ld_s = _orient(x, axis, codes, scales)
-    _call("mxq_quantize_fp4_sr", device, x.data_ptr(), _WIDE[x.dtype], x.shape[0], x.shape[1], ld, ax,
-          int(seed) & (2 ** 64 - 1), codes.data_ptr(), ld_c, scales.data_ptr(), ld_s)
+    rows, cols = x.shape
+    _call("mxq_quantize_fp4_sr", device, (x.data_ptr(), _WIDE[x.dtype], rows, cols, ld, ax, int(seed) & (2 ** 64 - 1),
+                                          codes.data_ptr(), ld_c, scales.data_ptr(), ld_s))
     return codes, scales
 
 
@@ -127,12 +132,12 @@ def quantize_fp4_dual(x):
     """Both orientations of a 2-D bf16/fp32 CUDA tensor from one read of it: (row_codes,
     row_scales, col_codes, col_scales), as quantize_fp4(x, "row") and quantize_fp4(x, "col")."""
     ld = _wide(x, "x")
-    device = _on_one_device(x)
+    device = _on_one_device(x, (), ())
     rows, cols = x.shape
-    rc, rs = _code_array(rows, cols, x.device)
-    cc, cs = _code_array(cols, rows, x.device)
-    _call("mxq_quantize_fp4_dual", device, x.data_ptr(), _WIDE[x.dtype], rows, cols, ld, rc.data_ptr(), rc.stride(0),
-          rs.data_ptr(), rs.stride(0), cc.data_ptr(), cc.stride(0), cs.data_ptr(), cs.stride(0))
+    rc, ld_rc, rs, ld_rs = _code_array(rows, cols, x.device)
+    cc, ld_cc, cs, ld_cs = _code_array(cols, rows, x.device)
+    _call("mxq_quantize_fp4_dual", device, (x.data_ptr(), _WIDE[x.dtype], rows, cols, ld, rc.data_ptr(), ld_rc,
+                                            rs.data_ptr(), ld_rs, cc.data_ptr(), ld_cc, cs.data_ptr(), ld_cs))
     return rc, rs, cc, cs
 
 
@@ -143,14 +148,15 @@ def dequantize_fp4(codes, scales, K: int, out_dtype=None):
         raise ValueError("out_dtype must be float32 or bfloat16")
     if K < 0:
         raise ValueError("K must be >= 0")
-    nb = _blocks(K)
+    nb = (K + 31) // 32
     ld_c = _lines(codes, "codes", _U8, None, 16 * nb)
     L = codes.shape[0]
     ld_s = _lines(scales, "scales", _U8, L, nb)
-    device = _on_one_device(codes, ("scales", scales))
-    dst = torch.empty((L, K), dtype=out_dtype, device=codes.device)
-    _call("mxq_dequantize_fp4", device, codes.data_ptr(), ld_c, scales.data_ptr(), ld_s, L, K, dst.data_ptr(),
-          _WIDE[out_dtype], max(K, 1))
+    device = _on_one_device(codes, (scales,), ("scales",))
+    ld = max(K, 1)
+    dst = _empty((L, K), (ld, 1), dtype=out_dtype, device=codes.device)
+    _call("mxq_dequantize_fp4", device, (codes.data_ptr(), ld_c, scales.data_ptr(), ld_s, L, K, dst.data_ptr(),
+                                         _WIDE[out_dtype], ld))
     return dst
 
 
@@ -163,7 +169,7 @@ def gemm_fp4(x, x_scales, w_codes, w_scales, K: int, alpha: float = 1.0, bias=No
     """
     if K < 0:
         raise ValueError("K must be >= 0")
-    nb = _blocks(K)
+    nb = (K + 31) // 32
     ld_w = _lines(w_codes, "w_codes", _U8, None, 16 * nb)
     N = w_codes.shape[0]
     ld_ws = _lines(w_scales, "w_scales", _U8, N, nb)
@@ -189,27 +195,45 @@ def gemm_fp4(x, x_scales, w_codes, w_scales, K: int, alpha: float = 1.0, bias=No
             raise ValueError("out must have shape (M, N) = (%d, %d), got %s" % (M, N, tuple(out.shape)))
     elif out_dtype is not None and out_dtype not in _WIDE:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    device = _on_one_device(x, ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("bias", bias),
-                            ("out", out))
+    device = _on_one_device(x, (x_scales, w_codes, w_scales, bias, out), _GEMM_NAMES)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=x.device)
-        ld_y = max(N, 1)
-    _call("mxq_gemm_fp4", device, M, N, K, x.data_ptr(), x_type, ld_x, xs_ptr, ld_xs, w_codes.data_ptr(), ld_w,
-          w_scales.data_ptr(), ld_ws, alpha, None if bias is None else bias.data_ptr(), _ACT[act], out.data_ptr(),
-          _WIDE[out.dtype], ld_y)
+        out_dtype, ld_y = out_dtype or torch.bfloat16, max(N, 1)
+        out = _empty((M, N), (ld_y, 1), dtype=out_dtype, device=x.device)
+        y_type = _WIDE[out_dtype]
+    else:
+        y_type = _WIDE[out.dtype]
+    _call("mxq_gemm_fp4", device, (M, N, K, x.data_ptr(), x_type, ld_x, xs_ptr, ld_xs, w_codes.data_ptr(), ld_w,
+                                   w_scales.data_ptr(), ld_ws, alpha, None if bias is None else bias.data_ptr(), _ACT[act],
+                                   out.data_ptr(), y_type, ld_y))
     return out
+
+
+_GEMM_NAMES = ("x_scales", "w_codes", "w_scales", "bias", "out")
+_MOE_NAMES = ("logits", "w13_codes", "w13_scales", "w2_codes", "w2_scales", "out")
 
 
 def _expert(t, name: str, experts: int, rows: int, cols: int):
     """Checks a stack of code or scale rows; the expert and row pitches."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _U8 or t.dim() != 3:
+    try:
+        e, r, c = t.shape
+        far, pitch, step = t.stride()
+        good = t.dtype is _U8
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
         raise ValueError("%s must be a 3-D uint8 tensor" % name)
-    shape, stride = t.shape, t.stride()
-    if shape[0] != experts or shape[1] != rows or shape[2] < cols:
-        raise ValueError("%s must have shape (%d, %d, >= %d), got %s" % (name, experts, rows, cols, tuple(shape)))
-    if shape[2] > 1 and stride[2] != 1:
+    if e != experts or r != rows or c < cols:
+        raise ValueError("%s must have shape (%d, %d, >= %d), got %s" % (name, experts, rows, cols, tuple(t.shape)))
+    if c > 1 and step != 1:
         raise ValueError("%s must have unit stride along its last dimension" % name)
-    return stride[0], stride[1]
+    return far, pitch
+
+
+@functools.lru_cache(maxsize=1024)
+def _moe_workspace(device: int, T: int, H: int, I: int, E: int, k: int, y_type: int) -> int:
+    """The plan, and with it the workspace, follows from the sizes and the device's CUs."""
+    with torch.cuda.device(device):
+        return mxq_moe_fp4_workspace(T, H, I, E, k, y_type)
 
 
 def moe_fp4(x, logits, w13_codes, w13_scales, w2_codes, w2_scales, k: int, renormalize: bool = True, out_dtype=None,
@@ -232,25 +256,28 @@ def moe_fp4(x, logits, w13_codes, w13_scales, w2_codes, w2_scales, k: int, renor
     I = w13_codes.shape[1] // 2
     if not 1 <= k <= E:
         raise ValueError("k must be between 1 and E = %d" % E)
-    e13, l13 = _expert(w13_codes, "w13_codes", E, 2 * I, 16 * _blocks(H))
-    es13, ls13 = _expert(w13_scales, "w13_scales", E, 2 * I, _blocks(H))
-    e2, l2 = _expert(w2_codes, "w2_codes", E, H, 16 * _blocks(I))
-    es2, ls2 = _expert(w2_scales, "w2_scales", E, H, _blocks(I))
+    nb_h, nb_i = (H + 31) // 32, (I + 31) // 32
+    e13, l13 = _expert(w13_codes, "w13_codes", E, 2 * I, 16 * nb_h)
+    es13, ls13 = _expert(w13_scales, "w13_scales", E, 2 * I, nb_h)
+    e2, l2 = _expert(w2_codes, "w2_codes", E, H, 16 * nb_i)
+    es2, ls2 = _expert(w2_scales, "w2_scales", E, H, nb_i)
     if out is not None:
         ld_y = _wide(out, "out")
         if tuple(out.shape) != (T, H):
             raise ValueError("out must have shape (T, H) = (%d, %d), got %s" % (T, H, tuple(out.shape)))
     elif out_dtype is not None and out_dtype not in _WIDE:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    device = _on_one_device(x, ("logits", logits), ("w13_codes", w13_codes), ("w13_scales", w13_scales),
-                            ("w2_codes", w2_codes), ("w2_scales", w2_scales), ("out", out))
+    device = _on_one_device(x, (logits, w13_codes, w13_scales, w2_codes, w2_scales, out), _MOE_NAMES)
     if out is None:
-        out = torch.empty((T, H), dtype=out_dtype or torch.bfloat16, device=x.device)
-        ld_y = max(H, 1)
-    y_type = _WIDE[out.dtype]
-    need = mxq_moe_fp4_workspace(T, H, I, E, k, y_type)
-    workspace = torch.empty((need,), dtype=_U8, device=x.device)
-    _call("mxq_moe_fp4", device, T, H, I, E, k, 1 if renormalize else 0, x.data_ptr(), ld_x, logits.data_ptr(), ld_l,
-          w13_codes.data_ptr(), l13, e13, w13_scales.data_ptr(), ls13, es13, w2_codes.data_ptr(), l2, e2,
-          w2_scales.data_ptr(), ls2, es2, out.data_ptr(), y_type, ld_y, workspace.data_ptr(), need)
+        out_dtype, ld_y = out_dtype or torch.bfloat16, max(H, 1)
+        out = _empty((T, H), (ld_y, 1), dtype=out_dtype, device=x.device)
+        y_type = _WIDE[out_dtype]
+    else:
+        y_type = _WIDE[out.dtype]
+    need = _moe_workspace(device, T, H, I, E, k, y_type)
+    workspace = _empty((need,), (1,), dtype=_U8, device=x.device)
+    _call("mxq_moe_fp4", device, (T, H, I, E, k, 1 if renormalize else 0, x.data_ptr(), ld_x, logits.data_ptr(), ld_l,
+                                  w13_codes.data_ptr(), l13, e13, w13_scales.data_ptr(), ls13, es13, w2_codes.data_ptr(),
+                                  l2, e2, w2_scales.data_ptr(), ls2, es2, out.data_ptr(), y_type, ld_y,
+                                  workspace.data_ptr(), need))
     return out

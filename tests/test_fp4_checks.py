@@ -168,6 +168,16 @@ def test_other_functions():
     refuses(mxq.dequantize_fp4, c, s, 70, match="CUDA")
 
 
+def test_one_row_with_steps():
+    """A single row whose elements are not neighbours."""
+    x = z(1, 160, dtype=torch.bfloat16)[:, ::2]
+    refuses(mxq.quantize_fp4, x, match="unit stride")
+    refuses(mxq.gemm_fp4, x, None, z(8, 48), z(8, 3), 80, match="unit stride")
+    refuses(mxq.dequantize_fp4, z(1, 96)[:, ::2], z(1, 3), 70, match="unit stride")
+    refuses(mxq.moe_fp4, x, z(1, 4, dtype=torch.float32), z(4, 80, 48), z(4, 80, 3), z(4, 80, 32), z(4, 80, 2), 2,
+            match="unit stride")
+
+
 def test_gemm_function():
     w, ws, xc, xs, xb = z(8, 48), z(8, 3), z(4, 48), z(4, 3), z(4, 80, dtype=torch.bfloat16)
     g = mxq.gemm_fp4
