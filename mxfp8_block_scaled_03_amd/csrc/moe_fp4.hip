@@ -22,71 +22,39 @@
 namespace mxq {
 namespace {
 
-// The rank of the lane's own expert j (key kj) in the row: how many come before it.
-__device__ __forceinline__ int rank_of(const float* row, int E, int j, uint32_t kj, int lane) {
-  int n = 0;
-  for (int i0 = 0; i0 < E; i0 += 64) {
-    const uint32_t ki = i0 + lane < E ? order_key(row[i0 + lane]) : 0u;
-#pragma unroll 16
-    for (int i = 0; i < 64; ++i) {
-      const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)ki, i);
-      n += i0 + i < E && (o > kj || (o == kj && i0 + i < j)) ? 1 : 0;
-    }
-  }
-  return n;
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
-
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
-}
-
-// ---- routing: a wave a token.  share = exp(l - max) over the sum of the chosen experts'
-// exponentials (renorm) or of all.
+// ---- routing: a wave a token, which takes its experts one maximum after the other.  share = exp(l - max)
+// over the sum of the chosen experts' exponentials (renorm) or of all.
+template <int KEYS>
 __global__ __launch_bounds__(kThreads) void k_moe_route(const MoeArgs a) {
   const int t = blockIdx.x * kWaves + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (t >= a.T) return;                                  // the whole wave
-  const float* row = a.logits + t * a.ld_logits;
-  float top = -__builtin_inff();
-  bool nan = false;
-  for (int j = lane; j < a.E; j += 64) {
-    const float l = row[j];
-    top = fmaxf(top, l);
-    nan |= l != l;
+  Logits<KEYS> lg;
+  lg.load(a, t, lane);
+  const float top = lg.top();
+  int rank[KEYS];
+#pragma unroll
+  for (int q = 0; q < KEYS; ++q) rank[q] = -1;
+  bool left = true;
+  for (int r = 0; r < a.k; ++r) {
+    const int e = left ? lg.take(lane) : -1;
+    left = e >= 0;
+    if (lane == 0) a.chosen[t * a.k + r] = e;
+#pragma unroll
+    for (int q = 0; q < KEYS; ++q)
+      if (e == 64 * q + lane) rank[q] = r;
   }
-  top = __any(nan) ? __builtin_nanf("") : wave_max(top);
-  // the first 64 experts stay in registers until the sum is known, further ones are looked at again
-  float sum = 0.0f, p0 = 0.0f;
-  int r0 = -1;
-  for (int j0 = 0; j0 < a.E; j0 += 64) {
-    const int j = j0 + lane;
-    const float l = j < a.E ? row[j] : -__builtin_inff();
-    const uint32_t kj = order_key(l);
-    const int r = rank_of(row, a.E, j, kj, lane);
-    const bool in = j < a.E && r < a.k;
-    const float p = expf(l - top);
-    if (a.renorm ? in : j < a.E) sum += p;
-    const int mine = in && kj != kMasked ? r : -1;
-    if (j < a.E) a.rank[(int64_t)j * a.T + t] = (int16_t)mine;
-    if (in) a.chosen[t * a.k + r] = mine >= 0 ? j : -1;
-    if (j0 == 0) {
-      p0 = p;
-      r0 = mine;
-    }
+  float p[KEYS], sum = 0.0f;
+#pragma unroll
+  for (int q = 0; q < KEYS; ++q) {
+    p[q] = expf(lg.l[q] - top);
+    if (a.renorm ? rank[q] >= 0 : 64 * q + lane < a.E) sum += p[q];
   }
   sum = wave_sum(sum);
-  if (r0 >= 0) a.share[t * a.k + r0] = p0 / sum;
-  for (int j0 = 64; j0 < a.E; j0 += 64) {
-    const int j = j0 + lane;
-    const int r = j < a.E ? a.rank[(int64_t)j * a.T + t] : -1;
-    if (r >= 0) a.share[t * a.k + r] = expf(row[j] - top) / sum;
+#pragma unroll
+  for (int q = 0; q < KEYS; ++q) {
+    const int j = 64 * q + lane;
+    if (j < a.E) a.rank[(int64_t)j * a.T + t] = (int16_t)rank[q];
+    if (rank[q] >= 0) a.share[t * a.k + rank[q]] = p[q] / sum;
   }
 }
 
@@ -268,17 +236,54 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_down(const MoeArgs a) {
 }
 
 // ---- y[t] = sum of the token's rows, in the order of rank; masked experts, which come last,
-// have none.
-__global__ __launch_bounds__(256) void k_moe_sum(const MoeArgs a) {
-  const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+// have none.  Four columns a thread, four rows on their way at a time (a column and a row at a time: 6.6
+// us against 5.1 for 16 tokens of 5120 columns).
+__global__ __launch_bounds__(64) void k_moe_sum(const MoeArgs a) {
+  const int t = blockIdx.y, n = 4 * (blockIdx.x * 64 + threadIdx.x);
+  int kept = 0;
+  for (int r = 0; r < a.k; ++r) kept += a.chosen[t * a.k + r] >= 0 ? 1 : 0;
   if (n >= a.H) return;
-  float s = 0.0f;
-  for (int r = 0; r < a.k && a.chosen[t * a.k + r] >= 0; ++r)
-    for (int p = 0; p < a.parts; ++p) s += a.part[(((int64_t)t * a.k + r) * a.parts + p) * a.H + n];
-  if (a.y_bf16)
-    reinterpret_cast<uint16_t*>(a.y)[t * a.ld_y + n] = (uint16_t)f32_to_bf16_rne(s);
-  else
-    reinterpret_cast<float*>(a.y)[t * a.ld_y + n] = s;
+  const float* part = a.part + (int64_t)t * a.k * a.parts * a.H + n;
+  const int rows = kept * a.parts, cols = min(4, a.H - n);
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int r0 = 0; r0 < rows; r0 += 4) {
+    float v[4][4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float* row = part + (int64_t)min(r0 + r, rows - 1) * a.H;
+      if (cols == 4) {
+        __builtin_memcpy(v[r], row, 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[r][e] = row[min(e, cols - 1)];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (r0 + r < rows) s[e] += v[r][e];
+  }
+  if (a.y_bf16) {
+    uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + t * a.ld_y + n;
+    const uint32_t d[2] = {pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
+    if (cols == 4) {
+      __builtin_memcpy(y, d, 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < cols) y[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+    }
+  } else {
+    float* y = reinterpret_cast<float*>(a.y) + t * a.ld_y + n;
+    if (cols == 4) {
+      __builtin_memcpy(y, s, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < cols) y[e] = s[e];
+    }
+  }
 }
 
 template <int NTW, int KIND>
@@ -363,7 +368,8 @@ Plan plan_of(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool f32) {
 template <int KIND>
 hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
   if (plan.few) return launch_moe_few(a, st);
-  hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
+  auto route = a.E <= 64 ? k_moe_route<1> : a.E <= 256 ? k_moe_route<4> : k_moe_route<16>;
+  hipLaunchKernelGGL(route, dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int nu = plan.up.tiles, nd = plan.down.tiles;
@@ -381,7 +387,7 @@ hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
     e = KIND == kTwo && nd == 8 ? launch_down<8, kTwo>(d, st)
         : KIND == kTwo && nd == 4 ? launch_down<4, kTwo>(d, st) : launch_down<2, KIND>(d, st);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), dim3(256), 0, st, d);
+  hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((a.H + 255) / 256), (unsigned)a.T), dim3(64), 0, st, d);
   return hipGetLastError();
 }
 

@@ -1,6 +1,8 @@
 // moe_fp4.hpp -- what the kernels of the expert layer share: their arguments, the order of
 // logits, and the layout of the hidden values.
 #pragma once
+#include <math.h>
+
 #include "fp4_stream.hpp"
 
 namespace mxq {
@@ -40,6 +42,80 @@ __device__ __forceinline__ uint32_t order_key(float l) {
   const uint32_t b = __float_as_uint(l + 0.0f);
   return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+  return v > o ? v : o;
+}
+
+// The greatest of the wave's values: within rows of 16 lanes, then across them; lane 63 has it.
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  v = max_dpp<0x111>(v);                     // row_shr 1, 2, 4, 8
+  v = max_dpp<0x112>(v);
+  v = max_dpp<0x114>(v);
+  v = max_dpp<0x118>(v);
+  v = max_dpp<0x142>(v);                     // row_bcast 15, 31
+  v = max_dpp<0x143>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// The logits of a token, lane l those of experts l, l + 64, ..., at most KEYS.
+template <int KEYS>
+struct Logits {
+  float l[KEYS];
+  uint32_t key[KEYS];                        // 0 past the last and once taken
+
+  __device__ __forceinline__ void load(const MoeArgs& a, int t, int lane) {
+    const float* row = a.logits + t * a.ld_logits;
+#pragma unroll
+    for (int q = 0; q < KEYS; ++q) {
+      const int j = 64 * q + lane;
+      l[q] = j < a.E ? row[j] : -__builtin_inff();
+    }
+#pragma unroll
+    for (int q = 0; q < KEYS; ++q) key[q] = 64 * q + lane < a.E ? order_key(l[q]) : 0u;
+  }
+
+  // The greatest of them, NaN if one is.
+  __device__ __forceinline__ float top() const {
+    float v = -__builtin_inff();
+    bool nan = false;
+#pragma unroll
+    for (int q = 0; q < KEYS; ++q) {
+      v = fmaxf(v, l[q]);
+      nan |= l[q] != l[q];
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+    return __any(nan) ? __builtin_nanf("") : v;
+  }
+
+  // Takes the greatest logit's expert, the lowest of equals; -1 where only masked ones are left.
+  __device__ __forceinline__ int take(int lane) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < KEYS; ++q) m = m > key[q] ? m : key[q];
+    m = wave_umax(m);
+    if (m <= kMasked) return -1;
+    int e = -1;
+#pragma unroll
+    for (int q = KEYS - 1; q >= 0; --q) {
+      const uint64_t b = __ballot(key[q] == m);
+      if (b != 0) e = 64 * q + __ffsll((unsigned long long)b) - 1;
+    }
+#pragma unroll
+    for (int q = 0; q < KEYS; ++q)
+      if (e == 64 * q + lane) key[q] = 0u;
+    return e;
+  }
+};
 
 // The hidden values go from one product to the next in the second one's fragment order, as bf16 terms
 // that the matrix cores take as they are, a plane of 16 bytes per 8 elements each (XWide): two terms,

@@ -29,65 +29,6 @@ constexpr int kKeys = 4;                     // logits of a lane: E <= 256
 constexpr int kUpWaves = 4;
 constexpr int kDownWaves = 8;
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
-  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
-  return v > o ? v : o;
-}
-
-// The greatest of the wave's values: within rows of 16 lanes, then across them; lane 63 has it.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max_dpp<0x111>(v);                     // row_shr 1, 2, 4, 8
-  v = max_dpp<0x112>(v);
-  v = max_dpp<0x114>(v);
-  v = max_dpp<0x118>(v);
-  v = max_dpp<0x142>(v);                     // row_bcast 15, 31
-  v = max_dpp<0x143>(v);
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
-
-// The logits of a token, lane l those of experts l, l + 64, ...
-struct Logits {
-  float l[kKeys];
-  uint32_t key[kKeys];                       // 0 past the last and once taken
-
-  __device__ __forceinline__ void load(const MoeArgs& a, int t, int lane) {
-    const float* row = a.logits + t * a.ld_logits;
-#pragma unroll
-    for (int q = 0; q < kKeys; ++q) {
-      const int j = 64 * q + lane;
-      l[q] = j < a.E ? row[j] : -__builtin_inff();
-    }
-#pragma unroll
-    for (int q = 0; q < kKeys; ++q) key[q] = 64 * q + lane < a.E ? order_key(l[q]) : 0u;
-  }
-
-  // Takes the greatest logit's expert, the lowest of equals; -1 where only masked ones are left.
-  __device__ __forceinline__ int take(int lane) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int q = 0; q < kKeys; ++q) m = m > key[q] ? m : key[q];
-    m = wave_max(m);
-    if (m <= kMasked) return -1;
-    int e = -1;
-#pragma unroll
-    for (int q = kKeys - 1; q >= 0; --q) {
-      const uint64_t b = __ballot(key[q] == m);
-      if (b != 0) e = 64 * q + __ffsll((unsigned long long)b) - 1;
-    }
-#pragma unroll
-    for (int q = 0; q < kKeys; ++q)
-      if (e == 64 * q + lane) key[q] = 0u;
-    return e;
-  }
-};
-
 // The lane's block of 8 rows: codes and scale bytes.
 struct Block {
   v4i w[kRows];
@@ -169,7 +110,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_few_up(const MoeArgs a
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nb = (a.H + 31) / 32, segs = (a.H + kSeg - 1) / kSeg;
-  Logits lg;
+  Logits<kKeys> lg;
   lg.load(a, t, lane);
   // x: thread's 16-byte pieces threadIdx.x + 256 n, the first two on their way while experts are chosen
   const uint8_t* xr = a.x + t * a.ld_x;
@@ -257,18 +198,9 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_few_down(const MoeAr
   const int lane = threadIdx.x & 63, waves = blockDim.x / 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nb = (a.I + 31) / 32, segs = (a.I + kSeg - 1) / kSeg;
-  Logits lg;
+  Logits<kKeys> lg;
   lg.load(a, t, lane);
-  float top = -__builtin_inff();
-  bool nan = false;
-#pragma unroll
-  for (int q = 0; q < kKeys; ++q) {
-    top = fmaxf(top, lg.l[q]);
-    nan |= lg.l[q] != lg.l[q];
-  }
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  if (__any(nan)) top = __builtin_nanf("");
+  const float top = lg.top();
   float all = 0.0f;
   if (!a.renorm) {
 #pragma unroll
