@@ -371,8 +371,10 @@ int mxq_gemm_exact_plan(int64_t M, int64_t N, int64_t K, int cus, int* tile_n, i
  * codes share a byte, the even element in the low half, so a block is 16 bytes.
  *
  * Code arrays [L][ld_codes]: ld_codes in BYTES, >= 16 * nb and a multiple of 16, pointer 16-byte
- * aligned.  Scale arrays [L][ld_scales], ld_scales >= nb, any alignment; nothing outside the
- * L x nb scale bytes and L x 16 nb code bytes is read or written.
+ * aligned.  Scale arrays [L][ld_scales], ld_scales >= nb, any alignment (rows aligned to 16 bytes
+ * are read fastest).  Nothing outside the L x nb scale bytes and L x 16 nb code bytes is written or
+ * has an influence; reading may touch the padding between rows and the rest of the aligned 4 bytes
+ * that hold a last scale byte.
  */
 
 /*
@@ -453,9 +455,10 @@ int mxq_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, int x_type, int
  * An expert whose logit is -inf is never taken, also when fewer than k are left; a token with
  * no expert left gets y = 0.  A NaN logit orders above every number and makes the token's
  * shares NaN.
- * Products exact, sums in FP32; the hidden values are carried as 2 (y_type MXQ_BF16) or 3
- * (MXQ_F32) bf16 terms, 16 or 24 bits.  The result does not depend on how workgroups are
- * scheduled.
+ * Products of x and the weights exact, sums in FP32.  The hidden values are FP32, or, where experts have
+ * several tokens, 2 (y_type MXQ_BF16) or 3 (MXQ_F32) bf16 terms, 16 or 24 bits.  The result does
+ * not depend on how workgroups are scheduled; the summation order is fixed for the sizes, the
+ * alignment and the device.  Two launches where hardly an expert has two tokens, else four.
  * workspace  256-byte aligned, at least the bytes that mxq_moe_fp4_workspace gives
  *          (MXQ_ERR_SCRATCH otherwise); it holds nothing between calls.
  * Limits   T <= 1024, E <= 1024, 1 <= k <= E, H and I < 2^24, (I + 128) * ld_w13 < 2^32.

