@@ -436,3 +436,103 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want)), r
+
+
+def test_experts_strided_of_many():
+    """Slices of wider arrays, scale rows at odd addresses and a column of logits' array, where routing has
+    a launch of its own."""
+    rng = np.random.default_rng(40)
+    E, T, H, I, k = 264, 20, 96, 72, 3
+    w13, s13, v13, w2, s2, v2 = experts(rng, E, H, I)
+
+    def embed(t, rows, cols):
+        big = torch.full((E, t.shape[1] + rows, t.shape[2] + cols), 0x7F, dtype=torch.uint8, device=DEV)
+        big[:, :t.shape[1], :t.shape[2]] = t
+        return big[:, :t.shape[1], :t.shape[2]]
+    x, _, xv = bf16_operand(rng, T, H, 5)
+    lg = torch.from_numpy(rng.standard_normal((T, E + 4)).astype(np.float32)).to(DEV)[:, 2:2 + E]
+    for dtype in (BF16, F32):
+        out = torch.full((T, H + 5), 3.0, dtype=dtype, device=DEV)
+        y = mxq.moe_fp4(x, lg, embed(w13, 3, 16), embed(s13, 1, 3), embed(w2, 2, 32), embed(s2, 4, 1), k, out=out[:, :H])
+        want, bound = ref.moe(xv, f64(lg), v13, v2, k, True, dtype == BF16)
+        check_product(y, want, bound, "strided")
+        assert (out[:, H:] == 3.0).all()
+
+
+@pytest.mark.parametrize("T,E", [(2, 6), (48, 264)])
+def test_experts_graph(T, E):
+    """The expert layer captured and replayed on new inputs, with eager calls between the replays, in two
+    launches and in four."""
+    rng = np.random.default_rng(41)
+    w13, s13, _, w2, s2, _ = experts(rng, E, 72, 40)
+    x = torch.from_numpy(rng.standard_normal((T, 72)).astype(np.float32)).to(BF16).to(DEV)
+    lg = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).to(DEV)
+
+    def step(x, lg):
+        return [mxq.moe_fp4(x, lg, w13, s13, w2, s2, 3, renormalize=n, out_dtype=d) for n in (True, False) for d in (F32, BF16)]
+    step(x, lg)
+    gx, gl = x.clone(), lg.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(gx, gl)
+    for r in range(4):
+        gx.copy_(torch.roll(x, r, 0) * (r + 1))
+        gl.copy_(torch.roll(lg, r, 1))
+        want = step(gx, gl)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want)), r
+
+
+def far(t, pitch):
+    """The rows of t, `pitch` elements apart in a buffer that is written nowhere else."""
+    big = torch.empty((t.shape[0] * pitch,), dtype=t.dtype, device=DEV).view(t.shape[0], pitch)[:, :t.shape[1]]
+    big.copy_(t)
+    return big
+
+
+def test_offsets_past_32_bits():
+    """Rows and experts further apart than 2^32 bytes reach."""
+    rng = np.random.default_rng(42)
+    K = 96
+    w, ws, wv = operand(rng, 600, K)
+    x, xs, xv = operand(rng, 520, K)
+    b, _, bv = bf16_operand(rng, 40, K)
+    say("gemm_fp4, rows of W 8 MiB apart")
+    wf, wsf = far(w, 1 << 23), far(ws, 1 << 23)
+    check_product(mxq.gemm_fp4(b, None, wf, wsf, K, out_dtype=F32), *ref.product(bv, wv), "bf16")
+    check_product(mxq.gemm_fp4(x, xs, wf, wsf, K, out_dtype=F32), *ref.product(xv, wv), "fp4")
+    check_product(mxq.gemm_fp4(far(x, 1 << 23), far(xs, 1 << 23), w, ws, K, out_dtype=F32), *ref.product(xv, wv), "far x")
+    say("gemm_fp4, rows of X and Y 128 MiB apart")
+    y = torch.empty((40 * (1 << 25),), dtype=F32, device=DEV).view(40, 1 << 25)[:, :600]
+    check_product(mxq.gemm_fp4(far(b, 1 << 26), None, w, ws, K, out=y), *ref.product(bv, wv), "far y")
+    del wf, wsf, y
+    say("quantize_fp4 and dequantize_fp4, rows 1 GiB apart")
+    v = data(rng, 6, 130, F32).to(DEV)
+    for got, want in zip(mxq.quantize_fp4_dual(far(v, 1 << 28)), mxq.quantize_fp4_dual(v)):
+        assert torch.equal(got, want)
+    c, s = mxq.quantize_fp4(v)
+    assert torch.equal(mxq.dequantize_fp4(far(c, 1 << 30), far(s, 1 << 30), 130), mxq.dequantize_fp4(c, s, 130))
+    say("moe_fp4, experts 3 GiB apart")
+    E, T, H, I = 3, 4, 64, 40
+    w13, s13, v13, w2, s2, v2 = experts(rng, E, H, I)
+
+    def apart(t):
+        big = torch.empty((E * 3 << 30,), dtype=torch.uint8, device=DEV)
+        out = big.as_strided(t.shape, (3 << 30, t.shape[2] + (-t.shape[2]) % 16, 1))
+        out.copy_(t)
+        return out
+    h, _, hv = bf16_operand(rng, T, H)
+    lg = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).to(DEV)
+    y = mxq.moe_fp4(h, lg, apart(w13), apart(s13), apart(w2), apart(s2), 2, out_dtype=F32)
+    check_product(y, *ref.moe(hv, f64(lg), v13, v2, 2, True, False), "far experts")
+
+
+def test_tile_product_with_far_rows():
+    """The 256 x 256 tiles with rows 1 MiB apart: 3 GB from the first row to the last."""
+    rng = np.random.default_rng(43)
+    M, N, K = 2900, 2900, 160
+    x, xs, xv = operand(rng, M, K)
+    w, ws, wv = operand(rng, N, K)
+    y = mxq.gemm_fp4(far(x, 1 << 20), far(xs, 1 << 20), far(w, 1 << 20), far(ws, 1 << 20), K, out_dtype=F32)
+    check_product(y, *ref.product(xv, wv), "far tiles")
