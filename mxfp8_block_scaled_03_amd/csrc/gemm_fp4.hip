@@ -46,7 +46,7 @@ __device__ __forceinline__ void store4(const GemmEpilogue& ep, int64_t row, int 
   }
 }
 
-// A workgroup computes a tile of 16 * MT rows x 16 * NT columns of Y; its eight waves split K in
+// A workgroup computes a tile of 16 * MT rows x 16 * NT columns of Y; its waves (1 to 8) split K in
 // runs of whole kRun elements, and their sums meet in LDS, added in wave order.  A wave has its
 // piece of both operands to itself: rows are loaded whole lines at a time into registers (8 lanes
 // a row; any alignment of X in bf16 and of the scales), put into the wave's own LDS, swizzled, and
@@ -346,16 +346,30 @@ hipError_t launch_split(Fp4Args a, const GemmEpilogue& ep, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The largest tile that still gives every CU a workgroup.
+// The tile and the split, from timing ten of them on 50 shapes (256 CUs).  Where 64 x 64 tiles fill the
+// CUs, as many waves a tile as the card holds at once (8 a CU), up to 8: 1000 x 1000 x 4001 10.2 us with
+// 8, 2000 x 1000 x 3000 13.0 with 4 (14.9 with 2), 2048^3 14.3 with 2 (15.3 with 4), 3000 x 2500 x 2500 35.3
+// with 1 (41.4 with 4); with X in bf16 512 x 4096 x 4096 25 with 4 (34 with 2), 1024 rows 43 with 2 (46 with
+// 4), 2048 rows 83 with 1 (141 with 4).  K of at most 1024 leaves many waves less than a piece each: 64 x 32
+// tiles by two waves for X in MXFP4 (3000 x 1500 x 800 13.3 us, 15.6 in 64 x 64 by four; 1500 x 4096 x 500
+// 11.3 and 17.3), and 32 x 32 by four where there are fewer.  Else the largest tile that still gives
+// every CU a workgroup.
 template <bool X_FP4>
 hipError_t launch_rows(const Fp4Args& a, const GemmEpilogue& ep, hipStream_t st) {
   const int64_t cus = device_cu_count();
   auto tiles = [&](int mt, int nt) { return (int64_t)((a.M + 16 * mt - 1) / (16 * mt)) * ((a.N + 16 * nt - 1) / (16 * nt)); };
-  if (a.M > 32) {
-    if (tiles(4, 4) > cus) return launch_split<X_FP4, 4, 4, 4>(a, ep, st);
-    if (tiles(4, 4) == cus) return launch_split<X_FP4, 8, 4, 4>(a, ep, st);
+  const bool brief = a.K <= 1024;
+  if (a.M > 32 && tiles(4, 4) > cus) {
+    if constexpr (X_FP4) {
+      if (brief) return launch_split<true, 2, 4, 2>(a, ep, st);
+    }
+    if (tiles(4, 4) <= 2 * cus) return launch_split<X_FP4, 4, 4, 4>(a, ep, st);
+    if (tiles(4, 4) <= 4 * cus) return launch_split<X_FP4, 2, 4, 4>(a, ep, st);
+    return launch_split<X_FP4, 1, 4, 4>(a, ep, st);
   }
+  if (a.M > 32 && !brief && tiles(4, 4) == cus) return launch_split<X_FP4, 8, 4, 4>(a, ep, st);
   if (a.M > 16) {
+    if (brief && tiles(2, 2) >= cus) return launch_split<X_FP4, 4, 2, 2>(a, ep, st);
     if (tiles(2, 4) >= cus) return launch_split<X_FP4, 8, 2, 4>(a, ep, st);
     if (tiles(2, 2) >= cus) return launch_split<X_FP4, 8, 2, 2>(a, ep, st);
     return launch_split<X_FP4, 8, 2, 1>(a, ep, st);
@@ -371,10 +385,11 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool 
                            int64_t ld_xs, const uint8_t* wc, int64_t ld_w, const uint8_t* ws, int64_t ld_ws,
                            const GemmEpilogue& ep, hipStream_t st) {
   auto whole = [](const void* p, int64_t ld, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0 && ld % n == 0; };
-  // 256 x 256 tiles once they fill half the CUs: 2048 x 4096 x 4096 takes 31 us so and 47 as a stream,
-  // 1024 x 4096 x 4096 (64 tiles) 30 and 23
+  // 256 x 256 tiles from two for five CUs on: 4096 x 2048 x 4096 (128 tiles) takes 32 us so and 45 in small
+  // tiles, 3000 x 2500 x 2500 (120) 28 and 36, 1500 x 4096 x 500 (96) 11.6 and 11.8, 1000 x 4096 x 4096 (64)
+  // 30 and 23
   const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
-  if (x_fp4 && K > 0 && 2 * tiles >= device_cu_count() && whole(xs, ld_xs, 16) && whole(ws, ld_ws, 16))
+  if (x_fp4 && K > 0 && 5 * tiles >= 2 * device_cu_count() && whole(xs, ld_xs, 16) && whole(ws, ld_ws, 16))
     return launch_gemm_fp4_tile(M, N, K, (const uint8_t*)x, ld_x, xs, ld_xs, wc, ld_w, ws, ld_ws, ep, st);
   Fp4Args a{};
   a.M = (int)M;

@@ -335,9 +335,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm4_tile(int M, int N, int K,
           for (int r = 0; r < 16; ++r) acc[fi][fj][r] = silu(acc[fi][fj][r]);
     }
   }
-  // interior tile, aligned y: stage the block in this wave's LDS region as row-major rows
-  // of 64 values with the 16-byte chunk index XOR (row & 7), then store whole 16-byte row
-  // pieces (E = bytes per value)
+  // stage the block in this wave's LDS region as row-major rows of 64 values with the 16-byte
+  // chunk index XOR (row & 7), then store whole 16-byte row pieces (E = bytes per value); where the tile
+  // or the matrix ends, or y is not aligned, piece by piece with its bounds (element by element, as the
+  // fragments lie, a ragged tile took 15 us longer than a whole one)
+  const bool whole = ep.y_vec16 && m0 + BM <= M && n0 + BN <= N;
   auto store_staged = [&](auto e_c) {
     constexpr int E = decltype(e_c)::value;
     constexpr int RB = 64 * E;                       // bytes per staged row
@@ -382,38 +384,31 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm4_tile(int M, int N, int K,
         const int c = lane % CPR;
         const uint32_t addr = wbase + (uint32_t)row * RB + (uint32_t)((c ^ (row & (CPR - 1) & 7)) << 4);
         const v4i v = *reinterpret_cast<const v4i*>(smem + addr);
-        uint8_t* dst = reinterpret_cast<uint8_t*>(ep.y) +
-                       ((int64_t)(wrow0 + pass * RP + row) * ep.ld_y + wcol0) * E + 16 * c;
-        *reinterpret_cast<v4i*>(dst) = v;
+        const int gr = wrow0 + pass * RP + row, gc = wcol0 + (16 / E) * c;
+        uint8_t* dst = reinterpret_cast<uint8_t*>(ep.y) + ((int64_t)gr * ep.ld_y + gc) * E;
+        if (whole) {
+          *reinterpret_cast<v4i*>(dst) = v;
+        } else if (gr < M) {
+          if (gc + 16 / E <= N) {
+            __builtin_memcpy(dst, &v, 16);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16 / E; ++e)
+              if (gc + e < N) {
+                if (E == 2)
+                  reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)((uint32_t)v[(e * E) >> 2] >> (16 * (e & 1)));
+                else
+                  reinterpret_cast<int*>(dst)[e] = v[e & 3];
+              }
+          }
+        }
       }
     }
   };
-  if (ep.y_vec16 && m0 + BM <= M && n0 + BN <= N) {
-    if (ep.y_bf16)
-      store_staged(std::integral_constant<int, 2>());
-    else
-      store_staged(std::integral_constant<int, 4>());
-  } else {
-#pragma unroll
-    for (int fj = 0; fj < 2; ++fj)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = wcol0 + 32 * fj + 8 * q + 4 * lg + e;
-#pragma unroll
-          for (int fi = 0; fi < 4; ++fi) {
-            const int row = wrow0 + 32 * fi + li;
-            if (row < M && col < N) {
-              const float v = acc[fi][fj][4 * q + e];
-              if (ep.y_bf16)
-                reinterpret_cast<uint16_t*>(ep.y)[(int64_t)row * ep.ld_y + col] = (uint16_t)f32_to_bf16_rne(v);
-              else
-                reinterpret_cast<float*>(ep.y)[(int64_t)row * ep.ld_y + col] = v;
-            }
-          }
-        }
-  }
+  if (ep.y_bf16)
+    store_staged(std::integral_constant<int, 2>());
+  else
+    store_staged(std::integral_constant<int, 4>());
 }
 
 template <bool TAIL>

@@ -536,3 +536,21 @@ def test_tile_product_with_far_rows():
     w, ws, wv = operand(rng, N, K)
     y = mxq.gemm_fp4(far(x, 1 << 20), far(xs, 1 << 20), far(w, 1 << 20), far(ws, 1 << 20), K, out_dtype=F32)
     check_product(y, *ref.product(xv, wv), "far tiles")
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp4"])
+@pytest.mark.parametrize("M,N,K", [(1100, 1100, 300), (1100, 1100, 1300), (2100, 2100, 1100), (1500, 2900, 129), (40, 2100, 200),
+                                   (3000, 1500, 65)])
+def test_gemm_tiles_and_splits(xt, M, N, K):
+    """Sizes for every tile and split of K that the product chooses from, with a ragged end on each axis,
+    bias and SiLU; y in bf16 with an odd pitch and in fp32, nothing written beside it."""
+    rng = np.random.default_rng(44)
+    x, xs, xv = operand(rng, M, K) if xt == "fp4" else bf16_operand(rng, M, K)
+    w, ws, wv = operand(rng, N, K, 0, K ** -0.5)
+    bias = torch.from_numpy(rng.standard_normal(N).astype(np.float32)).to(DEV)
+    say("gemm_fp4 %s %dx%dx%d" % (xt, M, N, K))
+    for out, pad, act in ((BF16, 3, "silu"), (F32, 1, None), (BF16, (-N) % 8 + 8, None)):
+        wide = torch.full((M + 2, N + pad), 7.0, dtype=out, device=DEV)
+        y = mxq.gemm_fp4(x, xs, w, ws, K, bias=bias, act=act, out=wide[1:M + 1, :N])
+        check_product(y, *ref.product(xv, wv, 1.0, f64(bias), act, out == BF16), "%s %s" % (out, act))
+        assert (wide[1:M + 1, N:] == 7.0).all() and (wide[0] == 7.0).all() and (wide[M + 1] == 7.0).all()
