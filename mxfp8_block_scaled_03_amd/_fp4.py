@@ -36,37 +36,37 @@ def _call(name: str, device: int, args: tuple) -> None:
 _empty = torch.empty_strided
 
 
-def _lines(t, name: str, dtype, rows, cols: int) -> int:
+def _lines(t, name: str, dtype, rows: int, cols: int) -> int:
     """Checks rows of at least `cols` elements, `rows` of them at least; the row pitch."""
     try:
         r, c = t.shape
         pitch, step = t.stride()
-        good = t.dtype is dtype and c >= cols and (rows is None or r >= rows)
+        if step == 1 and pitch >= c >= cols and r >= rows and t.dtype is dtype and c > 0 and r > 0:
+            return pitch
     except (AttributeError, TypeError, ValueError):
-        good = False
-    if not good or (step != 1 and c > 1 and r > 0) or (pitch < c and r > 1):
-        _req_2d(t, name, dtype, rows, cols)
+        pass
+    # no rows, one row or one column, or something wrong
+    _req_2d(t, name, dtype, rows, cols)
+    if step != 1 and c > 1 and r > 0:
         raise ValueError("%s must have unit stride along its last dimension" % name)
     return pitch if r > 0 and pitch >= c else max(c, 1)
 
 
-def _on_one_device(first, others: tuple, names: tuple) -> int:
-    """The index of the device that holds `first` and every other tensor."""
-    device = first.get_device()
-    for i, t in enumerate(others):
-        if t is not None and t.get_device() != device and device >= 0:
-            if t.get_device() < 0:
-                raise ValueError("%s must be a CUDA (HIP device) tensor, got device %s" % (names[i], t.device))
-            raise ValueError("%s is on %s, expected %s" % (names[i], t.device, first.device))
-    if device < 0:
-        raise ValueError("expected CUDA (HIP device) tensors, got device %s" % first.device)
-    return device
+def _same_device(named: tuple) -> int:
+    """The index of the device that holds every given tensor: the slow way, which finds what is wrong."""
+    first = named[0][1]
+    for name, t in named:
+        if t is not None and t.get_device() < 0:
+            raise ValueError("%s must be a CUDA (HIP device) tensor, got device %s" % (name, t.device))
+        if t is not None and t.get_device() != first.get_device():
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, first.device))
+    return first.get_device()
 
 
 def _wide(t, name: str) -> int:
     if not isinstance(t, torch.Tensor) or t.dtype not in _WIDE:
         _req_wide(t, name)
-    return _lines(t, name, t.dtype, None, 0)
+    return _lines(t, name, t.dtype, 0, 0)
 
 
 def _code_array(lines: int, k: int, device):
@@ -79,25 +79,27 @@ def _code_array(lines: int, k: int, device):
 
 
 def _orient(x, axis, codes, scales):
-    """What the one-orientation quantizers share: pitch of x, axis tag, device, outputs."""
+    """What the one-orientation quantizers share: sizes and pitch of x, axis tag, device, outputs."""
     ld = _wide(x, "x")
-    if axis not in _AXIS:
+    ax = _AXIS.get(axis)
+    if ax is None:
         raise ValueError("axis must be 'row' or 'col'")
-    ax = _AXIS[axis]
-    L, K = x.shape
-    if ax == MXQ_COLWISE:
-        L, K = K, L
+    rows, cols = x.shape
+    L, K = (cols, rows) if ax == MXQ_COLWISE else (rows, cols)
     nb = (K + 31) // 32
     ld_c = None if codes is None else _lines(codes, "codes", _U8, L, 16 * nb)
     ld_s = None if scales is None else _lines(scales, "scales", _U8, L, nb)
-    device = _on_one_device(x, (codes, scales), ("codes", "scales"))
+    device = x.get_device()
+    if device < 0 or (codes is not None and codes.get_device() != device) or \
+            (scales is not None and scales.get_device() != device):
+        _same_device((("x", x), ("codes", codes), ("scales", scales)))
     if codes is None or scales is None:
         c, pitch_c, s, pitch_s = _code_array(L, K, x.device)
         if codes is None:
             codes, ld_c = c, pitch_c
         if scales is None:
             scales, ld_s = s, pitch_s
-    return ld, ax, device, codes, ld_c, scales, ld_s
+    return rows, cols, ld, ax, device, codes, ld_c, scales, ld_s
 
 
 def quantize_fp4(x, axis="row", codes=None, scales=None, rule: str = "ceil"):
@@ -111,8 +113,7 @@ def quantize_fp4(x, axis="row", codes=None, scales=None, rule: str = "ceil"):
     """
     if rule not in _RULE:
         raise ValueError("rule must be 'ceil' or 'ocp'")
-    ld, ax, device, codes, ld_c, scales, ld_s = _orient(x, axis, codes, scales)
-    rows, cols = x.shape
+    rows, cols, ld, ax, device, codes, ld_c, scales, ld_s = _orient(x, axis, codes, scales)
     _call("mxq_quantize_fp4", device, (x.data_ptr(), _WIDE[x.dtype], rows, cols, ld, ax, _RULE[rule],
                                        codes.data_ptr(), ld_c, scales.data_ptr(), ld_s))
     return codes, scales
@@ -121,8 +122,7 @@ def quantize_fp4(x, axis="row", codes=None, scales=None, rule: str = "ceil"):
 def quantize_fp4_sr(x, seed: int, axis="row", codes=None, scales=None):
     """quantize_fp4() with stochastically rounded codes (Philox4x32-10 keyed by `seed`, see
     mxq_quantize_fp4_sr): for gradients."""
-    ld, ax, device, codes, ld_c, scales, ld_s = _orient(x, axis, codes, scales)
-    rows, cols = x.shape
+    rows, cols, ld, ax, device, codes, ld_c, scales, ld_s = _orient(x, axis, codes, scales)
     _call("mxq_quantize_fp4_sr", device, (x.data_ptr(), _WIDE[x.dtype], rows, cols, ld, ax, int(seed) & (2 ** 64 - 1),
                                           codes.data_ptr(), ld_c, scales.data_ptr(), ld_s))
     return codes, scales
@@ -132,7 +132,9 @@ def quantize_fp4_dual(x):
     """Both orientations of a 2-D bf16/fp32 CUDA tensor from one read of it: (row_codes,
     row_scales, col_codes, col_scales), as quantize_fp4(x, "row") and quantize_fp4(x, "col")."""
     ld = _wide(x, "x")
-    device = _on_one_device(x, (), ())
+    device = x.get_device()
+    if device < 0:
+        _same_device((("x", x),))
     rows, cols = x.shape
     rc, ld_rc, rs, ld_rs = _code_array(rows, cols, x.device)
     cc, ld_cc, cs, ld_cs = _code_array(cols, rows, x.device)
@@ -149,10 +151,12 @@ def dequantize_fp4(codes, scales, K: int, out_dtype=None):
     if K < 0:
         raise ValueError("K must be >= 0")
     nb = (K + 31) // 32
-    ld_c = _lines(codes, "codes", _U8, None, 16 * nb)
+    ld_c = _lines(codes, "codes", _U8, 0, 16 * nb)
     L = codes.shape[0]
     ld_s = _lines(scales, "scales", _U8, L, nb)
-    device = _on_one_device(codes, (scales,), ("scales",))
+    device = codes.get_device()
+    if device < 0 or scales.get_device() != device:
+        _same_device((("codes", codes), ("scales", scales)))
     ld = max(K, 1)
     dst = _empty((L, K), (ld, 1), dtype=out_dtype, device=codes.device)
     _call("mxq_dequantize_fp4", device, (codes.data_ptr(), ld_c, scales.data_ptr(), ld_s, L, K, dst.data_ptr(),
@@ -170,17 +174,17 @@ def gemm_fp4(x, x_scales, w_codes, w_scales, K: int, alpha: float = 1.0, bias=No
     if K < 0:
         raise ValueError("K must be >= 0")
     nb = (K + 31) // 32
-    ld_w = _lines(w_codes, "w_codes", _U8, None, 16 * nb)
+    ld_w = _lines(w_codes, "w_codes", _U8, 0, 16 * nb)
     N = w_codes.shape[0]
     ld_ws = _lines(w_scales, "w_scales", _U8, N, nb)
     if x_scales is None:
-        ld_x = _lines(x, "x", torch.bfloat16, None, K)
+        ld_x = _lines(x, "x", torch.bfloat16, 0, K)
         M = x.shape[0]
         if x.shape[1] != K:
             raise ValueError("x has %d columns, expected K = %d" % (x.shape[1], K))
         x_type, xs_ptr, ld_xs = MXQ_BF16, None, 0
     else:
-        ld_x = _lines(x, "x", _U8, None, 16 * nb)
+        ld_x = _lines(x, "x", _U8, 0, 16 * nb)
         M = x.shape[0]
         ld_xs = _lines(x_scales, "x_scales", _U8, M, nb)
         x_type, xs_ptr = MXQ_E2M1, x_scales.data_ptr()
@@ -195,7 +199,12 @@ def gemm_fp4(x, x_scales, w_codes, w_scales, K: int, alpha: float = 1.0, bias=No
             raise ValueError("out must have shape (M, N) = (%d, %d), got %s" % (M, N, tuple(out.shape)))
     elif out_dtype is not None and out_dtype not in _WIDE:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    device = _on_one_device(x, (x_scales, w_codes, w_scales, bias, out), _GEMM_NAMES)
+    device = x.get_device()
+    if device < 0 or w_codes.get_device() != device or w_scales.get_device() != device or \
+            (x_scales is not None and x_scales.get_device() != device) or \
+            (bias is not None and bias.get_device() != device) or (out is not None and out.get_device() != device):
+        _same_device((("x", x), ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("bias", bias),
+                      ("out", out)))
     if out is None:
         out_dtype, ld_y = out_dtype or torch.bfloat16, max(N, 1)
         out = _empty((M, N), (ld_y, 1), dtype=out_dtype, device=x.device)
@@ -206,10 +215,6 @@ def gemm_fp4(x, x_scales, w_codes, w_scales, K: int, alpha: float = 1.0, bias=No
                                    w_scales.data_ptr(), ld_ws, alpha, None if bias is None else bias.data_ptr(), _ACT[act],
                                    out.data_ptr(), y_type, ld_y))
     return out
-
-
-_GEMM_NAMES = ("x_scales", "w_codes", "w_scales", "bias", "out")
-_MOE_NAMES = ("logits", "w13_codes", "w13_scales", "w2_codes", "w2_scales", "out")
 
 
 def _expert(t, name: str, experts: int, rows: int, cols: int):
@@ -246,8 +251,8 @@ def moe_fp4(x, logits, w13_codes, w13_scales, w2_codes, w2_scales, k: int, renor
     renormalize: the k shares sum to 1.  Returns [T][H] in out_dtype (bf16 by default, or fp32).
     See mxq_moe_fp4 for ties, masked experts and precision.
     """
-    ld_x = _lines(x, "x", torch.bfloat16, None, 0)
-    ld_l = _lines(logits, "logits", torch.float32, None, 0)
+    ld_x = _lines(x, "x", torch.bfloat16, 0, 0)
+    ld_l = _lines(logits, "logits", torch.float32, 0, 0)
     (T, H), (rows, E) = x.shape, logits.shape
     if rows != T:
         raise ValueError("logits has %d rows, expected T = %d" % (rows, T))
@@ -267,7 +272,12 @@ def moe_fp4(x, logits, w13_codes, w13_scales, w2_codes, w2_scales, k: int, renor
             raise ValueError("out must have shape (T, H) = (%d, %d), got %s" % (T, H, tuple(out.shape)))
     elif out_dtype is not None and out_dtype not in _WIDE:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    device = _on_one_device(x, (logits, w13_codes, w13_scales, w2_codes, w2_scales, out), _MOE_NAMES)
+    device = x.get_device()
+    if device < 0 or logits.get_device() != device or w13_codes.get_device() != device or \
+            w13_scales.get_device() != device or w2_codes.get_device() != device or \
+            w2_scales.get_device() != device or (out is not None and out.get_device() != device):
+        _same_device((("x", x), ("logits", logits), ("w13_codes", w13_codes), ("w13_scales", w13_scales),
+                      ("w2_codes", w2_codes), ("w2_scales", w2_scales), ("out", out)))
     if out is None:
         out_dtype, ld_y = out_dtype or torch.bfloat16, max(H, 1)
         out = _empty((T, H), (ld_y, 1), dtype=out_dtype, device=x.device)

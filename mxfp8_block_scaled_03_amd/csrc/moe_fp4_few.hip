@@ -236,17 +236,13 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_few_down(const MoeAr
       ask_row += stride;
     }
   };
-  float x[32];
+  v4i hn[8];                                             // the lane's block of the next unit's h
   auto hidden = [&](int u) {
     const int r = u / segs, seg = u - r * segs;
     const uint8_t* h = a.h + (int64_t)(t * a.k + r) * hidden_bytes(a.I) + (int64_t)seg * (4 * kSeg);
     const int left = a.I - kSeg * seg - 32 * lane;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const v4i v = *reinterpret_cast<const v4i*>(h + (4 * q < left ? 1024u * q + 16u * lane : 0u));
-#pragma unroll
-      for (int d = 0; d < 4; ++d) x[4 * q + d] = __uint_as_float((uint32_t)v[d]);
-    }
+    for (int q = 0; q < 8; ++q) hn[q] = *reinterpret_cast<const v4i*>(h + (4 * q < left ? 1024u * q + 16u * lane : 0u));
   };
   Block next;
   ask(next);
@@ -257,19 +253,22 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_moe_few_down(const MoeAr
   for (int j = 0; j < own; ++j) {
 #pragma unroll 1
     for (int u = wave; u < units; u += waves) {
-      const Block now = next;
-      ask(next);
       const int r = u / segs, seg = u - r * segs;
+      const Block now = next;
+      float x[32];
+#pragma unroll
+      for (int q = 0; q < 32; ++q) x[q] = __uint_as_float((uint32_t)hn[q >> 2][q & 3]);
       if (kSeg * (seg + 1) > a.I) {                      // what lies past I was not stored
 #pragma unroll
         for (int q = 0; q < 32; ++q) x[q] = kSeg * seg + 32 * lane + q < a.I ? x[q] : 0.0f;
       }
+      ask(next);
+      if (!one) hidden(u + waves < units ? u + waves : wave);
       float dot[kRows] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
       now.dot(x, 64 * seg + lane < nb, dot);
       const float sh = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(share), r));
 #pragma unroll
       for (int q = 0; q < kRows; ++q) acc[q] = __builtin_fmaf(sh, dot[q], acc[q]);
-      if (!one) hidden(u + waves < units ? u + waves : wave);
     }
     const float s = sum_rows(acc, lane);
 #pragma unroll
