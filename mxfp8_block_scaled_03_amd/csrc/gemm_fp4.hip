@@ -335,8 +335,8 @@ __global__ __launch_bounds__(256) void k_gemm4_short(const Fp4Args a, const Gemm
 template <bool X_FP4, int SPLIT, int MT, int NT>
 hipError_t launch_split(Fp4Args a, const GemmEpilogue& ep, hipStream_t st) {
   static bool set[64] = {false};
-  a.tiles_m = (a.M + 16 * MT - 1) / (16 * MT);
-  a.tiles_n = (a.N + 16 * NT - 1) / (16 * NT);
+  a.tiles_m = (int)((a.M + 16ll * MT - 1) / (16 * MT));
+  a.tiles_n = (int)((a.N + 16ll * NT - 1) / (16 * NT));
   if ((int64_t)a.tiles_m * a.tiles_n > 0x7FFFFFFF) return hipErrorInvalidValue;
   auto kern = k_gemm4_split<X_FP4, SPLIT, MT, NT>;
   constexpr int lds = split_lds(X_FP4, SPLIT, MT, NT);
@@ -357,7 +357,7 @@ hipError_t launch_split(Fp4Args a, const GemmEpilogue& ep, hipStream_t st) {
 template <bool X_FP4>
 hipError_t launch_rows(const Fp4Args& a, const GemmEpilogue& ep, hipStream_t st) {
   const int64_t cus = device_cu_count();
-  auto tiles = [&](int mt, int nt) { return (int64_t)((a.M + 16 * mt - 1) / (16 * mt)) * ((a.N + 16 * nt - 1) / (16 * nt)); };
+  auto tiles = [&](int mt, int nt) { return ((a.M + 16ll * mt - 1) / (16 * mt)) * ((a.N + 16ll * nt - 1) / (16 * nt)); };
   const bool brief = a.K <= 1024;
   if (a.M > 32 && tiles(4, 4) > cus) {
     if constexpr (X_FP4) {
@@ -387,9 +387,9 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool 
   auto whole = [](const void* p, int64_t ld, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0 && ld % n == 0; };
   // 256 x 256 tiles from two for five CUs on: 4096 x 2048 x 4096 (128 tiles) takes 32 us so and 45 in small
   // tiles, 3000 x 2500 x 2500 (120) 28 and 36, 1500 x 4096 x 500 (96) 11.6 and 11.8, 1000 x 4096 x 4096 (64)
-  // 30 and 23
+  // 30 and 23.  Its bias is read with 32-bit offsets.
   const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
-  if (x_fp4 && K > 0 && 5 * tiles >= 2 * device_cu_count() && whole(xs, ld_xs, 16) && whole(ws, ld_ws, 16))
+  if (x_fp4 && K > 0 && 5 * tiles >= 2 * device_cu_count() && N < (int64_t)1 << 29 && whole(xs, ld_xs, 16) && whole(ws, ld_ws, 16))
     return launch_gemm_fp4_tile(M, N, K, (const uint8_t*)x, ld_x, xs, ld_xs, wc, ld_w, ws, ld_ws, ep, st);
   Fp4Args a{};
   a.M = (int)M;

@@ -339,7 +339,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm4_tile(int M, int N, int K,
   // chunk index XOR (row & 7), then store whole 16-byte row pieces (E = bytes per value); where the tile
   // or the matrix ends, or y is not aligned, piece by piece with its bounds (element by element, as the
   // fragments lie, a ragged tile took 15 us longer than a whole one)
-  const bool whole = ep.y_vec16 && m0 + BM <= M && n0 + BN <= N;
+  const bool whole = ep.y_vec16 && M - m0 >= BM && N - n0 >= BN;
   auto store_staged = [&](auto e_c) {
     constexpr int E = decltype(e_c)::value;
     constexpr int RB = 64 * E;                       // bytes per staged row
@@ -425,6 +425,7 @@ hipError_t launch(int64_t M, int64_t N, int64_t K, const uint8_t* xc, int64_t ld
     attr_set[dev] = true;
   }
   const int tiles_m = (int)((M + BM - 1) / BM), tiles_n = (int)((N + BN - 1) / BN);
+  if ((int64_t)tiles_m * tiles_n > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL(kern, dim3(tiles_m * tiles_n), dim3(kThreads), kLdsBytes, stream, (int)M, (int)N, (int)K, tiles_m,
                      tiles_n, xc, ld_x, xs, ld_xs, wc, ld_w, ws, ld_ws, ep);
   return hipGetLastError();
