@@ -237,8 +237,12 @@ __device__ __forceinline__ void multiply_bf16(uint32_t w, uint32_t x, int u, int
 
 template <bool X_FP4, int SPLIT, int MT, int NT>
 __global__ __launch_bounds__(64 * SPLIT, 2) void k_gemm4_split(const Fp4Args a, const GemmEpilogue ep) {
-  const int wg = xcd_order(blockIdx.x, a.tiles_m * a.tiles_n);
-  const int m0 = (wg % a.tiles_m) * 16 * MT, n0 = (wg / a.tiles_m) * 16 * NT;
+  // in groups of four tile rows, so that what an XCD works on at a time shares rows of both operands: column
+  // by column over all rows 8192 x 4096 x 4096 with X in bf16 took 565 us against 315, 8192 x 500 x 1500 in
+  // MXFP4 19.4 against 13.9
+  int tm, tn;
+  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
+  const int m0 = tm * 16 * MT, n0 = tn * 16 * NT;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lw = (uint32_t)wave * split_wave_lds(X_FP4, MT, NT), lx = lw + rows4_lds(NT);
