@@ -357,7 +357,9 @@ hipError_t launch_split(Fp4Args a, const GemmEpilogue& ep, hipStream_t st) {
 // 4), 2048 rows 83 with 1 (141 with 4).  K of at most 1024 leaves many waves less than a piece each: 64 x 32
 // tiles by two waves for X in MXFP4 (3000 x 1500 x 800 13.3 us, 15.6 in 64 x 64 by four; 1500 x 4096 x 500
 // 11.3 and 17.3), and 32 x 32 by four where there are fewer.  Else the largest tile that still gives
-// every CU a workgroup.
+// every CU a workgroup, by four waves where it gives one to some CUs twice (30 x 32768 x 4096 20.6 us, 24.8
+// by eight), and for up to 16 rows no wider than 32 columns (1 x 65536 x 4096 29.9 us, 40.5 with 64; 1 x 8192
+// x 5120 7.5 and 9.6).
 template <bool X_FP4>
 hipError_t launch_rows(const Fp4Args& a, const GemmEpilogue& ep, hipStream_t st) {
   const int64_t cus = device_cu_count();
@@ -374,11 +376,12 @@ hipError_t launch_rows(const Fp4Args& a, const GemmEpilogue& ep, hipStream_t st)
   if (a.M > 32 && !brief && tiles(4, 4) == cus) return launch_split<X_FP4, 8, 4, 4>(a, ep, st);
   if (a.M > 16) {
     if (brief && tiles(2, 2) >= cus) return launch_split<X_FP4, 4, 2, 2>(a, ep, st);
-    if (tiles(2, 4) >= cus) return launch_split<X_FP4, 8, 2, 4>(a, ep, st);
+    if (tiles(2, 4) > cus) return launch_split<X_FP4, 4, 2, 4>(a, ep, st);
+    if (tiles(2, 4) == cus) return launch_split<X_FP4, 8, 2, 4>(a, ep, st);
     if (tiles(2, 2) >= cus) return launch_split<X_FP4, 8, 2, 2>(a, ep, st);
     return launch_split<X_FP4, 8, 2, 1>(a, ep, st);
   }
-  if (tiles(1, 4) >= cus) return launch_split<X_FP4, 8, 1, 4>(a, ep, st);
+  if (brief) return tiles(1, 2) >= cus ? launch_split<X_FP4, 4, 1, 2>(a, ep, st) : launch_split<X_FP4, 4, 1, 1>(a, ep, st);
   if (tiles(1, 2) >= cus) return launch_split<X_FP4, 8, 1, 2>(a, ep, st);
   return launch_split<X_FP4, 8, 1, 1>(a, ep, st);
 }

@@ -554,3 +554,14 @@ def test_gemm_tiles_and_splits(xt, M, N, K):
         y = mxq.gemm_fp4(x, xs, w, ws, K, bias=bias, act=act, out=wide[1:M + 1, :N])
         check_product(y, *ref.product(xv, wv, 1.0, f64(bias), act, out == BF16), "%s %s" % (out, act))
         assert (wide[1:M + 1, N:] == 7.0).all() and (wide[0] == 7.0).all() and (wide[M + 1] == 7.0).all()
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp4"])
+@pytest.mark.parametrize("M,N,K", [(1, 9000, 1100), (16, 8200, 200), (3, 500, 1030), (20, 17000, 1040), (32, 4100, 1100), (48, 8300, 1100),
+                                   (9, 300, 700)])
+def test_gemm_few_rows_many_columns(xt, M, N, K):
+    rng = np.random.default_rng(45)
+    x, xs, xv = operand(rng, M, K) if xt == "fp4" else bf16_operand(rng, M, K, 1)
+    w, ws, wv = operand(rng, N, K, 1)
+    say("gemm_fp4 %s %dx%dx%d" % (xt, M, N, K))
+    check_product(mxq.gemm_fp4(x, xs, w, ws, K, out_dtype=F32), *ref.product(xv, wv), "%dx%dx%d" % (M, N, K))
