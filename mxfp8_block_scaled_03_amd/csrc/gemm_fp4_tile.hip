@@ -18,7 +18,7 @@
 // the matrix's rows return zero through the descriptors; in the last, partial step codes at
 // k >= K are zeroed and the scale of a block >= nb is 127.
 //
-// What bounds it: power and the movement of operands.  8192 x 4096 x 4096 takes 78 us (3.5 PFLOP/s),
+// What bounds it: power and the movement of operands.  8192 x 4096 x 4096 takes 75-80 us (3.4-3.7 PFLOP/s),
 // 16384 deep 318 us at a clock that falls to 1.7 GHz; there the MFMAs are busy 55 % of the cycles.  Of
 // the 318 us a copy of this kernel without the DMA needs 262, without the LDS reads of fragments
 // 324, without both 250, with all codes zero 221: taking a step's scales four at a time (their 4-byte
