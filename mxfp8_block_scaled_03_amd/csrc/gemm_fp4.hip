@@ -1,5 +1,6 @@
 // gemm_fp4.hip -- Y = act(alpha * (X W) + bias) with W in MXFP4 and X in bf16 or MXFP4, for
 // gfx950: the choice of kernel, and the kernel of few rows or tiles (fp4_stream.hpp).
+#include "fp4_ranges.hpp"
 #include "fp4_stream.hpp"
 
 namespace mxq {
@@ -27,7 +28,7 @@ __device__ __forceinline__ void store4(const GemmEpilogue& ep, int64_t row, int 
   if (ep.y_bf16) {
     uint16_t* p = reinterpret_cast<uint16_t*>(ep.y) + row * ep.ld_y + col;
     const uint32_t d[2] = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-    if (col + 4 <= N) {
+    if (whole_group(col, N)) {
       __builtin_memcpy(p, d, 8);
     } else {
 #pragma unroll
@@ -36,7 +37,7 @@ __device__ __forceinline__ void store4(const GemmEpilogue& ep, int64_t row, int 
     }
   } else {
     float* p = reinterpret_cast<float*>(ep.y) + row * ep.ld_y + col;
-    if (col + 4 <= N) {
+    if (whole_group(col, N)) {
       __builtin_memcpy(p, &v, 16);
     } else {
 #pragma unroll
@@ -315,9 +316,9 @@ __global__ __launch_bounds__(64 * SPLIT, 2) void k_gemm4_split(const Fp4Args a, 
   }
 }
 
-// K < 8 with X in bf16, where a row has no whole 16-byte piece: a thread a value of Y.
+// K < 8 with X in bf16, where a row has no whole 16-byte piece: a thread four columns of a row of Y.
 __global__ __launch_bounds__(256) void k_gemm4_short(const Fp4Args a, const GemmEpilogue ep) {
-  const int n4 = (a.N + 3) / 4;
+  const int n4 = column_groups(a.N);
   const int64_t q = blockIdx.x * 256ll + threadIdx.x;
   const int64_t m = q / n4;
   const int n0 = 4 * (int)(q % n4);
@@ -411,7 +412,7 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool 
   a.ws = ws;
   a.ld_ws = ld_ws;
   if (!x_fp4 && K > 0 && K < 8) {
-    const int64_t blocks = (M * ((N + 3) / 4) + 255) / 256;
+    const int64_t blocks = (M * column_groups(a.N) + 255) / 256;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL(k_gemm4_short, dim3((unsigned)blocks), dim3(256), 0, st, a, ep);
     return hipGetLastError();

@@ -1,0 +1,35 @@
+"""The index arithmetic of the MXFP4 kernels (csrc/fp4_ranges.hpp) at the ends of its range, compiled for
+the host and compared with Python's unbounded integers."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "mxfp8_block_scaled_03_amd", "csrc")
+SHIM = """
+#include "fp4_ranges.hpp"
+extern "C" {
+int column_groups(int n) { return mxq::column_groups(n); }
+int whole_group(int col, int n) { return mxq::whole_group(col, n); }
+}
+"""
+TOP = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def ranges(tmp_path_factory):
+    d = tmp_path_factory.mktemp("ranges")
+    (d / "shim.cpp").write_text(SHIM)
+    # -fwrapv: an overflow wraps, as it does on the GPU, instead of leaving the compiler free
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fwrapv", "-shared", "-fPIC", "-I", CSRC, str(d / "shim.cpp"), "-o",
+                    str(d / "shim.so")], check=True)
+    return ctypes.CDLL(str(d / "shim.so"))
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 8, 1000, 2 ** 24 + 1, TOP - 4, TOP - 3, TOP - 2, TOP - 1, TOP])
+def test_column_groups(ranges, n):
+    groups = -(-n // 4)
+    assert ranges.column_groups(n) == groups
+    for col in {0, 4 * (groups // 2), 4 * max(groups - 2, 0), 4 * (groups - 1)}:
+        assert ranges.whole_group(col, n) == (col + 4 <= n), col

@@ -565,3 +565,46 @@ def test_gemm_few_rows_many_columns(xt, M, N, K):
     w, ws, wv = operand(rng, N, K, 1)
     say("gemm_fp4 %s %dx%dx%d" % (xt, M, N, K))
     check_product(mxq.gemm_fp4(x, xs, w, ws, K, out_dtype=F32), *ref.product(xv, wv), "%dx%dx%d" % (M, N, K))
+
+
+# ------------------------------------------------------------ the most columns that there may be
+
+TOP = 2 ** 31 - 1
+PIECE = 1 << 24
+
+
+def top_weights(K):
+    """W with 2^31 - 1 rows: zeros but for the first and the last byte of a row, which repeat every PIECE
+    rows; and the float64 values of the elements that they hold."""
+    rng = np.random.default_rng(50)
+    w = torch.zeros((TOP, 16), dtype=torch.uint8, device=DEV)
+    s = torch.full((TOP, 1), 127, dtype=torch.uint8, device=DEV)
+    first, last = (rng.integers(0, 256, PIECE, dtype=np.uint8) for _ in range(2))
+    for at, b in ((0, first), ((K - 1) // 2, last)):
+        b = torch.from_numpy(b).to(DEV)
+        for c in range(0, TOP, PIECE):
+            w[c:c + PIECE, at] = b[:min(PIECE, TOP - c)]
+    table = np.concatenate([ref.MAG, -ref.MAG])
+    lo, hi = (table[v] for v in (first & 15, first >> 4))
+    return w, s, torch.from_numpy(np.stack([lo, hi, table[last & 15], table[last >> 4]])).to(DEV)
+
+
+def check_top(call, want, rows):
+    """call(y) fills y [rows][TOP]; every column against `want` [rows][PIECE], which repeats; nothing is
+    written beside y."""
+    flat = torch.full((rows * TOP + 64,), 7.0, dtype=BF16, device=DEV)
+    y = flat[32:32 + rows * TOP].view(rows, TOP)
+    call(y)
+    want = want.to(BF16)
+    for c in range(0, TOP, PIECE):
+        assert torch.equal(y[:, c:c + PIECE], want[:, :min(PIECE, TOP - c)]), c
+    assert (flat[:32] == 7.0).all() and (flat[-32:] == 7.0).all()
+
+
+def test_gemm_short_rows_of_most_columns():
+    """K < 8 at N = 2^31 - 1, whose last group of columns has three.  All sums are exact in bf16: multiples
+    of 1/2 of at most 54."""
+    w, s, v = top_weights(2)
+    x = torch.tensor([[1.0, 8.0], [-8.0, 1.0]], dtype=BF16, device=DEV)
+    say("gemm_fp4 bf16 2x%dx2" % TOP)
+    check_top(lambda y: mxq.gemm_fp4(x, None, w, s, 2, out=y), x.double() @ v[2:], 2)
