@@ -11,4 +11,16 @@ namespace mxq {
 constexpr int column_groups(int n) { return (n - 1) / 4 + 1; }
 constexpr bool whole_group(int col, int n) { return n - col >= 4; }
 
+// The grid of n workgroups (n < 2^31).  A launch takes less than 2^32 threads along x, 2^23 workgroups of
+// 512, so more than 2^22 workgroups continue along y; those that fill up the last row, numbers from n on,
+// have nothing to do.  2^22 is a multiple of the XCDs, so the order in which they are dealt goes on.
+constexpr int kGridX = 1 << 22;
+struct Grid {
+  uint32_t x, y;
+};
+constexpr Grid grid_of(int64_t n) {
+  return n <= kGridX ? Grid{(uint32_t)n, 1} : Grid{(uint32_t)kGridX, (uint32_t)((n + kGridX - 1) / kGridX)};
+}
+constexpr int workgroup_at(uint32_t x, uint32_t y) { return (int)(x + y * kGridX); }
+
 }  // namespace mxq

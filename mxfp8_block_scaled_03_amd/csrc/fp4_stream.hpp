@@ -22,6 +22,7 @@
 // for every row tile; the waves' sums meet in LDS at the end and are added in wave order.
 #pragma once
 #include "codec4.hpp"
+#include "fp4_ranges.hpp"
 #include "gemm_common.hpp"
 
 namespace mxq {

@@ -1,6 +1,5 @@
 // gemm_fp4.hip -- Y = act(alpha * (X W) + bias) with W in MXFP4 and X in bf16 or MXFP4, for
 // gfx950: the choice of kernel, and the kernel of few rows or tiles (fp4_stream.hpp).
-#include "fp4_ranges.hpp"
 #include "fp4_stream.hpp"
 
 namespace mxq {
@@ -241,8 +240,10 @@ __global__ __launch_bounds__(64 * SPLIT, 2) void k_gemm4_split(const Fp4Args a, 
   // in groups of four tile rows, so that what an XCD works on at a time shares rows of both operands: column
   // by column over all rows 8192 x 4096 x 4096 with X in bf16 took 565 us against 315, 8192 x 500 x 1500 in
   // MXFP4 19.4 against 13.9
+  const int wg = workgroup_at(blockIdx.x, blockIdx.y);
+  if (wg >= a.tiles_m * a.tiles_n) return;
   int tm, tn;
-  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
+  tile_of(wg, a.tiles_m, a.tiles_n, tm, tn);
   const int m0 = tm * 16 * MT, n0 = tn * 16 * NT;
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(64 * SPLIT, 2) void k_gemm4_split(const Fp4Args a, 
 // K < 8 with X in bf16, where a row has no whole 16-byte piece: a thread four columns of a row of Y.
 __global__ __launch_bounds__(256) void k_gemm4_short(const Fp4Args a, const GemmEpilogue ep) {
   const int n4 = column_groups(a.N);
-  const int64_t q = blockIdx.x * 256ll + threadIdx.x;
+  const int64_t q = workgroup_at(blockIdx.x, blockIdx.y) * 256ll + threadIdx.x;
   const int64_t m = q / n4;
   const int n0 = 4 * (int)(q % n4);
   if (m >= a.M) return;
@@ -347,7 +348,8 @@ hipError_t launch_split(Fp4Args a, const GemmEpilogue& ep, hipStream_t st) {
   constexpr int lds = split_lds(X_FP4, SPLIT, MT, NT);
   const hipError_t e = allow_lds(kern, lds, set);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(64 * SPLIT), lds, st, a, ep);
+  const Grid grid = grid_of((int64_t)a.tiles_m * a.tiles_n);
+  hipLaunchKernelGGL(kern, dim3(grid.x, grid.y), dim3(64 * SPLIT), lds, st, a, ep);
   return hipGetLastError();
 }
 
@@ -414,7 +416,8 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool 
   if (!x_fp4 && K > 0 && K < 8) {
     const int64_t blocks = (M * column_groups(a.N) + 255) / 256;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_gemm4_short, dim3((unsigned)blocks), dim3(256), 0, st, a, ep);
+    const Grid grid = grid_of(blocks);
+    hipLaunchKernelGGL(k_gemm4_short, dim3(grid.x, grid.y), dim3(256), 0, st, a, ep);
     return hipGetLastError();
   }
   return x_fp4 ? launch_rows<true>(a, ep, st) : launch_rows<false>(a, ep, st);

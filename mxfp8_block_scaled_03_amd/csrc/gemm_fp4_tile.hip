@@ -24,6 +24,7 @@
 // 324, without both 250, with all codes zero 221: taking a step's scales four at a time (their 4-byte
 // reads are the only LDS reads with bank conflicts), DMA in lines of 128 bytes and DMA beside the LDS
 // reads instead of between the MFMAs gain nothing.
+#include "fp4_ranges.hpp"
 #include "gemm_common.hpp"
 
 namespace mxq {
@@ -113,8 +114,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm4_tile(int M, int N, int K,
                                                            const uint8_t* __restrict__ wc, int64_t ld_w,
                                                            const uint8_t* __restrict__ ws, int64_t ld_ws,
                                                            const GemmEpilogue ep) {
+  const int wg = workgroup_at(blockIdx.x, blockIdx.y);
+  if (wg >= tiles_m * tiles_n) return;
   int tm, tn;
-  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  tile_of(wg, tiles_m, tiles_n, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
 
   const int lane = threadIdx.x & 63;
@@ -426,8 +429,9 @@ hipError_t launch(int64_t M, int64_t N, int64_t K, const uint8_t* xc, int64_t ld
   }
   const int tiles_m = (int)((M + BM - 1) / BM), tiles_n = (int)((N + BN - 1) / BN);
   if ((int64_t)tiles_m * tiles_n > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kern, dim3(tiles_m * tiles_n), dim3(kThreads), kLdsBytes, stream, (int)M, (int)N, (int)K, tiles_m,
-                     tiles_n, xc, ld_x, xs, ld_xs, wc, ld_w, ws, ld_ws, ep);
+  const Grid grid = grid_of((int64_t)tiles_m * tiles_n);
+  hipLaunchKernelGGL(kern, dim3(grid.x, grid.y), dim3(kThreads), kLdsBytes, stream, (int)M, (int)N, (int)K, tiles_m, tiles_n,
+                     xc, ld_x, xs, ld_xs, wc, ld_w, ws, ld_ws, ep);
   return hipGetLastError();
 }
 

@@ -58,10 +58,11 @@ __global__ __launch_bounds__(kThreads) void k_moe_route(const MoeArgs a) {
   }
 }
 
-// The work of a workgroup: neighbours on one XCD where every slot has some; dealt round where many
-// slots may have none, whose XCDs would be left idle.
+// The work of a workgroup, -1 where there is none: neighbours on one XCD where every slot has some; dealt
+// round where many slots may have none, whose XCDs would be left idle.
 __device__ __forceinline__ int work_of(const MoeArgs& a) {
-  return a.by_token ? (int)blockIdx.x : xcd_order(blockIdx.x, a.slots * a.tiles);
+  const int wg = workgroup_at(blockIdx.x, blockIdx.y);
+  return wg >= a.slots * a.tiles ? -1 : a.by_token ? wg : xcd_order(wg, a.slots * a.tiles);
 }
 
 // The expert of a slot, or -1.
@@ -96,6 +97,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
   int* s_row = reinterpret_cast<int*>(smem + stream_lds<1, NTW>());
   __shared__ int s_cnt;
   const int wg = work_of(a);
+  if (wg < 0) return;
   const int slot = wg / a.tiles, tile = wg % a.tiles;
   const int lane = threadIdx.x & 63, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -174,6 +176,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_down(const MoeArgs a) {
   int* s_row = reinterpret_cast<int*>(smem + stream_lds<1, NTW>());
   __shared__ int s_cnt;
   const int wg = work_of(a);
+  if (wg < 0) return;
   const int slot = wg / a.tiles, tile = wg % a.tiles;
   const int lane = threadIdx.x & 63, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -294,7 +297,8 @@ hipError_t launch_up(MoeArgs a, hipStream_t st) {
   auto kern = k_moe_up<NTW, KIND>;
   const hipError_t e = allow_lds(kern, stream_lds<1, NTW>() + 4 * 1024, set);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.slots * a.tiles)), dim3(kThreads), (stream_lds<1, NTW>() + 4 * a.T), st, a);
+  const Grid grid = grid_of((int64_t)a.slots * a.tiles);
+  hipLaunchKernelGGL(kern, dim3(grid.x, grid.y), dim3(kThreads), (stream_lds<1, NTW>() + 4 * a.T), st, a);
   return hipGetLastError();
 }
 
@@ -306,7 +310,8 @@ hipError_t launch_down(MoeArgs a, hipStream_t st) {
   auto kern = k_moe_down<NTW, KIND>;
   const hipError_t e = allow_lds(kern, stream_lds<1, NTW>() + 4 * 1024, set);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(a.slots * a.tiles)), dim3(kThreads), (stream_lds<1, NTW>() + 4 * a.T), st, a);
+  const Grid grid = grid_of((int64_t)a.slots * a.tiles);
+  hipLaunchKernelGGL(kern, dim3(grid.x, grid.y), dim3(kThreads), (stream_lds<1, NTW>() + 4 * a.T), st, a);
   return hipGetLastError();
 }
 

@@ -9,6 +9,7 @@
 // by the integer multiplies of Philox, five of 32 x 32 bits an element (4096 x 4096 bf16 19 us
 // along rows, 22 down columns; 4095 x 4001 fp32 down columns 25).
 #include "codec4.hpp"
+#include "fp4_ranges.hpp"
 #include "internal.hpp"
 
 namespace mxq {
@@ -124,8 +125,9 @@ __global__ __launch_bounds__(kThreads) void k_quant4_tile(const char* __restrict
   extern __shared__ __align__(16) uint32_t tile[];
   const int tid = threadIdx.x;
   const int lane = tid & 63, wv = tid >> 6;
-  const int64_t t = (int64_t)(blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
-  if (t >= ntiles) return;                           // the whole workgroup, before any barrier
+  const int wg = workgroup_at(blockIdx.x, blockIdx.y);
+  const int64_t t = (wg % kXcds) * per_xcd + wg / kXcds;
+  if (wg / kXcds >= per_xcd || t >= ntiles) return;  // the whole workgroup, before any barrier
   const int64_t gy = ntiles / gx;
   const int64_t band = t / (8 * gx), rem = t - band * 8 * gx;
   const int64_t hb = gy - 8 * band < 8 ? gy - 8 * band : 8;
@@ -205,7 +207,8 @@ hipError_t launch_tile(const void* src, int64_t rows, int64_t cols, int64_t ld_s
   const int64_t per_xcd = (n + kXcds - 1) / kXcds;
   if (kXcds * per_xcd > 0x7FFFFFFF) return hipErrorInvalidValue;
   const int lds = 128 * 128 * (SRC_BF16 ? 2 : 4);
-  hipLaunchKernelGGL((k_quant4_tile<SRC_BF16, ROWS, SR, R>), dim3((unsigned)(kXcds * per_xcd)), dim3(kThreads), lds, st,
+  const Grid grid = grid_of(kXcds * per_xcd);
+  hipLaunchKernelGGL((k_quant4_tile<SRC_BF16, ROWS, SR, R>), dim3(grid.x, grid.y), dim3(kThreads), lds, st,
                      (const char*)src, rows, cols, ld_src, rc, ld_rc, rs, ld_rs, cc, ld_cc, cs, ld_cs, gx, n, per_xcd,
                      seed);
   return hipGetLastError();

@@ -12,6 +12,8 @@ SHIM = """
 extern "C" {
 int column_groups(int n) { return mxq::column_groups(n); }
 int whole_group(int col, int n) { return mxq::whole_group(col, n); }
+void grid_of(int64_t n, uint32_t out[2]) { const mxq::Grid g = mxq::grid_of(n); out[0] = g.x; out[1] = g.y; }
+int64_t workgroup_at(uint32_t x, uint32_t y) { return mxq::workgroup_at(x, y); }
 }
 """
 TOP = 2 ** 31 - 1
@@ -33,3 +35,17 @@ def test_column_groups(ranges, n):
     assert ranges.column_groups(n) == groups
     for col in {0, 4 * (groups // 2), 4 * max(groups - 2, 0), 4 * (groups - 1)}:
         assert ranges.whole_group(col, n) == (col + 4 <= n), col
+
+
+@pytest.mark.parametrize("n", [1, 2, 255, 2 ** 20 + 1, 2 ** 22 - 1, 2 ** 22, 2 ** 22 + 1, 3 * 2 ** 22, 2 ** 24, 2 ** 26 + 5, TOP])
+def test_grid(ranges, n):
+    """Every number below n exactly once (the rows of the grid are whole but for the last), below 2^32
+    threads along x and 2^16 workgroups along y, the launch's limits, at up to 512 threads a workgroup."""
+    ranges.workgroup_at.restype = ctypes.c_int64
+    out = (ctypes.c_uint32 * 2)()
+    ranges.grid_of(ctypes.c_int64(n), out)
+    x, y = out
+    assert 1 <= x and x * 512 < 2 ** 32 and 1 <= y < 2 ** 16
+    assert x * (y - 1) < n <= x * y
+    for c, r in ((0, 0), (x - 1, 0), (0, y - 1), (x - 1, y - 1), (x // 2, y // 2)):
+        assert ranges.workgroup_at(c, r) == r * x + c

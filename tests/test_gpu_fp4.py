@@ -608,3 +608,90 @@ def test_gemm_short_rows_of_most_columns():
     x = torch.tensor([[1.0, 8.0], [-8.0, 1.0]], dtype=BF16, device=DEV)
     say("gemm_fp4 bf16 2x%dx2" % TOP)
     check_top(lambda y: mxq.gemm_fp4(x, None, w, s, 2, out=y), x.double() @ v[2:], 2)
+
+
+@pytest.mark.parametrize("xt", ["bf16", "fp4"])
+def test_gemm_one_row_of_most_columns(xt):
+    """One row and one block of K at N = 2^31 - 1: more workgroups than a row of the grid takes.  All sums are
+    exact in bf16: multiples of 1/2 of at most 72."""
+    K = 32
+    w, s, v = top_weights(K)
+    say("gemm_fp4 %s 1x%dx%d" % (xt, TOP, K))
+    xv = torch.zeros((1, K), dtype=F32, device=DEV)
+    xv[0, [0, 1, 30, 31]] = torch.tensor([1.0, 4.0, -4.0, 3.0], device=DEV)
+    x, xs = mxq.quantize_fp4(xv) if xt == "fp4" else (xv.to(BF16), None)
+    check_top(lambda y: mxq.gemm_fp4(x, xs, w, s, K, out=y), xv[:, [0, 1, 30, 31]].double() @ v, 1)
+
+
+def test_gemm_short_rows_of_many_rows_and_columns():
+    """K < 8 where four columns a thread are more than 2^32 threads."""
+    M, N, K = 1 << 17, (1 << 17) + 3, 1
+    w = torch.full((N, 16), 0x22, dtype=torch.uint8, device=DEV)           # all ones
+    s = (torch.arange(N, device=DEV) % 7 + 124).to(torch.uint8)[:, None].contiguous()
+    x = (torch.arange(M, device=DEV) % 251).to(BF16)[:, None]
+    say("gemm_fp4 bf16 %dx%dx%d" % (M, N, K))
+    y = mxq.gemm_fp4(x, None, w, s, K)
+    scale = torch.exp2(s[:, 0].float() - 127)
+    for c in range(0, M, 4096):
+        assert torch.equal(y[c:c + 4096], (x[c:c + 4096].float() * scale).to(BF16)), c
+
+
+def test_quantize_column_of_most_rows():
+    """2^24 tiles of a single column: more workgroups than a row of the grid takes."""
+    x = torch.zeros((TOP, 1), dtype=BF16, device=DEV)
+    n = 1 << 20
+    part = torch.randn((n, 1), device=DEV).to(BF16)
+    x[:n], x[TOP - n:] = part, part
+    x[1 << 30:(1 << 30) + n] = part
+    say("quantize_fp4 %dx1, columns" % TOP)
+    c, s = mxq.quantize_fp4(x, "col")
+    # the last rows begin inside a block, so their blocks are those of the rows from that block on
+    for r in (0, 1 << 30, (TOP - n) // 32 * 32):
+        want = mxq.quantize_fp4(x[r:r + n], "col")
+        assert torch.equal(c[:, r // 2:(r + n) // 2], want[0][:, :n // 2]) and torch.equal(s[:, r // 32:(r + n) // 32], want[1])
+    tail = mxq.quantize_fp4(x[TOP // 32 * 32:], "col")
+    assert torch.equal(c[:, TOP // 32 * 16:], tail[0]) and torch.equal(s[:, TOP // 32:], tail[1])
+    assert (c[:, n // 2:1 << 29] == 0).all() and (s[:, n // 32:1 << 25] == 127).all()
+
+
+def gpu_product(x, w):
+    """ref.product without an epilogue, in float64 on the GPU."""
+    y = x @ w.T
+    return y, (x.shape[1] / 32 + 40) * ref.U * (x.abs() @ w.abs().T) + ref.U * y.abs() + 2.0 ** -149
+
+
+def test_experts_over_many_workgroups():
+    """An up product over more workgroups than a row of the grid takes: 1024 experts, one token each, of 2^18
+    + 64 columns, 64 a workgroup.  H = 30 keeps the persistent kernel out and leaves codes past H to be
+    ignored.  Three of the 16 tokens against float64 on the GPU, with the bounds of ref.moe."""
+    T, H, I, E, k = 16, 30, (1 << 18) + 64, 1024, 64
+    g = torch.Generator(device=DEV)
+    g.manual_seed(51)
+
+    def random(*shape, low=0, high=256):
+        return torch.randint(low, high, shape, generator=g, device=DEV, dtype=torch.uint8)
+    w13, s13 = random(E, 2 * I, 16), random(E, 2 * I, 4, low=122, high=125)[..., :1]
+    w2, s2 = random(E, H, I // 2), random(E, H, I // 32, low=115, high=118)
+    x = torch.randn((T, H), generator=g, device=DEV).to(BF16)
+    own = torch.arange(E, device=DEV) % T == torch.arange(T, device=DEV)[:, None]
+    lg = torch.where(own, torch.randn((T, E), generator=g, device=DEV), torch.tensor(-20.0, device=DEV))
+    say("moe_fp4 T%d H%d I%d E%d k%d" % (T, H, I, E, k))
+    y = mxq.moe_fp4(x, lg, w13, s13, w2, s2, k, out_dtype=BF16).double()
+    for t in (0, 7, 15):
+        ids = torch.nonzero(own[t])[:, 0].tolist()
+        share = torch.softmax(lg[t, ids].double(), 0).tolist()
+        want, bound, total = (torch.zeros(H, dtype=torch.float64, device=DEV) for _ in range(3))
+        for e, p in zip(ids, share):
+            gu, d = gpu_product(x[t:t + 1].double(), mxq.dequantize_fp4(w13[e], s13[e], H).double())
+            gate, up, dg, du = gu[:, :I], gu[:, I:], d[:, :I], d[:, I:]
+            act = gate * torch.sigmoid(gate)
+            h = p * act * up
+            dh = p * (1.1 * dg * (up.abs() + du) + act.abs() * du) + (2.0 ** -19 + 2.0 ** -16) * h.abs()
+            v = mxq.dequantize_fp4(w2[e], s2[e], I).double()
+            size = ((h.abs() + dh) @ v.abs().T)[0]
+            want += (h @ v.T)[0]
+            total += size
+            bound += (dh @ v.abs().T)[0] + (I / 32 + 40) * ref.U * size
+        bound += k * ref.U * total
+        bound += 2.0 ** -8 * (want.abs() + bound) + 2.0 ** -149
+        assert ((y[t] - want).abs() <= bound).all(), t
