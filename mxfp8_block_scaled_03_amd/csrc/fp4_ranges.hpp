@@ -11,6 +11,12 @@ namespace mxq {
 constexpr int column_groups(int n) { return (n - 1) / 4 + 1; }
 constexpr bool whole_group(int col, int n) { return n - col >= 4; }
 
+// Bytes from the first of `rows` rows of scales to the last one's end: its nb bytes, or, where rows are read
+// by 4-byte words, the word that holds the last of them.  What lies behind may be another's, or no memory.
+constexpr uint32_t scale_bytes(int64_t rows, int64_t ld, int nb, bool words) {
+  return (uint32_t)((rows - 1) * ld + (words ? (nb + 3) & ~3 : nb));
+}
+
 // The grid of n workgroups (n < 2^31).  A launch takes less than 2^32 threads along x, 2^23 workgroups of
 // 512, so more than 2^22 workgroups continue along y; those that fill up the last row, numbers from n on,
 // have nothing to do.  2^22 is a multiple of the XCDs, so the order in which they are dealt goes on.

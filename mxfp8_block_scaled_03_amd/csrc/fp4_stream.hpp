@@ -87,7 +87,7 @@ __device__ __forceinline__ Lines lines_of(const uint8_t* c, int64_t ld_c, const 
   l.ld_c = (uint32_t)ld_c;
   l.ld_s = (uint32_t)ld_s;
   l.c_bytes = (uint32_t)((int64_t)(rows - 1) * ld_c + 16 * nb);
-  l.s_bytes = (uint32_t)((int64_t)(rows - 1) * ld_s + ((nb + 3) & ~3));
+  l.s_bytes = scale_bytes(rows, ld_s, nb, s_words);
   l.s_words = s_words;
   l.first = 1 << 30;
   l.far_c = l.far_s = 0;

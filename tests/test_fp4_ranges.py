@@ -14,6 +14,7 @@ int column_groups(int n) { return mxq::column_groups(n); }
 int whole_group(int col, int n) { return mxq::whole_group(col, n); }
 void grid_of(int64_t n, uint32_t out[2]) { const mxq::Grid g = mxq::grid_of(n); out[0] = g.x; out[1] = g.y; }
 int64_t workgroup_at(uint32_t x, uint32_t y) { return mxq::workgroup_at(x, y); }
+uint32_t scale_bytes(int64_t rows, int64_t ld, int nb, int words) { return mxq::scale_bytes(rows, ld, nb, words); }
 }
 """
 TOP = 2 ** 31 - 1
@@ -49,3 +50,14 @@ def test_grid(ranges, n):
     assert x * (y - 1) < n <= x * y
     for c, r in ((0, 0), (x - 1, 0), (0, y - 1), (x - 1, y - 1), (x // 2, y // 2)):
         assert ranges.workgroup_at(c, r) == r * x + c
+
+
+@pytest.mark.parametrize("rows,ld,nb", [(1, 1, 1), (16, 5, 5), (11, 5, 5), (3, 7, 6), (9, 21, 18), (64, 2 ** 24 - 1, 2 ** 19)])
+def test_scale_bytes(ranges, rows, ld, nb):
+    """Read byte by byte, scales end with the last row's last one, wherever that lies; read by words (rows
+    that are whole 4-byte words apart), with the word that holds it."""
+    ranges.scale_bytes.restype = ctypes.c_uint32
+    args = ctypes.c_int64(rows), ctypes.c_int64(ld), nb
+    assert ranges.scale_bytes(*args, 0) == (rows - 1) * ld + nb
+    ld = -(-ld // 4) * 4
+    assert ranges.scale_bytes(args[0], ctypes.c_int64(ld), nb, 1) == -(-((rows - 1) * ld + nb) // 4) * 4
