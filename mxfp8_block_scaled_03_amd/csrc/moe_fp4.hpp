@@ -132,7 +132,8 @@ __device__ __forceinline__ int64_t h_offset(int m, int k) {
 }
 
 // Four hidden values, elements 4 half .. 4 half + 3 of the eight at `to` (plane 0).  The terms are
-// rounded to nearest, so each is exact to 2^-9 of the one before; an infinity has no further term.
+// rounded to nearest, so each is exact to 2^-9 of the one before; an infinity has no further term.  The
+// first term of a finite value past bf16's greatest is that one, and the rest, below 2^120, is for the next.
 template <int KIND>
 __device__ __forceinline__ void store_hidden(uint8_t* to, int half, const float v[4]) {
   uint32_t t[KIND][4];
@@ -142,6 +143,7 @@ __device__ __forceinline__ void store_hidden(uint8_t* to, int half, const float 
 #pragma unroll
     for (int p = 0; p < KIND; ++p) {
       t[p][e] = f32_to_bf16_rne(rest);
+      if (p == 0 && (t[0][e] & 0x7FFFu) == 0x7F80u && __builtin_fabsf(rest) < __builtin_inff()) --t[0][e];
       rest = (t[p][e] & 0x7F80u) == 0x7F80u ? 0.0f : rest - __uint_as_float(t[p][e] << 16);
     }
   }

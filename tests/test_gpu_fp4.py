@@ -695,3 +695,41 @@ def test_experts_over_many_workgroups():
         bound += k * ref.U * total
         bound += 2.0 ** -8 * (want.abs() + bound) + 2.0 ** -149
         assert ((y[t] - want).abs() <= bound).all(), t
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("T,H,I,E", [(3, 32, 16, 4), (3, 32, 16, 264), (200, 72, 120, 512)])
+def test_experts_largest_hidden_values(out, T, H, I, E):
+    """Hidden values next to FP32's largest, which no single bf16 holds: finite ones stay finite and as exact as
+    others, in two and in four launches and in the persistent kernels; infinite ones stay infinite.  h = gate * up
+    with gate = 2^60 and up = +-1.998046875 * 2^67, the sum of two bf16, in column 0, share 1 (k = 1)."""
+    rng = np.random.default_rng(52)
+    w13 = np.zeros((E, 2 * I, 16 * ref.blocks(H)), np.uint8)
+    w13[:, 0, 0] = 0x02                                                    # column 0's gate, element 0: 1
+    w13[:, I, 0], w13[:, I, 1] = 0x20, 0x02                                # and up, elements 1 and 2: 1
+    s13 = np.full((E, 2 * I, ref.blocks(H)), 127, np.uint8)
+    w2 = np.zeros((E, H, 16 * ref.blocks(I)), np.uint8)
+    w2[:, :, 0] = 0x01                                                     # element 0: 1/2
+    s2 = np.full((E, H, ref.blocks(I)), 107, np.uint8)                     # 2^-20
+    x = np.zeros((T, H))
+    x[:, 0], x[:, 1], x[:, 2] = 2.0 ** 60, 1.9921875 * 2.0 ** 67, 0.75 * 2.0 ** 60
+    x[1::3, 1:] *= -1
+    lg = rng.standard_normal((T, E)).astype(np.float32)
+
+    def stack(t):
+        wide = torch.zeros(t.shape[:2] + ((t.shape[2] + 15) // 16 * 16,), dtype=torch.uint8, device=DEV)
+        wide[..., :t.shape[2]] = torch.from_numpy(t).to(DEV)
+        return wide[..., :t.shape[2]]
+    weights = [stack(t) for t in (w13, s13, w2, s2)]
+    xd = torch.from_numpy(x.astype(np.float32)).to(BF16).to(DEV)
+    assert torch.equal(xd.double().cpu(), torch.from_numpy(x))
+    lgd = torch.from_numpy(lg).to(DEV)
+    y = mxq.moe_fp4(xd, lgd, *weights, 1, out_dtype=out)
+    v13 = ref.values(w13.reshape(-1, w13.shape[2]), s13.reshape(-1, s13.shape[2]), H).reshape(E, 2 * I, H)
+    v2 = ref.values(w2.reshape(-1, w2.shape[2]), s2.reshape(-1, s2.shape[2]), I).reshape(E, H, I)
+    want, bound = ref.moe(x[:3], lg[:3].astype(np.float64), v13, v2, 1, True, out == BF16)
+    n = (T + 2) // 3
+    check_product(y, np.tile(want, (n, 1))[:T], np.tile(bound, (n, 1))[:T], "largest hidden values")
+    xd[0, 0] = 2.0 ** 62
+    y = mxq.moe_fp4(xd, lgd, *weights, 1, out_dtype=out)
+    assert torch.isinf(y[0]).all() and torch.isfinite(y[1:]).all()
