@@ -19,7 +19,7 @@ constexpr uint32_t scale_bytes(int64_t rows, int64_t ld, int nb, bool words) {
 
 // The grid of n workgroups (n < 2^31).  A launch takes less than 2^32 threads along x, 2^23 workgroups of
 // 512, so more than 2^22 workgroups continue along y; those that fill up the last row, numbers from n on,
-// have nothing to do.  2^22 is a multiple of the XCDs, so the order in which they are dealt goes on.
+// have nothing to do (a kernel asks only where y > 0: the question waits for its arguments).  2^22 is a multiple of the XCDs, so the order in which they are dealt goes on.
 constexpr int kGridX = 1 << 22;
 struct Grid {
   uint32_t x, y;

@@ -241,7 +241,7 @@ __global__ __launch_bounds__(64 * SPLIT, 2) void k_gemm4_split(const Fp4Args a, 
   // by column over all rows 8192 x 4096 x 4096 with X in bf16 took 565 us against 315, 8192 x 500 x 1500 in
   // MXFP4 19.4 against 13.9
   const int wg = workgroup_at(blockIdx.x, blockIdx.y);
-  if (wg >= a.tiles_m * a.tiles_n) return;
+  if (blockIdx.y > 0 && wg >= a.tiles_m * a.tiles_n) return;
   int tm, tn;
   tile_of(wg, a.tiles_m, a.tiles_n, tm, tn);
   const int m0 = tm * 16 * MT, n0 = tn * 16 * NT;

@@ -115,7 +115,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm4_tile(int M, int N, int K,
                                                            const uint8_t* __restrict__ ws, int64_t ld_ws,
                                                            const GemmEpilogue ep) {
   const int wg = workgroup_at(blockIdx.x, blockIdx.y);
-  if (wg >= tiles_m * tiles_n) return;
+  if (blockIdx.y > 0 && wg >= tiles_m * tiles_n) return;
   int tm, tn;
   tile_of(wg, tiles_m, tiles_n, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;

@@ -58,11 +58,10 @@ __global__ __launch_bounds__(kThreads) void k_moe_route(const MoeArgs a) {
   }
 }
 
-// The work of a workgroup, -1 where there is none: neighbours on one XCD where every slot has some; dealt
-// round where many slots may have none, whose XCDs would be left idle.
-__device__ __forceinline__ int work_of(const MoeArgs& a) {
-  const int wg = workgroup_at(blockIdx.x, blockIdx.y);
-  return wg >= a.slots * a.tiles ? -1 : a.by_token ? wg : xcd_order(wg, a.slots * a.tiles);
+// The work of a workgroup: neighbours on one XCD where every slot has some; dealt round where many
+// slots may have none, whose XCDs would be left idle.
+__device__ __forceinline__ int work_of(const MoeArgs& a, int wg) {
+  return a.by_token ? wg : xcd_order(wg, a.slots * a.tiles);
 }
 
 // The expert of a slot, or -1.
@@ -96,9 +95,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_moe_up(const MoeArgs a) {
   constexpr int IC = 8 * NTW, NG = NTW / 2;
   int* s_row = reinterpret_cast<int*>(smem + stream_lds<1, NTW>());
   __shared__ int s_cnt;
-  const int wg = work_of(a);
-  if (wg < 0) return;
-  const int slot = wg / a.tiles, tile = wg % a.tiles;
+  const int wg = workgroup_at(blockIdx.x, blockIdx.y);
+  if (blockIdx.y > 0 && wg >= a.slots * a.tiles) return;
+  const int work = work_of(a, wg), slot = work / a.tiles, tile = work % a.tiles;
   const int lane = threadIdx.x & 63, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = slot_expert(a, slot);
@@ -175,9 +174,9 @@ template <int NTW, int KIND>
 __global__ __launch_bounds__(kThreads, 2) void k_moe_down(const MoeArgs a) {
   int* s_row = reinterpret_cast<int*>(smem + stream_lds<1, NTW>());
   __shared__ int s_cnt;
-  const int wg = work_of(a);
-  if (wg < 0) return;
-  const int slot = wg / a.tiles, tile = wg % a.tiles;
+  const int wg = workgroup_at(blockIdx.x, blockIdx.y);
+  if (blockIdx.y > 0 && wg >= a.slots * a.tiles) return;
+  const int work = work_of(a, wg), slot = work / a.tiles, tile = work % a.tiles;
   const int lane = threadIdx.x & 63, i = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = slot_expert(a, slot);

@@ -132,19 +132,20 @@ __device__ __forceinline__ int64_t h_offset(int m, int k) {
 }
 
 // Four hidden values, elements 4 half .. 4 half + 3 of the eight at `to` (plane 0).  The terms are
-// rounded to nearest, so each is exact to 2^-9 of the one before; an infinity has no further term.  The
-// first term of a finite value past bf16's greatest is that one, and the rest, below 2^120, is for the next.
+// rounded to nearest, so each is exact to 2^-9 of the one before.  The first one is finite, at most
+// bf16's greatest, so that what FP32 holds beyond it is not lost: the rest, an infinity or a NaN too, is for
+// the next; an infinity has no further term.
 template <int KIND>
 __device__ __forceinline__ void store_hidden(uint8_t* to, int half, const float v[4]) {
+  const float most = __uint_as_float(0x7F7F7FFFu);       // the last that rounds to bf16's greatest
   uint32_t t[KIND][4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     float rest = v[e];
 #pragma unroll
     for (int p = 0; p < KIND; ++p) {
-      t[p][e] = f32_to_bf16_rne(rest);
-      if (p == 0 && (t[0][e] & 0x7FFFu) == 0x7F80u && __builtin_fabsf(rest) < __builtin_inff()) --t[0][e];
-      rest = (t[p][e] & 0x7F80u) == 0x7F80u ? 0.0f : rest - __uint_as_float(t[p][e] << 16);
+      t[p][e] = f32_to_bf16_rne(p == 0 ? __builtin_amdgcn_fmed3f(rest, -most, most) : rest);
+      rest = p > 0 && (t[p][e] & 0x7F80u) == 0x7F80u ? 0.0f : rest - __uint_as_float(t[p][e] << 16);
     }
   }
 #pragma unroll
