@@ -471,6 +471,24 @@ int mxq_moe_fp4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int renor
                 int64_t expert_s2, void* y, int y_type, int64_t ld_y, void* workspace, int64_t workspace_bytes,
                 void* stream);
 
+/*
+ * mxq_gemm_fp4_plan, mxq_moe_fp4_plan -- how mxq_gemm_fp4 and mxq_moe_fp4 would run these sizes on a device of
+ * `cus` compute units (host logic only, no device is touched).  For tuning and tests; they launch nothing.
+ * aligned (0 or 1): scale rows are 16-byte aligned, and for the expert layer rows of x too.
+ *
+ * Outputs (host pointers, all required).  Product: the tile of Y and the waves that share one along K; 256 x 256
+ * by 8 is the kernel of two MXFP4 operands, whose waves share the tile's rows and columns instead, and 1 x 4 by
+ * 0 a thread's columns where K < 8.  Expert layer: launches, 2 (the other outputs are 0) or 4; the columns of I
+ * and of H that a workgroup takes at a time (128 and 256: persistent workgroups); the ranges of I that the down
+ * product is cut into.
+ * Return MXQ_OK, MXQ_ERR_NULL, MXQ_ERR_DTYPE, MXQ_ERR_SHAPE (a size below 1, K < 0, or past the operator's
+ * limits) or MXQ_ERR_ARG (k, aligned, cus < 1).
+ */
+int mxq_gemm_fp4_plan(int64_t M, int64_t N, int64_t K, int x_type, int aligned, int cus, int* tile_m, int* tile_n,
+                      int* waves);
+int mxq_moe_fp4_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int y_type, int aligned, int cus,
+                     int* launches, int* up_columns, int* down_columns, int* down_parts);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* mxq_status_string(int status);
 

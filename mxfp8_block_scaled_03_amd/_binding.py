@@ -82,6 +82,10 @@ def lib():
         L.mxq_gemm_fp4.restype = ci
         L.mxq_gemm_fp4.argtypes = [i64, i64, i64, vp, ci, i64, vp, i64, vp, i64, vp, i64, ctypes.c_float, vp, ci, vp,
                                    ci, i64, vp]
+        L.mxq_gemm_fp4_plan.restype = ci
+        L.mxq_gemm_fp4_plan.argtypes = [i64, i64, i64, ci, ci, ci, ip, ip, ip]
+        L.mxq_moe_fp4_plan.restype = ci
+        L.mxq_moe_fp4_plan.argtypes = [i64, i64, i64, i64, i64, ci, ci, ci, ip, ip, ip, ip]
         L.mxq_moe_fp4_workspace.restype = ci
         L.mxq_moe_fp4_workspace.argtypes = [i64, i64, i64, i64, i64, ci, ctypes.POINTER(i64)]
         L.mxq_moe_fp4.restype = ci
@@ -195,6 +199,22 @@ def mxq_gemm_fp4(M, N, K, x, x_type, ld_x, x_scales, ld_xs, w_codes, ld_w, w_sca
                  y_type, ld_y, stream=None) -> int:
     return lib().mxq_gemm_fp4(M, N, K, x, x_type, ld_x, x_scales, ld_xs, w_codes, ld_w, w_scales, ld_ws, alpha, bias,
                               act, y, y_type, ld_y, stream)
+
+
+def mxq_gemm_fp4_plan(M: int, N: int, K: int, x_type: int, aligned: bool, cus: int) -> tuple:
+    """(tile_m, tile_n, waves) of the MXFP4 product (host logic only); raises MxqError."""
+    out = [ctypes.c_int() for _ in range(3)]
+    st = lib().mxq_gemm_fp4_plan(M, N, K, x_type, aligned, cus, *(ctypes.byref(v) for v in out))
+    _check(st, "mxq_gemm_fp4_plan")
+    return tuple(v.value for v in out)
+
+
+def mxq_moe_fp4_plan(T: int, H: int, I: int, E: int, k: int, y_type: int, aligned: bool, cus: int) -> tuple:
+    """(launches, up_columns, down_columns, down_parts) of the expert layer (host logic only); raises MxqError."""
+    out = [ctypes.c_int() for _ in range(4)]
+    st = lib().mxq_moe_fp4_plan(T, H, I, E, k, y_type, aligned, cus, *(ctypes.byref(v) for v in out))
+    _check(st, "mxq_moe_fp4_plan")
+    return tuple(v.value for v in out)
 
 
 def mxq_moe_fp4_workspace(T, H, I, E, k, y_type) -> int:

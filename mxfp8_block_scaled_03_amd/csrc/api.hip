@@ -46,7 +46,7 @@ const char* mxq_status_string(int status) {
   }
 }
 
-int mxq_version(void) { return 103; }
+int mxq_version(void) { return 104; }
 
 int mxq_gemm_exact_plan(int64_t M, int64_t N, int64_t K, int cus, int* tile_n, int* ranges_per_tile,
                         int* split_tiles, int* whole_tiles, int64_t* workspace_bytes) {

@@ -141,6 +141,34 @@ int mxq_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, int x_type, int
                                          (hipStream_t)stream));
 }
 
+int mxq_gemm_fp4_plan(int64_t M, int64_t N, int64_t K, int x_type, int aligned, int cus, int* tile_m, int* tile_n,
+                      int* waves) {
+  if (!tile_m || !tile_n || !waves) return MXQ_ERR_NULL;
+  if (x_type != MXQ_BF16 && x_type != MXQ_E2M1) return MXQ_ERR_DTYPE;
+  if (M < 1 || N < 1 || K < 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxK) return MXQ_ERR_SHAPE;
+  if (cus < 1 || (aligned != 0 && aligned != 1)) return MXQ_ERR_ARG;
+  const mxq::GemmFp4Plan p = mxq::gemm_fp4_plan(M, N, K, x_type == MXQ_E2M1, aligned != 0, cus);
+  *tile_m = p.tile_m;
+  *tile_n = p.tile_n;
+  *waves = p.waves;
+  return MXQ_OK;
+}
+
+int mxq_moe_fp4_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int y_type, int aligned, int cus,
+                     int* launches, int* up_columns, int* down_columns, int* down_parts) {
+  if (!launches || !up_columns || !down_columns || !down_parts) return MXQ_ERR_NULL;
+  if (!is_wide(y_type)) return MXQ_ERR_DTYPE;
+  if (T < 1 || T > kMaxMoeTokens || H < 1 || H >= kMaxK || I < 1 || I >= kMaxK || E < 1 || E > kMaxExperts)
+    return MXQ_ERR_SHAPE;
+  if (k < 1 || k > E || cus < 1 || (aligned != 0 && aligned != 1)) return MXQ_ERR_ARG;
+  const mxq::MoeFp4Plan p = mxq::moe_fp4_plan(T, H, I, E, k, y_type == MXQ_BF16, aligned != 0, cus);
+  *launches = p.launches;
+  *up_columns = p.up_columns;
+  *down_columns = p.down_columns;
+  *down_parts = p.down_parts;
+  return MXQ_OK;
+}
+
 int mxq_moe_fp4_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int y_type, int64_t* bytes) {
   if (!bytes) return MXQ_ERR_NULL;
   if (!is_wide(y_type)) return MXQ_ERR_DTYPE;

@@ -363,43 +363,65 @@ hipError_t launch_split(Fp4Args a, const GemmEpilogue& ep, hipStream_t st) {
 // every CU a workgroup, by four waves where it gives one to some CUs twice (30 x 32768 x 4096 20.6 us, 24.8
 // by eight), and for up to 16 rows no wider than 32 columns (1 x 65536 x 4096 29.9 us, 40.5 with 64; 1 x 8192
 // x 5120 7.5 and 9.6).
+GemmFp4Plan rows_plan(int64_t M, int64_t N, int64_t K, bool x_fp4, int64_t cus) {
+  auto tiles = [&](int mt, int nt) { return ((M + 16ll * mt - 1) / (16 * mt)) * ((N + 16ll * nt - 1) / (16 * nt)); };
+  auto plan = [](int waves, int mt, int nt) { return GemmFp4Plan{16 * mt, 16 * nt, waves}; };
+  const bool brief = K <= 1024;
+  if (M > 32 && tiles(4, 4) > cus) {
+    if (x_fp4 && brief) return plan(2, 4, 2);
+    return plan(tiles(4, 4) <= 2 * cus ? 4 : tiles(4, 4) <= 4 * cus ? 2 : 1, 4, 4);
+  }
+  if (M > 32 && !brief && tiles(4, 4) == cus) return plan(8, 4, 4);
+  if (M > 16) {
+    if (brief && tiles(2, 2) >= cus) return plan(4, 2, 2);
+    if (tiles(2, 4) > cus) return plan(4, 2, 4);
+    if (tiles(2, 4) == cus) return plan(8, 2, 4);
+    return plan(8, 2, tiles(2, 2) >= cus ? 2 : 1);
+  }
+  return plan(brief ? 4 : 8, 1, tiles(1, 2) >= cus ? 2 : 1);
+}
+
 template <bool X_FP4>
-hipError_t launch_rows(const Fp4Args& a, const GemmEpilogue& ep, hipStream_t st) {
-  const int64_t cus = device_cu_count();
-  auto tiles = [&](int mt, int nt) { return ((a.M + 16ll * mt - 1) / (16 * mt)) * ((a.N + 16ll * nt - 1) / (16 * nt)); };
-  const bool brief = a.K <= 1024;
-  if (a.M > 32 && tiles(4, 4) > cus) {
-    if constexpr (X_FP4) {
-      if (brief) return launch_split<true, 2, 4, 2>(a, ep, st);
-    }
-    if (tiles(4, 4) <= 2 * cus) return launch_split<X_FP4, 4, 4, 4>(a, ep, st);
-    if (tiles(4, 4) <= 4 * cus) return launch_split<X_FP4, 2, 4, 4>(a, ep, st);
-    return launch_split<X_FP4, 1, 4, 4>(a, ep, st);
+hipError_t launch_rows(const GemmFp4Plan& p, const Fp4Args& a, const GemmEpilogue& ep, hipStream_t st) {
+  const int mt = p.tile_m / 16, nt = p.tile_n / 16;
+  auto is = [&](int waves, int m, int n) { return p.waves == waves && mt == m && nt == n; };
+  if constexpr (X_FP4) {
+    if (is(2, 4, 2)) return launch_split<true, 2, 4, 2>(a, ep, st);
   }
-  if (a.M > 32 && !brief && tiles(4, 4) == cus) return launch_split<X_FP4, 8, 4, 4>(a, ep, st);
-  if (a.M > 16) {
-    if (brief && tiles(2, 2) >= cus) return launch_split<X_FP4, 4, 2, 2>(a, ep, st);
-    if (tiles(2, 4) > cus) return launch_split<X_FP4, 4, 2, 4>(a, ep, st);
-    if (tiles(2, 4) == cus) return launch_split<X_FP4, 8, 2, 4>(a, ep, st);
-    if (tiles(2, 2) >= cus) return launch_split<X_FP4, 8, 2, 2>(a, ep, st);
-    return launch_split<X_FP4, 8, 2, 1>(a, ep, st);
-  }
-  if (brief) return tiles(1, 2) >= cus ? launch_split<X_FP4, 4, 1, 2>(a, ep, st) : launch_split<X_FP4, 4, 1, 1>(a, ep, st);
-  if (tiles(1, 2) >= cus) return launch_split<X_FP4, 8, 1, 2>(a, ep, st);
-  return launch_split<X_FP4, 8, 1, 1>(a, ep, st);
+  if (is(8, 4, 4)) return launch_split<X_FP4, 8, 4, 4>(a, ep, st);
+  if (is(4, 4, 4)) return launch_split<X_FP4, 4, 4, 4>(a, ep, st);
+  if (is(2, 4, 4)) return launch_split<X_FP4, 2, 4, 4>(a, ep, st);
+  if (is(1, 4, 4)) return launch_split<X_FP4, 1, 4, 4>(a, ep, st);
+  if (is(8, 2, 4)) return launch_split<X_FP4, 8, 2, 4>(a, ep, st);
+  if (is(4, 2, 4)) return launch_split<X_FP4, 4, 2, 4>(a, ep, st);
+  if (is(8, 2, 2)) return launch_split<X_FP4, 8, 2, 2>(a, ep, st);
+  if (is(4, 2, 2)) return launch_split<X_FP4, 4, 2, 2>(a, ep, st);
+  if (is(8, 2, 1)) return launch_split<X_FP4, 8, 2, 1>(a, ep, st);
+  if (is(8, 1, 2)) return launch_split<X_FP4, 8, 1, 2>(a, ep, st);
+  if (is(4, 1, 2)) return launch_split<X_FP4, 4, 1, 2>(a, ep, st);
+  if (is(8, 1, 1)) return launch_split<X_FP4, 8, 1, 1>(a, ep, st);
+  if (is(4, 1, 1)) return launch_split<X_FP4, 4, 1, 1>(a, ep, st);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
+
+GemmFp4Plan gemm_fp4_plan(int64_t M, int64_t N, int64_t K, bool x_fp4, bool aligned, int cus) {
+  // 256 x 256 tiles from two for five CUs on: 4096 x 2048 x 4096 (128 tiles) takes 32 us so and 45 in small
+  // tiles, 3000 x 2500 x 2500 (120) 28 and 36, 1500 x 4096 x 500 (96) 11.6 and 11.8, 1000 x 4096 x 4096 (64)
+  // 30 and 23.  Its bias is read with 32-bit offsets.
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  if (x_fp4 && K > 0 && 5 * tiles >= 2 * (int64_t)cus && N < (int64_t)1 << 29 && aligned) return GemmFp4Plan{256, 256, 8};
+  if (!x_fp4 && K > 0 && K < 8) return GemmFp4Plan{1, 4, 0};
+  return rows_plan(M, N, K, x_fp4, cus);
+}
 
 hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool x_fp4, int64_t ld_x, const uint8_t* xs,
                            int64_t ld_xs, const uint8_t* wc, int64_t ld_w, const uint8_t* ws, int64_t ld_ws,
                            const GemmEpilogue& ep, hipStream_t st) {
   auto whole = [](const void* p, int64_t ld, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0 && ld % n == 0; };
-  // 256 x 256 tiles from two for five CUs on: 4096 x 2048 x 4096 (128 tiles) takes 32 us so and 45 in small
-  // tiles, 3000 x 2500 x 2500 (120) 28 and 36, 1500 x 4096 x 500 (96) 11.6 and 11.8, 1000 x 4096 x 4096 (64)
-  // 30 and 23.  Its bias is read with 32-bit offsets.
-  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
-  if (x_fp4 && K > 0 && 5 * tiles >= 2 * device_cu_count() && N < (int64_t)1 << 29 && whole(xs, ld_xs, 16) && whole(ws, ld_ws, 16))
+  const GemmFp4Plan p = gemm_fp4_plan(M, N, K, x_fp4, whole(xs, ld_xs, 16) && whole(ws, ld_ws, 16), device_cu_count());
+  if (p.tile_m == 256)
     return launch_gemm_fp4_tile(M, N, K, (const uint8_t*)x, ld_x, xs, ld_xs, wc, ld_w, ws, ld_ws, ep, st);
   Fp4Args a{};
   a.M = (int)M;
@@ -413,14 +435,14 @@ hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool 
   a.ld_w = ld_w;
   a.ws = ws;
   a.ld_ws = ld_ws;
-  if (!x_fp4 && K > 0 && K < 8) {
+  if (p.waves == 0) {
     const int64_t blocks = (M * column_groups(a.N) + 255) / 256;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     const Grid grid = grid_of(blocks);
     hipLaunchKernelGGL(k_gemm4_short, dim3(grid.x, grid.y), dim3(256), 0, st, a, ep);
     return hipGetLastError();
   }
-  return x_fp4 ? launch_rows<true>(a, ep, st) : launch_rows<false>(a, ep, st);
+  return x_fp4 ? launch_rows<true>(p, a, ep, st) : launch_rows<false>(p, a, ep, st);
 }
 
 }  // namespace mxq

@@ -106,6 +106,13 @@ hipError_t launch_quant4_dual(const void* src, int src_bf16, int64_t rows, int64
 hipError_t launch_dequant4(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales, int64_t L,
                            int64_t K, void* dst, int dst_bf16, int64_t ld_dst, hipStream_t stream);
 
+// How the MXFP4 product runs M x N x K on `cus` CUs (host logic only): its tile and the waves that share
+// one, 0 where a thread takes a row of a tile of 1 x 4.  aligned: the scale rows are 16-byte aligned.
+struct GemmFp4Plan {
+  int tile_m, tile_n, waves;
+};
+GemmFp4Plan gemm_fp4_plan(int64_t M, int64_t N, int64_t K, bool x_fp4, bool aligned, int cus);
+
 // X in bf16 (ld_x in elements, xs null) or MXFP4 (ld_x in bytes), W in MXFP4.
 hipError_t launch_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, bool x_fp4, int64_t ld_x, const uint8_t* xs,
                            int64_t ld_xs, const uint8_t* wc, int64_t ld_w, const uint8_t* ws, int64_t ld_ws,
@@ -138,6 +145,13 @@ struct MoeFp4 {
   bool y_bf16;
   void* workspace;
 };
+// How the expert layer runs on `cus` CUs (host logic only): its launches, 2 or 4; of 4, the columns of I and of
+// H that a workgroup takes (128 and 256: the persistent kernels) and the ranges of I of the down product.
+// aligned: rows of x and scale rows are 16-byte aligned.
+struct MoeFp4Plan {
+  int launches, up_columns, down_columns, down_parts;
+};
+MoeFp4Plan moe_fp4_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16, bool aligned, int cus);
 int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16);
 hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t stream);
 

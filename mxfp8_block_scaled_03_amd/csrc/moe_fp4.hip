@@ -334,8 +334,8 @@ struct Way {
   double us;
 };
 
-Way way_of(double experts, int64_t rows, int64_t K, bool up, bool f32) {
-  const double cus = device_cu_count(), mb = experts * rows * K * 17 / 32 * 1e-6;
+Way way_of(double experts, int64_t rows, int64_t K, bool up, bool f32, double cus) {
+  const double mb = experts * rows * K * 17 / 32 * 1e-6;
   const int64_t chunks = (K + kChunk - 1) / kChunk;
   Way best{false, 8, 1, 1e30};
   for (int t = f32 && !up ? 2 : 8; t >= 2; t /= 2) {   // three terms of h leave registers for two row tiles
@@ -362,12 +362,18 @@ struct Plan {
   bool few;
 };
 
-Plan plan_of(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool f32) {
+Plan plan_of(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool f32, int cus) {
   const double experts = active_experts(T, E, k);
-  Plan p{way_of(experts, 2 * I, H, true, f32), way_of(experts, H, I, false, f32), false};
-  p.few = moe_few_us(T, H, I, E, k) < 1.2 * (p.up.us + p.down.us) + 12;
+  Plan p{way_of(experts, 2 * I, H, true, f32, cus), way_of(experts, H, I, false, f32, cus), false};
+  p.few = moe_few_us(T, H, I, E, k, cus) < 1.2 * (p.up.us + p.down.us) + 12;
   return p;
 }
+
+// The persistent kernels need whole 16-byte pieces: of rows of X and of scales going up, of scales down.
+bool up_wide(const Plan& p, int64_t H, bool pieces) { return p.up.wide && H % 8 == 0 && pieces; }
+bool down_wide(const Plan& p, bool pieces) { return p.down.wide && pieces; }
+// Row tiles of a workgroup going down otherwise: three terms of h leave registers for two.
+int down_tiles(const Plan& p, bool f32) { return f32 ? 2 : p.down.tiles; }
 
 template <int KIND>
 hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
@@ -376,14 +382,14 @@ hipError_t launch_all(const MoeArgs& a, const Plan& plan, hipStream_t st) {
   hipLaunchKernelGGL(route, dim3((unsigned)((a.T + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int nu = plan.up.tiles, nd = plan.down.tiles;
-  if (plan.up.wide && a.x_pieces && a.H % 8 == 0 && a.s13_pieces)
+  const int nu = plan.up.tiles, nd = down_tiles(plan, KIND == kThree);
+  if (up_wide(plan, a.H, a.x_pieces && a.s13_pieces))
     e = launch_moe_up_wide<KIND>(a, st);
   else
     e = nu == 8 ? launch_up<8, KIND>(a, st) : nu == 4 ? launch_up<4, KIND>(a, st) : launch_up<2, KIND>(a, st);
   if (e != hipSuccess) return e;
   MoeArgs d = a;
-  const bool wide = plan.down.wide && a.s2_pieces;
+  const bool wide = down_wide(plan, a.s2_pieces);
   d.parts = wide ? plan.down.parts : 1;
   if (wide)
     e = launch_moe_down_wide<KIND>(d, st);
@@ -414,10 +420,17 @@ void moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int kind,
 
 }  // namespace
 
+MoeFp4Plan moe_fp4_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16, bool aligned, int cus) {
+  const Plan p = plan_of(T, H, I, E, k, !y_bf16, cus);
+  if (p.few) return MoeFp4Plan{2, 0, 0, 0};
+  const bool up = up_wide(p, H, aligned), down = down_wide(p, aligned);
+  return MoeFp4Plan{4, up ? 128 : 8 * p.up.tiles, down ? 256 : 16 * down_tiles(p, !y_bf16), down ? p.down.parts : 1};
+}
+
 int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16) {
   MoeArgs a{};
   int64_t off[5], total;
-  const Plan plan = plan_of(T, H, I, E, k, !y_bf16);
+  const Plan plan = plan_of(T, H, I, E, k, !y_bf16, device_cu_count());
   if (plan.few) return moe_few_bytes(T, I, k);
   moe_layout(T, H, I, E, k, y_bf16 ? kTwo : kThree, plan.down.parts, &a, off, &total);
   return total;
@@ -426,7 +439,7 @@ int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int6
 hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t st) {
   MoeArgs a{};
   int64_t off[5], total;
-  const Plan plan = plan_of(p.T, p.H, p.I, p.E, p.k, !p.y_bf16);
+  const Plan plan = plan_of(p.T, p.H, p.I, p.E, p.k, !p.y_bf16, device_cu_count());
   moe_layout(p.T, p.H, p.I, p.E, p.k, p.y_bf16 ? kTwo : kThree, plan.down.parts, &a, off, &total);
   a.T = (int)p.T;
   a.H = (int)p.H;

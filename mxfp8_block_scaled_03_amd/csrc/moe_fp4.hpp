@@ -167,7 +167,7 @@ hipError_t launch_moe_down_wide(const MoeArgs& a, hipStream_t st);
 
 // The layer where hardly an expert has two tokens (moe_fp4_few.hip): from the logits to y, with h as its
 // only workspace.  The estimate of its time is without bound where it does not take the sizes.
-double moe_few_us(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k);
+double moe_few_us(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int cus);
 int64_t moe_few_bytes(int64_t T, int64_t I, int64_t k);
 hipError_t launch_moe_few(const MoeArgs& a, hipStream_t st);
 

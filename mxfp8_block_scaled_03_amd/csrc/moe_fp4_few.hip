@@ -294,8 +294,8 @@ namespace {
 namespace few {
 
 // Column groups of a wave going up, with two workgroups a CU, as many as the registers allow.
-int64_t up_per(int64_t T, int64_t I, int64_t k) {
-  const int64_t tiles = (I + 4 * kUpWaves - 1) / (4 * kUpWaves), room = 2 * (int64_t)device_cu_count();
+int64_t up_per(int64_t T, int64_t I, int64_t k, int cus) {
+  const int64_t tiles = (I + 4 * kUpWaves - 1) / (4 * kUpWaves), room = 2 * (int64_t)cus;
   return (T * k * tiles + room - 1) / room;
 }
 
@@ -307,11 +307,11 @@ struct Down {
   double cost;
 };
 
-Down down_of(int64_t T, int64_t H, int64_t I, int64_t k) {
-  const int64_t cus = device_cu_count(), units = k * ((I + kSeg - 1) / kSeg), groups = (H + kRows - 1) / kRows;
+Down down_of(int64_t T, int64_t H, int64_t I, int64_t k, int cus) {
+  const int64_t units = k * ((I + kSeg - 1) / kSeg), groups = (H + kRows - 1) / kRows;
   Down best{1, 0, 1e30};
   for (int w = 1; w <= kDownWaves && w <= units; ++w) {
-    const int64_t room = (cus * (kDownWaves / w) + T - 1) / T, own = (groups + room - 1) / room;
+    const int64_t room = ((int64_t)cus * (kDownWaves / w) + T - 1) / T, own = (groups + room - 1) / room;
     const double cost = own * ((units + w - 1) / w + 0.5);
     if (cost < best.cost) best = Down{w, own, cost};
   }
@@ -324,9 +324,10 @@ Down down_of(int64_t T, int64_t H, int64_t I, int64_t k) {
 // Fits to runs on 256 CUs: 2.9 us for an item of 8 rows x 2048 elements going up, 3 us down.  Measured
 // and estimated: up 13.9 and 9.8 us, down 9.3 and 7.5 (1 token, 4 of 64 experts of 4096 x 2048); 51 and
 // 50, 32 and 30 (8 tokens of the same); 24.8 and 21, 22.1 and 22 (7 tokens, 6 of 60, 2000 x 1064).
-double moe_few_us(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
+double moe_few_us(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int cus) {
   if (H > 8 * few::kSeg || E > 64 * few::kKeys || k > 64) return 1e30;
-  return 7 + 2.9 * (double)few::up_per(T, I, k) * (double)((H + few::kSeg - 1) / few::kSeg) + 3.0 * few::down_of(T, H, I, k).cost;
+  return 7 + 2.9 * (double)few::up_per(T, I, k, cus) * (double)((H + few::kSeg - 1) / few::kSeg) +
+         3.0 * few::down_of(T, H, I, k, cus).cost;
 }
 
 int64_t moe_few_bytes(int64_t T, int64_t I, int64_t k) { return T * k * few::hidden_bytes(I); }
@@ -334,14 +335,15 @@ int64_t moe_few_bytes(int64_t T, int64_t I, int64_t k) { return T * k * few::hid
 hipError_t launch_moe_few(const MoeArgs& args, hipStream_t st) {
   MoeArgs a = args;
   const int64_t tiles = (a.I + 4 * few::kUpWaves - 1) / (4 * few::kUpWaves), slots = (int64_t)a.T * a.k;
-  a.per = (int)few::up_per(a.T, a.I, a.k);
+  const int cus = device_cu_count();
+  a.per = (int)few::up_per(a.T, a.I, a.k, cus);
   a.tiles = (int)((tiles + a.per - 1) / a.per);
   if (slots * a.tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
   const int segs = (a.H + few::kSeg - 1) / few::kSeg;
   hipLaunchKernelGGL(few::k_moe_few_up, dim3((unsigned)(slots * a.tiles)), dim3(64 * few::kUpWaves), 2 * few::kSeg * segs, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const few::Down d = few::down_of(a.T, a.H, a.I, a.k);
+  const few::Down d = few::down_of(a.T, a.H, a.I, a.k, cus);
   const int64_t groups = (a.H + few::kRows - 1) / few::kRows;
   hipLaunchKernelGGL(few::k_moe_few_down, dim3((unsigned)((groups + d.own - 1) / d.own), (unsigned)a.T), dim3(64 * d.waves), 0, st,
                      a);
