@@ -393,7 +393,8 @@ int mxq_quantize_fp4(const void* src, int src_type, int64_t rows, int64_t cols, 
  * mxq_quantize_fp4_sr -- mxq_quantize_fp4 (ceil rule) with stochastically rounded codes, for
  * gradients.  Random numbers and decision as mxq_quantize_sr: element n = line * Kp + k draws
  * word n % 4 of Philox4x32-10(counter n / 4, key seed) and its top 24 bits r round up iff
- * r < 2^24 * (|x/S| - l) / (u - l), decided exactly.
+ * r < 2^24 * (|x/S| - l) / (u - l), decided exactly.  Both orientations are two calls (with two seeds, for
+ * independent roundings): the random numbers, not the reading of src, take the time.
  */
 int mxq_quantize_fp4_sr(const void* src, int src_type, int64_t rows, int64_t cols, int64_t ld_src, int axis,
                         uint64_t seed, uint8_t* codes, int64_t ld_codes, uint8_t* scales, int64_t ld_scales,
@@ -433,7 +434,8 @@ int mxq_dequantize_fp4(const uint8_t* codes, int64_t ld_codes, const uint8_t* sc
  *          between shapes.  Epilogue, bias, act, alpha, y as mxq_gemm_ex.
  * The gradients of a linear layer are two such products: dX from dY quantized along its rows
  * and W along its outputs, dW from dY quantized along its columns and X along the tokens.
- * Limits   M, N < 2^31, K < 2^24, ld_w and ld_ws < 2^24.
+ * Limits   M, N < 2^31, K < 2^24; ld_w, ld_ws and, with X in MXFP4, ld_x and ld_xs < 2^24, with X in bf16
+ *          ld_x < 2^31.
  */
 int mxq_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, int x_type, int64_t ld_x, const uint8_t* x_scales,
                  int64_t ld_xs, const uint8_t* w_codes, int64_t ld_w, const uint8_t* w_scales, int64_t ld_ws,
@@ -454,14 +456,15 @@ int mxq_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, int x_type, int
  * y        [T][ld_y] of y_type.
  * An expert whose logit is -inf is never taken, also when fewer than k are left; a token with
  * no expert left gets y = 0.  A NaN logit orders above every number and makes the token's
- * shares NaN.
+ * shares NaN.  Codes past H and I in a last block are ignored under scale bytes 0 .. 252.
  * Products of x and the weights exact, sums in FP32.  The hidden values are FP32, or, where experts have
  * several tokens, 2 (y_type MXQ_BF16) or 3 (MXQ_F32) bf16 terms, 16 or 24 bits.  The result does
  * not depend on how workgroups are scheduled; the summation order is fixed for the sizes, the
  * alignment and the device.  Two launches where hardly an expert has two tokens, else four.
  * workspace  256-byte aligned, at least the bytes that mxq_moe_fp4_workspace gives
  *          (MXQ_ERR_SCRATCH otherwise); it holds nothing between calls.
- * Limits   T <= 1024, E <= 1024, 1 <= k <= E, H and I < 2^24, (I + 128) * ld_w13 < 2^32.
+ * Limits   T <= 1024, E <= 1024, 1 <= k <= E, H and I < 2^24; ld_w13, ld_s13, ld_w2 and ld_s2 < 2^24, (I + 128) *
+ *          ld_w13 and (I + 128) * ld_s13 < 2^32; ld_x, ld_logits and ld_y < 2^31.
  */
 int mxq_moe_fp4_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int y_type, int64_t* bytes);
 int mxq_moe_fp4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int renormalize, const void* x, int64_t ld_x,

@@ -22,11 +22,10 @@ int64_t blocks_of(int64_t k) { return (k + 31) / 32; }
 int hip_status(hipError_t e) { return e == hipSuccess ? MXQ_OK : MXQ_ERR_HIP; }
 
 // A code array of L lines: 16 bytes per block, 16-byte aligned.
-int check_codes(const void* p, int64_t L, int64_t ld, const void* scales, int64_t ld_scales, int64_t nb) {
+int check_codes(const void* p, int64_t L, int64_t ld, int64_t ld_scales, int64_t nb) {
   if (ld < 16 * nb || ld_scales < nb) return MXQ_ERR_LD;
   if (!mul_ok(L, ld) || !mul_ok(L, ld_scales)) return MXQ_ERR_SHAPE;
   if (!aligned(p, 16) || ld % 16 != 0) return MXQ_ERR_ALIGN;
-  (void)scales;
   return MXQ_OK;
 }
 
@@ -42,7 +41,7 @@ int quantize(const void* src, int src_type, int64_t rows, int64_t cols, int64_t 
   const int64_t es = src_type == MXQ_BF16 ? 2 : 4;
   if (ld_src < cols) return MXQ_ERR_LD;
   if (!mul_ok(ld_src, es) || !mul_ok(rows, ld_src * es)) return MXQ_ERR_SHAPE;
-  const int st = check_codes(codes, L, ld_codes, scales, ld_scales, blocks_of(K));
+  const int st = check_codes(codes, L, ld_codes, ld_scales, blocks_of(K));
   if (st != MXQ_OK) return st;
   if (!aligned(src, (uintptr_t)es)) return MXQ_ERR_ALIGN;
   return hip_status(mxq::launch_quant4(src, src_type == MXQ_BF16, rows, cols, ld_src, axis == MXQ_COLWISE,
@@ -77,8 +76,8 @@ int mxq_quantize_fp4_dual(const void* src, int src_type, int64_t rows, int64_t c
   const int64_t es = src_type == MXQ_BF16 ? 2 : 4;
   if (ld_src < cols) return MXQ_ERR_LD;
   if (!mul_ok(ld_src, es) || !mul_ok(rows, ld_src * es)) return MXQ_ERR_SHAPE;
-  int st = check_codes(row_codes, rows, ld_row_codes, row_scales, ld_row_scales, blocks_of(cols));
-  if (st == MXQ_OK) st = check_codes(col_codes, cols, ld_col_codes, col_scales, ld_col_scales, blocks_of(rows));
+  int st = check_codes(row_codes, rows, ld_row_codes, ld_row_scales, blocks_of(cols));
+  if (st == MXQ_OK) st = check_codes(col_codes, cols, ld_col_codes, ld_col_scales, blocks_of(rows));
   if (st != MXQ_OK) return st;
   if (!aligned(src, (uintptr_t)es)) return MXQ_ERR_ALIGN;
   return hip_status(mxq::launch_quant4_dual(src, src_type == MXQ_BF16, rows, cols, ld_src, row_codes, ld_row_codes,
@@ -95,7 +94,7 @@ int mxq_dequantize_fp4(const uint8_t* codes, int64_t ld_codes, const uint8_t* sc
   const int64_t es = dst_type == MXQ_BF16 ? 2 : 4;
   if (ld_dst < K) return MXQ_ERR_LD;
   if (!mul_ok(ld_dst, es) || !mul_ok(L, ld_dst * es)) return MXQ_ERR_SHAPE;
-  const int st = check_codes(codes, L, ld_codes, scales, ld_scales, blocks_of(K));
+  const int st = check_codes(codes, L, ld_codes, ld_scales, blocks_of(K));
   if (st != MXQ_OK) return st;
   if (!aligned(dst, (uintptr_t)es)) return MXQ_ERR_ALIGN;
   return hip_status(mxq::launch_dequant4(codes, ld_codes, scales, ld_scales, L, K, dst, dst_type == MXQ_BF16, ld_dst,
@@ -116,8 +115,8 @@ int mxq_gemm_fp4(int64_t M, int64_t N, int64_t K, const void* x, int x_type, int
   if (K > 0) {
     if (ld_w >= kMaxK || ld_ws >= kMaxK || ld_x >= (x_fp4 ? kMaxK : kMaxDim) || ld_xs >= (x_fp4 ? kMaxK : INT64_MAX))
       return MXQ_ERR_LD;
-    int st = check_codes(w_codes, N, ld_w, w_scales, ld_ws, nb);
-    if (st == MXQ_OK && x_fp4) st = check_codes(x, M, ld_x, x_scales, ld_xs, nb);
+    int st = check_codes(w_codes, N, ld_w, ld_ws, nb);
+    if (st == MXQ_OK && x_fp4) st = check_codes(x, M, ld_x, ld_xs, nb);
     if (st != MXQ_OK) return st;
     if (!x_fp4) {
       if (ld_x < K) return MXQ_ERR_LD;
@@ -195,10 +194,11 @@ int mxq_moe_fp4(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int renor
   const int64_t ey = y_type == MXQ_BF16 ? 2 : 4;
   if (ld_x < H || ld_logits < E || ld_y < H) return MXQ_ERR_LD;
   if (ld_x >= kMaxDim || ld_logits >= kMaxDim || ld_y >= kMaxDim) return MXQ_ERR_LD;
-  st = check_codes(w13_codes, 2 * I, ld_w13, w13_scales, ld_s13, blocks_of(H));
-  if (st == MXQ_OK) st = check_codes(w2_codes, H, ld_w2, w2_scales, ld_s2, blocks_of(I));
+  st = check_codes(w13_codes, 2 * I, ld_w13, ld_s13, blocks_of(H));
+  if (st == MXQ_OK) st = check_codes(w2_codes, H, ld_w2, ld_s2, blocks_of(I));
   if (st != MXQ_OK) return st;
-  // the kernels reach a gate row and its up row with one 32-bit offset
+  // row tiles are reached with 32-bit offsets; a gate row and its up row, which have 64-bit addresses, are kept
+  // within 4 GiB all the same, as the contract says
   if (ld_w13 >= kMaxK || ld_w2 >= kMaxK || ld_s13 >= kMaxK || ld_s2 >= kMaxK) return MXQ_ERR_LD;
   if ((I + 128) * ld_w13 > 0xFFFFFFFFll || (I + 128) * ld_s13 > 0xFFFFFFFFll) return MXQ_ERR_SHAPE;
   if (expert_w13 < (E > 1 ? 2 * I * ld_w13 : 0) || expert_w2 < (E > 1 ? H * ld_w2 : 0)) return MXQ_ERR_LD;

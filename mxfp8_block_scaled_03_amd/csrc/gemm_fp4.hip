@@ -1,5 +1,6 @@
 // gemm_fp4.hip -- Y = act(alpha * (X W) + bias) with W in MXFP4 and X in bf16 or MXFP4, for
-// gfx950: the choice of kernel, and the kernel of few rows or tiles (fp4_stream.hpp).
+// gfx950: the choice of kernel, the kernel of few rows or tiles, and the one of K < 8.  The large product of two
+// MXFP4 operands is in gemm_fp4_tile.hip.
 #include "fp4_stream.hpp"
 
 namespace mxq {
@@ -354,15 +355,15 @@ hipError_t launch_split(Fp4Args a, const GemmEpilogue& ep, hipStream_t st) {
 }
 
 // The tile and the split, from timing ten of them on 50 shapes (256 CUs).  Where 64 x 64 tiles fill the
-// CUs, as many waves a tile as the card holds at once (8 a CU), up to 8: 1000 x 1000 x 4001 10.2 us with
-// 8, 2000 x 1000 x 3000 13.0 with 4 (14.9 with 2), 2048^3 14.3 with 2 (15.3 with 4), 3000 x 2500 x 2500 35.3
-// with 1 (41.4 with 4); with X in bf16 512 x 4096 x 4096 25 with 4 (34 with 2), 1024 rows 43 with 2 (46 with
-// 4), 2048 rows 83 with 1 (141 with 4).  K of at most 1024 leaves many waves less than a piece each: 64 x 32
-// tiles by two waves for X in MXFP4 (3000 x 1500 x 800 13.3 us, 15.6 in 64 x 64 by four; 1500 x 4096 x 500
-// 11.3 and 17.3), and 32 x 32 by four where there are fewer.  Else the largest tile that still gives
-// every CU a workgroup, by four waves where it gives one to some CUs twice (30 x 32768 x 4096 20.6 us, 24.8
-// by eight), and for up to 16 rows no wider than 32 columns (1 x 65536 x 4096 29.9 us, 40.5 with 64; 1 x 8192
-// x 5120 7.5 and 9.6).
+// CUs, as many waves a tile as the card holds at once (8 a CU), up to 8: 1000 x 1000 x 4001 10.4 us with
+// 8 (12.5 with 2), 2000 x 1000 x 3000 12.9 with 4 (14.8 with 2), 2048^3 14.1 with 2 (15.6 with 4), 3000 x 2500 x
+// 2500 34.3 with 1 (36.1 with 4); with X in bf16 512 x 4096 x 4096 25 with 4 (35 with 2), 1024 rows 44 with 2 (46
+// with 4), 2048 rows 81 with 1 (98 with 2).  K of at most 1024 leaves many waves less than a piece each: 64 x 32
+// tiles by two waves for X in MXFP4 (3000 x 1500 x 800 12.8 us, 15.2 in 64 x 64 by four; 1500 x 4096 x 500
+// 11.7 and 17.2), and 32 x 32 by four where there are fewer.  Else the largest tile that still gives
+// every CU a workgroup, by four waves where it gives one to some CUs twice (30 x 32768 x 4096 20.7 us, 24.8
+// by eight), and for up to 16 rows no wider than 32 columns (1 x 65536 x 4096 30.0 us, 46 with 64; 1 x 8192
+// x 5120 7.1 and 11.3).
 GemmFp4Plan rows_plan(int64_t M, int64_t N, int64_t K, bool x_fp4, int64_t cus) {
   auto tiles = [&](int mt, int nt) { return ((M + 16ll * mt - 1) / (16 * mt)) * ((N + 16ll * nt - 1) / (16 * nt)); };
   auto plan = [](int waves, int mt, int nt) { return GemmFp4Plan{16 * mt, 16 * nt, waves}; };
@@ -407,9 +408,10 @@ hipError_t launch_rows(const GemmFp4Plan& p, const Fp4Args& a, const GemmEpilogu
 }  // namespace
 
 GemmFp4Plan gemm_fp4_plan(int64_t M, int64_t N, int64_t K, bool x_fp4, bool aligned, int cus) {
-  // 256 x 256 tiles from two for five CUs on: 4096 x 2048 x 4096 (128 tiles) takes 32 us so and 45 in small
-  // tiles, 3000 x 2500 x 2500 (120) 28 and 36, 1500 x 4096 x 500 (96) 11.6 and 11.8, 1000 x 4096 x 4096 (64)
-  // 30 and 23.  Its bias is read with 32-bit offsets.
+  // 256 x 256 tiles from two for five CUs on: 4096 x 2048 x 4096 (128 tiles) takes 32 us so and 43 in small
+  // tiles, 3000 x 2500 x 2500 (120) 28 and 34, 1500 x 4096 x 500 (96) 11.4 and 11.7, 1000 x 4096 x 4096 (64)
+  // 30 and 24.  The tiles are counted, not how full they are: 30 x 32768 x 4096 (128) takes 29 us and would take
+  // 13 in small ones.  The bias is read with 32-bit offsets.
   const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
   if (x_fp4 && K > 0 && 5 * tiles >= 2 * (int64_t)cus && N < (int64_t)1 << 29 && aligned) return GemmFp4Plan{256, 256, 8};
   if (!x_fp4 && K > 0 && K < 8) return GemmFp4Plan{1, 4, 0};

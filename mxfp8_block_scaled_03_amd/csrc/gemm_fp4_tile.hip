@@ -18,8 +18,9 @@
 // the matrix's rows return zero through the descriptors; in the last, partial step codes at
 // k >= K are zeroed and the scale of a block >= nb is 127.
 //
-// What bounds it: power and the movement of operands.  8192 x 4096 x 4096 takes 75-80 us (3.4-3.7 PFLOP/s),
-// 16384 deep 318 us at a clock that falls to 1.7 GHz; there the MFMAs are busy 55 % of the cycles.  Of
+// What bounds it: power and the movement of operands.  8192 x 4096 x 4096 takes 75-81 us (3.4-3.7 PFLOP/s),
+// 16384 deep 318 us at a clock that falls to 1.7 GHz; there the MFMAs are busy 55 % of the cycles.  MFMAs alone, on
+// operands that stay in registers, hold 6.4-6.6 PFLOP/s for 30 ms (random codes; zeros 9.7).  Of
 // the 318 us a copy of this kernel without the DMA needs 262, without the LDS reads of fragments
 // 324, without both 250, with all codes zero 221: taking a step's scales four at a time (their 4-byte
 // reads are the only LDS reads with bank conflicts), DMA in lines of 128 bytes and DMA beside the LDS

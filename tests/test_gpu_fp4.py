@@ -701,7 +701,7 @@ def test_experts_over_many_workgroups():
 @pytest.mark.parametrize("T,H,I,E", [(3, 32, 16, 4), (3, 32, 16, 264), (200, 72, 120, 512)])
 def test_experts_largest_hidden_values(out, T, H, I, E):
     """Hidden values next to FP32's largest, which no single bf16 holds: finite ones stay finite and as exact as
-    others, in two and in four launches and in the persistent kernels; infinite ones stay infinite.  h = gate * up
+    others, in two and in four launches and in the persistent up product; infinite ones stay infinite.  h = gate * up
     with gate = 2^60 and up = +-1.998046875 * 2^67, the sum of two bf16, in column 0, share 1 (k = 1)."""
     rng = np.random.default_rng(52)
     w13 = np.zeros((E, 2 * I, 16 * ref.blocks(H)), np.uint8)
