@@ -1,0 +1,513 @@
+"""FP8 in blocks of 128 and the routing of a mixture of experts, as measured cases: what goes in,
+one pass, and the exact answer.
+
+Blocks of 128: 128 consecutive values along the contraction axis (a line's block, "1 x 128") or a
+tile of 128 x 128 values share one FP32 scale s = amax / fmax; each value is an E4M3 or E5M2 code,
+nearest even of x * (fmax / amax).  Code lines hold whole blocks, zero past the last value; the
+scales of a block of lines lie side by side, so line l's scale of block b is at [b][l].  Four
+operators:
+
+  quantize   x -> codes and scales: along rows, along columns (transposed), both from one read, or
+             in tiles with the transposed codes beside them
+  product    Y = act(X W + bias), both operands in blocks of 128: W in tiles (weights) or in lines;
+             and the two gradient products of a linear layer
+  experts    the same product for the rows of each expert in turn (rows sorted by expert, offsets
+             on the device), from bf16 rows on; and its two gradient products
+  route      router logits -> softmax, the k greatest, shares, per-expert counts, the order of the
+             slots by expert, the balance loss; and the gradient of the logits
+
+``own`` chooses between the plain torch form (False) and the framework's kernels (True).
+"""
+import torch
+
+own = False
+
+DEV = "cuda"
+B = 128
+FMAX = {"e4m3": 448.0, "e5m2": 57344.0}
+FP8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+WIDE = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+# ------------------------------------------------------------------------------- the cases
+
+def listed():
+    return [
+        # activations of 64 sequences that are decoded together, before a product
+        {"name": "quantize 64x4096 bf16 row", "op": "quantize", "rows": 64, "cols": 4096, "type": "bf16", "axis": "row",
+         "elem": "e4m3"},
+        # a training step's activations: along K for the product, along the tokens for the weight gradient
+        {"name": "quantize 8192x4096 bf16 dual", "op": "quantize", "rows": 8192, "cols": 4096, "type": "bf16",
+         "axis": "dual", "elem": "e4m3"},
+        # fp32 master weights of a ragged layer, after an optimizer step: tiles, both ways round
+        {"name": "quantize 4095x4001 fp32 tiles", "op": "quantize", "rows": 4095, "cols": 4001, "type": "fp32",
+         "axis": "tile", "elem": "e4m3"},
+        # a projection for 16 sequences, one token each: the weights are read once
+        {"name": "product 16x4096x4096 fp8", "op": "product", "M": 16, "N": 4096, "K": 4096, "accum": "fp8",
+         "out": "bf16", "lines": False, "bias": False, "act": ""},
+        # a projection over a prompt or a training batch
+        {"name": "product 8192x4096x4096 fp8", "op": "product", "M": 8192, "N": 4096, "K": 4096, "accum": "fp8",
+         "out": "bf16", "lines": False, "bias": False, "act": ""},
+        # odd sizes, exact products: a short prompt against a ragged weight
+        {"name": "product 1000x1000x4001 fp32", "op": "product", "M": 1000, "N": 1000, "K": 4001, "accum": "fp32",
+         "out": "fp32", "lines": False, "bias": True, "act": "silu"},
+        # the gradients of a linear layer: quantize dY both ways, dX and (exact, FP32) dW
+        {"name": "backward 4096x4096x4096", "op": "backward", "M": 4096, "N": 4096, "K": 4096},
+        # decoding: 128 (token, expert) slots over 64 experts, some of them without a row
+        {"name": "experts 128 of 64x4096x2048", "op": "experts", "R": 128, "N": 4096, "K": 2048, "E": 64, "accum": "fp8",
+         "out": "bf16"},
+        # a prompt: 8192 slots over 32 experts, unevenly
+        {"name": "experts 8192 of 32x4096x2048", "op": "experts", "R": 8192, "N": 4096, "K": 2048, "E": 32,
+         "accum": "fp8", "out": "bf16"},
+        # training: the gradients of the experts' product
+        {"name": "experts backward 8192 of 16x4096x2048", "op": "experts backward", "R": 8192, "N": 4096, "K": 2048,
+         "E": 16},
+        # the router of a decoding step
+        {"name": "route 64x64 k 8", "op": "route", "T": 64, "E": 64, "k": 8, "type": "fp32", "renorm": True,
+         "masked": False},
+        # the router of a training step, some of its tokens padding
+        {"name": "route 16384x256 k 8", "op": "route", "T": 16384, "E": 256, "k": 8, "type": "fp32", "renorm": True,
+         "masked": True},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(lo * (hi / lo) ** rng.random()))
+
+
+def draw(rng):
+    op = rng.choice(("quantize", "quantize", "product", "product", "product", "backward", "experts", "experts",
+                     "experts backward", "route", "route"))
+    if op == "quantize":
+        rows, cols = _log(rng, 1, 8192), _log(rng, 32, 8192)
+        if rows * cols > 8192 * 4096:
+            cols //= 2
+        return {"op": op, "rows": rows, "cols": cols, "type": rng.choice(("bf16", "fp32")),
+                "axis": rng.choice(("row", "col", "dual", "tile")), "elem": rng.choice(("e4m3", "e5m2"))}
+    if op == "product":
+        accum = rng.choice(("fp8", "fp32"))
+        return {"op": op, "M": _log(rng, 1, 8192), "N": _log(rng, 64, 4096), "K": _log(rng, 64, 4096), "accum": accum,
+                "out": "bf16" if accum == "fp8" else rng.choice(("bf16", "fp32")), "lines": rng.random() < 0.3,
+                "bias": rng.random() < 0.5, "act": rng.choice(("", "silu"))}
+    if op == "backward":
+        return {"op": op, "M": _log(rng, 128, 4096), "N": _log(rng, 128, 4096), "K": _log(rng, 128, 4096)}
+    if op == "route":
+        T, E = _log(rng, 1, 16384), _log(rng, 4, 256)
+        return {"op": op, "T": T, "E": E, "k": rng.randint(1, min(8, E)), "type": rng.choice(("bf16", "fp32")),
+                "renorm": rng.random() < 0.5, "masked": rng.random() < 0.5}
+    E, N, K = _log(rng, 4, 64), _log(rng, 128, 4096), _log(rng, 128, 4096)
+    while E * N * K > (64 if op == "experts" else 16) * 4096 * 2048:
+        N //= 2
+    c = {"op": op, "R": _log(rng, 1 if op == "experts" else 128, 8192), "N": N, "K": K, "E": E}
+    if op == "experts":
+        c["accum"] = rng.choice(("fp8", "fp32"))
+        c["out"] = "bf16" if c["accum"] == "fp8" else rng.choice(("bf16", "fp32"))
+    return c
+
+
+def _blocks(k):
+    return (k + B - 1) // B
+
+
+def _coded(lines, k, tiles=False):
+    """Bytes of codes and scales of `lines` x k values."""
+    return lines * k + 4 * _blocks(k) * (_blocks(lines) if tiles else lines)
+
+
+def work(case):
+    c = case
+    if c["op"] == "quantize":
+        es, r, k = 2 if c["type"] == "bf16" else 4, c["rows"], c["cols"]
+        out = {"row": _coded(r, k), "col": _coded(k, r), "dual": _coded(r, k) + _coded(k, r),
+               "tile": _coded(r, k, True) + r * k}[c["axis"]]
+        return {"bytes": r * k * es + out, "flops": 2 * r * k * (1 if c["axis"] in ("row", "col") else 2)}
+    if c["op"] == "product":
+        M, N, K = c["M"], c["N"], c["K"]
+        return {"bytes": _coded(M, K) + _coded(N, K, not c["lines"]) + M * N * (2 if c["out"] == "bf16" else 4)
+                + (4 * N if c["bias"] else 0), "flops": 2 * M * N * K}
+    if c["op"] == "backward":
+        M, N, K = c["M"], c["N"], c["K"]
+        return {"bytes": 2 * M * N + _coded(K, N, True) + _coded(K, M) + 2 * M * K + 4 * N * K, "flops": 4 * M * N * K}
+    if c["op"] == "route":
+        T, E, k, es = c["T"], c["E"], c["k"], 2 if c["type"] == "bf16" else 4
+        return {"bytes": 2 * T * E * es + 16 * T * k + 8 * E + (T if c["masked"] else 0), "flops": 10 * T * E}
+    R, N, K, E = c["R"], c["N"], c["K"], c["E"]
+    if c["op"] == "experts":
+        used = E * (1 - (1 - 1 / E) ** R)                           # experts with a row, on average
+        return {"bytes": 2 * R * K + used * _coded(N, K, True) + R * N * (2 if c["out"] == "bf16" else 4),
+                "flops": 2 * R * N * K}
+    return {"bytes": 2 * R * N + _coded(K, R) + E * _coded(K, N, True) + 2 * R * K + 4 * E * N * K,
+            "flops": 4 * R * N * K}
+
+
+# ------------------------------------------------------------------ the inputs, from the seed
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed))
+    return g
+
+
+def _normal(g, shape, std=1.0, dtype=torch.float32):
+    return (torch.randn(shape, generator=g, device=DEV) * std).to(dtype)
+
+
+def _activations(g, shape, dtype=torch.bfloat16):
+    """N(0, 1) with a thousandth of the entries a hundred times as large."""
+    x = torch.randn(shape, generator=g, device=DEV)
+    spike = torch.rand(shape, generator=g, device=DEV) < 1e-3
+    return torch.where(spike, x * 100, x).to(dtype)
+
+
+def _gradients(g, shape, dtype=torch.bfloat16):
+    """1e-3 times Student's t with three degrees of freedom: heavy tails."""
+    z = torch.randn((3,) + tuple(shape), generator=g, device=DEV).square_().sum(0)
+    return (1e-3 * torch.randn(shape, generator=g, device=DEV) / torch.sqrt(z / 3)).to(dtype)
+
+
+def _sizes(g, R, E):
+    """Rows of each expert: drawn from probabilities that differ up to some ten times."""
+    p = torch.exp(torch.randn(E, generator=g, device=DEV) * 0.7)
+    e = torch.multinomial(p, R, replacement=True, generator=g)
+    n = torch.bincount(e, minlength=E)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    offsets[1:] = n.cumsum(0)
+    return offsets, n.tolist()
+
+
+def _starts(sizes):
+    """The first padded column of each expert where lines run along the rows: whole blocks each."""
+    at = [0]
+    for n in sizes:
+        at.append(at[-1] + _blocks(n) * B)
+    return at
+
+
+def _pad_groups(x, sizes):
+    """Rows [R][C] -> [C][R padded]: each expert's rows from its own first block on."""
+    at, R = _starts(sizes), x.shape[0]
+    wide = torch.zeros((x.shape[1], (R + (B - 1) * len(sizes)) // B * B), dtype=x.dtype, device=x.device)
+    first = 0
+    for n, a in zip(sizes, at):
+        wide[:, a:a + n] = x[first:first + n].T
+        first += n
+    return wide
+
+
+def prepare(case, seed):
+    c, g = case, _gen(seed)
+    s = dict(c)
+    if c["op"] == "quantize":
+        make = _gradients if c["elem"] == "e5m2" else _activations
+        s["x"] = make(g, (c["rows"], c["cols"]), WIDE[c["type"]])
+    elif c["op"] == "product":
+        M, N, K = c["M"], c["N"], c["K"]
+        s["x"], s["xs"] = _lines(_activations(g, (M, K)), "e4m3")
+        w = _normal(g, (N, K), 0.02, torch.bfloat16)
+        s["w"], s["ws"] = _lines(w, "e4m3") if c["lines"] else _tiles(w, "e4m3")
+        s["b"] = _normal(g, (N,), 0.02) if c["bias"] else None
+    elif c["op"] == "backward":
+        M, N, K = c["M"], c["N"], c["K"]
+        s["dy"] = _gradients(g, (M, N))
+        wt, ws = _tiles(_normal(g, (N, K), 0.02, torch.bfloat16).T, "e4m3")
+        s["wt"], s["wts"] = wt, ws                                  # [K][N], tiles
+        s["xt"], s["xts"] = _lines(_activations(g, (M, K)).T, "e4m3")   # [K][M]
+    elif c["op"] == "route":
+        T, E = c["T"], c["E"]
+        s["logits"] = (_normal(g, (T, E)) + _normal(g, (E,), 0.5)).to(WIDE[c["type"]])
+        s["mask"] = torch.rand(T, generator=g, device=DEV) < 0.9 if c["masked"] else None
+        s["d_shares"] = _normal(g, (T, c["k"]), 1e-3)
+        s["d_loss"] = torch.full((1,), 1e-2, device=DEV)
+    else:
+        R, N, K, E = c["R"], c["N"], c["K"], c["E"]
+        s["offsets"], s["sizes"] = _sizes(g, R, E)                  # the sizes: for the plain form
+        back = c["op"] != "experts"
+        w = [_normal(g, (N, K), 0.02, torch.bfloat16) for _ in range(E)]
+        w = [_tiles(m.T if back else m, "e4m3") for m in w]
+        s["w"], s["ws"] = torch.stack([m[0] for m in w]), torch.stack([m[1] for m in w])
+        if back:
+            s["dy"] = _gradients(g, (R, N))
+            s["xt"], s["xts"] = _lines(_pad_groups(_activations(g, (R, K)), s["sizes"]), "e4m3")
+        else:
+            s["x"] = _activations(g, (R, K))
+    return s
+
+
+# --------------------------------------------------------------------------- the plain forms
+
+def _whole(x):
+    """[L][K] -> fp32 [L][whole blocks], zeros behind."""
+    return torch.nn.functional.pad(x.float(), (0, _blocks(x.shape[1]) * B - x.shape[1]))
+
+
+def _scale(amax, elem):
+    """The scale amax / fmax and the factor fmax / amax, each rounded once to fp32; 1 and 1 for a
+    zero block; amax is taken as at least 2^-100."""
+    a = amax.clamp(min=2.0 ** -100)
+    one, f = torch.ones_like(a), torch.full_like(a, FMAX[elem])     # (torch divides by a plain number in two roundings)
+    return torch.where(amax == 0, one, a / f), torch.where(amax == 0, one, f / a)
+
+
+def _encode(x, r, elem):
+    return (x * r).clamp(-FMAX[elem], FMAX[elem]).to(FP8[elem]).view(torch.uint8)
+
+
+def _lines(x, elem):
+    """Codes [L][whole blocks] and scales [L][blocks] (stored block by block) of blocks along lines."""
+    v = _whole(x).unflatten(1, (-1, B))
+    s, r = _scale(v.abs().amax(-1), elem)
+    return _encode(v, r[..., None], elem).flatten(1), s.T.contiguous().T
+
+
+def _tiles(x, elem):
+    """Codes [L][whole blocks] and scales [tiles of L][blocks]."""
+    L, v = x.shape[0], _whole(x)
+    pad = torch.nn.functional.pad(v, (0, 0, 0, _blocks(L) * B - L)).view(-1, B, v.shape[1] // B, B)
+    s, r = _scale(pad.abs().amax((1, 3)), elem)
+    return _encode(pad, r[:, None, :, None], elem).view(-1, v.shape[1])[:L], s
+
+
+def _values(codes, scales, K, elem="e4m3"):
+    """The values that codes [L][..] under scales [L or its tiles][blocks] stand for, [L][K]."""
+    L = codes.shape[0]
+    v = codes.view(FP8[elem]).float().unflatten(1, (-1, B))
+    s = scales if scales.shape[0] == L else scales.repeat_interleave(B, 0)[:L]
+    return (v * s[..., None]).flatten(1)[:, :K]
+
+
+def _quantized(codes, scales, k, elem):
+    """Codes as the FP8 numbers that they are, without the zeros behind, and scales."""
+    return {"codes": codes[:, :k].view(FP8[elem]), "scales": scales}
+
+
+def _grouped_values(codes, scales, sizes):
+    """[C][R padded] codes and scales -> [C][n] values of each expert."""
+    v, at = _values(codes, scales, codes.shape[1]), _starts(sizes)
+    return [v[:, a:a + n] for n, a in zip(sizes, at)]
+
+
+def _route_plain(s, f):
+    """The router in the type `f`: what the forward pass gives, and the gradient of the logits."""
+    T, E, k = s["T"], s["E"], s["k"]
+    logits = s["logits"].to(f)
+    live = torch.ones(T, dtype=torch.bool, device=logits.device) if s["mask"] is None else s["mask"]
+    p = torch.exp(logits - logits.amax(-1, keepdim=True))
+    p = p / p.sum(-1, keepdim=True)
+    ids = torch.sort(logits, dim=-1, descending=True, stable=True)[1][:, :k]
+    chosen = torch.gather(p, 1, ids)
+    total = chosen.sum(-1, keepdim=True) if s["renorm"] else torch.ones_like(chosen[:, :1])
+    shares = torch.where(live[:, None], chosen / total, torch.zeros_like(chosen))
+    experts = torch.where(live[:, None], ids, torch.full_like(ids, -1))
+    flat = torch.where(experts < 0, torch.full_like(experts, E), experts).flatten()
+    counts = torch.zeros(E + 1, dtype=torch.int64, device=flat.device).scatter_add_(0, flat, torch.ones_like(flat))[:E]
+    offsets = torch.nn.functional.pad(counts.cumsum(0), (1, 0))
+    order = torch.sort(flat, stable=True)[1]
+    order = torch.where(torch.arange(T * k, device=flat.device) < offsets[E], order, torch.full_like(order, -1))
+    n = live.sum().to(f).clamp(min=1)
+    slope = E * counts.to(f) / (n * k) / n                          # dL / dp of each token that counts
+    loss = (slope * torch.where(live[:, None], p, torch.zeros_like(p)).sum(0)).sum()
+    # gradients: the balance loss through p; the shares through p, or through the softmax of the chosen
+    d_p = slope * s["d_loss"].to(f) * torch.ones_like(p)
+    d = s["d_shares"].to(f)
+    if not s["renorm"]:
+        d_p = d_p.scatter_add(1, ids, d)
+    d_logits = p * (d_p - (p * d_p).sum(-1, keepdim=True))
+    if s["renorm"]:
+        sh = chosen / total
+        d_logits = d_logits.scatter_add(1, ids, sh * (d - (sh * d).sum(-1, keepdim=True)))
+    d_logits = torch.where(live[:, None], d_logits, torch.zeros_like(d_logits))
+    return {"experts": experts.int(), "shares": shares, "counts": counts.int(), "offsets": offsets.int(),
+            "order": order.int(), "loss": loss.reshape(1), "d_logits": d_logits}
+
+
+def _plain(s):
+    if s["op"] == "quantize":
+        x, elem, axis = s["x"], s["elem"], s["axis"]
+        if axis == "tile":
+            c, sc = _tiles(x, elem)
+            return [_quantized(c, sc, x.shape[1], elem), _quantized(_whole(c[:, :x.shape[1]].T).to(torch.uint8), sc.T,
+                                                                    x.shape[0], elem)]
+        sides = {"row": (x,), "col": (x.T,), "dual": (x, x.T)}[axis]
+        return [_quantized(*_lines(v, elem), v.shape[1], elem) for v in sides]
+    if s["op"] == "product":
+        y = _values(s["x"], s["xs"], s["K"]) @ _values(s["w"], s["ws"], s["K"]).T
+        y = y if s["b"] is None else y + s["b"]
+        y = y * torch.sigmoid(y) if s["act"] == "silu" else y
+        return y.to(WIDE[s["out"]])
+    if s["op"] == "backward":
+        M, N = s["M"], s["N"]
+        row, col = _values(*_lines(s["dy"], "e5m2"), N, "e5m2"), _values(*_lines(s["dy"].T, "e5m2"), M, "e5m2")
+        return {"dx": (row @ _values(s["wt"], s["wts"], N).T).to(torch.bfloat16),
+                "dw": col @ _values(s["xt"], s["xts"], M).T}
+    if s["op"] == "route":
+        out = _route_plain(s, torch.float64)                        # 64 bits: sums over all tokens
+        return {**out, "shares": out["shares"].float(), "loss": out["loss"].float(),
+                "d_logits": out["d_logits"].to(s["logits"].dtype)}
+    N, K = s["N"], s["K"]
+    if s["op"] == "experts":
+        x = _values(*_lines(s["x"], "e4m3"), K)
+        y = [v @ _values(w, ws, K).T for v, w, ws in zip(x.split(s["sizes"]), s["w"], s["ws"])]
+        return torch.cat(y).to(WIDE[s["out"]])
+    row = _values(*_lines(s["dy"], "e5m2"), N, "e5m2").split(s["sizes"])
+    cols = [_values(*_lines(v.T, "e5m2"), v.shape[0], "e5m2") for v in s["dy"].split(s["sizes"])]
+    xt = _grouped_values(s["xt"], s["xts"], s["sizes"])
+    return {"dx": torch.cat([v @ _values(w, ws, N).T for v, w, ws in zip(row, s["w"], s["ws"])]).to(torch.bfloat16),
+            "dw": torch.stack([d @ v.T for d, v in zip(cols, xt)])}
+
+
+# --------------------------------------------------------------------- the framework's calls
+
+def _own(s):
+    import mxfp8_block_scaled_03_amd as mxq
+
+    if s["op"] == "quantize":
+        x, elem, axis = s["x"], s["elem"], s["axis"]
+        if axis in ("row", "col"):
+            c, sc = mxq.quantize_b128(x, elem, axis)
+            return [_quantized(c, sc, x.shape[1] if axis == "row" else x.shape[0], elem)]
+        rc, rs, cc, cs = mxq.quantize_b128_dual(x, elem, tile=axis == "tile")
+        return [_quantized(rc, rs, x.shape[1], elem), _quantized(cc, cs, x.shape[0], elem)]
+    if s["op"] == "product":
+        return mxq.gemm_b128(s["x"], s["xs"], s["w"], s["ws"], s["K"], bias=s["b"], act=s["act"] or None,
+                             out_dtype=WIDE[s["out"]], accum=s["accum"])
+    if s["op"] == "backward":
+        rc, rs, cc, cs = mxq.quantize_b128_dual(s["dy"], "e5m2")
+        return {"dx": mxq.gemm_b128(rc, rs, s["wt"], s["wts"], s["N"], x_elem="e5m2", accum="fp8"),
+                "dw": mxq.gemm_b128(cc, cs, s["xt"], s["xts"], s["M"], x_elem="e5m2", out_dtype=torch.float32)}
+    if s["op"] == "route":
+        r = mxq.moe_route(s["logits"], s["k"], renormalize=s["renorm"], mask=s["mask"])
+        d = mxq.moe_route_grad(s["logits"], r, s["d_shares"], s["d_loss"], renormalize=s["renorm"], mask=s["mask"])
+        return {"experts": r.experts, "shares": r.shares, "counts": r.counts, "offsets": r.offsets, "order": r.order,
+                "loss": r.loss, "d_logits": d}
+    if s["op"] == "experts":
+        c, sc = mxq.quantize_b128(s["x"])
+        return mxq.moe_gemm_b128(c, sc, s["w"], s["ws"], s["offsets"], s["K"], out_dtype=WIDE[s["out"]],
+                                 accum=s["accum"])
+    rc, rs, cc, cs = mxq.quantize_b128_dual(s["dy"], "e5m2", offsets=s["offsets"])
+    return {"dx": mxq.moe_gemm_b128(rc, rs, s["w"], s["ws"], s["offsets"], s["N"], x_elem="e5m2", accum="fp8"),
+            "dw": mxq.moe_wgrad_b128(cc, cs, s["xt"], s["xts"], s["offsets"], x_elem="e5m2", out_dtype=torch.float32)}
+
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+# ------------------------------------------------------------- the definition, in 64 bits
+
+def _exact_decode(codes, elem):
+    """Codes to float64 by their bits: (-1)^s 2^(E - bias) (1 + m / 2^b), without the 1 where E = 0."""
+    bits, bias = (3, 7) if elem == "e4m3" else (2, 15)
+    n = torch.arange(256)
+    ex, m = ((n & 127) >> bits).double(), (n & (2 ** bits - 1)).double() / 2 ** bits
+    two = torch.tensor([2.0 ** (max(int(e), 1) - bias) for e in ex], dtype=torch.float64)
+    v = two * (m + (ex > 0).double()) * (1 - 2 * (n >> 7).double())
+    return v.to(codes.device)[codes.long()]
+
+
+def _exact_encode(v, elem):
+    """The FP8 number nearest to each v (|v| <= fmax): ties to the even mantissa."""
+    bits, low = (3, -6) if elem == "e4m3" else (2, -14)
+    ex = torch.frexp(v)[1].long() - 1                               # |v| in [2^ex, 2^(ex + 1))
+    ulp = torch.where(v == 0, low, ex.clamp(min=low)) - bits
+    unit = ((ulp + 1023) << 52).view(torch.float64)                 # 2^ulp from its bits
+    return torch.round(v / unit) * unit                             # torch rounds halves to even
+
+
+def _exact_parts(x, elem, tile=False):
+    """FP8 numbers [L][K] and scales of x, block by block, in 64 bits.  The definition rounds scale
+    and factor to fp32 and the product of value and factor to fp32: each is rounded from 64 bits,
+    which the 53 bits leave correct."""
+    L, K = x.shape
+    nb, nl = -(-K // B), -(-L // B) if tile else L
+    rows = B if tile else 1
+    w = torch.zeros((nl * rows, nb * B), dtype=torch.float64, device=x.device)
+    w[:L, :K] = x.double()
+    w = w.view(nl, rows, nb, B)
+    amax = w.abs().amax(3).amax(1)
+    a = torch.where(amax < 2.0 ** -100, torch.full_like(amax, 2.0 ** -100), amax)
+    f = FMAX[elem]
+    s = torch.where(amax == 0, torch.ones_like(a), a / f).float().double()
+    r = torch.where(amax == 0, torch.ones_like(a), f / a).float().double()
+    q = (w * r[:, None, :, None]).float().double().clamp(-f, f)
+    return _exact_encode(q, elem).view(nl * rows, nb * B)[:L, :K], s
+
+
+def _exact_values(codes, scales, K, elem="e4m3"):
+    L = codes.shape[0]
+    s = scales.double().repeat_interleave(B, 1)[:, :K]
+    if s.shape[0] != L:
+        s = s.repeat_interleave(B, 0)[:L]
+    return _exact_decode(codes[:, :K], elem) * s
+
+
+def _exact_quantized(x, elem):
+    v, s = _exact_parts(x, elem)
+    return v * s.repeat_interleave(B, 1)[:, :x.shape[1]]
+
+
+def _exact_route(s):
+    """Token by token in 64 bits, from the definition: one-hot rows in place of gathers and scatters."""
+    T, E, k = s["T"], s["E"], s["k"]
+    z = s["logits"].double()
+    live = torch.ones(T, device=z.device) if s["mask"] is None else s["mask"].double()
+    live = live.double()
+    p = torch.exp(z - torch.logsumexp(z, -1, keepdim=True))
+    left, taken = z.clone(), []
+    for _ in range(k):                                              # one maximum after the other, the lowest index
+        best = left == left.amax(-1, keepdim=True)
+        first = best & (best.cumsum(-1) == 1)
+        taken.append(first.double())
+        left = left.masked_fill(first, float("-inf"))
+    hot = torch.stack(taken, 1)                                     # [T][k][E]
+    share = (hot * p[:, None]).sum(-1)
+    if s["renorm"]:
+        share = share / share.sum(-1, keepdim=True)
+    n = live.sum().clamp(min=1)
+    f = (hot.sum(1) * live[:, None]).sum(0) / (n * k)
+    loss = E * (f * (p * live[:, None]).sum(0) / n).sum()
+    up, d = s["d_loss"].double(), s["d_shares"].double()
+    g = (E * f / n * up).expand(T, E)
+    direct = (hot * d[..., None]).sum(1)                            # the shares' gradient, expert by expert
+    if s["renorm"]:
+        q = (hot * share[..., None]).sum(1)
+        grad = p * (g - (p * g).sum(-1, keepdim=True)) + q * (direct - (q * direct).sum(-1, keepdim=True))
+    else:
+        g = g + direct
+        grad = p * (g - (p * g).sum(-1, keepdim=True))
+    return {"experts": None, "shares": share * live[:, None], "counts": None, "offsets": None, "order": None,
+            "loss": loss.reshape(1), "d_logits": grad * live[:, None]}
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if s["op"] == "quantize":
+        x, elem, axis = s["x"], s["elem"], s["axis"]
+        if axis == "tile":
+            v, sc = _exact_parts(x, elem, True)
+            return [{"codes": v, "scales": sc}, {"codes": v.T, "scales": sc.T}]
+        sides = {"row": (x,), "col": (x.T,), "dual": (x, x.T)}[axis]
+        return [dict(zip(("codes", "scales"), _exact_parts(v, elem))) for v in sides]
+    if s["op"] == "product":
+        y = _exact_values(s["x"], s["xs"], s["K"]) @ _exact_values(s["w"], s["ws"], s["K"]).T
+        y = y if s["b"] is None else y + s["b"].double()
+        return y / (1 + torch.exp(-y)) if s["act"] == "silu" else y
+    if s["op"] == "backward":
+        M, N = s["M"], s["N"]
+        return {"dx": _exact_quantized(s["dy"], "e5m2") @ _exact_values(s["wt"], s["wts"], N).T,
+                "dw": _exact_quantized(s["dy"].T, "e5m2") @ _exact_values(s["xt"], s["xts"], M).T}
+    if s["op"] == "route":
+        return _exact_route(s)
+    N, K, first, at = s["N"], s["K"], 0, 0
+    ys, dws = [], []
+    back = s["op"] != "experts"
+    xt = _exact_values(s["xt"], s["xts"], s["xt"].shape[1]) if back else None
+    for e, n in enumerate(s["sizes"]):
+        rows = s["dy" if back else "x"][first:first + n]
+        ys.append(_exact_quantized(rows, "e5m2" if back else "e4m3")
+                  @ _exact_values(s["w"][e], s["ws"][e], N if back else K).T)
+        if back:
+            dw = torch.zeros((N, K), dtype=torch.float64, device=xt.device)
+            dws.append(dw if n == 0 else _exact_quantized(rows.T, "e5m2") @ xt[:, at:at + n].T)
+        first += n
+        at += -(-n // B) * B
+    return torch.cat(ys) if s["op"] == "experts" else {"dx": torch.cat(ys), "dw": torch.stack(dws)}
