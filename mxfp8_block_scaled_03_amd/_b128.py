@@ -1,0 +1,362 @@
+"""FP8 in blocks of 128 with FP32 scales, and expert routing, on torch tensors (the ``*_b128`` and
+``mxq_moe_route*`` entry points of include/mxq.h).  Argument checks and marshalling only, like
+``_binding``; every call raises if the library is missing.
+
+Codes are uint8 [lines][128 * blocks]; scales float32 [lines][blocks] (a tile's: [tiles][blocks]),
+those of lines stored block by block (stride 1 along the lines), as the quantizer gives them."""
+from __future__ import annotations
+
+import functools
+from typing import NamedTuple
+
+import torch
+
+from ._binding import _ACC, _ACT, _ELEM, MXQ_SCALE_AMAX, MXQ_SCALE_CEIL, mxq_moe_route_workspace
+from ._fp4 import _WIDE, _call, _empty, _lines, _same_device, _U8, _wide
+
+B = 128
+_RULES = {"amax": MXQ_SCALE_AMAX, "ceil": MXQ_SCALE_CEIL}
+_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
+
+
+def _blocks(k: int) -> int:
+    return (k + B - 1) // B
+
+
+def _elem(name: str, *elems) -> None:
+    for e in elems:
+        if e not in _ELEM:
+            raise ValueError("%s must be 'e4m3' or 'e5m2'" % name)
+
+
+def _offsets(t) -> int:
+    """Checks expert offsets; the number of experts."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.dim() != 1 or t.shape[0] < 2 or t.stride(0) != 1:
+        raise ValueError("offsets must be a contiguous 1-D int32 tensor of E + 1 elements")
+    return t.shape[0] - 1
+
+
+def _devices(x, *named) -> int:
+    """The device of x, which all given tensors have to be on."""
+    device = x.get_device()
+    if device < 0 or any(t is not None and t.get_device() != device for _, t in named):
+        _same_device((("the first tensor", x),) + named)
+    return device
+
+
+def _line_scales(t, name: str, lines: int, nb: int) -> int:
+    """Checks scales of lines; the pitch from block to block."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.dim() != 2:
+        raise ValueError("%s must be a 2-D float32 tensor" % name)
+    if t.shape[0] != lines or t.shape[1] < nb:
+        raise ValueError("%s must have shape (%d, >= %d), got %s" % (name, lines, nb, tuple(t.shape)))
+    step, pitch = t.stride()
+    if lines > 1 and nb > 0 and step != 1:
+        raise ValueError("%s must be stored block by block (stride 1 along the lines)" % name)
+    if nb > 1 and pitch < lines:
+        raise ValueError("%s has overlapping blocks" % name)
+    return pitch if nb > 1 else max(lines, 1)
+
+
+def _weight_scales(t, name: str, lines: int, nb: int, line_dim: int = 0):
+    """Checks scales of lines or of tiles, by their number; (block, line or tile stride, block stride)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.dim() != 2 + line_dim:
+        raise ValueError("%s must be a %d-D float32 tensor" % (name, 2 + line_dim))
+    n, b = t.shape[-2:]
+    if (n != lines and n != _blocks(lines)) or b < nb:
+        raise ValueError("%s must have %d (lines) or %d (tiles) rows and at least %d columns, got %s"
+                         % (name, lines, _blocks(lines), nb, tuple(t.shape)))
+    step, pitch = t.stride()[-2:]
+    if n != lines:
+        return B, step, pitch
+    if lines > 1 and nb > 0 and step != 1:
+        raise ValueError("%s must be stored block by block (stride 1 along the lines)" % name)
+    return 1, 1, pitch if nb > 1 else max(lines, 1)
+
+
+def _code_lines(lines: int, nb: int, device):
+    return _empty((lines, B * nb), (max(B * nb, 1), 1), dtype=_U8, device=device)
+
+
+def _scale_lines(lines: int, nb: int, device):
+    return _empty((lines, nb), (1, max(lines, 1)), dtype=_F32, device=device)
+
+
+def _rule(rule: str) -> int:
+    if rule not in _RULES:
+        raise ValueError("rule must be 'amax' or 'ceil'")
+    return _RULES[rule]
+
+
+def _run_quantize(x, ld, elem, rule, tile, rc, rs, cc, cs, offsets, experts, device):
+    if x.shape[0] == 0 or x.shape[1] == 0:
+        return
+    _call("mxq_quantize_b128", device, (
+        x.data_ptr(), _WIDE[x.dtype], x.shape[0], x.shape[1], ld, _ELEM[elem], rule, 1 if tile else 0,
+        None if rc is None else rc.data_ptr(), 0 if rc is None else max(rc.shape[1], 1),
+        None if rs is None else rs.data_ptr(), 0 if rs is None else rs.stride(0 if tile else 1),
+        None if cc is None else cc.data_ptr(), 0 if cc is None else max(cc.shape[1], 1),
+        None if cs is None or tile else cs.data_ptr(), 0 if cs is None else cs.stride(1),
+        None if offsets is None else offsets.data_ptr(), experts))
+
+
+def quantize_b128(x, elem: str = "e4m3", axis: str = "row", rule: str = "amax", offsets=None):
+    """FP8-quantize a 2-D bf16/fp32 CUDA tensor in blocks of 128: (codes, scales).
+
+    axis="row": blocks along each row -> codes [rows][128 nb], scales [rows][nb];
+    axis="col": blocks down each column, transposed -> codes [cols][128 nb], scales [cols][nb];
+    axis="tile": tiles of 128 x 128 -> codes [rows][128 nb], scales [ceil(rows/128)][nb].
+    rule "amax": scale amax / fmax; "ceil": that rounded up to a power of two.  offsets (int32
+    [E + 1], axis="col"): blocks begin anew with every expert's rows; rows past the last
+    expert's are skipped.  See mxq_quantize_b128.
+    """
+    ld = _wide(x, "x")
+    _elem("elem", elem)
+    r = _rule(rule)
+    if axis not in ("row", "col", "tile"):
+        raise ValueError("axis must be 'row', 'col' or 'tile'")
+    experts = 1
+    if offsets is not None:
+        if axis != "col":
+            raise ValueError("offsets need axis='col'")
+        experts = _offsets(offsets)
+    device = _devices(x, ("offsets", offsets))
+    rows, cols = x.shape
+    if axis == "col":
+        nb = (rows + (B - 1) * experts) // B
+        c, s = _code_lines(cols, nb, x.device), _scale_lines(cols, nb, x.device)
+        _run_quantize(x, ld, elem, r, False, None, None, c, s, offsets, experts, device)
+    else:
+        nb = _blocks(cols)
+        c = _code_lines(rows, nb, x.device)
+        tile = axis == "tile"
+        s = _empty((_blocks(rows), nb), (max(nb, 1), 1), dtype=_F32, device=x.device) if tile else \
+            _scale_lines(rows, nb, x.device)
+        _run_quantize(x, ld, elem, r, tile, c, s, None, None, None, 1, device)
+    return c, s
+
+
+def quantize_b128_dual(x, elem: str = "e4m3", tile: bool = False, rule: str = "amax", offsets=None):
+    """Both orientations from one read: (row_codes, row_scales, col_codes, col_scales), as
+    quantize_b128 along rows and columns; with tile=True the codes of 128 x 128 tiles and the same
+    codes transposed, whose scales are the transposed view of row_scales.  With offsets only the
+    experts' rows are quantized, in both orientations.
+    """
+    ld = _wide(x, "x")
+    _elem("elem", elem)
+    r = _rule(rule)
+    experts = 1
+    if offsets is not None:
+        if tile:
+            raise ValueError("tiles cannot follow offsets")
+        experts = _offsets(offsets)
+    device = _devices(x, ("offsets", offsets))
+    rows, cols = x.shape
+    nbc, nbr = _blocks(cols), (rows + (B - 1) * experts) // B
+    rc, cc = _code_lines(rows, nbc, x.device), _code_lines(cols, nbr, x.device)
+    if tile:
+        rs = _empty((nbr, nbc), (max(nbc, 1), 1), dtype=_F32, device=x.device)
+        cs = rs.t()
+    else:
+        rs, cs = _scale_lines(rows, nbc, x.device), _scale_lines(cols, nbr, x.device)
+    _run_quantize(x, ld, elem, r, tile, rc, rs, cc, cs, offsets, experts, device)
+    return rc, rs, cc, cs
+
+
+def _out(out, shape, out_dtype, device):
+    """The output tensor and its row pitch."""
+    if out is not None:
+        if tuple(out.shape) != shape:
+            raise ValueError("out must have shape %s, got %s" % (shape, tuple(out.shape)))
+        return out
+    if out_dtype is not None and out_dtype not in _WIDE:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    return torch.empty(shape, dtype=out_dtype or _BF16, device=device)
+
+
+def _accum(accum: str) -> int:
+    if accum not in _ACC:
+        raise ValueError("accum must be 'fp32' or 'fp8'")
+    return _ACC[accum]
+
+
+def gemm_b128(x_codes, x_scales, w_codes, w_scales, K: int, x_elem: str = "e4m3", w_elem: str = "e4m3",
+              alpha: float = 1.0, bias=None, out_dtype=None, out=None, accum: str = "fp32", act=None):
+    """Y[M][N] = act(alpha * (X W) + bias), both operands in blocks of 128: x_codes [M][128 nb] and
+    x_scales [M][nb] of lines; w_codes [N][128 nb] and w_scales [N][nb] of lines or [ceil(N/128)][nb] of
+    tiles.  accum="fp32": exact products, FP32 sums; "fp8": the FP8 matrix cores, faster (see
+    mxq_gemm_b128).  act: None or "silu"; out_dtype bf16 (default) or fp32, or a preallocated `out`.
+    """
+    if K < 0:
+        raise ValueError("K must be >= 0")
+    nb = _blocks(K)
+    ld_x, ld_w = _lines(x_codes, "x_codes", _U8, 0, B * nb), _lines(w_codes, "w_codes", _U8, 0, B * nb)
+    M, N = x_codes.shape[0], w_codes.shape[0]
+    ld_xs = _line_scales(x_scales, "x_scales", M, nb)
+    w_block, ws_n, ws_k = _weight_scales(w_scales, "w_scales", N, nb)
+    _elem("element formats", x_elem, w_elem)
+    acc = _accum(accum)
+    if bias is not None and (not isinstance(bias, torch.Tensor) or bias.dtype != _F32 or bias.dim() != 1
+                             or bias.shape[0] != N or (N > 1 and bias.stride(0) != 1)):
+        raise ValueError("bias must be a contiguous 1-D float32 tensor of N = %d elements" % N)
+    if act not in _ACT:
+        raise ValueError("act must be None or 'silu'")
+    if out is not None:
+        _wide(out, "out")
+    device = _devices(x_codes, ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("bias", bias),
+                      ("out", out))
+    out = _out(out, (M, N), out_dtype, x_codes.device)
+    _call("mxq_gemm_b128", device, (
+        M, N, K, x_codes.data_ptr(), ld_x, x_scales.data_ptr(), ld_xs, _ELEM[x_elem], w_codes.data_ptr(), ld_w,
+        w_scales.data_ptr(), ws_n, ws_k, w_block, _ELEM[w_elem], alpha, None if bias is None else bias.data_ptr(),
+        _ACT[act], acc, out.data_ptr(), _WIDE[out.dtype], _lines(out, "out", out.dtype, 0, 0)))
+    return out
+
+
+def moe_gemm_b128(x_codes, x_scales, w_codes, w_scales, offsets, K: int, x_elem: str = "e4m3", w_elem: str = "e4m3",
+                  out_dtype=None, out=None, accum: str = "fp32"):
+    """Every expert's rows times its own matrix: Y[r] = X[r] W_e for r in offsets[e] .. offsets[e+1] - 1.
+    x_codes [R][128 nb] and x_scales [R][nb], rows sorted by expert; w_codes [E][N][128 nb], w_scales
+    [E][N or ceil(N/128)][nb]; offsets int32 [E + 1] on the device.  Rows of no expert are left as they
+    were (without `out`: unset).  Otherwise as gemm_b128; see mxq_moe_gemm_b128.
+    """
+    if K < 0:
+        raise ValueError("K must be >= 0")
+    nb, E = _blocks(K), _offsets(offsets)
+    ld_x = _lines(x_codes, "x_codes", _U8, 0, B * nb)
+    if not isinstance(w_codes, torch.Tensor) or w_codes.dim() != 3 or w_codes.shape[0] != E:
+        raise ValueError("w_codes must be a 3-D tensor of E = %d matrices" % E)
+    if not isinstance(w_scales, torch.Tensor) or w_scales.dim() != 3 or w_scales.shape[0] != E:
+        raise ValueError("w_scales must be a 3-D tensor of E = %d matrices" % E)
+    R, N = x_codes.shape[0], w_codes.shape[1]
+    ld_w = _lines(w_codes[0], "w_codes", _U8, 0, B * nb)
+    ld_xs = _line_scales(x_scales, "x_scales", R, nb)
+    w_block, ws_n, ws_k = _weight_scales(w_scales, "w_scales", N, nb, 1)
+    _elem("element formats", x_elem, w_elem)
+    acc = _accum(accum)
+    if out is not None:
+        _wide(out, "out")
+    device = _devices(x_codes, ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales),
+                      ("offsets", offsets), ("out", out))
+    out = _out(out, (R, N), out_dtype, x_codes.device)
+    _call("mxq_moe_gemm_b128", device, (
+        R, N, K, E, offsets.data_ptr(), x_codes.data_ptr(), ld_x, x_scales.data_ptr(), ld_xs, _ELEM[x_elem],
+        w_codes.data_ptr(), ld_w, w_codes.stride(0), w_scales.data_ptr(), ws_n, ws_k, w_scales.stride(0), w_block,
+        _ELEM[w_elem], acc, out.data_ptr(), _WIDE[out.dtype], _lines(out, "out", out.dtype, 0, 0)))
+    return out
+
+
+def moe_wgrad_b128(dy_codes, dy_scales, x_codes, x_scales, offsets, x_elem: str = "e5m2", w_elem: str = "e4m3",
+                   out_dtype=None, out=None, accum: str = "fp32"):
+    """Every expert's weight gradient: dW[e] = sum over its rows r of dY[r]^T X[r] -> [E][N][K], fp32 by default.
+    dy_codes [N][128 nb] in format x_elem and x_codes [K][128 nb] in w_elem, with their scales, from
+    quantize_b128(..., "col" or dual, offsets=offsets).  An expert without rows gets zeros.  See
+    mxq_moe_wgrad_b128.
+    """
+    E = _offsets(offsets)
+    if not isinstance(dy_codes, torch.Tensor) or dy_codes.dim() != 2:
+        raise ValueError("dy_codes must be a 2-D uint8 tensor")
+    nb = dy_codes.shape[1] // B
+    rows = max(B * nb + B - 1 - (B - 1) * E, 0)         # the most rows that give lines of nb blocks
+    ld_dy, ld_x = _lines(dy_codes, "dy_codes", _U8, 0, B * nb), _lines(x_codes, "x_codes", _U8, 0, B * nb)
+    N, K = dy_codes.shape[0], x_codes.shape[0]
+    ld_ds, ld_xs = _line_scales(dy_scales, "dy_scales", N, nb), _line_scales(x_scales, "x_scales", K, nb)
+    _elem("element formats", x_elem, w_elem)
+    acc = _accum(accum)
+    if out is not None and (not isinstance(out, torch.Tensor) or out.dim() != 3 or out.dtype not in _WIDE
+                            or out.stride(2) != 1):
+        raise ValueError("out must be a 3-D float32 or bfloat16 tensor with unit stride along its last dimension")
+    device = _devices(dy_codes, ("dy_scales", dy_scales), ("x_codes", x_codes), ("x_scales", x_scales),
+                      ("offsets", offsets), ("out", out))
+    out = _out(out, (E, N, K), out_dtype or _F32, dy_codes.device)
+    _call("mxq_moe_wgrad_b128", device, (
+        N, K, rows, E, offsets.data_ptr(), dy_codes.data_ptr(), ld_dy, dy_scales.data_ptr(), ld_ds, _ELEM[x_elem],
+        x_codes.data_ptr(), ld_x, x_scales.data_ptr(), ld_xs, _ELEM[w_elem], acc, out.data_ptr(), _WIDE[out.dtype],
+        max(out.stride(1), K, 1), out.stride(0)))
+    return out
+
+
+class MoeRoute(NamedTuple):
+    """What moe_route gives, see there."""
+    experts: torch.Tensor
+    shares: torch.Tensor
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    order: torch.Tensor
+    loss: torch.Tensor
+    slope: torch.Tensor
+
+
+@functools.lru_cache(maxsize=1024)
+def _route_workspace(T: int, E: int, k: int) -> int:
+    return mxq_moe_route_workspace(T, E, k)
+
+
+def _route_inputs(logits, mask):
+    ld = _wide(logits, "logits")
+    T, E = logits.shape
+    if mask is not None and (not isinstance(mask, torch.Tensor) or mask.dtype not in (torch.bool, _U8)
+                             or mask.dim() != 1 or mask.shape[0] != T or (T > 1 and mask.stride(0) != 1)):
+        raise ValueError("mask must be a contiguous 1-D bool or uint8 tensor of T = %d elements" % T)
+    return T, E, ld
+
+
+def moe_route(logits, k: int, renormalize: bool = True, mask=None) -> MoeRoute:
+    """Routes tokens to experts: softmax of logits [T][E] (fp32 or bf16), the k greatest, shares, per-expert
+    counts and order, and the balance loss E sum_e f_e P_e.  mask [T] (bool): tokens that count.
+
+    experts [T][k] int32 (-1 where there is none), shares [T][k] fp32, counts [E] and offsets [E + 1]
+    int32, order [T k] int32 (the slots t k + rank by expert: order // k are the rows to gather for
+    moe_gemm_b128; -1 from offsets[E] on), loss [1] and slope [E] fp32.  See mxq_moe_route.
+    """
+    T, E, ld = _route_inputs(logits, mask)
+    if not 1 <= k <= min(E, 64):
+        raise ValueError("k must be between 1 and min(E, 64) = %d" % min(E, 64))
+    device = _devices(logits, ("mask", mask))
+    dev = logits.device
+    experts = _empty((T, k), (k, 1), dtype=_I32, device=dev)
+    shares = _empty((T, k), (k, 1), dtype=_F32, device=dev)
+    counts = _empty((E,), (1,), dtype=_I32, device=dev)
+    offsets = _empty((E + 1,), (1,), dtype=_I32, device=dev)
+    order = _empty((T * k,), (1,), dtype=_I32, device=dev)
+    loss = _empty((1,), (1,), dtype=_F32, device=dev)
+    slope = _empty((E,), (1,), dtype=_F32, device=dev)
+    need = _route_workspace(T, E, k)
+    workspace = _empty((need,), (1,), dtype=_U8, device=dev) if need else None
+    _call("mxq_moe_route", device, (
+        T, E, k, 1 if renormalize else 0, logits.data_ptr(), _WIDE[logits.dtype], ld,
+        None if mask is None else mask.data_ptr(), experts.data_ptr(), shares.data_ptr(), counts.data_ptr(),
+        offsets.data_ptr(), order.data_ptr(), loss.data_ptr(), slope.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), need))
+    return MoeRoute(experts, shares, counts, offsets, order, loss, slope)
+
+
+def moe_route_grad(logits, route: MoeRoute, d_shares=None, d_loss=None, renormalize: bool = True, mask=None):
+    """The gradient of the logits (in their type) from those of moe_route's shares (fp32 [T][k]) and loss (one fp32
+    element on the device); either may be None.  route, renormalize and mask: of the forward call.  See
+    mxq_moe_route_grad.
+    """
+    T, E, ld = _route_inputs(logits, mask)
+    experts, shares, slope = route.experts, route.shares, route.slope
+    k = experts.shape[1]
+    if tuple(experts.shape) != (T, k) or tuple(shares.shape) != (T, k) or tuple(slope.shape) != (E,):
+        raise ValueError("route is of other sizes than logits (%d, %d)" % (T, E))
+    for name, t, dtype in (("experts", experts, _I32), ("shares", shares, _F32), ("slope", slope, _F32)):
+        if t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError("route.%s must be a contiguous %s tensor" % (name, dtype))
+    ld_ds = 0
+    if d_shares is not None:
+        ld_ds = _lines(d_shares, "d_shares", _F32, T, k)
+        if tuple(d_shares.shape) != (T, k):
+            raise ValueError("d_shares must have shape (%d, %d), got %s" % (T, k, tuple(d_shares.shape)))
+    if d_loss is not None and (not isinstance(d_loss, torch.Tensor) or d_loss.dtype is not _F32 or d_loss.numel() != 1):
+        raise ValueError("d_loss must be a float32 tensor of one element")
+    device = _devices(logits, ("mask", mask), ("experts", experts), ("shares", shares), ("slope", slope),
+                      ("d_shares", d_shares), ("d_loss", d_loss))
+    d = _empty((T, E), (max(E, 1), 1), dtype=logits.dtype, device=logits.device)
+    _call("mxq_moe_route_grad", device, (
+        T, E, k, 1 if renormalize else 0, logits.data_ptr(), _WIDE[logits.dtype], ld,
+        None if mask is None else mask.data_ptr(), experts.data_ptr(), shares.data_ptr(), slope.data_ptr(),
+        None if d_shares is None else d_shares.data_ptr(), ld_ds, None if d_loss is None else d_loss.data_ptr(),
+        d.data_ptr(), max(E, 1)))
+    return d

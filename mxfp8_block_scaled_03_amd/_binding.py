@@ -11,7 +11,7 @@ MXQ_F32, MXQ_BF16, MXQ_E4M3, MXQ_E5M2, MXQ_E2M1 = 0, 1, 2, 3, 4
 MXQ_ROWWISE, MXQ_COLWISE = 0, 1
 MXQ_ACC_FP8_MFMA, MXQ_ACC_FP32 = 0, 1
 MXQ_ACT_NONE, MXQ_ACT_SILU = 0, 1
-MXQ_SCALE_CEIL, MXQ_SCALE_OCP = 0, 1
+MXQ_SCALE_CEIL, MXQ_SCALE_OCP, MXQ_SCALE_AMAX = 0, 1, 2
 
 _ELEM = {"e4m3": MXQ_E4M3, "e5m2": MXQ_E5M2}
 _ACC = {"fp8": MXQ_ACC_FP8_MFMA, "fp32": MXQ_ACC_FP32}
@@ -91,6 +91,26 @@ def lib():
         L.mxq_moe_fp4.restype = ci
         L.mxq_moe_fp4.argtypes = [i64, i64, i64, i64, i64, ci, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, i64,
                                   i64, vp, i64, i64, vp, ci, i64, vp, i64, vp]
+        f32 = ctypes.c_float
+        L.mxq_quantize_b128.restype = ci
+        L.mxq_quantize_b128.argtypes = [vp, ci, i64, i64, i64, ci, ci, ci, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+        L.mxq_gemm_b128.restype = ci
+        L.mxq_gemm_b128.argtypes = [i64, i64, i64, vp, i64, vp, i64, ci, vp, i64, vp, i64, i64, ci, ci, f32, vp, ci, ci, vp,
+                                    ci, i64, vp]
+        L.mxq_moe_gemm_b128.restype = ci
+        L.mxq_moe_gemm_b128.argtypes = [i64, i64, i64, i64, vp, vp, i64, vp, i64, ci, vp, i64, i64, vp, i64, i64, i64, ci,
+                                        ci, ci, vp, ci, i64, vp]
+        L.mxq_moe_wgrad_b128.restype = ci
+        L.mxq_moe_wgrad_b128.argtypes = [i64, i64, i64, i64, vp, vp, i64, vp, i64, ci, vp, i64, vp, i64, ci, ci, vp, ci, i64,
+                                         i64, vp]
+        L.mxq_gemm_b128_plan.restype = ci
+        L.mxq_gemm_b128_plan.argtypes = [ci, i64, i64, i64, i64, ci, ci, ci, ip, ip, ip]
+        L.mxq_moe_route_workspace.restype = ci
+        L.mxq_moe_route_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+        L.mxq_moe_route.restype = ci
+        L.mxq_moe_route.argtypes = [i64, i64, i64, ci, vp, ci, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+        L.mxq_moe_route_grad.restype = ci
+        L.mxq_moe_route_grad.argtypes = [i64, i64, i64, ci, vp, ci, i64, vp, vp, vp, vp, vp, i64, vp, vp, i64, vp]
         _lib = L
     return _lib
 
@@ -230,6 +250,59 @@ def mxq_moe_fp4(T, H, I, E, k, renormalize, x, ld_x, logits, ld_logits, w13_code
     return lib().mxq_moe_fp4(T, H, I, E, k, renormalize, x, ld_x, logits, ld_logits, w13_codes, ld_w13, expert_w13,
                              w13_scales, ld_s13, expert_s13, w2_codes, ld_w2, expert_w2, w2_scales, ld_s2, expert_s2,
                              y, y_type, ld_y, workspace, workspace_bytes, stream)
+
+
+def mxq_quantize_b128(src, src_type, rows, cols, ld_src, elem, rule, tile, row_codes, ld_row_codes, row_scales,
+                      ld_row_scales, col_codes, ld_col_codes, col_scales, ld_col_scales, offsets, experts,
+                      stream=None) -> int:
+    return lib().mxq_quantize_b128(src, src_type, rows, cols, ld_src, elem, rule, tile, row_codes, ld_row_codes, row_scales,
+                                   ld_row_scales, col_codes, ld_col_codes, col_scales, ld_col_scales, offsets, experts,
+                                   stream)
+
+
+def mxq_gemm_b128(M, N, K, x_codes, ld_x, x_scales, ld_xs, x_elem, w_codes, ld_w, w_scales, ws_line, ws_block, w_block,
+                  w_elem, alpha, bias, act, accum, y, y_type, ld_y, stream=None) -> int:
+    return lib().mxq_gemm_b128(M, N, K, x_codes, ld_x, x_scales, ld_xs, x_elem, w_codes, ld_w, w_scales, ws_line, ws_block,
+                               w_block, w_elem, alpha, bias, act, accum, y, y_type, ld_y, stream)
+
+
+def mxq_moe_gemm_b128(rows, N, K, E, offsets, x_codes, ld_x, x_scales, ld_xs, x_elem, w_codes, ld_w, expert_w, w_scales,
+                      ws_line, ws_block, expert_ws, w_block, w_elem, accum, y, y_type, ld_y, stream=None) -> int:
+    return lib().mxq_moe_gemm_b128(rows, N, K, E, offsets, x_codes, ld_x, x_scales, ld_xs, x_elem, w_codes, ld_w, expert_w,
+                                   w_scales, ws_line, ws_block, expert_ws, w_block, w_elem, accum, y, y_type, ld_y, stream)
+
+
+def mxq_moe_wgrad_b128(M, N, rows, E, offsets, x_codes, ld_x, x_scales, ld_xs, x_elem, w_codes, ld_w, w_scales, ld_ws,
+                       w_elem, accum, y, y_type, ld_y, expert_y, stream=None) -> int:
+    return lib().mxq_moe_wgrad_b128(M, N, rows, E, offsets, x_codes, ld_x, x_scales, ld_xs, x_elem, w_codes, ld_w, w_scales,
+                                    ld_ws, w_elem, accum, y, y_type, ld_y, expert_y, stream)
+
+
+def mxq_gemm_b128_plan(mode: int, M: int, N: int, K: int, E: int, w_block: int, accum: int, cus: int) -> tuple:
+    """(tile_m, tile_n, waves) of a product in blocks of 128 on `cus` CUs (host logic only); raises MxqError."""
+    out = [ctypes.c_int() for _ in range(3)]
+    _check(lib().mxq_gemm_b128_plan(mode, M, N, K, E, w_block, accum, cus, *[ctypes.byref(v) for v in out]),
+           "mxq_gemm_b128_plan")
+    return tuple(v.value for v in out)
+
+
+def mxq_moe_route_workspace(T: int, E: int, k: int) -> int:
+    """Bytes of workspace that mxq_moe_route needs (host logic only); raises MxqError."""
+    n = ctypes.c_int64()
+    _check(lib().mxq_moe_route_workspace(T, E, k, ctypes.byref(n)), "mxq_moe_route_workspace")
+    return n.value
+
+
+def mxq_moe_route(T, E, k, renormalize, logits, logits_type, ld_logits, mask, experts, shares, counts, offsets, order, loss,
+                  slope, workspace, workspace_bytes, stream=None) -> int:
+    return lib().mxq_moe_route(T, E, k, renormalize, logits, logits_type, ld_logits, mask, experts, shares, counts, offsets,
+                               order, loss, slope, workspace, workspace_bytes, stream)
+
+
+def mxq_moe_route_grad(T, E, k, renormalize, logits, logits_type, ld_logits, mask, experts, shares, slope, d_shares,
+                       ld_d_shares, d_loss, d_logits, ld_d_logits, stream=None) -> int:
+    return lib().mxq_moe_route_grad(T, E, k, renormalize, logits, logits_type, ld_logits, mask, experts, shares, slope,
+                                    d_shares, ld_d_shares, d_loss, d_logits, ld_d_logits, stream)
 
 
 # ----------------------------------------------------------------- torch conveniences

@@ -155,4 +155,68 @@ MoeFp4Plan moe_fp4_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, b
 int64_t moe_fp4_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, bool y_bf16);
 hipError_t launch_moe_fp4(const MoeFp4& p, hipStream_t stream);
 
+// ---- FP8 in blocks of 128 with FP32 scales (quantize_b128.hip, gemm_b128*.hip).  Code lines hold 128 bytes
+// per block; scales are [block][line], or [tile][block] of tiles.
+
+// rc / rs: along rows; cc / cs: along columns (either pair may be null).  tile: one scale for each 128 x 128, in
+// rs; rc as it is, cc transposed.  offsets (device, experts + 1): columns' blocks begin anew with each expert's rows.
+hipError_t launch_quant_b128(const void* src, int src_bf16, int64_t rows, int64_t cols, int64_t ld_src, int fmt, int rule,
+                             bool tile, uint8_t* rc, int64_t ld_rc, float* rs, int64_t ld_rs, uint8_t* cc, int64_t ld_cc,
+                             float* cs, int64_t ld_cs, const int* offsets, int experts, hipStream_t stream);
+
+// Y = act(alpha X W + bias).  mode: one matrix; the rows of each expert with its W; each expert's blocks of K.
+enum : int { kB128Plain = 0, kB128Rows = 1, kB128Blocks = 2 };
+struct GemmB128 {
+  int mode, M, N, nb;          // nb: blocks of K; kB128Blocks: those that a line has room for
+  int x_fmt, w_fmt, exact, w_line;
+  const uint8_t* x;
+  int64_t ld_x;
+  const float* xs;             // line m, block b: xs[b ld_xs + m]
+  int64_t ld_xs;
+  const uint8_t* w;
+  int64_t ld_w, st_w;          // st_: from one expert to the next
+  const float* ws;             // line (w_line) or tile n, block b: ws[n ws_n + b ws_k]
+  int64_t ws_n, ws_k, st_ws;
+  const int* offsets;
+  int experts, rows;           // rows: sorted lines (kB128Blocks; M where they are X's own)
+  float alpha;
+  const float* bias;
+  int act;
+  void* y;
+  int y_bf16, y_vec16;
+  int64_t ld_y, st_y;
+};
+// The most tiles of tm x tn outputs that the problem may have.
+int64_t gemm_b128_tiles(const GemmB128& a, int tm, int tn);
+// How it runs on `cus` CUs (host logic only): its tile, and the waves that share one along K (0: 256 x 256).
+struct GemmB128Plan {
+  int tile_m, tile_n, waves;
+};
+GemmB128Plan gemm_b128_plan(const GemmB128& a, int cus);
+hipError_t launch_gemm_b128(const GemmB128& a, hipStream_t stream);
+hipError_t launch_gemm_b128_tile(const GemmB128& a, hipStream_t stream);
+hipError_t launch_gemm_b128_rows(const GemmB128& a, const GemmB128Plan& p, hipStream_t stream);
+
+// ---- routing (moe_route.hip): experts and shares [T][k], counts [E], offsets [E + 1], order [T k], loss [1], slope [E]
+struct MoeRoute {
+  int64_t T, E, k;
+  int renorm, bf16;
+  const void* logits;
+  int64_t ld_logits;
+  const uint8_t* mask;
+  int* experts;
+  float* shares;
+  int* counts;
+  int* offsets;
+  int* order;
+  float* loss;
+  float* slope;
+  void* workspace;
+};
+int64_t moe_route_workspace_bytes(int64_t T, int64_t E, int64_t k);
+hipError_t launch_moe_route(const MoeRoute& p, hipStream_t stream);
+// Uses logits, mask, experts, shares and slope.
+hipError_t launch_moe_route_grad(const MoeRoute& p, const float* d_shares, int64_t ld_ds, const float* d_loss, void* d,
+                                 int64_t ld_d, hipStream_t stream);
+
 }  // namespace mxq

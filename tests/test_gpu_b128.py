@@ -1,0 +1,406 @@
+"""FP8 in blocks of 128 on the GPU against 64 bits (b128_reference.py): the quantizer bit for bit, the products
+within derived bounds."""
+import pytest
+import torch
+
+import b128_reference as ref
+import mxfp8_block_scaled_03_amd as mxq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def wide(rows, cols, dtype, seed, spikes=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((rows, cols), generator=g)
+    if spikes:
+        x = torch.where(torch.rand((rows, cols), generator=g) < 1e-2, x * 1000, x)
+        x = x * torch.exp2(torch.randint(-20, 20, (rows, 1), generator=g).float())
+    return x.to(dtype)
+
+
+def coded(lines, K, elem, seed, tile=False):
+    """Codes and scales as the reference quantizes them, on the CPU."""
+    return ref.quantize(wide(lines, K, F32, seed), elem, tile=tile)
+
+
+def by_block(scales):
+    """Scales of lines as the library takes them: stored block by block."""
+    return scales.float().to(DEV).t().contiguous().t()
+
+
+def same(codes, scales, want, what):
+    c, s = want
+    assert torch.equal(codes.cpu(), c), "%s: %d codes differ" % (what, int((codes.cpu() != c).sum()))
+    assert torch.equal(torch.nan_to_num(scales.cpu().double(), -1.0), torch.nan_to_num(s.double(), -1.0)), what
+
+
+# ---------------------------------------------------------------------------------- quantize
+
+SIZES = [(1, 1), (1, 128), (3, 129), (128, 128), (127, 255), (130, 300), (17, 1000), (300, 64), (257, 513), (512, 640)]
+
+
+@pytest.mark.parametrize("rule", ["amax", "ceil"])
+@pytest.mark.parametrize("elem", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,cols", SIZES)
+def test_quantize(rows, cols, dtype, elem, rule):
+    x = wide(rows, cols, dtype, rows * 1000 + cols)
+    d = x.to(DEV)
+    row, col = ref.quantize(x, elem, rule), ref.quantize(x.T, elem, rule)
+    same(*mxq.quantize_b128(d, elem, "row", rule), row, "row")
+    same(*mxq.quantize_b128(d, elem, "col", rule), col, "col")
+    rc, rs, cc, cs = mxq.quantize_b128_dual(d, elem, rule=rule)
+    same(rc, rs, row, "dual rows")
+    same(cc, cs, col, "dual columns")
+    tile = ref.quantize(x, elem, rule, tile=True)
+    same(*mxq.quantize_b128(d, elem, "tile", rule), tile, "tile")
+    tc, ts, ttc, tts = mxq.quantize_b128_dual(d, elem, tile=True, rule=rule)
+    same(tc, ts, tile, "tiles")
+    same(ttc, tts, ref.quantize(x.T, elem, rule, tile=True), "tiles transposed")
+
+
+def test_quantize_large_rows_take_the_wide_kernel():
+    x = wide(2048, 4200, BF16, 5)
+    same(*mxq.quantize_b128(x.to(DEV)), ref.quantize(x, "e4m3"), "row")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("elem", ["e4m3", "e5m2"])
+def test_quantize_special_values(dtype, elem):
+    """Zero blocks, signed zeros, subnormals, tiny and huge blocks, NaN and infinities (each in a block of its own)."""
+    x = wide(130, 400, F32, 9)
+    x[0] = 0.0
+    x[1] = -0.0
+    x[2] *= 2.0 ** -140
+    x[3] = 2.0 ** -101
+    x[4] = 3.0e38 * torch.sign(x[4])
+    x[5, 3] = float("nan")
+    x[6, 130] = float("inf")
+    x[7, 399] = float("-inf")
+    x[129, 0] = 1e-45
+    x = x.to(dtype)
+    d = x.to(DEV)
+    for rule in ("amax", "ceil"):
+        same(*mxq.quantize_b128(d, elem, "row", rule), ref.quantize(x, elem, rule), "row " + rule)
+        rc, rs, cc, cs = mxq.quantize_b128_dual(d, elem, rule=rule)
+        same(cc, cs, ref.quantize(x.T, elem, rule), "col " + rule)
+        tc, ts, ttc, tts = mxq.quantize_b128_dual(d, elem, tile=True, rule=rule)
+        same(tc, ts, ref.quantize(x, elem, rule, tile=True), "tile " + rule)
+        same(ttc, tts, ref.quantize(x.T, elem, rule, tile=True), "tile transposed " + rule)
+
+
+@pytest.mark.parametrize("elem", ["e4m3", "e5m2"])
+def test_quantize_every_bf16_value(elem):
+    """Every finite bf16 value beside a block maximum that it does not pass."""
+    v = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF16)
+    v = v[torch.isfinite(v)]
+    a = torch.where(v.float().abs() == 0, torch.ones(len(v)), v.float().abs() * 1.37).clamp(max=3.3e38)
+    x = torch.zeros((len(v), 2))
+    x[:, 0], x[:, 1] = v.float(), a
+    same(*mxq.quantize_b128(x.to(DEV), elem), ref.quantize(x, elem), "row")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quantize_strides_and_alignment(dtype):
+    """Row pitches and bases that no 16-byte load can take, and ones that it can."""
+    big = wide(140, 517, dtype, 3).to(DEV)
+    for x in (big[3:133, 1:300], big[:, 8:264], big[::2, :511], big[:1].expand(1, 517)):
+        want = ref.quantize(x.cpu(), "e4m3")
+        same(*mxq.quantize_b128(x), want, "row %s" % (x.stride(),))
+        same(*mxq.quantize_b128(x, axis="col"), ref.quantize(x.cpu().T, "e4m3"), "col")
+
+
+SPLITS = [[5], [128, 128], [0, 7, 0, 300, 128, 1], [0, 0, 0], [129, 0, 127, 1, 1, 255] + [0] * 60 + [3] * 10]
+
+
+@pytest.mark.parametrize("sizes", SPLITS)
+def test_quantize_by_expert(sizes):
+    """Blocks of columns begin anew with every expert; rows of no expert are skipped."""
+    E, used = len(sizes), sum(sizes)
+    x = wide(used + 9, 200, BF16, 11 + E)
+    offsets = torch.tensor([0] + sizes).cumsum(0).int().to(DEV)
+    rc, rs, cc, cs = mxq.quantize_b128_dual(x.to(DEV), offsets=offsets)
+    c1, s1 = mxq.quantize_b128(x.to(DEV), axis="col", offsets=offsets)
+    row = ref.quantize(x, "e4m3")
+    same(rc[:used], rs[:used], (row[0][:used], row[1][:used]), "rows")
+    first = block = 0
+    assert cc.shape[1] == (used + 9 + 127 * E) // 128 * 128
+    for n in sizes:
+        want = ref.quantize(x[first:first + n].T, "e4m3")
+        nb = ref.blocks(n)
+        for c, s in ((cc, cs), (c1, s1)):
+            same(c[:, 128 * block:128 * (block + nb)], s[:, block:block + nb], want, "expert of %d rows" % n)
+        first, block = first + n, block + nb
+
+
+def test_quantize_empty():
+    for shape in ((0, 5), (5, 0), (0, 0)):
+        x = torch.empty(shape, device=DEV)
+        c, s = mxq.quantize_b128(x)
+        assert c.shape == (shape[0], 128 * ref.blocks(shape[1])) and s.shape == (shape[0], ref.blocks(shape[1]))
+        mxq.quantize_b128_dual(x, tile=True)
+
+
+# ---------------------------------------------------------------------------------- products
+
+def run_product(M, N, K, fx="e4m3", fw="e4m3", lines=False, accum="fp32", out=F32, alpha=1.0, bias=False, act=None, seed=0):
+    xc, xs = coded(M, K, fx, seed + 1)
+    wc, ws = coded(N, K, fw, seed + 2, tile=not lines)
+    g = torch.Generator().manual_seed(seed)
+    b = torch.randn(N, generator=g) if bias else None
+    want, tol = ref.product(xc, xs.float(), fx, wc, ws.float(), fw, accum, alpha, b, act, out)
+    got = mxq.gemm_b128(xc.to(DEV), by_block(xs), wc.to(DEV), by_block(ws) if lines else ws.float().to(DEV), K, fx, fw,
+                        alpha=alpha, bias=None if b is None else b.to(DEV), out_dtype=out, accum=accum, act=act)
+    ref.check(got, want, tol, "%dx%dx%d %s %s %s" % (M, N, K, accum, out, "lines" if lines else "tiles"))
+
+
+# every kernel: rows of 16 to 64, 64 x 64 tiles and 256 x 256 ones, whole and ragged
+SHAPES = [(1, 1, 1), (1, 130, 128), (16, 64, 256), (15, 17, 1100), (20, 200, 300), (33, 95, 2100), (64, 256, 640),
+          (70, 130, 129), (200, 70, 1000), (257, 300, 400)]
+
+
+@pytest.mark.parametrize("lines", [False, True])
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product(M, N, K, out, accum, lines):
+    run_product(M, N, K, lines=lines, accum=accum, out=out, seed=M + N)
+
+
+@pytest.mark.parametrize("fx,fw", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("M,N,K", [(10, 40, 200), (130, 70, 300)])
+def test_product_formats(M, N, K, accum, fx, fw):
+    for lines in (False, True):
+        run_product(M, N, K, fx, fw, lines, accum, seed=7)
+
+
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("M,N,K", [(5, 37, 300), (100, 201, 300)])
+def test_product_epilogue(M, N, K, act):
+    for out in (F32, BF16):
+        run_product(M, N, K, accum="fp32", out=out, alpha=-0.375, bias=True, act=act, seed=3)
+
+
+def big_tiles(M, N, K, accum, lines, out, fx="e4m3", fw="e4m3", y=None):
+    """A problem that takes the 256 x 256 kernel: every 17th row against the reference."""
+    assert mxq.mxq_gemm_b128_plan(0, M, N, K, 1, 1 if lines else 128, 0 if accum == "fp8" else 1, 256)[2] == 0
+    x, w = wide(M, K, BF16, 21).to(DEV), wide(N, K, BF16, 22).to(DEV)
+    xc, xs = mxq.quantize_b128(x, fx)
+    wc, ws = mxq.quantize_b128(w, fw, "row" if lines else "tile")
+    got = mxq.gemm_b128(xc, xs, wc, ws, K, fx, fw, accum=accum, out_dtype=out, out=y)
+    rows = sorted(set(range(0, M, 17)) | {M - 1})
+    pick = torch.tensor(rows, device=DEV)
+    cols = torch.tensor(sorted(set(range(0, N, 13)) | set(range(max(0, N - 20), N))))
+    wcc = wc.cpu()
+    wsc = ws.cpu().repeat_interleave(128, 0)[:N] if not lines else ws.cpu()
+    want, tol = ref.product(xc[pick].cpu(), xs[pick].cpu(), fx, wcc[cols], wsc[cols], fw, accum, out=out)
+    ref.check(got[pick].cpu()[:, cols], want, tol, "%dx%dx%d %s" % (M, N, K, accum))
+    return got
+
+
+@pytest.mark.parametrize("lines", [False, True])
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("M,N,K", [(2560, 2816, 128), (2561, 2900, 900), (3000, 2603, 260), (2816, 2560, 1280)])
+def test_product_big_tiles(M, N, K, accum, lines):
+    big_tiles(M, N, K, accum, lines, F32)
+    big_tiles(M, N, K, accum, lines, BF16)
+
+
+def test_product_big_tiles_formats():
+    for fx, fw in (("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")):
+        for accum in ("fp32", "fp8"):
+            big_tiles(2600, 2700, 200, accum, True, F32, fx, fw)
+
+
+def test_product_into_strided_output_leaves_the_rest():
+    for M, N, K in ((5, 33, 256), (100, 100, 256), (2570, 2600, 256)):
+        for dtype in (F32, BF16):
+            for pad in (3, 8):
+                whole = torch.full((M + 2, N + pad), 7.0, dtype=dtype, device=DEV)
+                xc, xs = mxq.quantize_b128(wide(M, K, BF16, 1).to(DEV))
+                wc, ws = mxq.quantize_b128(wide(N, K, BF16, 2).to(DEV), axis="tile")
+                want = mxq.gemm_b128(xc, xs, wc, ws, K, out_dtype=dtype)
+                mxq.gemm_b128(xc, xs, wc, ws, K, out=whole[1:1 + M, :N])
+                assert torch.equal(whole[1:1 + M, :N], want)
+                rest = whole.clone()
+                rest[1:1 + M, :N] = 7.0
+                assert bool((rest == 7.0).all())
+
+
+def test_product_no_blocks():
+    b = torch.randn(40, device=DEV)
+    z = torch.empty((3, 0), dtype=torch.uint8, device=DEV)
+    w = torch.empty((40, 0), dtype=torch.uint8, device=DEV)
+    xs, ws = torch.empty((3, 0), device=DEV), torch.empty((1, 0), device=DEV)
+    assert torch.equal(mxq.gemm_b128(z, xs, w, ws, 0, bias=b, out_dtype=F32), b.expand(3, 40))
+    assert bool((mxq.gemm_b128(z, xs, w, ws, 0, out_dtype=F32) == 0).all())
+
+
+def test_product_nan_scale():
+    """A block whose scale is NaN makes its row (of X) or its columns (of W) NaN and nothing else."""
+    for M, N in ((4, 300), (300, 300)):
+        x, w = wide(M, 300, F32, 1, False), wide(N, 300, F32, 2, False)
+        x[2, 150] = float("nan")
+        w[5, 0] = float("inf")
+        for lines in (True, False):
+            for accum in ("fp32", "fp8"):
+                xc, xs = mxq.quantize_b128(x.to(DEV))
+                wc, ws = mxq.quantize_b128(w.to(DEV), axis="row" if lines else "tile")
+                y = mxq.gemm_b128(xc, xs, wc, ws, 300, accum=accum, out_dtype=F32).cpu()
+                nan = torch.zeros((M, N), dtype=torch.bool)
+                nan[2] = True
+                nan[:, 5:6] = True
+                if not lines:
+                    nan[:, :128] = True
+                assert torch.equal(torch.isnan(y), nan)
+
+
+def test_transposed_tiles_are_the_weights_transposed():
+    """dX = dY W from the transposed codes of the same tiles."""
+    N, K, M = 300, 200, 50
+    w = wide(N, K, BF16, 4).to(DEV)
+    wc, ws, wt, wts = mxq.quantize_b128_dual(w, tile=True)
+    dc, ds = mxq.quantize_b128(wide(M, N, BF16, 5).to(DEV), "e5m2")
+    got = mxq.gemm_b128(dc, ds, wt, wts, N, "e5m2", out_dtype=F32)
+    wv = ref.values(wc.cpu(), ws.cpu(), "e4m3")[:, :K]
+    dv = ref.values(dc.cpu(), ds.cpu(), "e5m2")[:, :N]
+    tol = (ref.blocks(N) + 50) * ref.U * (dv.abs() @ wv.abs())
+    ref.check(got, dv @ wv, tol, "dx")
+
+
+# ---------------------------------------------------------------------------------- experts
+
+def experts_case(sizes, N, K, extra, accum, out, lines, seed=0):
+    E, used = len(sizes), sum(sizes)
+    R = used + extra
+    xc, xs = coded(R, K, "e4m3", seed + 1)
+    w = [coded(N, K, "e4m3", seed + 10 + e, tile=not lines) for e in range(E)]
+    wc, ws = torch.stack([c for c, _ in w]), torch.stack([s for _, s in w]).float()
+    offsets = torch.tensor([0] + sizes).cumsum(0).int().to(DEV)
+    y = torch.full((R, N), 5.0, dtype=out, device=DEV)
+    wsd = ws.to(DEV)
+    if lines:
+        wsd = wsd.transpose(1, 2).contiguous().transpose(1, 2)
+    mxq.moe_gemm_b128(xc.to(DEV), by_block(xs), wc.to(DEV), wsd, offsets, K, out=y, accum=accum)
+    first = 0
+    for e, n in enumerate(sizes):
+        if n:
+            want, tol = ref.product(xc[first:first + n], xs[first:first + n].float(), "e4m3", wc[e], ws[e], "e4m3", accum, out=out)
+            ref.check(y[first:first + n], want, tol, "expert %d of %d rows" % (e, n))
+        first += n
+    assert bool((y[used:] == 5.0).all()), "rows of no expert were written"
+
+
+@pytest.mark.parametrize("lines", [False, True])
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("sizes", [[1], [0, 3, 0, 17, 1], [40, 0, 33, 70], [100, 200, 0, 90], [0, 0], [1] * 70])
+def test_experts(sizes, accum, lines):
+    for out in (F32, BF16):
+        experts_case(sizes, 100, 300, 3, accum, out, lines)
+
+
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+def test_experts_big_tiles(accum):
+    sizes = [300, 0, 1, 700, 256, 513]
+    E, N, K, R = len(sizes), 5000, 384, sum(sizes) + 11
+    assert mxq.mxq_gemm_b128_plan(1, R, N, K, E, 128, 1 if accum == "fp32" else 0, 256)[2] == 0
+    xc, xs = mxq.quantize_b128(wide(R, K, BF16, 3).to(DEV))
+    wc, ws = mxq.quantize_b128(wide(E * N, K, BF16, 4).to(DEV), axis="row")
+    wc, ws = wc.view(E, N, -1), ws.t().contiguous().view(-1, E, N).permute(1, 2, 0)
+    offsets = torch.tensor([0] + sizes).cumsum(0).int().to(DEV)
+    y = torch.full((R, N), 5.0, device=DEV)
+    mxq.moe_gemm_b128(xc, xs, wc, ws, offsets, K, out=y, accum=accum)
+    first = 0
+    for e, n in enumerate(sizes):
+        rows = torch.arange(first, first + n, 7, device=DEV)
+        cols = torch.arange(e, N, 23, device=DEV)
+        if n:
+            want, tol = ref.product(xc[rows].cpu(), xs[rows].cpu(), "e4m3", wc[e][cols].cpu(), ws[e][cols].cpu(), "e4m3", accum)
+            ref.check(y[rows][:, cols], want, tol, "expert %d" % e)
+        first += n
+    assert bool((y[first:] == 5.0).all())
+
+
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("N,K", [(20, 30), (300, 70), (2600, 2500)])
+@pytest.mark.parametrize("sizes", [[40], [0, 130, 1, 0, 257], [128, 0, 128]])
+def test_expert_weight_gradients(sizes, N, K, accum):
+    E, R = len(sizes), sum(sizes) + 5
+    dy, x = wide(R, N, BF16, 6, False), wide(R, K, BF16, 7, False)
+    offsets = torch.tensor([0] + sizes).cumsum(0).int().to(DEV)
+    dc, ds = mxq.quantize_b128(dy.to(DEV), "e5m2", "col", offsets=offsets)
+    xc, xs = mxq.quantize_b128(x.to(DEV), "e4m3", "col", offsets=offsets)
+    for out in (F32, BF16):
+        got = mxq.moe_wgrad_b128(dc, ds, xc, xs, offsets, out_dtype=out, accum=accum)
+        block = 0
+        pick_n, pick_k = torch.arange(0, N, 1 + N // 150), torch.arange(0, K, 1 + K // 150)
+        for e, n in enumerate(sizes):
+            nb = ref.blocks(n)
+            part = [t.cpu() for t in (dc[:, 128 * block:128 * (block + nb)], ds[:, block:block + nb],
+                                      xc[:, 128 * block:128 * (block + nb)], xs[:, block:block + nb])]
+            want, tol = ref.product(part[0][pick_n], part[1][pick_n], "e5m2", part[2][pick_k], part[3][pick_k], "e4m3", accum,
+                                    out=out)
+            ref.check(got[e].cpu()[pick_n][:, pick_k], want, tol, "expert %d of %d rows" % (e, n))
+            block += nb
+
+
+def test_wrong_offsets_stay_inside():
+    """Offsets out of order or past the rows: unspecified results, but none outside the arrays."""
+    R, N, K, E = 70, 40, 130, 4
+    xc, xs = mxq.quantize_b128(wide(R, K, BF16, 1).to(DEV))
+    wc, ws = mxq.quantize_b128(wide(E * N, K, BF16, 2).to(DEV))
+    wc, ws = wc.view(E, N, -1), ws.t().contiguous().view(-1, E, N).permute(1, 2, 0)
+    for o in ([0, 900, -5, 60, 70], [50, 10, 70, 0, 80], [-3, -2, -1, 0, 1]):
+        off = torch.tensor(o, dtype=torch.int32, device=DEV)
+        whole = torch.full((R + 64, N), 5.0, device=DEV)
+        mxq.moe_gemm_b128(xc, xs, wc, ws, off, K, out=whole[:R])
+        assert bool((whole[R:] == 5.0).all())
+        rc, rs, cc, cs = mxq.quantize_b128_dual(wide(R, K, BF16, 3).to(DEV), offsets=off)
+        mxq.moe_wgrad_b128(cc, cs, cc, cs, off, x_elem="e4m3")
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------------- streams, graphs
+
+def test_side_stream_and_graph():
+    """On a stream of its own, and captured: every replay on new inputs equals the eager result."""
+    M, N, K, E = 300, 260, 400, 5
+    x = wide(M, K, BF16, 1).to(DEV)
+    w = wide(E * N, K, BF16, 2).to(DEV)
+    wc, ws = mxq.quantize_b128(w)
+    wc, ws = wc.view(E, N, -1), ws.t().contiguous().view(-1, E, N).permute(1, 2, 0)
+    offsets = torch.tensor([0, 20, 20, 150, 290, 300], dtype=torch.int32, device=DEV)
+
+    def step():
+        rc, rs, cc, cs = mxq.quantize_b128_dual(x, offsets=offsets)
+        y = mxq.moe_gemm_b128(rc, rs, wc, ws, offsets, K)
+        dw = mxq.moe_wgrad_b128(cc, cs, cc, cs, offsets, x_elem="e4m3", accum="fp8")
+        return y, dw, mxq.gemm_b128(rc, rs, wc[0], ws[0], K, accum="fp8")
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for seed in (3, 4, 5):
+        x.copy_(wide(M, K, BF16, seed).to(DEV))
+        offsets.copy_(torch.tensor([0, 20 * seed, 20 * seed, 150, 290, 300], dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, step()):
+            assert torch.equal(a, b)
+
+
+def test_results_do_not_change_from_run_to_run():
+    M, N, K = 900, 1000, 2000
+    xc, xs = mxq.quantize_b128(wide(M, K, BF16, 1).to(DEV))
+    wc, ws = mxq.quantize_b128(wide(N, K, BF16, 2).to(DEV), axis="tile")
+    y = mxq.gemm_b128(xc, xs, wc, ws, K, out_dtype=F32)
+    for _ in range(5):
+        assert torch.equal(mxq.gemm_b128(xc, xs, wc, ws, K, out_dtype=F32), y)
