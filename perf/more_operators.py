@@ -210,8 +210,9 @@ def prepare(case, seed):
         M, N, K = c["M"], c["N"], c["K"]
         s["dy"] = _gradients(g, (M, N))
         wt, ws = _tiles(_normal(g, (N, K), 0.02, torch.bfloat16).T, "e4m3")
-        s["wt"], s["wts"] = wt, ws                                  # [K][N], tiles
-        s["xt"], s["xts"] = _lines(_activations(g, (M, K)).T, "e4m3")   # [K][M]
+        xt, s["xts"] = _lines(_activations(g, (M, K)).T, "e4m3")
+        s["wt"], s["wts"] = wt.contiguous(), ws                     # [K][N], tiles; rows of codes, as the calls take them
+        s["xt"] = xt.contiguous()                                   # [K][M]
     elif c["op"] == "route":
         T, E = c["T"], c["E"]
         s["logits"] = (_normal(g, (T, E)) + _normal(g, (E,), 0.5)).to(WIDE[c["type"]])
