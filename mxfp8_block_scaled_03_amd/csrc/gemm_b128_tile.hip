@@ -40,6 +40,9 @@ __device__ __forceinline__ void dma4(uint32_t lds, uint32_t voff, v4i rsrc) {
 }
 #pragma clang diagnostic pop
 
+// Results of vector instructions (never of matrix instructions) that have to be there at this point.
+__device__ __forceinline__ void pin(v4f a[4]) { asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3])); }
+
 template <int FX, int FW, bool EXACT, bool WLINE>
 __global__ __launch_bounds__(kThreads, 2) void k_gemm_b128(const GemmB128 a) {
   const B128Tile t = b128_tile<kTile, kTile, WLINE>(a, workgroup_at(blockIdx.x, blockIdx.y));
@@ -128,12 +131,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_b128(const GemmB128 a) {
   issue_x(0, 1);
   issue_middle(1);
   issue_x(1, 1);
+  wait_vm<11>();
+  lds_barrier();
   for (int s = 0; s < nb; ++s) {
     const uint32_t so = (uint32_t)(s & 1) * kStage, ss = (uint32_t)(s & 3) * kScaleSlot;
     // W, the first half of X and the scales of step s: all but the second half of X of this step, and the
     // next step's nine
-    wait_vm<11>();
-    lds_barrier();
     v8i w[4];
     Wide ww[4];
 #pragma unroll
@@ -141,32 +144,44 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_b128(const GemmB128 a) {
       w[j] = fragment(rw + so, j);
       if (EXACT) ww[j] = widen<FW>(w[j]);
     }
-    v4f sw[4];
     float sw1 = 0.0f;
-    if (WLINE) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sw[j] = *reinterpret_cast<const v4f*>(smem + rsw + ss + 64 * j);
-    } else {
-      sw1 = *reinterpret_cast<const float*>(smem + rsw + ss);
-    }
+    if (!WLINE) sw1 = *reinterpret_cast<const float*>(smem + rsw + ss);
     auto half_step = [&](int h) {
 #pragma unroll
       for (int f = 4 * h; f < 4 * h + 4; ++f) {
         const v8i x = fragment(rx + so, f);
         const float sx = *reinterpret_cast<const float*>(smem + rsx + ss + 64 * f);
-        Wide xw;
-        if (EXACT) xw = widen<FX>(x);
+        v4f d[4];
+        if (EXACT) {
+          // the four chains of four in turn: an instruction never waits for the one before it
+          const Wide xw = widen<FX>(x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[j].p[q], xw.p[q], d[j], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j] = block_fp8<FX, FW>(w[j], x);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const v4f d = EXACT ? block_exact(ww[j], xw) : block_fp8<FX, FW>(w[j], x);
           if (WLINE) {
+            const v4f sw = *reinterpret_cast<const v4f*>(smem + rsw + ss + 64 * j);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[f][j][r] = __builtin_fmaf(d[r], sx * sw[j][r], acc[f][j][r]);
+            for (int r = 0; r < 4; ++r) acc[f][j][r] = __builtin_fmaf(d[j][r], sx * sw[r], acc[f][j][r]);
           } else {
             const float sc = sx * sw1;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[f][j][r] = __builtin_fmaf(d[r], sc, acc[f][j][r]);
+            for (int r = 0; r < 4; ++r) acc[f][j][r] = __builtin_fmaf(d[j][r], sc, acc[f][j][r]);
           }
+        }
+        // the sums of this X fragment are added here and now: the compiler would keep them, in registers that
+        // there are not, past the middle of the step
+        if (EXACT) {
+          pin(acc[f]);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     };
@@ -176,6 +191,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_b128(const GemmB128 a) {
     lds_barrier();
     issue_middle(s + 2);
     half_step(1);
+    wait_vm<9>();
     lds_barrier();
     issue_x(s + 2, 1);
   }
