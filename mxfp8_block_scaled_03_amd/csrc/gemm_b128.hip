@@ -17,6 +17,7 @@ int64_t gemm_b128_tiles(const GemmB128& a, int tm, int tn) {
 
 GemmB128Plan gemm_b128_plan(const GemmB128& a, int cus) {
   const int64_t rows = a.mode == kB128Rows ? cover(a.M, a.experts) : a.M;
+  if (a.mode == kB128Rows && rows <= 64) return rows <= 12 ? GemmB128Plan{16, 64, 1} : rows <= 24 ? GemmB128Plan{32, 64, 1} : GemmB128Plan{64, 64, 1};
   if (rows <= 16) return {16, 16, 8};
   if (rows <= 32) return {32, 16, 8};
   const int64_t tiles = gemm_b128_tiles(a, 256, 256);

@@ -32,7 +32,7 @@ struct B128Tile {
 // Tile `wg` of TM x TN outputs.  Plain: tiles of one matrix in XCD order.  Rows of experts: each expert's
 // tiles in turn, W and its scales the expert's.  Blocks of experts (the weight gradient): every expert has
 // the whole matrix of tiles, its blocks of K only.
-template <int TM, int TN, bool WLINE>
+template <int TM, int TN, bool WLINE, bool XCD = true>
 __device__ __forceinline__ B128Tile b128_tile(const GemmB128& a, int wg) {
   B128Tile t{};
   int tm, tn;
@@ -50,10 +50,10 @@ __device__ __forceinline__ B128Tile b128_tile(const GemmB128& a, int wg) {
     t.ws = a.ws;
     t.y = (int64_t)tm * TM * a.ld_y;
   } else if (a.mode == kB128Rows) {
-    // the grid is an upper bound: the tiles that there are come first in XCD order
-    Group g = find_group(a.offsets, a.experts, a.M, TM, tiles_n, 0x7FFFFFFF);
+    // the grid is an upper bound: the tiles that there are come first, in XCD order where tiles share operands
+    Group g = find_group(a.offsets, a.experts, a.M, TM, tiles_n, XCD ? 0x7FFFFFFF : wg);
     if (wg >= g.total) return t;
-    g = find_group(a.offsets, a.experts, a.M, TM, tiles_n, xcd_order(wg, g.total));
+    if (XCD) g = find_group(a.offsets, a.experts, a.M, TM, tiles_n, xcd_order(wg, g.total));
     tile_at(g.tile, g.tiles / tiles_n, tiles_n, tm, tn);
     const int64_t row = g.row0 + (int64_t)tm * TM;
     t.m = g.rows - tm * TM;

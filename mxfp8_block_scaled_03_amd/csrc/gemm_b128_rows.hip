@@ -1,97 +1,158 @@
-// gemm_b128_rows.hip -- the product in blocks of 128 by small tiles whose eight waves split K: few rows (a
-// decoding step, a few tokens an expert), and outputs too small to fill the card with 256 x 256 tiles.
+// gemm_b128_rows.hip -- the product in blocks of 128 by small tiles: few rows (a decoding step, a few tokens an
+// expert), and outputs too small to fill the card with 256 x 256 tiles.
 //
-// Bound by the weights' bytes and by latency.  A workgroup owns 16 MT x 16 NT outputs; wave v takes blocks v,
-// v + 8, ..., so that the eight together read 1 KiB runs of each line.  Codes come straight from memory into
-// the fragments' registers, U blocks at a time and the next U on their way while these are multiplied; the
-// eight waves' sums meet in LDS, are added in the waves' order, and finished by all threads.
+// Bound by the weights' bytes and by latency.  A wave owns 16 MT x 16 NT outputs.  Where there are few tiles
+// (WK = 8) eight waves share them along K: wave v takes blocks v, v + 8, ..., so that the eight together read
+// 1 KiB runs of each line; their sums meet in LDS, are added in the waves' order, and finished by all
+// threads.  Where there are many (WK = 1: experts) each of four waves has a tile of its own, side by side along N,
+// and all of K.  Codes come straight from memory into the fragments' registers, U blocks ahead: a block's
+// registers are refilled as soon as they have been read.
 #include "gemm_b128.hpp"
 
 namespace mxq {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = 8;
-
-template <int FX, int FW, bool EXACT, bool WLINE, int MT, int NT, int U>
+template <int FX, int FW, bool EXACT, bool WLINE, int MT, int NT, int U, int WK>
 struct RowsWave {
-  struct Batch {
-    v4i x[U][MT][2], w[U][NT][2];
-    float sx[U][MT];
-    v4f sw[U][WLINE ? NT : 1];
-  };
   __amdgpu_buffer_rsrc_t rx, rw, rsx, rsw;
   uint32_t vx, vw;
   int64_t ld_xs, ws_k;
   uint32_t x16, w16;
   int nb, i, g;
+  // U blocks' codes and scales, each refilled with the block U further on as soon as it has been read
+  v4i x[U][MT][2], w[U][NT][2];
+  float sx[U][MT];
+  v4f sw[U][WLINE ? NT : 1];
 
-  __device__ __forceinline__ void load(Batch& q, int b0) const {
+  // past the last block: an offset past every range (each below 2^31), for which loads give zeros
+  __device__ __forceinline__ uint32_t dead(int b) const { return b < nb ? 0u : 0x80000000u; }
+  __device__ __forceinline__ void load_w(int u, int b) {
+    const uint32_t at = (uint32_t)b * kB, d = dead(b);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int b = b0 + kWaves * u;
-      const uint32_t dead = b < nb ? 0u : 0x80000000u;     // past every range (each below 2^31): loads give zeros
-      const uint32_t at = (uint32_t)b * kB;
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        w[u][j][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)((vw + j * w16 + 64 * h + at) | d), 0, 0));
+    const uint32_t wa = (uint32_t)(4 * (b * ws_k + (WLINE ? 4 * g : 0)));
+    if (WLINE) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          q.w[u][j][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rw, (int)((vw + j * w16 + 64 * h + at) | dead), 0, 0));
-#pragma unroll
-      for (int f = 0; f < MT; ++f)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          q.x[u][f][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)((vx + f * x16 + 64 * h + at) | dead), 0, 0));
-      const uint32_t sa = (uint32_t)(4 * (b * ld_xs + i));
-#pragma unroll
-      for (int f = 0; f < MT; ++f)
-        q.sx[u][f] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsx, (int)((sa + 64 * f) | dead), 0, 0));
-      const uint32_t wa = (uint32_t)(4 * (b * ws_k + (WLINE ? 4 * g : 0)));
-      if (WLINE) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          q.sw[u][j] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsw, (int)((wa + 64 * j) | dead), 0, 0));
-      } else {
-        q.sw[u][0][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsw, (int)(wa | dead), 0, 0));
-      }
+        sw[u][j] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsw, (int)((wa + 64 * j) | d), 0, 0));
+    } else {
+      sw[u][0][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsw, (int)(wa | d), 0, 0));
     }
   }
-  __device__ __forceinline__ void multiply(const Batch& q, v4f acc[MT][NT]) const {
+  __device__ __forceinline__ void load_x(int u, int f, int b) {
+    const uint32_t at = (uint32_t)b * kB, d = dead(b);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      x[u][f][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)((vx + f * x16 + 64 * h + at) | d), 0, 0));
+    sx[u][f] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsx, (int)((uint32_t)(4 * (b * ld_xs + i) + 64 * f) | d), 0, 0));
+  }
+  __device__ __forceinline__ void fill(int b0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      v8i w[NT];
+      load_w(u, b0 + WK * u);
+#pragma unroll
+      for (int f = 0; f < MT; ++f) load_x(u, f, b0 + WK * u);
+    }
+  }
+  // U blocks from b0 on; MORE: there are blocks behind them, which take their places
+  template <bool MORE>
+  __device__ __forceinline__ void multiply(int b0, v4f acc[MT][NT]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int next = b0 + WK * (U + u);
+      v8i wu[NT];
       Wide ww[NT];
+      v4f su[WLINE ? NT : 1];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        w[j] = __builtin_shufflevector(q.w[u][j][0], q.w[u][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-        if (EXACT) ww[j] = widen<FW>(w[j]);
+        wu[j] = __builtin_shufflevector(w[u][j][0], w[u][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+        if (EXACT) ww[j] = widen<FW>(wu[j]);
+        if (WLINE || j == 0) su[j] = sw[u][j];
       }
+      if (MORE && EXACT) load_w(u, next);
 #pragma unroll
       for (int f = 0; f < MT; ++f) {
-        const v8i x = __builtin_shufflevector(q.x[u][f][0], q.x[u][f][1], 0, 1, 2, 3, 4, 5, 6, 7);
-        Wide xw;
-        if (EXACT) xw = widen<FX>(x);
+        const v8i xu = __builtin_shufflevector(x[u][f][0], x[u][f][1], 0, 1, 2, 3, 4, 5, 6, 7);
+        const float sxu = sx[u][f];
+        v4f d[NT];
+        if (EXACT) {
+          const Wide xw = widen<FX>(xu);
+          if (MORE) load_x(u, f, next);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const v4f d = EXACT ? block_exact(ww[j], xw) : block_fp8<FX, FW>(w[j], x);
+          for (int j = 0; j < NT; ++j) d[j] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) d[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[j].p[q], xw.p[q], d[j], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) d[j] = block_fp8<FX, FW>(wu[j], xu);
+          if (MORE) load_x(u, f, next);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[f][j][r] = __builtin_fmaf(d[r], q.sx[u][f] * (WLINE ? q.sw[u][j][r] : q.sw[u][0][0]), acc[f][j][r]);
-        }
+            acc[f][j][r] = __builtin_fmaf(d[j][r], sxu * (WLINE ? su[j][r] : su[0][0]), acc[f][j][r]);
       }
+      if (MORE && !EXACT) load_w(u, next);
     }
   }
 };
 
-template <int FX, int FW, bool EXACT, bool WLINE, int MT, int NT>
-__global__ __launch_bounds__(kThreads, 2) void k_gemm_b128_rows(const GemmB128 a) {
+// Four outputs of row m from column n on (both of the tile), `left` of them inside.
+__device__ __forceinline__ void store4(const GemmB128& a, const B128Tile& t, v4f s, int m, int n, int left) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) s[r] = finish(s[r], a.alpha, a.bias && r < left ? a.bias[t.n0 + n + r] : -0.0f, a.act);
+  const int64_t at = t.y + (int64_t)m * a.ld_y + n;
+  if (a.y_bf16) {
+    uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + at;
+    const v2u d = {pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
+    if (a.y_vec16 && left >= 4) {
+      *reinterpret_cast<v2u*>(y) = d;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < left) y[r] = (uint16_t)(d[r >> 1] >> (16 * (r & 1)));
+    }
+  } else {
+    float* y = reinterpret_cast<float*>(a.y) + at;
+    if (a.y_vec16 && left >= 4) {
+      *reinterpret_cast<v4f*>(y) = s;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < left) y[r] = s[r];
+    }
+  }
+}
+
+constexpr int waves_of(int wk) { return wk == 1 ? 4 : wk; }
+
+template <int FX, int FW, bool EXACT, bool WLINE, int MT, int NT, int WK>
+__global__ __launch_bounds__(64 * waves_of(WK), 2) void k_gemm_b128_rows(const GemmB128 a) {
+  constexpr int kThreads = 64 * waves_of(WK), WN = waves_of(WK) / WK;
   constexpr int U = MT + NT <= 2 ? 4 : MT + NT <= 4 ? 2 : 1;
-  const B128Tile t = b128_tile<16 * MT, 16 * NT, WLINE>(a, workgroup_at(blockIdx.x, blockIdx.y));
+  B128Tile t = b128_tile<16 * MT, 16 * NT * WN, WLINE, WK != 1>(a, workgroup_at(blockIdx.x, blockIdx.y));
   if (!t.any) return;
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wk = wid % WK;
+  if (WN > 1) {
+    // this wave's columns (a tile of W's scales may end between two waves)
+    const int n = 16 * NT * (wid / WK);
+    if (n >= t.n) return;
+    t.w += n * a.ld_w;
+    t.ws += WLINE ? n : ((t.n0 + n) / kB - t.n0 / kB) * a.ws_n;
+    t.y += n;
+    t.n -= n;
+    t.n0 += n;
+  }
   const int rows_x = min(16 * MT, t.m), rows_w = min(16 * NT, t.n);
-  using Wave = RowsWave<FX, FW, EXACT, WLINE, MT, NT, U>;
+  using Wave = RowsWave<FX, FW, EXACT, WLINE, MT, NT, U, WK>;
   Wave v;
   v.i = lane & 15;
   v.g = lane >> 4;
@@ -113,14 +174,20 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_b128_rows(const GemmB128 a
   for (int f = 0; f < MT; ++f)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[f][j] = {0.0f, 0.0f, 0.0f, 0.0f};
-  typename Wave::Batch p, q;
-  constexpr int step = kWaves * U;
-  v.load(p, wid);
-  for (int b = wid; b < t.nb; b += 2 * step) {
-    v.load(q, b + step);
-    v.multiply(p, acc);
-    v.load(p, b + 2 * step);
-    v.multiply(q, acc);
+  constexpr int step = WK * U;
+  int b = wk;
+  v.fill(b);
+  for (; b + step < t.nb; b += step) v.template multiply<true>(b, acc);
+  v.template multiply<false>(b, acc);
+  if (WK == 1) {
+#pragma unroll
+    for (int f = 0; f < MT; ++f)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int m = 16 * f + v.i, n = 16 * j + 4 * v.g;
+        if (m < rows_x && n < rows_w) store4(a, t, acc[f][j], m, n, rows_w - n);
+      }
+    return;
   }
   v4f* part = reinterpret_cast<v4f*>(smem);
 #pragma unroll
@@ -131,46 +198,21 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_b128_rows(const GemmB128 a
   for (int o = threadIdx.x; o < MT * NT * 64; o += kThreads) {
     v4f s = part[o];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
+    for (int w = 1; w < WK; ++w) {
       const v4f e = part[w * MT * NT * 64 + o];
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[r] += e[r];
     }
     const int l = o & 63, f = (o >> 6) / NT, j = (o >> 6) % NT;
     const int m = 16 * f + (l & 15), n = 16 * j + 4 * (l >> 4);
-    if (m >= rows_x || n >= rows_w) continue;
-    const int left = rows_w - n;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      s[r] = finish(s[r], a.alpha, a.bias && r < left ? a.bias[t.n0 + n + r] : -0.0f, a.act);
-    const int64_t at = t.y + (int64_t)m * a.ld_y + n;
-    if (a.y_bf16) {
-      uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + at;
-      const v2u d = {pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
-      if (a.y_vec16 && left >= 4) {
-        *reinterpret_cast<v2u*>(y) = d;
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (r < left) y[r] = (uint16_t)(d[r >> 1] >> (16 * (r & 1)));
-      }
-    } else {
-      float* y = reinterpret_cast<float*>(a.y) + at;
-      if (a.y_vec16 && left >= 4) {
-        *reinterpret_cast<v4f*>(y) = s;
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (r < left) y[r] = s[r];
-      }
-    }
+    if (m < rows_x && n < rows_w) store4(a, t, s, m, n, rows_w - n);
   }
 }
 
-template <int FX, int FW, bool EXACT, bool WLINE, int MT, int NT>
+template <int FX, int FW, bool EXACT, bool WLINE, int MT, int NT, int WK>
 hipError_t launch_t(const GemmB128& a, hipStream_t stream) {
-  constexpr int lds = kWaves * MT * NT * 1024;
-  auto kern = k_gemm_b128_rows<FX, FW, EXACT, WLINE, MT, NT>;
+  constexpr int waves = waves_of(WK), lds = WK == 1 ? 0 : WK * MT * NT * 1024;
+  auto kern = k_gemm_b128_rows<FX, FW, EXACT, WLINE, MT, NT, WK>;
   if (lds > 65536) {
     static bool set[64] = {false};
     int dev = 0;
@@ -181,16 +223,22 @@ hipError_t launch_t(const GemmB128& a, hipStream_t stream) {
       set[dev] = true;
     }
   }
-  const Grid grid = grid_of(gemm_b128_tiles(a, 16 * MT, 16 * NT));
-  hipLaunchKernelGGL(kern, dim3(grid.x, grid.y), dim3(kThreads), lds, stream, a);
+  const Grid grid = grid_of(gemm_b128_tiles(a, 16 * MT, 16 * NT * (waves / WK)));
+  hipLaunchKernelGGL(kern, dim3(grid.x, grid.y), dim3(64 * waves), lds, stream, a);
   return hipGetLastError();
 }
 
 template <int FX, int FW, bool EXACT, bool WLINE>
 hipError_t launch_p(const GemmB128& a, const GemmB128Plan& p, hipStream_t s) {
-  if (p.tile_m == 16) return p.tile_n == 16 ? launch_t<FX, FW, EXACT, WLINE, 1, 1>(a, s) : launch_t<FX, FW, EXACT, WLINE, 1, 2>(a, s);
-  if (p.tile_m == 32) return p.tile_n == 16 ? launch_t<FX, FW, EXACT, WLINE, 2, 1>(a, s) : launch_t<FX, FW, EXACT, WLINE, 2, 2>(a, s);
-  return p.tile_n == 32 ? launch_t<FX, FW, EXACT, WLINE, 4, 2>(a, s) : launch_t<FX, FW, EXACT, WLINE, 4, 4>(a, s);
+  // the plans of gemm_b128_plan, and no others
+  if (p.waves == 1) {
+    if (p.tile_m == 16) return launch_t<FX, FW, EXACT, WLINE, 1, 1, 1>(a, s);
+    if (p.tile_m == 32) return launch_t<FX, FW, EXACT, WLINE, 2, 1, 1>(a, s);
+    return launch_t<FX, FW, EXACT, WLINE, 4, 1, 1>(a, s);
+  }
+  if (p.tile_m == 16) return launch_t<FX, FW, EXACT, WLINE, 1, 1, 8>(a, s);
+  if (p.tile_m == 32) return launch_t<FX, FW, EXACT, WLINE, 2, 1, 8>(a, s);
+  return p.tile_n == 32 ? launch_t<FX, FW, EXACT, WLINE, 4, 2, 8>(a, s) : launch_t<FX, FW, EXACT, WLINE, 4, 4, 8>(a, s);
 }
 
 template <int FX, int FW>
