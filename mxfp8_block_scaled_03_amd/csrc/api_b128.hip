@@ -97,8 +97,6 @@ void fill(mxq::GemmB128& a, int64_t M, int64_t N, int64_t nb, int x_elem, int w_
   a.w_line = w_block == 1;
   a.act = act == MXQ_ACT_SILU ? 1 : 0;
   a.y_bf16 = y_type == MXQ_BF16;
-  const int64_t ey = a.y_bf16 ? 2 : 4;
-  a.y_vec16 = aligned(a.y, 16) && (a.ld_y * ey) % 16 == 0 && (a.st_y * ey) % 16 == 0;
 }
 
 }  // namespace

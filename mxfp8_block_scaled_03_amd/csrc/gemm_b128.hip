@@ -1,4 +1,6 @@
 // gemm_b128.hip -- the product in blocks of 128: how a problem runs.
+#include <math.h>
+
 #include "b128.hpp"
 #include "internal.hpp"
 
@@ -15,19 +17,53 @@ int64_t gemm_b128_tiles(const GemmB128& a, int tm, int tn) {
   return n * cover(a.M, tm) * (a.mode == kB128Blocks ? a.experts : 1);
 }
 
+// The plan is the cheapest of the kernels' estimates, in us, from timing all of them on 30 shapes (256 CUs, graphs of 20
+// calls, other weights each; the estimates are within some 10 % of what they were fitted to):
+//   small tiles  1.8 and, in rounds of a tile for each CU, 1.1 and 33 KB of both sides' lines a us (16 x 4096 x 4096
+//                7.0 us by 16 x 16 and 11.0 by 64 x 32; 128 rows 31.9 and 15.3)
+//   64 x 64      4 and 0.34 a block (exact 0.47) for one tile a CU, 0.55 (0.83) for two
+//                (512 x 4096 x 4096 22.8 fp8, 128 x 128 25.1; exact 28.7 and 39.5)
+//   128 x 128    5 and 0.66 (1.1) for one tile a CU, 1.2 (2.06) for two (1024 rows 27, 256 x 256 55; exact 42 and 109)
+//                (experts: 2048 rows of 64 x 4096 x 2048 114, 64 x 64 117, 256 x 256 138)
+//   256 x 256    5 and a round of 1.75 (3.2) a block (4096 rows 63, 128 x 128 99; up to half the CUs 1.55)
 GemmB128Plan gemm_b128_plan(const GemmB128& a, int cus) {
-  const int64_t rows = a.mode == kB128Rows ? cover(a.M, a.experts) : a.M;
-  if (a.mode == kB128Rows && rows <= 64) return rows <= 12 ? GemmB128Plan{16, 64, 1} : rows <= 24 ? GemmB128Plan{32, 64, 1} : GemmB128Plan{64, 64, 1};
-  if (rows <= 16) return {16, 16, 8};
-  if (rows <= 32) return {32, 16, 8};
-  const int64_t tiles = gemm_b128_tiles(a, 256, 256);
-  if (rows > 64 && 5 * tiles >= 2 * cus) return {256, 256, 0};
-  return rows <= 64 ? GemmB128Plan{64, 32, 8} : GemmB128Plan{64, 64, 8};
+  const double nb = a.mode == kB128Blocks ? (double)cover(a.rows, (int64_t)kB * a.experts) : a.nb;
+  // Rows of experts: of E experts E (1 - (1 - 1/E)^rows) have some, if rows choose freely; their last tiles are taken
+  // to be a quarter full, since some have many more rows than others.  The weights come at 5.5 MB a us at best.
+  const double E = a.experts, active = E * (1 - pow(1 - 1 / E, (double)a.M)), mean = a.M / active;
+  const bool by_rows = a.mode == kB128Rows;
+  auto tiles = [&](int tm, int tn) {
+    if (!by_rows) return (double)gemm_b128_tiles(a, tm, tn);
+    return active * fmax(1.0, mean / tm + 0.75) * (double)cover(a.N, tn);
+  };
+  const double memory = by_rows ? active * a.N * nb * kB / 5.5e6 : 0;
+  GemmB128Plan best{};
+  double least = 1e30;
+  auto offer = [&](int tm, int tn, int waves, double us) {
+    us = fmax(us, memory + 4);
+    if (us < least) least = us, best = GemmB128Plan{tm, tn, waves};
+  };
+  const int small[3][2] = {{16, 16}, {32, 16}, {64, 32}};
+  // (a row or two each: 128 rows of 64 x 4096 x 2048 67-71 us by 16 x 64, 74 by 64 x 64; 32 of 8 x 8192 x 5120 58 and 49)
+  if (by_rows && a.M <= 3 * E) return {16, 64, 1};
+  for (const auto& s : small)
+    if (!by_rows) offer(s[0], s[1], 8, 1.8 + ceil(tiles(s[0], s[1]) / cus) * (1.1 + (s[0] + s[1]) * nb * kB / 33e3));
+  const double t64 = tiles(64, 64), t128 = tiles(128, 128), t256 = tiles(256, 256);
+  // rounds of two tiles a CU, the last of one where that is enough
+  auto pairs = [&](double n, double one, double two) {
+    const double whole = floor(n / (2 * cus)), rest = n - whole * 2 * cus;
+    return whole * two + (rest > cus ? two : rest > 0 ? one : 0);
+  };
+  offer(64, 64, 0, 4 + nb * (a.exact ? pairs(t64, 0.47, 0.83) : pairs(t64, 0.34, 0.55)));
+  offer(128, 128, 0, 5 + nb * (a.exact ? pairs(t128, 1.1, 2.06) : pairs(t128, 0.66, 1.2)));
+  offer(256, 256, 0, 5 + ceil(t256 / cus) * (nb * (a.exact ? 3.2 : 2 * t256 <= cus ? 1.55 : 1.75) + 2));
+  return best;
 }
 
 hipError_t launch_gemm_b128(const GemmB128& a, hipStream_t stream) {
   const GemmB128Plan p = gemm_b128_plan(a, device_cu_count());
-  return p.waves == 0 ? launch_gemm_b128_tile(a, stream) : launch_gemm_b128_rows(a, p, stream);
+  if (p.waves != 0) return launch_gemm_b128_rows(a, p, stream);
+  return p.tile_m == 256 ? launch_gemm_b128_tile(a, stream) : launch_gemm_b128_mid(a, p, stream);
 }
 
 }  // namespace mxq

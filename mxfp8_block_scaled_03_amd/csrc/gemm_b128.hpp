@@ -120,16 +120,107 @@ __device__ __forceinline__ Wide widen(v8i c) {
   for (int q = 0; q < 4; ++q) r.p[q] = codes_to_bf16<F>((uint32_t)c[2 * q], (uint32_t)c[2 * q + 1], 1.0f);
   return r;
 }
-__device__ __forceinline__ v4f block_exact(const Wide& w, const Wide& x) {
-  v4f t = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.p[q], x.p[q], t, 0, 0, 0);
-  return t;
-}
-
 __device__ __forceinline__ float finish(float acc, float alpha, float bias, int act) {
   const float v = __builtin_fmaf(alpha, acc, bias);
   return act ? silu(v) : v;
+}
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// 4 bytes per lane from buffer offset voff into LDS at lds + 4 * lane.
+__device__ __forceinline__ void dma4(uint32_t lds, uint32_t voff, v4i rsrc) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Four sums of a wave that have to be there at this point: results of vector instructions, never of matrix ones.
+template <int N>
+__device__ __forceinline__ void pin(v4f (&a)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) asm volatile("" : "+v"(a[j]));
+}
+
+// The epilogue of a wave that holds 16 FM x 16 FN outputs: lane (i, g) has Y[row0 + 16 f + i][col0 + 16 j + 4 g + r]
+// of the tile in acc[f][j][r].  act(alpha v + bias), then rows of 16 FN values through REGION bytes of LDS of the
+// wave's own, 16-byte piece c of row r at c ^ (r & 7), and out in 16-byte pieces, value by value in the last
+// columns.
+template <int E, int FM, int FN, int REGION>
+__device__ __forceinline__ void store_rows(const GemmB128& a, const B128Tile& t, const v4f (&acc)[FM][FN], int wid, int lane,
+                                           int row0, int col0) {
+  constexpr int RB = 16 * FN * E, CPR = RB / 16, RP = REGION / RB < 16 * FM ? REGION / RB : 16 * FM, FPP = RP / 16;
+  constexpr int XOR = (CPR < 8 ? CPR : 8) - 1;
+  static_assert(RP % 16 == 0 && FM % FPP == 0 && 1024 % RB == 0, "rows of a pass");
+  const int i = lane & 15, g = lane >> 4;
+  const uint32_t base = (uint32_t)wid * REGION;
+#pragma unroll
+  for (int pass = 0; pass < FM / FPP; ++pass) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int fl = 0; fl < FPP; ++fl) {
+        const int f = pass * FPP + fl, row = 16 * fl + i;
+        const uint32_t byte = (uint32_t)((16 * j + 4 * g) * E);
+        const uint32_t at = base + (uint32_t)row * RB + (((byte >> 4) ^ (uint32_t)(row & XOR)) << 4) + (byte & 15);
+        if (E == 2) {
+          const v2u p = {pack_bf16(acc[f][j][0], acc[f][j][1]), pack_bf16(acc[f][j][2], acc[f][j][3])};
+          *reinterpret_cast<v2u*>(smem + at) = p;
+        } else {
+          *reinterpret_cast<v4f*>(smem + at) = acc[f][j];
+        }
+      }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    constexpr int RPI = 1024 / RB;
+    const int c = lane % CPR, left = t.n - col0 - c * (16 / E);   // columns from this piece on
+#pragma unroll 4
+    for (int it = 0; it < RP / RPI; ++it) {
+      const int row = it * RPI + lane / CPR, m = row0 + pass * RP + row;
+      const v4i v = lds16(base + (uint32_t)row * RB + (uint32_t)((c ^ (row & XOR)) << 4), 0);
+      if (m >= t.m) continue;
+      uint8_t* dst = reinterpret_cast<uint8_t*>(a.y) + (t.y + (int64_t)m * a.ld_y + col0) * E + 16 * c;
+      if (left >= 16 / E) {
+        __builtin_memcpy(dst, &v, 16);     // one store, whatever y's alignment
+      } else {
+#pragma unroll
+        for (int q = 0; q < 16 / E; ++q)
+          if (q < left) {
+            if (E == 2)
+              reinterpret_cast<uint16_t*>(dst)[q] = (uint16_t)((uint32_t)v[q >> 1] >> (16 * (q & 1)));
+            else
+              reinterpret_cast<uint32_t*>(dst)[q] = (uint32_t)v[q];
+          }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+  }
+}
+
+template <int FM, int FN, int REGION>
+__device__ __forceinline__ void epilogue(const GemmB128& a, const B128Tile& t, v4f (&acc)[FM][FN], int wid, int lane, int row0,
+                                         int col0) {
+  const bool has_bias = a.bias != nullptr;
+  const __amdgpu_buffer_rsrc_t brs = bias_rsrc(a.bias, a.N);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int col = t.n0 + col0 + 16 * j + 4 * (lane >> 4);
+    const v4f bq = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(brs, 4 * col, 0, 0));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float bv = has_bias && col + r < a.N ? bq[r] : -0.0f;
+#pragma unroll
+      for (int f = 0; f < FM; ++f) acc[f][j][r] = finish(acc[f][j][r], a.alpha, bv, a.act);
+    }
+  }
+  if (a.y_bf16)
+    store_rows<2, FM, FN, REGION>(a, t, acc, wid, lane, row0, col0);
+  else
+    store_rows<4, FM, FN, REGION>(a, t, acc, wid, lane, row0, col0);
 }
 
 }  // namespace

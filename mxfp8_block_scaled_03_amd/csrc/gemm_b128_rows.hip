@@ -4,7 +4,8 @@
 // Bound by the weights' bytes and by latency.  A wave owns 16 MT x 16 NT outputs.  Where there are few tiles
 // (WK = 8) eight waves share them along K: wave v takes blocks v, v + 8, ..., so that the eight together read
 // 1 KiB runs of each line; their sums meet in LDS, are added in the waves' order, and finished by all
-// threads.  Where there are many (WK = 1: experts) each of four waves has a tile of its own, side by side along N,
+// threads.  Where there are many (WK = 1: experts of a
+// row or two) each of four waves has a tile of its own, side by side along N,
 // and all of K.  Codes come straight from memory into the fragments' registers, U blocks ahead: a block's
 // registers are refilled as soon as they have been read.
 #include "gemm_b128.hpp"
@@ -111,8 +112,8 @@ __device__ __forceinline__ void store4(const GemmB128& a, const B128Tile& t, v4f
   if (a.y_bf16) {
     uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + at;
     const v2u d = {pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
-    if (a.y_vec16 && left >= 4) {
-      *reinterpret_cast<v2u*>(y) = d;
+    if (left >= 4) {
+      __builtin_memcpy(y, &d, 8);
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -120,8 +121,8 @@ __device__ __forceinline__ void store4(const GemmB128& a, const B128Tile& t, v4f
     }
   } else {
     float* y = reinterpret_cast<float*>(a.y) + at;
-    if (a.y_vec16 && left >= 4) {
-      *reinterpret_cast<v4f*>(y) = s;
+    if (left >= 4) {
+      __builtin_memcpy(y, &s, 16);
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -213,16 +214,7 @@ template <int FX, int FW, bool EXACT, bool WLINE, int MT, int NT, int WK>
 hipError_t launch_t(const GemmB128& a, hipStream_t stream) {
   constexpr int waves = waves_of(WK), lds = WK == 1 ? 0 : WK * MT * NT * 1024;
   auto kern = k_gemm_b128_rows<FX, FW, EXACT, WLINE, MT, NT, WK>;
-  if (lds > 65536) {
-    static bool set[64] = {false};
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
-    if (!set[dev]) {
-      const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-      if (e != hipSuccess) return e;
-      set[dev] = true;
-    }
-  }
+  static_assert(lds <= 65536, "no more than a launch may have unasked");
   const Grid grid = grid_of(gemm_b128_tiles(a, 16 * MT, 16 * NT * (waves / WK)));
   hipLaunchKernelGGL(kern, dim3(grid.x, grid.y), dim3(64 * waves), lds, stream, a);
   return hipGetLastError();
@@ -231,14 +223,10 @@ hipError_t launch_t(const GemmB128& a, hipStream_t stream) {
 template <int FX, int FW, bool EXACT, bool WLINE>
 hipError_t launch_p(const GemmB128& a, const GemmB128Plan& p, hipStream_t s) {
   // the plans of gemm_b128_plan, and no others
-  if (p.waves == 1) {
-    if (p.tile_m == 16) return launch_t<FX, FW, EXACT, WLINE, 1, 1, 1>(a, s);
-    if (p.tile_m == 32) return launch_t<FX, FW, EXACT, WLINE, 2, 1, 1>(a, s);
-    return launch_t<FX, FW, EXACT, WLINE, 4, 1, 1>(a, s);
-  }
+  if (p.waves == 1) return launch_t<FX, FW, EXACT, WLINE, 1, 1, 1>(a, s);
   if (p.tile_m == 16) return launch_t<FX, FW, EXACT, WLINE, 1, 1, 8>(a, s);
   if (p.tile_m == 32) return launch_t<FX, FW, EXACT, WLINE, 2, 1, 8>(a, s);
-  return p.tile_n == 32 ? launch_t<FX, FW, EXACT, WLINE, 4, 2, 8>(a, s) : launch_t<FX, FW, EXACT, WLINE, 4, 4, 8>(a, s);
+  return launch_t<FX, FW, EXACT, WLINE, 4, 2, 8>(a, s);
 }
 
 template <int FX, int FW>

@@ -29,20 +29,6 @@ constexpr int kScaleSlot = 2 * kTile * 4;       // X, then W
 constexpr int kLds = kOffScale + 4 * kScaleSlot;   // 136 KiB
 constexpr int kWaveOut = 16384;                 // a wave's staging of the epilogue, in the code stages
 
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// 4 bytes per lane from buffer offset voff into LDS at lds + 4 * lane.
-__device__ __forceinline__ void dma4(uint32_t lds, uint32_t voff, v4i rsrc) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :
-               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc)
-               : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-// Results of vector instructions (never of matrix instructions) that have to be there at this point.
-__device__ __forceinline__ void pin(v4f a[4]) { asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3])); }
-
 template <int FX, int FW, bool EXACT, bool WLINE>
 __global__ __launch_bounds__(kThreads, 2) void k_gemm_b128(const GemmB128 a) {
   const B128Tile t = b128_tile<kTile, kTile, WLINE>(a, workgroup_at(blockIdx.x, blockIdx.y));
@@ -199,78 +185,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_b128(const GemmB128 a) {
   wait_vm<0>();
   lds_barrier();
 
-  // ---- epilogue: lane (i, g) holds Y[128 gp + 16 f + i][64 wq + 16 j + 4 g + r] in acc[f][j][r]
-  const int wrow = 128 * gp, wcol = 64 * wq;
-  {
-    const bool has_bias = a.bias != nullptr;
-    const __amdgpu_buffer_rsrc_t brs = bias_rsrc(a.bias, a.N);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = t.n0 + wcol + 16 * j + 4 * g;
-      const v4f bq = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(brs, 4 * col, 0, 0));
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float bv = has_bias && col + r < a.N ? bq[r] : -0.0f;
-#pragma unroll
-        for (int f = 0; f < 8; ++f) acc[f][j][r] = finish(acc[f][j][r], a.alpha, bv, a.act);
-      }
-    }
-  }
-  // Rows of 64 values through the wave's own LDS, 16-byte piece c of row r at c ^ (r & 7), and out in
-  // 16-byte pieces where y's rows allow it, value by value in the last columns and elsewhere.
-  auto store = [&](auto e_c) {
-    constexpr int E = decltype(e_c)::value;           // bytes a value
-    constexpr int RB = 64 * E, CPR = RB / 16, RP = kWaveOut / RB, FPP = RP / 16;
-    const uint32_t base = (uint32_t)wid * kWaveOut;
-#pragma unroll
-    for (int pass = 0; pass < 128 / RP; ++pass) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int fl = 0; fl < FPP; ++fl) {
-          const int f = pass * FPP + fl, row = 16 * fl + i;
-          const uint32_t byte = (uint32_t)((16 * j + 4 * g) * E);
-          const uint32_t at = base + (uint32_t)row * RB + (((byte >> 4) ^ (uint32_t)(row & 7)) << 4) + (byte & 15);
-          if (E == 2) {
-            const v2u p = {pack_bf16(acc[f][j][0], acc[f][j][1]), pack_bf16(acc[f][j][2], acc[f][j][3])};
-            *reinterpret_cast<v2u*>(smem + at) = p;
-          } else {
-            *reinterpret_cast<v4f*>(smem + at) = acc[f][j];
-          }
-        }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-      constexpr int RPI = 1024 / RB;
-      const int c = lane % CPR, left = t.n - wcol - c * (16 / E);   // columns from this piece on
-#pragma unroll 4
-      for (int it = 0; it < RP / RPI; ++it) {
-        const int row = it * RPI + lane / CPR, m = wrow + pass * RP + row;
-        const v4i v = lds16(base + (uint32_t)row * RB + (uint32_t)((c ^ (row & 7)) << 4), 0);
-        if (m >= t.m) continue;
-        uint8_t* dst = reinterpret_cast<uint8_t*>(a.y) + (t.y + (int64_t)m * a.ld_y + wcol) * E + 16 * c;
-        if (a.y_vec16 && left >= 16 / E) {
-          *reinterpret_cast<v4i*>(dst) = v;
-        } else {
-#pragma unroll
-          for (int q = 0; q < 16 / E; ++q)
-            if (q < left) {
-              if (E == 2)
-                reinterpret_cast<uint16_t*>(dst)[q] = (uint16_t)((uint32_t)v[q >> 1] >> (16 * (q & 1)));
-              else
-                reinterpret_cast<uint32_t*>(dst)[q] = (uint32_t)v[q];
-            }
-        }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-    }
-  };
-  if (a.y_bf16)
-    store(std::integral_constant<int, 2>());
-  else
-    store(std::integral_constant<int, 4>());
+  epilogue<8, 4, kWaveOut>(a, t, acc, wid, lane, 128 * gp, 64 * wq);
 }
 
 template <int FX, int FW, bool EXACT, bool WLINE>

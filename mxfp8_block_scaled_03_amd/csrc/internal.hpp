@@ -183,18 +183,20 @@ struct GemmB128 {
   const float* bias;
   int act;
   void* y;
-  int y_bf16, y_vec16;
+  int y_bf16;
   int64_t ld_y, st_y;
 };
 // The most tiles of tm x tn outputs that the problem may have.
 int64_t gemm_b128_tiles(const GemmB128& a, int tm, int tn);
-// How it runs on `cus` CUs (host logic only): its tile, and the waves that share one along K (0: 256 x 256).
+// How it runs on `cus` CUs (host logic only): its tile, and the waves that share one along K (0: a workgroup's
+// waves share its tile's rows and columns, step by step).
 struct GemmB128Plan {
   int tile_m, tile_n, waves;
 };
 GemmB128Plan gemm_b128_plan(const GemmB128& a, int cus);
 hipError_t launch_gemm_b128(const GemmB128& a, hipStream_t stream);
 hipError_t launch_gemm_b128_tile(const GemmB128& a, hipStream_t stream);
+hipError_t launch_gemm_b128_mid(const GemmB128& a, const GemmB128Plan& p, hipStream_t stream);
 hipError_t launch_gemm_b128_rows(const GemmB128& a, const GemmB128Plan& p, hipStream_t stream);
 
 // ---- routing (moe_route.hip): experts and shares [T][k], counts [E], offsets [E + 1], order [T k], loss [1], slope [E]
