@@ -36,16 +36,29 @@ def _offsets(t) -> int:
     return t.shape[0] - 1
 
 
+# These calls are short, as those of _fp4 are: what is needed is read once, and the slow ways only find what is wrong.
+
 def _devices(x, *named) -> int:
     """The device of x, which all given tensors have to be on."""
     device = x.get_device()
-    if device < 0 or any(t is not None and t.get_device() != device for _, t in named):
+    for _, t in named:
+        if t is not None and t.get_device() != device:
+            device = -1
+    if device < 0:
         _same_device((("the first tensor", x),) + named)
     return device
 
 
 def _line_scales(t, name: str, lines: int, nb: int) -> int:
     """Checks scales of lines; the pitch from block to block."""
+    try:
+        n, b = t.shape
+        step, pitch = t.stride()
+        if n == lines and b >= nb > 1 and step == 1 and pitch >= n > 1 and t.dtype is _F32:
+            return pitch
+    except (AttributeError, TypeError, ValueError):
+        pass
+    # one line, one block or none, or something wrong
     if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.dim() != 2:
         raise ValueError("%s must be a 2-D float32 tensor" % name)
     if t.shape[0] != lines or t.shape[1] < nb:
@@ -88,16 +101,6 @@ def _rule(rule: str) -> int:
     return _RULES[rule]
 
 
-def _run_quantize(x, ld, elem, rule, tile, rc, rs, cc, cs, offsets, experts, device):
-    if x.shape[0] == 0 or x.shape[1] == 0:
-        return
-    _call("mxq_quantize_b128", device, (
-        x.data_ptr(), _WIDE[x.dtype], x.shape[0], x.shape[1], ld, _ELEM[elem], rule, 1 if tile else 0,
-        None if rc is None else rc.data_ptr(), 0 if rc is None else max(rc.shape[1], 1),
-        None if rs is None else rs.data_ptr(), 0 if rs is None else rs.stride(0 if tile else 1),
-        None if cc is None else cc.data_ptr(), 0 if cc is None else max(cc.shape[1], 1),
-        None if cs is None or tile else cs.data_ptr(), 0 if cs is None else cs.stride(1),
-        None if offsets is None else offsets.data_ptr(), experts))
 
 
 def quantize_b128(x, elem: str = "e4m3", axis: str = "row", rule: str = "amax", offsets=None):
@@ -115,24 +118,30 @@ def quantize_b128(x, elem: str = "e4m3", axis: str = "row", rule: str = "amax", 
     r = _rule(rule)
     if axis not in ("row", "col", "tile"):
         raise ValueError("axis must be 'row', 'col' or 'tile'")
-    experts = 1
+    experts, off = 1, None
     if offsets is not None:
         if axis != "col":
             raise ValueError("offsets need axis='col'")
-        experts = _offsets(offsets)
-    device = _devices(x, ("offsets", offsets))
+        experts, off = _offsets(offsets), offsets.data_ptr()
+    device = x.get_device()
+    if device < 0 or (offsets is not None and offsets.get_device() != device):
+        _devices(x, ("offsets", offsets))
     rows, cols = x.shape
-    if axis == "col":
+    where, head = x.device, (x.data_ptr(), _WIDE[x.dtype], rows, cols, ld, _ELEM[elem], r)
+    if axis == "row":
+        nb = (cols + (B - 1)) // B
+        c, s = _code_lines(rows, nb, where), _scale_lines(rows, nb, where)
+        args = head + (0, c.data_ptr(), B * nb, s.data_ptr(), rows, None, 0, None, 0, None, 1)
+    elif axis == "col":
         nb = (rows + (B - 1) * experts) // B
-        c, s = _code_lines(cols, nb, x.device), _scale_lines(cols, nb, x.device)
-        _run_quantize(x, ld, elem, r, False, None, None, c, s, offsets, experts, device)
+        c, s = _code_lines(cols, nb, where), _scale_lines(cols, nb, where)
+        args = head + (0, None, 0, None, 0, c.data_ptr(), B * nb, s.data_ptr(), cols, off, experts)
     else:
-        nb = _blocks(cols)
-        c = _code_lines(rows, nb, x.device)
-        tile = axis == "tile"
-        s = _empty((_blocks(rows), nb), (max(nb, 1), 1), dtype=_F32, device=x.device) if tile else \
-            _scale_lines(rows, nb, x.device)
-        _run_quantize(x, ld, elem, r, tile, c, s, None, None, None, 1, device)
+        nb = (cols + (B - 1)) // B
+        c, s = _code_lines(rows, nb, where), _empty((_blocks(rows), nb), (max(nb, 1), 1), dtype=_F32, device=where)
+        args = head + (1, c.data_ptr(), B * nb, s.data_ptr(), nb, None, 0, None, 0, None, 1)
+    if rows and cols:
+        _call("mxq_quantize_b128", device, args)
     return c, s
 
 
@@ -145,33 +154,43 @@ def quantize_b128_dual(x, elem: str = "e4m3", tile: bool = False, rule: str = "a
     ld = _wide(x, "x")
     _elem("elem", elem)
     r = _rule(rule)
-    experts = 1
+    experts, off = 1, None
     if offsets is not None:
         if tile:
             raise ValueError("tiles cannot follow offsets")
-        experts = _offsets(offsets)
-    device = _devices(x, ("offsets", offsets))
+        experts, off = _offsets(offsets), offsets.data_ptr()
+    device = x.get_device()
+    if device < 0 or (offsets is not None and offsets.get_device() != device):
+        _devices(x, ("offsets", offsets))
     rows, cols = x.shape
-    nbc, nbr = _blocks(cols), (rows + (B - 1) * experts) // B
-    rc, cc = _code_lines(rows, nbc, x.device), _code_lines(cols, nbr, x.device)
+    where, nbc, nbr = x.device, (cols + (B - 1)) // B, (rows + (B - 1) * experts) // B
+    rc, cc = _code_lines(rows, nbc, where), _code_lines(cols, nbr, where)
     if tile:
-        rs = _empty((nbr, nbc), (max(nbc, 1), 1), dtype=_F32, device=x.device)
-        cs = rs.t()
+        rs = _empty((nbr, nbc), (max(nbc, 1), 1), dtype=_F32, device=where)
+        cs, tail = rs.t(), (rs.data_ptr(), nbc, cc.data_ptr(), B * nbr, None, 0, None, 1)
     else:
-        rs, cs = _scale_lines(rows, nbc, x.device), _scale_lines(cols, nbr, x.device)
-    _run_quantize(x, ld, elem, r, tile, rc, rs, cc, cs, offsets, experts, device)
+        rs, cs = _scale_lines(rows, nbc, where), _scale_lines(cols, nbr, where)
+        tail = (rs.data_ptr(), rows, cc.data_ptr(), B * nbr, cs.data_ptr(), cols, off, experts)
+    if rows and cols:
+        _call("mxq_quantize_b128", device, (x.data_ptr(), _WIDE[x.dtype], rows, cols, ld, _ELEM[elem], r,
+                                            1 if tile else 0, rc.data_ptr(), B * nbc) + tail)
     return rc, rs, cc, cs
 
 
-def _out(out, shape, out_dtype, device):
-    """The output tensor and its row pitch."""
-    if out is not None:
-        if tuple(out.shape) != shape:
-            raise ValueError("out must have shape %s, got %s" % (shape, tuple(out.shape)))
-        return out
-    if out_dtype is not None and out_dtype not in _WIDE:
-        raise ValueError("out_dtype must be float32 or bfloat16")
-    return torch.empty(shape, dtype=out_dtype or _BF16, device=device)
+def _out(out, rows: int, cols: int, out_dtype, like):
+    """The output [rows][cols] on the device of `like`, its type tag and row pitch."""
+    if out is None:
+        dtype = out_dtype or _BF16
+        if dtype not in _WIDE:
+            raise ValueError("out_dtype must be float32 or bfloat16")
+        pitch = cols if cols > 0 else 1
+        return _empty((rows, cols), (pitch, 1), dtype=dtype, device=like.device), _WIDE[dtype], pitch
+    pitch = _wide(out, "out")
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError("out must have shape (%d, %d), got %s" % (rows, cols, tuple(out.shape)))
+    if out.get_device() != like.get_device():
+        _devices(like, ("out", out))
+    return out, _WIDE[out.dtype], pitch
 
 
 def _accum(accum: str) -> int:
@@ -201,15 +220,15 @@ def gemm_b128(x_codes, x_scales, w_codes, w_scales, K: int, x_elem: str = "e4m3"
         raise ValueError("bias must be a contiguous 1-D float32 tensor of N = %d elements" % N)
     if act not in _ACT:
         raise ValueError("act must be None or 'silu'")
-    if out is not None:
-        _wide(out, "out")
-    device = _devices(x_codes, ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("bias", bias),
-                      ("out", out))
-    out = _out(out, (M, N), out_dtype, x_codes.device)
+    device = x_codes.get_device()
+    if device < 0 or x_scales.get_device() != device or w_codes.get_device() != device or \
+            w_scales.get_device() != device or (bias is not None and bias.get_device() != device):
+        _devices(x_codes, ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales), ("bias", bias))
+    out, y_type, ld_y = _out(out, M, N, out_dtype, x_codes)
     _call("mxq_gemm_b128", device, (
         M, N, K, x_codes.data_ptr(), ld_x, x_scales.data_ptr(), ld_xs, _ELEM[x_elem], w_codes.data_ptr(), ld_w,
         w_scales.data_ptr(), ws_n, ws_k, w_block, _ELEM[w_elem], alpha, None if bias is None else bias.data_ptr(),
-        _ACT[act], acc, out.data_ptr(), _WIDE[out.dtype], _lines(out, "out", out.dtype, 0, 0)))
+        _ACT[act], acc, out.data_ptr(), y_type, ld_y))
     return out
 
 
@@ -234,15 +253,13 @@ def moe_gemm_b128(x_codes, x_scales, w_codes, w_scales, offsets, K: int, x_elem:
     w_block, ws_n, ws_k = _weight_scales(w_scales, "w_scales", N, nb, 1)
     _elem("element formats", x_elem, w_elem)
     acc = _accum(accum)
-    if out is not None:
-        _wide(out, "out")
     device = _devices(x_codes, ("x_scales", x_scales), ("w_codes", w_codes), ("w_scales", w_scales),
-                      ("offsets", offsets), ("out", out))
-    out = _out(out, (R, N), out_dtype, x_codes.device)
+                      ("offsets", offsets))
+    out, y_type, ld_y = _out(out, R, N, out_dtype, x_codes)
     _call("mxq_moe_gemm_b128", device, (
         R, N, K, E, offsets.data_ptr(), x_codes.data_ptr(), ld_x, x_scales.data_ptr(), ld_xs, _ELEM[x_elem],
         w_codes.data_ptr(), ld_w, w_codes.stride(0), w_scales.data_ptr(), ws_n, ws_k, w_scales.stride(0), w_block,
-        _ELEM[w_elem], acc, out.data_ptr(), _WIDE[out.dtype], _lines(out, "out", out.dtype, 0, 0)))
+        _ELEM[w_elem], acc, out.data_ptr(), y_type, ld_y))
     return out
 
 
@@ -263,16 +280,23 @@ def moe_wgrad_b128(dy_codes, dy_scales, x_codes, x_scales, offsets, x_elem: str 
     ld_ds, ld_xs = _line_scales(dy_scales, "dy_scales", N, nb), _line_scales(x_scales, "x_scales", K, nb)
     _elem("element formats", x_elem, w_elem)
     acc = _accum(accum)
-    if out is not None and (not isinstance(out, torch.Tensor) or out.dim() != 3 or out.dtype not in _WIDE
-                            or out.stride(2) != 1):
-        raise ValueError("out must be a 3-D float32 or bfloat16 tensor with unit stride along its last dimension")
     device = _devices(dy_codes, ("dy_scales", dy_scales), ("x_codes", x_codes), ("x_scales", x_scales),
-                      ("offsets", offsets), ("out", out))
-    out = _out(out, (E, N, K), out_dtype or _F32, dy_codes.device)
+                      ("offsets", offsets))
+    if out is None:
+        if out_dtype is not None and out_dtype not in _WIDE:
+            raise ValueError("out_dtype must be float32 or bfloat16")
+        out = _empty((E, N, K), (max(N * K, 1), max(K, 1), 1), dtype=out_dtype or _F32, device=dy_codes.device)
+    else:
+        if not isinstance(out, torch.Tensor) or out.dim() != 3 or out.dtype not in _WIDE or \
+                (out.shape[2] > 1 and out.stride(2) != 1):
+            raise ValueError("out must be a 3-D float32 or bfloat16 tensor with unit stride along its last dimension")
+        if tuple(out.shape) != (E, N, K):
+            raise ValueError("out must have shape (%d, %d, %d), got %s" % (E, N, K, tuple(out.shape)))
+        _devices(dy_codes, ("out", out))
     _call("mxq_moe_wgrad_b128", device, (
         N, K, rows, E, offsets.data_ptr(), dy_codes.data_ptr(), ld_dy, dy_scales.data_ptr(), ld_ds, _ELEM[x_elem],
         x_codes.data_ptr(), ld_x, x_scales.data_ptr(), ld_xs, _ELEM[w_elem], acc, out.data_ptr(), _WIDE[out.dtype],
-        max(out.stride(1), K, 1), out.stride(0)))
+        out.stride(1) if N > 1 else max(K, 1), out.stride(0)))
     return out
 
 
