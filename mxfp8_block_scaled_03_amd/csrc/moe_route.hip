@@ -10,24 +10,24 @@
 //
 // A wave has a token: lane l holds the logits of experts l, 64 + l, ...; the maximum of a wave takes six lane
 // steps (DPP), its expert a ballot.  Waves take runs of consecutive tokens, so that one wave's counters (lane l
-// those of experts l, 64 + l, ...) number the slots of an expert in order, and a scan over the waves' counts
-// gives every slot its place: no atomics, and nothing depends on how workgroups are scheduled.  Bound by
-// HBM for many tokens (logits once), by launches for few: up to 256 tokens take one workgroup and one launch, more
-// take three (tokens; scan over waves; places and loss).
+// those of experts l, 64 + l, ...) number the slots of an expert in order, and sums over the waves' and
+// workgroups' counts give every slot its place: no atomics, and nothing depends on how workgroups are scheduled.
+// Up to 256 tokens take one workgroup and one launch, more take three (tokens; sums over the groups; places and
+// loss).
 #include "codec.hpp"
 #include "internal.hpp"
 
 namespace mxq {
 namespace {
 
-constexpr int kUnits = 1024;      // runs of tokens, at most
+constexpr int kGroups = 512, kWaves = 8;      // workgroups at most, and a workgroup's runs of tokens
 constexpr int kSmallTokens = 256, kSmallSlots = 4096, kSmallExperts = 256, kSmallWaves = 16;
 
 struct RouteArgs {
   const void* logits;
   int64_t ld;
   const uint8_t* mask;
-  int T, E, k, renorm, bf16, units;
+  int T, E, k, renorm, bf16, groups;
   int* experts;
   float* shares;
   int* counts;
@@ -35,10 +35,12 @@ struct RouteArgs {
   int* order;
   float* loss;
   float* slope;
-  // workspace: per unit, E + 1 slot counts (the last: tokens that count) and E sums of p; each slot's number
-  // among its unit's slots of the expert; E sums of p; the number of tokens that count
+  // workspace: per group, E + 1 slot counts (the last: tokens that count) and E sums of p; per wave, E counts of
+  // the group's waves before it; each slot's number among its wave's slots of the expert; E sums of p; the
+  // number of tokens that count
   int* cnt;
   float* psum;
+  int* before;
   int* rank;
   float* total;
   int* live;
@@ -80,17 +82,35 @@ __device__ __forceinline__ float logit(const RouteArgs& a, int64_t t, int e) {
                 : reinterpret_cast<const float*>(a.logits)[at];
 }
 
-// A token's logits, their maximum and the softmax; all zero where every expert is masked.
+// e^x for x <= 0 within a few u: 2^(x log2 e) by v_exp_f32, the rounding of the exponent put back by its first-order term
+// (ocml's expf is the same to the last bits at three times the instructions; the kernels are bound by those).
+__device__ __forceinline__ float exp_below(float x) {
+  x = fmaxf(x, -200.0f);                         // (e^-200 is 0, and -inf has no remainder)
+  const float t = x * 0x1.715476p+0f;
+  const float r = __builtin_fmaf(x, 0x1.4ae0c0p-26f, __builtin_fmaf(x, 0x1.715476p+0f, -t));   // log2 e = high + low
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, r * 0x1.62e430p-1f, e);
+}
+
 template <int V>
-__device__ __forceinline__ void softmax(const RouteArgs& a, int64_t t, int lane, float x[V], float ex[V], float& sum) {
+__device__ __forceinline__ void load_token(const RouteArgs& a, int64_t t, int lane, float x[V]) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = 64 * v + lane;
     x[v] = e < a.E ? logit(a, t, e) : -INFINITY;
   }
+}
+
+// The softmax of a token's logits before division by `sum`, all zero where every expert is masked; their keys.
+template <int V>
+__device__ __forceinline__ void softmax(const RouteArgs& a, int lane, const float x[V], uint32_t key[V], float ex[V],
+                                        float& sum) {
   uint32_t top = 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) top = max(top, key_of(x[v]));
+  for (int v = 0; v < V; ++v) {
+    key[v] = key_of(x[v]);
+    top = max(top, key[v]);
+  }
   top = dpp_max(top);
   if (top == kMasked) {
 #pragma unroll
@@ -98,69 +118,96 @@ __device__ __forceinline__ void softmax(const RouteArgs& a, int64_t t, int lane,
     sum = 1.0f;
     return;
   }
-  const float m = top == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u)
-                                     : __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
   float s = 0.0f;
+  if (top >= 0xFF800000u) {                      // +inf or NaN: NaN all over
+#pragma unroll
+    for (int v = 0; v < V; ++v) ex[v] = __uint_as_float(0x7FC00000u);
+    sum = ex[0];
+    return;
+  }
+  const float m = __uint_as_float(top & 0x80000000u ? top & 0x7FFFFFFFu : ~top);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    // (an expert past the last one stays 0 also beside a NaN)
-    ex[v] = 64 * v + lane < a.E ? expf(x[v] - m) : 0.0f;
+    ex[v] = exp_below(x[v] - m);                 // (experts past the last one are -inf here: 0)
     s += ex[v];
   }
   sum = dpp_sum(s);
 }
 
-// The tokens of one unit in turn: experts, shares, and slot by slot the number among the unit's slots of the
-// expert; `put` takes (slot in the array, expert or -1, number).
+// The tokens t0 .. t1 - 1 in turn: experts, shares, and slot by slot the number among the run's slots of the
+// expert; `put` takes (slot in the array, expert or -1, number).  In the loop over the k greatest a lane only
+// learns which of its experts was taken and when (28 instructions a round with four experts a lane, and those
+// bound the kernel); the lanes that own the chosen write what there is to write.
 template <int V, typename Put>
 __device__ __forceinline__ void route_unit(const RouteArgs& a, int t0, int t1, int lane, int cnt[V], float psum[V], int& live,
                                            Put put) {
 #pragma unroll
   for (int v = 0; v < V; ++v) cnt[v] = 0, psum[v] = 0.0f;
   live = 0;
+  float next[V];
+  uint32_t next_on = 0;          // (compared where it is used: a comparison here would wait for the loads)
+  if (t0 < t1) {
+    load_token<V>(a, t0, lane, next);
+    next_on = a.mask == nullptr ? 1 : a.mask[t0];
+  }
   for (int t = t0; t < t1; ++t) {
-    int mine = -1, number = 0;   // lane j: slot j
-    float share = 0.0f;
-    if (a.mask == nullptr || a.mask[t]) {
+    float x[V];
+    const bool on = next_on != 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = next[v];
+    if (t + 1 < t1) {            // the next token's logits are on their way while this one is routed
+      load_token<V>(a, t + 1, lane, next);
+      next_on = a.mask == nullptr ? 1 : a.mask[t + 1];
+    }
+    int taken = 0;
+    const int64_t row = (int64_t)t * a.k;
+    if (on) {
       ++live;
-      float x[V], ex[V], sum;
-      softmax<V>(a, t, lane, x, ex, sum);
-      const float inv = 1.0f / sum;
       uint32_t key[V];
+      float ex[V], sum;
+      softmax<V>(a, lane, x, key, ex, sum);
+      const float inv = 1.0f / sum;
+      int slot[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         psum[v] += ex[v] * inv;
-        key[v] = 64 * v + lane < a.E ? key_of(x[v]) : 0u;
+        slot[v] = -1;              // (experts past the last one have -inf's key, which nobody takes)
       }
-      float chosen = 0.0f;
-      for (int j = 0; j < a.k; ++j) {
-        uint32_t top = 0;
+      for (; taken < a.k; ++taken) {
+        uint32_t top = key[0];
 #pragma unroll
-        for (int v = 0; v < V; ++v) top = max(top, key[v]);
+        for (int v = 1; v < V; ++v) top = max(top, key[v]);
         top = dpp_max(top);
         if (top <= kMasked) break;
         bool found = false;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const uint64_t who = __ballot(key[v] == top);
-          if (!found && who) {
-            found = true;
-            const int l = __builtin_ctzll(who);
-            const float e = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ex[v]), l));
-            const int n = __builtin_amdgcn_readlane(cnt[v], l);
-            if (lane == l) key[v] = 0u, ++cnt[v];
-            chosen += e;
-            if (lane == j) mine = 64 * v + l, number = n, share = e;
-          }
+          const bool me = __builtin_amdgcn_inverse_ballot_w64(found ? 0 : who & (0 - who));
+          found = found || who != 0;
+          key[v] = me ? 0u : key[v];
+          slot[v] = me ? taken : slot[v];
         }
       }
-      if (mine >= 0) share *= a.renorm ? 1.0f / chosen : inv;
+      float scale = inv;
+      if (a.renorm) {
+        float chosen = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) chosen += slot[v] >= 0 ? ex[v] : 0.0f;
+        scale = 1.0f / dpp_sum(chosen);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (slot[v] >= 0) {
+          a.experts[row + slot[v]] = 64 * v + lane;
+          a.shares[row + slot[v]] = ex[v] * scale;
+          put(row + slot[v], 64 * v + lane, cnt[v]++);
+        }
     }
-    if (lane < a.k) {
-      const int64_t at = (int64_t)t * a.k + lane;
-      a.experts[at] = mine;
-      a.shares[at] = share;
-      put(at, mine, number);
+    if (lane >= taken && lane < a.k) {
+      a.experts[row + lane] = -1;
+      a.shares[row + lane] = 0.0f;
+      put(row + lane, -1, 0);
     }
   }
 }
@@ -245,60 +292,96 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_route_small(const RouteArg
   }
 }
 
-// ---- many tokens, one: a unit a wave
+// Wave w of the `groups` x 8: its run of tokens.
+__device__ __forceinline__ int first_token(const RouteArgs& a, int w) { return (int)((int64_t)a.T * w / (a.groups * kWaves)); }
+
+// ---- many tokens, one: a run of tokens a wave, then the counts and sums of the group
 template <int V>
-__global__ __launch_bounds__(256) void k_route_tokens(const RouteArgs a) {
-  const int lane = threadIdx.x & 63, unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (unit >= a.units) return;
-  const int t0 = (int)((int64_t)a.T * unit / a.units), t1 = (int)((int64_t)a.T * (unit + 1) / a.units);
+__global__ __launch_bounds__(64 * kWaves) void k_route_tokens(const RouteArgs a) {
+  __shared__ int s_sum[kWaves][64 * V];
+  __shared__ int s_live[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w = blockIdx.x * kWaves + wave;
   int cnt[V], live;
   float psum[V];
-  route_unit<V>(a, t0, t1, lane, cnt, psum, live, [&](int64_t at, int, int n) { a.rank[at] = n; });
+  route_unit<V>(a, first_token(a, w), first_token(a, w + 1), lane, cnt, psum, live,
+                [&](int64_t at, int, int n) { a.rank[at] = n; });
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = 64 * v + lane;
-    if (e < a.E) {
-      a.cnt[(int64_t)unit * (a.E + 1) + e] = cnt[v];
-      a.psum[(int64_t)unit * a.E + e] = psum[v];
+  for (int v = 0; v < V; ++v) s_sum[wave][64 * v + lane] = cnt[v];
+  if (lane == 0) s_live[wave] = live;
+  __syncthreads();
+  for (int e = tid; e < a.E; e += 64 * kWaves) {
+    int sum = 0;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) {
+      a.before[(int64_t)(blockIdx.x * kWaves + u) * a.E + e] = sum;
+      sum += s_sum[u][e];
     }
+    a.cnt[(int64_t)blockIdx.x * (a.E + 1) + e] = sum;
   }
-  if (lane == 0) a.cnt[(int64_t)unit * (a.E + 1) + a.E] = live;
+  if (tid == 0) {
+    int n = 0;
+    for (int u = 0; u < kWaves; ++u) n += s_live[u];
+    a.cnt[(int64_t)blockIdx.x * (a.E + 1) + a.E] = n;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) s_sum[wave][64 * v + lane] = __float_as_int(psum[v]);
+  __syncthreads();
+  for (int e = tid; e < a.E; e += 64 * kWaves) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) sum += __int_as_float(s_sum[u][e]);
+    a.psum[(int64_t)blockIdx.x * a.E + e] = sum;
+  }
 }
 
-// ---- two: sums over the units, 16 columns (experts, then the tokens that count) a workgroup, 64 runs of units
+// ---- two: sums over the groups, 8 columns (experts, then the tokens that count) a workgroup, 128 runs of at
+// most four groups, whose counts stay in registers
 __global__ __launch_bounds__(1024) void k_route_scan(const RouteArgs a) {
-  __shared__ int s_c[64][17];
-  __shared__ float s_p[64][17];
-  const int c = threadIdx.x & 15, run = threadIdx.x >> 4, e = blockIdx.x * 16 + c;
-  const int u0 = a.units * run / 64, u1 = a.units * (run + 1) / 64;
+  constexpr int kRuns = 128, kRun = kGroups / kRuns;
+  __shared__ int s_c[kRuns][9];
+  __shared__ float s_p[kRuns][9];
+  const int c = threadIdx.x & 7, run = threadIdx.x >> 3, e = blockIdx.x * 8 + c;
+  int n[kRun];
   int sum = 0;
   float p = 0.0f;
-  if (e <= a.E)
-    for (int u = u0; u < u1; ++u) {
-      sum += a.cnt[(int64_t)u * (a.E + 1) + e];
-      if (e < a.E) p += a.psum[(int64_t)u * a.E + e];
+#pragma unroll
+  for (int u = 0; u < kRun; ++u) {
+    const int g = run * kRun + u;
+    n[u] = 0;
+    if (g < a.groups && e <= a.E) {
+      n[u] = a.cnt[(int64_t)g * (a.E + 1) + e];
+      if (e < a.E) p += a.psum[(int64_t)g * a.E + e];
     }
+    sum += n[u];
+  }
   s_c[run][c] = sum;
   s_p[run][c] = p;
-  __syncthreads();
-  if (e > a.E) return;
-  int before = 0;
-  for (int r = 0; r < run; ++r) before += s_c[r][c];
-  if (run == 63) {
-    float q = 0.0f;
-    for (int r = 0; r < 64; ++r) q += s_p[r][c];
-    if (e < a.E) {
-      a.counts[e] = before + sum;
-      a.total[e] = q;
-    } else {
-      a.live[0] = before + sum;
-    }
+  // sums of the runs up to each, and of all p: log2(128) steps
+  for (int d = 1; d < kRuns; d <<= 1) {
+    __syncthreads();
+    const int oc = run >= d ? s_c[run - d][c] : 0;
+    const float op = run >= d ? s_p[run - d][c] : 0.0f;
+    __syncthreads();
+    s_c[run][c] += oc;
+    s_p[run][c] += op;
   }
-  for (int u = u0; u < u1; ++u) {
-    int* at = a.cnt + (int64_t)u * (a.E + 1) + e;
-    const int n = *at;
-    *at = before;
-    before += n;
+  if (e > a.E) return;
+  int before = s_c[run][c] - sum;
+#pragma unroll
+  for (int u = 0; u < kRun; ++u) {
+    const int g = run * kRun + u;
+    if (g < a.groups) a.cnt[(int64_t)g * (a.E + 1) + e] = before;
+    before += n[u];
+  }
+  if (run == kRuns - 1) {
+    if (e < a.E) {
+      a.counts[e] = before;
+      a.total[e] = s_p[run][c];
+    } else {
+      a.live[0] = before;
+    }
   }
 }
 
@@ -334,11 +417,11 @@ __global__ __launch_bounds__(256) void k_route_order(const RouteArgs a) {
   for (int64_t at = (int64_t)blockIdx.x * 256 + tid; at < slots; at += (int64_t)gridDim.x * 256) {
     const int e = a.experts[at];
     if (e >= 0) {
-      const int t = (int)(at / a.k);
-      // the unit whose run [T u / units, T (u + 1) / units) has the token
-      int u = (int)(((int64_t)t * a.units) / a.T);
-      while (u + 1 < a.units && (int64_t)a.T * (u + 1) / a.units <= t) ++u;
-      a.order[s_off[e] + a.cnt[(int64_t)u * (a.E + 1) + e] + a.rank[at]] = (int)at;
+      const int t = (int)(at / a.k), waves = a.groups * kWaves;
+      // the wave whose run has the token
+      int w = (int)(((int64_t)t * waves) / a.T);
+      while (w + 1 < waves && first_token(a, w + 1) <= t) ++w;
+      a.order[s_off[e] + a.cnt[(int64_t)(w / kWaves) * (a.E + 1) + e] + a.before[(int64_t)w * a.E + e] + a.rank[at]] = (int)at;
     }
     if (at >= s_total) a.order[at] = -1;
   }
@@ -354,8 +437,17 @@ struct GradArgs {
   int64_t ld_d;
 };
 
+// Orders the wave's own LDS accesses.
+__device__ __forceinline__ void wave_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 template <int V>
 __global__ __launch_bounds__(256) void k_route_grad(const GradArgs a) {
+  __shared__ float s_row[4][64 * V];
+  float* row = s_row[threadIdx.x >> 6];
   const int lane = threadIdx.x & 63;
   const int wave = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = gridDim.x * 4;
   const float up = a.d_loss ? a.d_loss[0] : 0.0f;
@@ -363,35 +455,43 @@ __global__ __launch_bounds__(256) void k_route_grad(const GradArgs a) {
 #pragma unroll
   for (int v = 0; v < V; ++v) slope[v] = a.d_loss && 64 * v + lane < a.r.E ? a.r.slope[64 * v + lane] * up : 0.0f;
   for (int64_t t = wave; t < a.r.T; t += waves) {
-    float out[V];
+    float out[V], x[V];
+    const uint32_t on = a.r.mask == nullptr ? 1 : a.r.mask[t];
+    load_token<V>(a.r, t, lane, x);
+    // lane j: slot j
+    int ej = -1;
+    float d = 0.0f, share = 0.0f;
+    if (a.d_shares && lane < a.r.k) {
+      ej = a.r.experts[t * a.r.k + lane];
+      d = a.d_shares[t * a.ld_ds + lane];
+      share = a.r.renorm ? a.r.shares[t * a.r.k + lane] : 0.0f;
+      if (ej < 0) d = share = 0.0f;
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) out[v] = 0.0f;
-    if (a.r.mask == nullptr || a.r.mask[t]) {
-      float x[V], p[V], g[V], sum;
-      softmax<V>(a.r, t, lane, x, p, sum);
+    if (on != 0) {
+      uint32_t key[V];
+      float p[V], g[V], sum;
+      softmax<V>(a.r, lane, x, key, p, sum);
       const float inv = 1.0f / sum;
 #pragma unroll
       for (int v = 0; v < V; ++v) p[v] *= inv, g[v] = slope[v];
       if (a.d_shares) {
-        const int e = lane < a.r.k ? a.r.experts[t * a.r.k + lane] : -1;
-        const float d = e >= 0 ? a.d_shares[t * a.ld_ds + lane] : 0.0f;
-        float q = d;
-        if (a.r.renorm) {
-          const float s = e >= 0 ? a.r.shares[t * a.r.k + lane] : 0.0f;
-          q = s * (d - dpp_sum(e >= 0 ? s * d : 0.0f));
-        }
-        for (int j = 0; j < a.r.k; ++j) {
-          const int ej = __builtin_amdgcn_readlane(e, j);
-          const float qj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(q), j));
+        const float q = a.r.renorm ? share * (d - dpp_sum(share * d)) : d;
+        // slot by slot to expert by expert, through the wave's own LDS
 #pragma unroll
-          for (int v = 0; v < V; ++v)
-            if (ej == 64 * v + lane) {
-              if (a.r.renorm)
-                out[v] = qj;
-              else
-                g[v] += qj;
-            }
+        for (int v = 0; v < V; ++v) row[64 * v + lane] = 0.0f;
+        wave_lds();
+        if (ej >= 0) row[ej] = q;
+        wave_lds();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (a.r.renorm)
+            out[v] = row[64 * v + lane];
+          else
+            g[v] += row[64 * v + lane];
         }
+        wave_lds();
       }
       float dot = 0.0f;
 #pragma unroll
@@ -413,7 +513,7 @@ __global__ __launch_bounds__(256) void k_route_grad(const GradArgs a) {
 }
 
 bool small(int64_t T, int64_t E, int64_t k) { return T <= kSmallTokens && T * k <= kSmallSlots && E <= kSmallExperts; }
-int64_t units_of(int64_t T) { return T < kUnits ? T : kUnits; }
+int64_t groups_of(int64_t T) { return T < kGroups * kWaves ? (T + kWaves - 1) / kWaves : kGroups; }
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 template <int V>
@@ -422,10 +522,10 @@ hipError_t launch_v(RouteArgs a, hipStream_t s) {
     if constexpr (V <= kSmallExperts / 64) hipLaunchKernelGGL(k_route_small<V>, dim3(1), dim3(64 * kSmallWaves), 0, s, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(k_route_tokens<V>, dim3((a.units + 3) / 4), dim3(256), 0, s, a);
-  hipLaunchKernelGGL(k_route_scan, dim3((a.E + 16) / 16), dim3(1024), 0, s, a);
-  const int64_t groups = ((int64_t)a.T * a.k + 255) / 256;
-  hipLaunchKernelGGL(k_route_order, dim3((unsigned)(groups < 1024 ? groups : 1024)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(k_route_tokens<V>, dim3(a.groups), dim3(64 * kWaves), 0, s, a);
+  hipLaunchKernelGGL(k_route_scan, dim3(a.E / 8 + 1), dim3(1024), 0, s, a);
+  const int64_t n = ((int64_t)a.T * a.k + 255) / 256;
+  hipLaunchKernelGGL(k_route_order, dim3((unsigned)(n < 1024 ? n : 1024)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -446,7 +546,7 @@ RouteArgs args_of(const MoeRoute& p) {
   a.k = (int)p.k;
   a.renorm = p.renorm;
   a.bf16 = p.bf16;
-  a.units = (int)units_of(p.T);
+  a.groups = (int)groups_of(p.T);
   a.experts = p.experts;
   a.shares = p.shares;
   a.counts = p.counts;
@@ -461,8 +561,8 @@ RouteArgs args_of(const MoeRoute& p) {
 
 int64_t moe_route_workspace_bytes(int64_t T, int64_t E, int64_t k) {
   if (small(T, E, k)) return 0;
-  const int64_t u = units_of(T);
-  return up256(4 * u * (E + 1)) + up256(4 * u * E) + up256(4 * T * k) + up256(4 * E) + 256;
+  const int64_t g = groups_of(T);
+  return up256(4 * g * (E + 1)) + up256(4 * g * E) + up256(4 * g * kWaves * E) + up256(4 * T * k) + up256(4 * E) + 256;
 }
 
 hipError_t launch_moe_route(const MoeRoute& p, hipStream_t s) {
@@ -470,9 +570,11 @@ hipError_t launch_moe_route(const MoeRoute& p, hipStream_t s) {
   if (!small(p.T, p.E, p.k)) {
     char* w = (char*)p.workspace;
     a.cnt = (int*)w;
-    w += up256(4 * (int64_t)a.units * (a.E + 1));
+    w += up256(4 * (int64_t)a.groups * (a.E + 1));
     a.psum = (float*)w;
-    w += up256(4 * (int64_t)a.units * a.E);
+    w += up256(4 * (int64_t)a.groups * a.E);
+    a.before = (int*)w;
+    w += up256(4 * (int64_t)a.groups * kWaves * a.E);
     a.rank = (int*)w;
     w += up256(4 * p.T * p.k);
     a.total = (float*)w;
