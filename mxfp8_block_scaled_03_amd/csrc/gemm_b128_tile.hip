@@ -172,6 +172,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_b128(const GemmB128 a) {
       }
     };
     half_step(0);
+    // (as in the exact kernels: without this the sums of the first half wait, multiplied twice each, in registers that
+    // spill; 4096 x 4096 x 4096 137 us, with it 76; with W's tiles they fit, and 120 us become 125)
+    if (WLINE && !EXACT) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) pin(acc[f]);
+    }
     // the second half of X of this step: all but the next step's nine
     wait_vm<9>();
     lds_barrier();
