@@ -59,7 +59,7 @@ GemmB128Plan gemm_b128_plan(const GemmB128& a, int cus) {
   // (W's scales by lines: a product more for each sum, 76 us instead of 63 and 131 instead of 113; experts' own
   // blocks differ in number, which large tiles show: 8192 rows over 4 experts, 4096 x 2048 exact 197 us, 128 x 128 156)
   const double step = a.exact ? (a.w_line ? 3.8 : 3.2) : a.w_line ? 2.15 : 2 * t256 <= cus ? 1.55 : 1.75;
-  offer(256, 256, 0, (5 + ceil(t256 / cus) * (nb * step + 2)) * (a.mode == kB128Blocks ? 1.2 : 1));
+  offer(256, 256, 0, (5 + ceil(t256 / cus) * (nb * step + 2)) * (a.mode == kB128Blocks && a.exact ? 1.2 : 1));
   return best;
 }
 

@@ -465,7 +465,7 @@ __global__ __launch_bounds__(256) void k_route_grad(const GradArgs a) {
       ej = a.r.experts[t * a.r.k + lane];
       d = a.d_shares[t * a.ld_ds + lane];
       share = a.r.renorm ? a.r.shares[t * a.r.k + lane] : 0.0f;
-      if (ej < 0) d = share = 0.0f;
+      if ((uint32_t)ej >= (uint32_t)a.r.E) ej = -1, d = share = 0.0f;   // (also what no forward pass writes)
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) out[v] = 0.0f;

@@ -138,60 +138,50 @@ def check(got, want, tol, what=""):
 
 
 def route(logits, k, renorm, mask=None, d_shares=None, d_loss=None):
-    """The router in 64 bits, token by token."""
+    """The router in 64 bits, from the definition; the gradient from one-hot rows of the choice."""
     T, E = logits.shape
     z = logits.double()
-    experts = torch.full((T, k), -1)
-    shares, p = torch.zeros((T, k), dtype=F64), torch.zeros((T, E), dtype=F64)
     live = torch.ones(T, dtype=torch.bool) if mask is None else mask.bool()
-    for t in range(T):
-        if not live[t]:
-            continue
-        nan = bool(torch.isnan(z[t]).any())
-        top = z[t].max()
-        if nan or not bool(top == float("-inf")):
-            e = torch.exp(z[t] - (float("nan") if nan else top))
-            p[t] = e / e.sum()
-        order = sorted(range(E), key=lambda i: (0 if torch.isnan(z[t, i]) else 1, 0.0 if torch.isnan(z[t, i]) else -float(z[t, i]), i))
-        taken = [i for i in order[:k] if not float(z[t, i]) == float("-inf")]
-        for j, i in enumerate(taken):
-            experts[t, j], shares[t, j] = i, p[t, i]
-        if renorm and taken:
-            shares[t] /= shares[t, :len(taken)].sum()
+    nan = torch.isnan(z).any(1)
+    none = (z == float("-inf")).all(1) | ~live
+    p = torch.exp(z - torch.where(none, 0.0, z.amax(1))[:, None])
+    p = torch.where(none[:, None], 0.0, p / p.sum(1, keepdim=True))
+    p = torch.where((nan & live)[:, None], float("nan"), p)
+    # NaN first, then falling, ties to the lower index (a stable sort keeps them)
+    rank = torch.where(torch.isnan(z), float("inf"), z)
+    order = torch.sort(rank + torch.zeros_like(rank), dim=1, descending=True, stable=True)[1]
+    if bool(nan.any()):
+        assert not bool((z == float("inf")).any()), "a NaN beside an infinity needs an order of its own"
+    ids = order[:, :k]
+    taken = live[:, None] & ~(torch.gather(z, 1, ids) == float("-inf"))
+    experts = torch.where(taken, ids, -1)
+    shares = torch.where(taken, torch.gather(p, 1, ids), 0.0)
+    if renorm:
+        total = shares.sum(1, keepdim=True)
+        shares = torch.where(taken, shares / torch.where(total == 0, 1.0, total), 0.0)
     flat = experts.flatten()
-    counts = torch.tensor([int((flat == e).sum()) for e in range(E)])
+    counts = torch.bincount(flat[flat >= 0], minlength=E)
     offsets = torch.cat((torch.zeros(1, dtype=torch.int64), counts.cumsum(0)))
-    order = torch.full((T * k,), -1)
+    slots = torch.full((T * k,), -1)
     n_slots = int(offsets[-1])
-    order[:n_slots] = torch.tensor([i for _, i in sorted((int(e), i) for i, e in enumerate(flat.tolist()) if e >= 0)],
-                                   dtype=torch.int64)
+    slots[:n_slots] = torch.sort(torch.where(flat < 0, E, flat), stable=True)[1][:n_slots]
     n = max(int(live.sum()), 1)
     slope = E * counts.double() / (n * k) / n
-    loss = (slope * p.sum(0)).sum()
-    out = {"experts": experts, "shares": shares, "counts": counts, "offsets": offsets, "order": order, "loss": loss,
-           "slope": slope, "p": p}
+    out = {"experts": experts, "shares": shares, "counts": counts, "offsets": offsets, "order": slots,
+           "loss": (slope * p.sum(0)).sum(), "slope": slope, "p": p}
     if d_shares is not None or d_loss is not None:
-        ds = torch.zeros((T, k), dtype=F64) if d_shares is None else d_shares.double()
+        ds = torch.where(taken, torch.zeros((T, k), dtype=F64) if d_shares is None else d_shares.double(), 0.0)
         g = (slope * (0.0 if d_loss is None else float(d_loss))).expand(T, E).clone()
         d = torch.zeros((T, E), dtype=F64)
-        for t in range(T):
-            if not live[t]:
-                continue
-            for j in range(k):
-                e = int(experts[t, j])
-                if e >= 0:
-                    if renorm:
-                        d[t, e] = shares[t, j] * (ds[t, j] - (shares[t] * ds[t]).nansum() if not torch.isnan(shares[t]).any()
-                                                  else float("nan"))
-                    else:
-                        g[t, e] += ds[t, j]
-            d[t] += p[t] * (g[t] - (p[t] * g[t]).sum())
-        out["d"] = d
-        # what the gradient is made of, for its bound
-        out["size"] = p * (g.abs() + (p * g.abs()).sum(1, keepdim=True)) + d.abs()
+        size = torch.zeros((T, E), dtype=F64)                 # what the gradient is made of, for its bound
+        at = torch.where(taken, ids, 0)
         if renorm:
-            for t in range(T):
-                for j in range(k):
-                    if int(experts[t, j]) >= 0:
-                        out["size"][t, int(experts[t, j])] += shares[t, j] * (ds[t, j].abs() + (shares[t] * ds[t].abs()).sum())
+            dot = (shares * ds).sum(1, keepdim=True)
+            d.scatter_add_(1, at, torch.where(taken, shares * (ds - dot), 0.0))
+            size.scatter_add_(1, at, shares * (ds.abs() + (shares * ds.abs()).sum(1, keepdim=True)))
+        else:
+            g.scatter_add_(1, at, ds)
+        d += p * (g - (p * g).sum(1, keepdim=True))
+        d = torch.where(live[:, None], d, 0.0)
+        out["d"], out["size"] = d, size + p * (g.abs() + (p * g.abs()).sum(1, keepdim=True))
     return out

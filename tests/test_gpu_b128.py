@@ -184,39 +184,59 @@ def test_product_epilogue(M, N, K, act):
         run_product(M, N, K, accum="fp32", out=out, alpha=-0.375, bias=True, act=act, seed=3)
 
 
-def big_tiles(M, N, K, accum, lines, out, fx="e4m3", fw="e4m3", y=None):
-    """A problem that takes the 256 x 256 kernel: every 17th row against the reference."""
-    assert mxq.mxq_gemm_b128_plan(0, M, N, K, 1, 1 if lines else 128, 0 if accum == "fp8" else 1, 256)[2] == 0
+# sizes that take each kernel of tiles, whole and ragged, two tiles a CU and one, and the tile of the 256 x 256 kernel that
+# is the last of its row and column
+TILED = [((64, 64, 0), (1280, 640, 1280)), ((64, 64, 0), (1300, 1090, 300)), ((64, 64, 0), (2570, 700, 129)),
+         ((128, 128, 0), (2048, 2048, 1280)), ((128, 128, 0), (1900, 2100, 900)), ((128, 128, 0), (3000, 3000, 640)),
+         ((256, 256, 0), (4000, 4090, 1300)), ((256, 256, 0), (4090, 4001, 1700))]
+
+
+def tiled(M, N, K, accum, lines, out, fx="e4m3", fw="e4m3"):
+    """A large problem: every 17th row and 13th column, and the last ones, against the reference."""
     x, w = wide(M, K, BF16, 21).to(DEV), wide(N, K, BF16, 22).to(DEV)
     xc, xs = mxq.quantize_b128(x, fx)
     wc, ws = mxq.quantize_b128(w, fw, "row" if lines else "tile")
-    got = mxq.gemm_b128(xc, xs, wc, ws, K, fx, fw, accum=accum, out_dtype=out, out=y)
-    rows = sorted(set(range(0, M, 17)) | {M - 1})
-    pick = torch.tensor(rows, device=DEV)
+    got = mxq.gemm_b128(xc, xs, wc, ws, K, fx, fw, accum=accum, out_dtype=out)
+    rows = torch.tensor(sorted(set(range(0, M, 17)) | set(range(max(0, M - 20), M))))
     cols = torch.tensor(sorted(set(range(0, N, 13)) | set(range(max(0, N - 20), N))))
-    wcc = wc.cpu()
-    wsc = ws.cpu().repeat_interleave(128, 0)[:N] if not lines else ws.cpu()
-    want, tol = ref.product(xc[pick].cpu(), xs[pick].cpu(), fx, wcc[cols], wsc[cols], fw, accum, out=out)
-    ref.check(got[pick].cpu()[:, cols], want, tol, "%dx%dx%d %s" % (M, N, K, accum))
-    return got
+    wsl = ws.cpu() if lines else ws.cpu().repeat_interleave(128, 0)[:N]
+    want, tol = ref.product(xc.cpu()[rows], xs.cpu()[rows], fx, wc.cpu()[cols], wsl[cols], fw, accum, out=out)
+    ref.check(got.cpu()[rows][:, cols], want, tol, "%dx%dx%d %s" % (M, N, K, accum))
 
 
 @pytest.mark.parametrize("lines", [False, True])
 @pytest.mark.parametrize("accum", ["fp32", "fp8"])
-@pytest.mark.parametrize("M,N,K", [(2560, 2816, 128), (2561, 2900, 900), (3000, 2603, 260), (2816, 2560, 1280)])
-def test_product_big_tiles(M, N, K, accum, lines):
-    big_tiles(M, N, K, accum, lines, F32)
-    big_tiles(M, N, K, accum, lines, BF16)
+@pytest.mark.parametrize("tile,size", TILED)
+def test_product_tiled(tile, size, accum, lines):
+    M, N, K = size
+    assert mxq.mxq_gemm_b128_plan(0, M, N, K, 1, 1 if lines else 128, 0 if accum == "fp8" else 1, 256) == tile
+    tiled(M, N, K, accum, lines, F32)
+    tiled(M, N, K, accum, lines, BF16)
 
 
-def test_product_big_tiles_formats():
+@pytest.mark.parametrize("M,N,K", [(700, 900, 200), (1900, 2100, 200), (4001, 4003, 1300)])
+def test_product_tiled_formats(M, N, K):
     for fx, fw in (("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")):
         for accum in ("fp32", "fp8"):
-            big_tiles(2600, 2700, 200, accum, True, F32, fx, fw)
+            for lines in (False, True):
+                tiled(M, N, K, accum, lines, F32, fx, fw)
+
+
+def test_product_tiled_epilogue():
+    """Bias, alpha and SiLU in every kernel, columns that end inside a group of four."""
+    for M, N, K in ((20, 203, 200), (120, 803, 1000), (640, 1201, 200), (4001, 4003, 200), (4001, 4003, 1300)):
+        for act in (None, "silu"):
+            xc, xs = mxq.quantize_b128(wide(M, K, BF16, 1, False).to(DEV))
+            wc, ws = mxq.quantize_b128(wide(N, K, BF16, 2, False).to(DEV))
+            b = torch.randn(N, generator=torch.Generator().manual_seed(3))
+            got = mxq.gemm_b128(xc, xs, wc, ws, K, alpha=0.625, bias=b.to(DEV), act=act, out_dtype=F32)
+            rows = torch.arange(0, M, 1 + M // 60)
+            want, tol = ref.product(xc.cpu()[rows], xs.cpu()[rows], "e4m3", wc.cpu(), ws.cpu(), "e4m3", "fp32", 0.625, b, act)
+            ref.check(got.cpu()[rows], want, tol, "%dx%d %s" % (M, N, act))
 
 
 def test_product_into_strided_output_leaves_the_rest():
-    for M, N, K in ((5, 33, 256), (100, 100, 256), (2570, 2600, 256)):
+    for M, N, K in ((5, 33, 256), (100, 100, 256), (640, 1203, 256), (4001, 4003, 256), (4001, 4003, 1300)):
         for dtype in (F32, BF16):
             for pad in (3, 8):
                 whole = torch.full((M + 2, N + pad), 7.0, dtype=dtype, device=DEV)
@@ -302,31 +322,41 @@ def test_experts(sizes, accum, lines):
         experts_case(sizes, 100, 300, 3, accum, out, lines)
 
 
+# the kernels that rows of experts may take: their numbers of rows, columns and plan
+EXPERT_TILES = [((16, 64, 1), [2, 0, 17, 1] + [1] * 6 + [0] * 10, 4200, 384), ((64, 64, 0), [300, 0, 1, 70, 64, 65], 900, 384),
+                ((128, 128, 0), [700, 0, 1, 1300], 4100, 640), ((256, 256, 0), [1300, 0, 2500], 3000, 1280)]
+
+
 @pytest.mark.parametrize("accum", ["fp32", "fp8"])
-def test_experts_big_tiles(accum):
-    sizes = [300, 0, 1, 700, 256, 513]
-    E, N, K, R = len(sizes), 5000, 384, sum(sizes) + 11
-    assert mxq.mxq_gemm_b128_plan(1, R, N, K, E, 128, 1 if accum == "fp32" else 0, 256)[2] == 0
+@pytest.mark.parametrize("lines", [False, True])
+@pytest.mark.parametrize("tile,sizes,N,K", EXPERT_TILES)
+def test_experts_tiled(tile, sizes, N, K, lines, accum):
+    E, R = len(sizes), sum(sizes) + 11
+    assert mxq.mxq_gemm_b128_plan(1, R, N, K, E, 1 if lines else 128, 0 if accum == "fp8" else 1, 256) == tile
     xc, xs = mxq.quantize_b128(wide(R, K, BF16, 3).to(DEV))
     wc, ws = mxq.quantize_b128(wide(E * N, K, BF16, 4).to(DEV), axis="row")
     wc, ws = wc.view(E, N, -1), ws.t().contiguous().view(-1, E, N).permute(1, 2, 0)
+    wl = ws
+    if not lines:       # (any scales may be a tile's)
+        ws = torch.exp2(torch.randint(-12, -4, (E, ref.blocks(N), ref.blocks(K)), device=DEV).float()) * 1.25
+        wl = ws.repeat_interleave(128, 1)[:, :N]
     offsets = torch.tensor([0] + sizes).cumsum(0).int().to(DEV)
     y = torch.full((R, N), 5.0, device=DEV)
     mxq.moe_gemm_b128(xc, xs, wc, ws, offsets, K, out=y, accum=accum)
     first = 0
     for e, n in enumerate(sizes):
-        rows = torch.arange(first, first + n, 7, device=DEV)
-        cols = torch.arange(e, N, 23, device=DEV)
+        rows = torch.tensor(sorted(set(range(first, first + n, 7)) | set(range(first + max(0, n - 3), first + n))), dtype=torch.int64)
+        cols = torch.tensor(sorted(set(range(e, N, 23)) | {N - 1}))
         if n:
-            want, tol = ref.product(xc[rows].cpu(), xs[rows].cpu(), "e4m3", wc[e][cols].cpu(), ws[e][cols].cpu(), "e4m3", accum)
-            ref.check(y[rows][:, cols], want, tol, "expert %d" % e)
+            want, tol = ref.product(xc.cpu()[rows], xs.cpu()[rows], "e4m3", wc[e].cpu()[cols], wl[e].cpu()[cols], "e4m3", accum)
+            ref.check(y.cpu()[rows][:, cols], want, tol, "expert %d" % e)
         first += n
     assert bool((y[first:] == 5.0).all())
 
 
 @pytest.mark.parametrize("accum", ["fp32", "fp8"])
-@pytest.mark.parametrize("N,K", [(20, 30), (300, 70), (2600, 2500)])
-@pytest.mark.parametrize("sizes", [[40], [0, 130, 1, 0, 257], [128, 0, 128]])
+@pytest.mark.parametrize("N,K", [(20, 30), (300, 70), (600, 900), (2600, 2500)])
+@pytest.mark.parametrize("sizes", [[40], [0, 130, 1, 0, 257], [128, 0, 128], [1000, 0, 3]])
 def test_expert_weight_gradients(sizes, N, K, accum):
     E, R = len(sizes), sum(sizes) + 5
     dy, x = wide(R, N, BF16, 6, False), wide(R, K, BF16, 7, False)
@@ -404,3 +434,95 @@ def test_results_do_not_change_from_run_to_run():
     y = mxq.gemm_b128(xc, xs, wc, ws, K, out_dtype=F32)
     for _ in range(5):
         assert torch.equal(mxq.gemm_b128(xc, xs, wc, ws, K, out_dtype=F32), y)
+
+
+def test_subnormal_and_extreme_codes():
+    """Every finite code against every finite code, exactly: one product each in a block of its own."""
+    for fx, fw in (("e4m3", "e4m3"), ("e5m2", "e5m2"), ("e4m3", "e5m2")):
+        tx, tw = ref.decode_table(fx), ref.decode_table(fw)
+        cx, cw = [torch.arange(256)[torch.isfinite(t)].to(torch.uint8) for t in (tx, tw)]
+        x = torch.zeros((len(cx), 128), dtype=torch.uint8)
+        w = torch.zeros((len(cw), 128), dtype=torch.uint8)
+        x[:, 5], w[:, 5] = cx, cw
+        one = [torch.ones((len(c), 1), device=DEV) for c in (cx, cw)]
+        want = tx[cx.long()][:, None] * tw[cw.long()][None]
+        for accum in ("fp32", "fp8"):
+            got = mxq.gemm_b128(x.to(DEV), one[0], w.to(DEV), one[1], 128, fx, fw, accum=accum, out_dtype=F32)
+            assert torch.equal(got.cpu().double(), want), (fx, fw, accum)
+            big = [t.to(DEV).repeat(12, 1) for t in (x, w)]
+            ones = [torch.ones((t.shape[0], 1), device=DEV) for t in big]
+            got = mxq.gemm_b128(big[0], ones[0], big[1], ones[1], 128, fx, fw, accum=accum, out_dtype=F32)
+            assert torch.equal(got.cpu().double(), want.repeat(12, 12)), (fx, fw, accum)
+
+
+def test_nan_codes():
+    """A NaN code under a finite scale makes its row and column NaN, in both modes and every kernel."""
+    for M, N in ((3, 40), (100, 80), (700, 900), (4001, 4003)):
+        for accum in ("fp32", "fp8"):
+            x, w = torch.full((M, 128), 0x38, dtype=torch.uint8), torch.full((N, 128), 0x38, dtype=torch.uint8)
+            x[2, 77], w[N - 1, 0] = 0x7F, 0xFF
+            y = mxq.gemm_b128(x.to(DEV), torch.ones((M, 1), device=DEV), w.to(DEV), torch.ones((N, 1), device=DEV), 128,
+                              accum=accum, out_dtype=F32).cpu()
+            nan = torch.zeros((M, N), dtype=torch.bool)
+            nan[2], nan[:, N - 1] = True, True
+            assert torch.equal(torch.isnan(y), nan) and bool((y[~nan] == 128.0).all())
+
+
+def test_rows_past_32_bit_offsets():
+    """Codes and outputs whose byte offsets pass 2^32."""
+    M, K, N = 70000, 65536, 40
+    codes = torch.zeros((M, K), dtype=torch.uint8, device=DEV)
+    codes[-3:] = torch.randint(1, 100, (3, K), device=DEV).to(torch.uint8)
+    scales = torch.ones((K // 128, M), device=DEV).t()
+    w, ws = mxq.quantize_b128(wide(N, K, BF16, 1, False).to(DEV))
+    y = mxq.gemm_b128(codes, scales, w, ws, K, out_dtype=F32)
+    few = mxq.gemm_b128(codes[-3:].clone(), scales[-3:].t().contiguous().t(), w, ws, K, out_dtype=F32)
+    want, tol = ref.product(codes[-3:].cpu(), scales[-3:].cpu(), "e4m3", w.cpu(), ws.cpu(), "e4m3", "fp32")
+    ref.check(y[-3:], want, tol, "last rows")
+    ref.check(few, want, tol, "the same alone")
+    assert bool((y[:-3] == 0).all())
+    del codes, y
+    x = torch.zeros((70000, 32768), dtype=BF16, device=DEV)        # 4.6e9 bytes
+    x[-1] = wide(1, 32768, BF16, 2, False)[0].to(DEV)
+    rc, rs, cc, cs = mxq.quantize_b128_dual(x)
+    c, s = ref.quantize(x[-1:].cpu(), "e4m3")
+    same(rc[-1:], rs[-1:], (c, s), "last row")
+    assert bool((rc[:-1] == 0).all()) and bool((rs[:-1] == 1).all())
+    amax = x[-1].float().abs().cpu().double()
+    assert torch.equal(cs[:, -1].cpu().double(), torch.where(amax == 0, 1.0, (amax / 448).float().double()))
+
+
+def test_broadcast_and_strided_operands():
+    """Scales of one tile for all, weights of one expert for all, rows of a wider array."""
+    M, N, K, E = 60, 70, 260, 3
+    xw, xs = mxq.quantize_b128(wide(M, K, BF16, 1).to(DEV))
+    wide_codes = torch.zeros((M, 640), dtype=torch.uint8, device=DEV)
+    wide_codes[:, :384] = xw
+    wc, ws = mxq.quantize_b128(wide(N, K, BF16, 2).to(DEV))
+    one = torch.full((1, 1), 0.5, device=DEV).expand(1, 3)
+    got = mxq.gemm_b128(wide_codes, xs, wc, one, K, out_dtype=F32)
+    want, tol = ref.product(xw.cpu(), xs.cpu(), "e4m3", wc.cpu(), torch.full((N, 3), 0.5), "e4m3", "fp32")
+    ref.check(got, want, tol, "one scale for all")
+    offsets = torch.tensor([0, 10, 40, 60], dtype=torch.int32, device=DEV)
+    y = mxq.moe_gemm_b128(wide_codes, xs, wc.expand(E, N, -1), ws.expand(E, N, 3), offsets, K, out_dtype=F32)
+    want, tol = ref.product(xw.cpu(), xs.cpu(), "e4m3", wc.cpu(), ws.cpu(), "e4m3", "fp32")
+    ref.check(y, want, tol, "one expert for all")
+
+
+def test_two_streams_at_once():
+    """The same operands on two streams, call beside call."""
+    M, N, K, E = 500, 600, 700, 4
+    xc, xs = mxq.quantize_b128(wide(M, K, BF16, 1).to(DEV))
+    wc, ws = mxq.quantize_b128(wide(E * N, K, BF16, 2).to(DEV))
+    wc, ws = wc.view(E, N, -1), ws.t().contiguous().view(-1, E, N).permute(1, 2, 0)
+    offsets = torch.tensor([0, 100, 130, 131, 500], dtype=torch.int32, device=DEV)
+    want = mxq.moe_gemm_b128(xc, xs, wc, ws, offsets, K), mxq.gemm_b128(xc, xs, wc[1], ws[1], K)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append((mxq.moe_gemm_b128(xc, xs, wc, ws, offsets, K), mxq.gemm_b128(xc, xs, wc[1], ws[1], K)))
+    torch.cuda.synchronize()
+    for g in got:
+        assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
