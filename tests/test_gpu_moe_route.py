@@ -100,6 +100,38 @@ def test_route_nan():
         assert bool(torch.isnan(d[4:6]).all()) and not bool(torch.isnan(d[keep]).any())
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), torch.finfo(F32).min])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_padding_of_any_value(renorm, bad):
+    """What a padded token holds, logits and incoming gradients, changes nothing, and its own gradients are zero."""
+    for T in (40, 700):
+        z, mask = logits_of(T, 48, F32, 6), torch.arange(T) % 3 != 1
+        clean, filled = z.to(DEV), z.clone()
+        filled[~mask] = bad
+        filled = filled.to(DEV)
+        m, up = mask.to(DEV), torch.ones(1, device=DEV)
+        want, got = (mxq.moe_route(x, 5, renormalize=renorm, mask=m) for x in (clean, filled))
+        for name in want._fields:
+            assert torch.equal(getattr(got, name), getattr(want, name)), name
+        ds = torch.randn((T, 5), device=DEV)
+        d = mxq.moe_route_grad(clean, want, ds, up, renormalize=renorm, mask=m)
+        ds[~m] = bad
+        assert torch.equal(mxq.moe_route_grad(filled, got, ds, up, renormalize=renorm, mask=m), d)
+        assert bool((d[~m] == 0).all()) and bool((d[m] != 0).any())
+
+
+def test_route_slots_of_no_expert_pass_nothing_back():
+    """Incoming gradients of slots without an expert are not read into the token's own."""
+    z = logits_of(90, 20, F32, 7, masked=0.85).to(DEV)
+    for renorm in (True, False):
+        r = mxq.moe_route(z, 6, renormalize=renorm)
+        assert bool((r.experts < 0).any())
+        ds = torch.randn((90, 6), device=DEV)
+        d = mxq.moe_route_grad(z, r, ds, renormalize=renorm)
+        ds[r.experts < 0] = float("nan")
+        assert torch.equal(mxq.moe_route_grad(z, r, ds, renormalize=renorm), d)
+
+
 def test_route_no_tokens():
     r = mxq.moe_route(torch.empty((0, 6), device=DEV), 2)
     assert r.counts.tolist() == [0] * 6 and r.offsets.tolist() == [0] * 7 and r.loss.item() == 0 and r.slope.tolist() == [0] * 6
