@@ -17,6 +17,7 @@ namespace mxq {
 namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef int v4i_any __attribute__((ext_vector_type(4), aligned(1)));
 
 // What a workgroup multiplies: lines of X and W from the tile's first on, `nb` blocks of K, and where Y goes.
 struct B128Tile {
@@ -148,8 +149,8 @@ __device__ __forceinline__ void pin(v4f (&a)[N]) {
 // The epilogue of a wave that holds 16 FM x 16 FN outputs: lane (i, g) has Y[row0 + 16 f + i][col0 + 16 j + 4 g + r]
 // of the tile in acc[f][j][r].  act(alpha v + bias), then rows of 16 FN values through REGION bytes of LDS of the
 // wave's own, 16-byte piece c of row r at c ^ (r & 7), and out in 16-byte pieces, value by value in the last
-// columns.
-template <int E, int FM, int FN, int REGION>
+// columns.  PAST: past the caches.
+template <int E, bool PAST, int FM, int FN, int REGION>
 __device__ __forceinline__ void store_rows(const GemmB128& a, const B128Tile& t, const v4f (&acc)[FM][FN], int wid, int lane,
                                            int row0, int col0) {
   constexpr int RB = 16 * FN * E, CPR = RB / 16, RP = REGION / RB < 16 * FM ? REGION / RB : 16 * FM, FPP = RP / 16;
@@ -185,7 +186,11 @@ __device__ __forceinline__ void store_rows(const GemmB128& a, const B128Tile& t,
       if (m >= t.m) continue;
       uint8_t* dst = reinterpret_cast<uint8_t*>(a.y) + (t.y + (int64_t)m * a.ld_y + col0) * E + 16 * c;
       if (left >= 16 / E) {
-        __builtin_memcpy(dst, &v, 16);     // one store, whatever y's alignment
+        v4i_any* out = reinterpret_cast<v4i_any*>(dst);     // one store, whatever y's alignment
+        if (PAST)
+          __builtin_nontemporal_store((v4i_any)v, out);
+        else
+          *out = v;
       } else {
 #pragma unroll
         for (int q = 0; q < 16 / E; ++q)
@@ -219,10 +224,17 @@ __device__ __forceinline__ void epilogue(const GemmB128& a, const B128Tile& t, v
       for (int f = 0; f < FM; ++f) acc[f][j][r] = finish(acc[f][j][r], a.alpha, bv, a.act);
     }
   }
-  if (a.y_bf16)
-    store_rows<2, FM, FN, REGION>(a, t, acc, wid, lane, row0, col0);
-  else
-    store_rows<4, FM, FN, REGION>(a, t, acc, wid, lane, row0, col0);
+  if (a.past_caches) {
+    if (a.y_bf16)
+      store_rows<2, true, FM, FN, REGION>(a, t, acc, wid, lane, row0, col0);
+    else
+      store_rows<4, true, FM, FN, REGION>(a, t, acc, wid, lane, row0, col0);
+  } else {
+    if (a.y_bf16)
+      store_rows<2, false, FM, FN, REGION>(a, t, acc, wid, lane, row0, col0);
+    else
+      store_rows<4, false, FM, FN, REGION>(a, t, acc, wid, lane, row0, col0);
+  }
 }
 
 }  // namespace

@@ -185,6 +185,7 @@ struct GemmB128 {
   void* y;
   int y_bf16;
   int64_t ld_y, st_y;
+  int past_caches;             // y is written past the caches
 };
 // The most tiles of tm x tn outputs that the problem may have.
 int64_t gemm_b128_tiles(const GemmB128& a, int tm, int tn);

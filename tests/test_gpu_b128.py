@@ -259,6 +259,26 @@ def test_product_no_blocks():
     assert bool((mxq.gemm_b128(z, xs, w, ws, 0, out_dtype=F32) == 0).all())
 
 
+def test_experts_without_rows_or_blocks():
+    """No rows: nothing is written, and weight gradients are zero; no blocks along K: zeros."""
+    off = torch.tensor([0, 2, 2, 5], dtype=torch.int32, device=DEV)
+    y = torch.full((7, 40), 5.0, device=DEV)
+    for accum in ("fp32", "fp8"):
+        y.fill_(5.0)
+        mxq.moe_gemm_b128(torch.empty((7, 0), dtype=torch.uint8, device=DEV), torch.empty((7, 0), device=DEV),
+                          torch.empty((3, 40, 0), dtype=torch.uint8, device=DEV), torch.empty((3, 1, 0), device=DEV),
+                          off, 0, out=y, accum=accum)
+        assert bool((y[:5] == 0).all()) and bool((y[5:] == 5.0).all())
+        z, none = torch.empty((0, 130), device=DEV), torch.zeros(4, dtype=torch.int32, device=DEV)
+        c, s = mxq.quantize_b128(z)
+        wc = torch.zeros((3, 40, 256), dtype=torch.uint8, device=DEV)
+        assert mxq.moe_gemm_b128(c, s, wc, torch.ones((3, 1, 2), device=DEV), none, 130, accum=accum).shape == (0, 40)
+        gc, gs = mxq.quantize_b128(torch.empty((0, 40), device=DEV), "e5m2", "col", offsets=none)
+        c, s = mxq.quantize_b128(z, "e4m3", "col", offsets=none)
+        dw = mxq.moe_wgrad_b128(gc, gs, c, s, none, out=torch.full((3, 40, 130), 5.0, device=DEV), accum=accum)
+        assert bool((dw == 0).all())
+
+
 def test_product_nan_scale():
     """A block whose scale is NaN makes its row (of X) or its columns (of W) NaN and nothing else."""
     for M, N in ((4, 300), (300, 300)):
@@ -375,6 +395,39 @@ def test_expert_weight_gradients(sizes, N, K, accum):
                                     out=out)
             ref.check(got[e].cpu()[pick_n][:, pick_k], want, tol, "expert %d of %d rows" % (e, n))
             block += nb
+
+
+# the kernels that the experts' weight gradients may take; the later ones' outputs in fp32 are past 128 MiB
+GRAD_TILES = [((64, 64, 0), [100, 0, 70, 300], 512, 500), ((128, 128, 0), [30, 0, 129] + [1] * 7, 1999, 2003),
+              ((256, 256, 0), [4000, 5000, 0, 6000], 8001, 2041)]
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("tile,sizes,N,K", GRAD_TILES)
+def test_expert_weight_gradients_tiled(tile, sizes, N, K, accum, out):
+    """Every kernel, into an output of odd pitch: every expert's values, and nothing beside them."""
+    E, R = len(sizes), sum(sizes) + 5
+    assert mxq.mxq_gemm_b128_plan(2, N, K, R, E, 1, 0 if accum == "fp8" else 1, 256) == tile
+    dy, x = torch.randn((R, N), device=DEV, dtype=BF16), torch.randn((R, K), device=DEV, dtype=BF16)
+    offsets = torch.tensor([0] + sizes).cumsum(0).int().to(DEV)
+    dc, ds = mxq.quantize_b128(dy, "e5m2", "col", offsets=offsets)
+    xc, xs = mxq.quantize_b128(x, "e4m3", "col", offsets=offsets)
+    whole = torch.full((E, N + 1, K + 3), 5.0, dtype=out, device=DEV)
+    got = mxq.moe_wgrad_b128(dc, ds, xc, xs, offsets, out=whole[:, :N, :K], accum=accum)
+    pick_n = torch.tensor(sorted(set(range(0, N, 1 + N // 60)) | {N - 1}))
+    pick_k = torch.tensor(sorted(set(range(0, K, 1 + K // 60)) | {K - 1}))
+    block = 0
+    for e, n in enumerate(sizes):
+        nb = ref.blocks(n)
+        part = [t.cpu() for t in (dc[:, 128 * block:128 * (block + nb)], ds[:, block:block + nb],
+                                  xc[:, 128 * block:128 * (block + nb)], xs[:, block:block + nb])]
+        want, tol = ref.product(part[0][pick_n], part[1][pick_n], "e5m2", part[2][pick_k], part[3][pick_k], "e4m3", accum, out=out)
+        ref.check(got[e].cpu()[pick_n][:, pick_k], want, tol, "expert %d of %d rows" % (e, n))
+        block += nb
+    assert bool((whole[:, N:] == 5.0).all()) and bool((whole[:, :, K:] == 5.0).all())
+    dense = torch.empty((E, N, K), dtype=out, device=DEV)
+    assert torch.equal(mxq.moe_wgrad_b128(dc, ds, xc, xs, offsets, out=dense, accum=accum), got)
 
 
 def test_wrong_offsets_stay_inside():
