@@ -146,14 +146,27 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& a, Shared<COL>& s
   const int64_t col = (int64_t)bc * kB + 8 * c;
   const int cols = WHOLE ? 8 : (int)min((int64_t)8, a.cols - col);   // of this thread's eight, 0 or less past the end
   Values<BF16, Q> v;
+  if (WHOLE || cols >= 8) {
+    // (two or one 16-byte loads, whatever the alignment; rows past the last ask for it again, without a branch: 8192 x
+    // 4096 of 16 experts of any lengths, both orientations, 38.6 us value by value, 28.0 so, 25.8
+    // without experts; 64 experts 57.5 and 30.6; 4095 x 4001 fp32 by tiles 21.3 and 16.5)
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    const int r = Q * rg + q;
-    const int64_t at = (row0 + r) * a.ld + col;
-    if (WHOLE) {
-      // (two or one 16-byte loads, whatever the alignment)
+    for (int q = 0; q < Q; ++q) {
+      const int r = Q * rg + q;
+      const int64_t at = (row0 + (WHOLE ? r : min(r, rows - 1))) * a.ld + col;
       __builtin_memcpy(v.w[q], reinterpret_cast<const uint8_t*>(a.src) + at * (BF16 ? 2 : 4), sizeof v.w[q]);
-    } else {
+    }
+    if (!WHOLE) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int e = 0; e < (BF16 ? 4 : 8); ++e) v.w[q][e] = Q * rg + q < rows ? v.w[q][e] : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int r = Q * rg + q;
+      const int64_t at = (row0 + r) * a.ld + col;
 #pragma unroll
       for (int e = 0; e < (BF16 ? 4 : 8); ++e) v.w[q][e] = 0;
 #pragma unroll
