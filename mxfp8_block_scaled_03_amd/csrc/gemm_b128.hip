@@ -21,7 +21,7 @@ int64_t gemm_b128_tiles(const GemmB128& a, int tm, int tn) {
 // calls, other weights each; the estimates are within some 10 % of what they were fitted to):
 //   small tiles  1.8 and, in rounds of a tile for each CU, 1.1 and 33 KB of both sides' lines a us (16 x 4096 x 4096
 //                7.0 us by 16 x 16 and 11.0 by 64 x 32; 128 rows 31.9 and 15.3)
-//   64 x 64      4 and 0.34 a block (exact 0.47) for one tile a CU, 0.55 (0.83) for two
+//   64 x 64      4 and 0.34 a block (exact 0.4, after a round of two 0.47) for one tile a CU, 0.55 (0.83) for two
 //                (512 x 4096 x 4096 22.8 fp8, 128 x 128 25.1; exact 28.7 and 39.5)
 //   128 x 128    5 and 0.66 (1.1) for one tile a CU, 1.2 (2.06) for two (1024 rows 27, 256 x 256 55; exact 42 and 109)
 //                (experts: 2048 rows of 64 x 4096 x 2048 114, 64 x 64 117, 256 x 256 138)
@@ -59,7 +59,8 @@ GemmB128Plan gemm_b128_plan(const GemmB128& a, int cus) {
     return whole * two + (rest > cus ? two : rest > 0 ? one : 0);
   };
   auto out = [&](double n, double us) { return grads ? ceil(n / (2 * cus)) * us : 0; };
-  offer(64, 64, 0, 4 + nb * (a.exact ? pairs(t64, 0.47, 0.83) : pairs(t64, 0.34, 0.55)) + out(t64, a.exact ? 0.9 : 1.2));
+  const double one64 = !a.exact ? 0.34 : t64 <= cus ? 0.4 : 0.47;
+  offer(64, 64, 0, 4 + nb * pairs(t64, one64, a.exact ? 0.83 : 0.55) + out(t64, a.exact ? 0.9 : 1.2));
   offer(128, 128, 0, 5 + nb * (a.exact ? pairs(t128, 1.1, 2.06) : pairs(t128, 0.66, 1.2)) + out(t128, a.exact ? 4.0 : 4.7));
   // (W's scales by lines: a product more for each sum, 76 us instead of 63 and 131 instead of 113; experts' own blocks
   // differ in number, which a round or two of large tiles show: 16384 rows over 8 experts, exact fp32, 2048 x 1024

@@ -1,8 +1,8 @@
 // gemm_b128_mid.hip -- the product in blocks of 128 by tiles of 64 x 64 and 128 x 128, where 256 x 256 would leave the
 // card empty.
 //
-// WM x WN waves share a tile; a step is one block of K, and S steps' codes lie in LDS, so that the loads of a
-// step have S - U steps to arrive.  Lines, pieces, fragments and sums as in gemm_b128_tile.hip; a step is short, so
+// WM x WN waves share a tile (KS = 2: twice, every other step for each half, whose sums meet in LDS); a step is one
+// block of K, and S steps' codes lie in LDS, so that the loads of a step have S - U steps to arrive.  Lines, pieces, fragments and sums as in gemm_b128_tile.hip; a step is short, so
 // rounds of U steps have one barrier: the one that says that a round's codes are there also says that nobody
 // reads the round before it any more, whose place is filled next.
 #include "gemm_b128.hpp"
@@ -10,23 +10,24 @@
 namespace mxq {
 namespace {
 
-template <int TM, int TN, int WM, int WN, int S, int U>
+template <int TM, int TN, int WM, int WN, int KS, int S, int U>
 struct Mid {
-  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int kWaves = WM * WN * KS, kThreads = 64 * kWaves;
   static constexpr int kX = TM * kB, kStage = (TM + TN) * kB;
   static constexpr int kOffScale = S * kStage, kScaleSlot = 4 * (TM + TN);
   static constexpr int kLds = kOffScale + S * kScaleSlot;
   static constexpr int kLoadsX = TM / 8 / kWaves, kLoadsW = TN / 8 / kWaves;      // instructions a wave and step
   static constexpr int kLoads = kLoadsX + kLoadsW + 1;
   static constexpr int FM = TM / WM / 16, FN = TN / WN / 16;
-  static constexpr int kRegion = kOffScale / kWaves;
-  static_assert(S % U == 0 && S >= 2 * U, "rounds of U steps");
+  static constexpr int kRegion = kOffScale / (WM * WN);
+  static_assert(S % U == 0 && S >= 2 * U && U % KS == 0, "rounds of U steps, of U / KS for each wave");
+  static_assert(KS <= 2 && 1024 * FM * FN <= kRegion, "the second waves' sums");
   static_assert((TM + TN) / 64 <= kWaves, "a wave for each 64 scales");
 };
 
-template <int FX, int FW, bool EXACT, bool WLINE, int TM, int TN, int WM, int WN, int S, int U>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm_b128_mid(const GemmB128 a) {
-  using C = Mid<TM, TN, WM, WN, S, U>;
+template <int FX, int FW, bool EXACT, bool WLINE, int TM, int TN, int WM, int WN, int KS, int S, int U>
+__global__ __launch_bounds__(64 * WM * WN * KS, 2) void k_gemm_b128_mid(const GemmB128 a) {
+  using C = Mid<TM, TN, WM, WN, KS, S, U>;
   constexpr int FM = C::FM, FN = C::FN;
   const B128Tile t = b128_tile<TM, TN, WLINE>(a, workgroup_at(blockIdx.x, blockIdx.y));
   if (!t.any) return;
@@ -75,7 +76,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm_b128_mid(const GemmB12
     }
   };
 
-  const int m0 = 16 * FM * (wid / WN), n0 = 16 * FN * (wid % WN);
+  const int part = wid / (WM * WN), m0 = 16 * FM * (wid / WN % WM), n0 = 16 * FN * (wid % WN);
   const uint32_t frag = (uint32_t)i * kB + (uint32_t)((g ^ (i >> 1)) << 4);
   const uint32_t rx = (uint32_t)m0 * kB + frag, rw = C::kX + (uint32_t)n0 * kB + frag;
   const uint32_t rsx = C::kOffScale + 4u * (uint32_t)(m0 + i);
@@ -104,8 +105,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm_b128_mid(const GemmB12
 #pragma unroll
     for (int u = 0; u < U; ++u) issue(s0 + S - U + u, (first == 0 ? S : first) - U + u);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int slot = first + u;
+    for (int u = 0; u < U; u += KS) {
+      const int slot = first + u + part;
       const uint32_t so = (uint32_t)slot * C::kStage, ss = (uint32_t)slot * C::kScaleSlot;
       v8i w[FN];
       Wide ww[FN];
@@ -151,14 +152,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm_b128_mid(const GemmB12
   }
   wait_vm<0>();
   lds_barrier();
+  if (KS == 2) {
+    // the second waves' sums to the first, through what will be those's own staging
+    v4f* const sums = reinterpret_cast<v4f*>(smem + C::kRegion * (wid - part * WM * WN)) + lane;
+    if (part != 0) {
+#pragma unroll
+      for (int f = 0; f < FM; ++f)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) sums[64 * (f * FN + j)] = acc[f][j];
+    }
+    lds_barrier();
+    if (part != 0) return;
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[f][j] += sums[64 * (f * FN + j)];
+  }
   epilogue<FM, FN, C::kRegion>(a, t, acc, wid, lane, m0, n0);
 }
 
-template <int FX, int FW, bool EXACT, bool WLINE, int TM, int TN, int WM, int WN, int S, int U>
+template <int FX, int FW, bool EXACT, bool WLINE, int TM, int TN, int WM, int WN, int KS, int S, int U>
 hipError_t launch_t(const GemmB128& a, hipStream_t stream) {
-  using C = Mid<TM, TN, WM, WN, S, U>;
+  using C = Mid<TM, TN, WM, WN, KS, S, U>;
   static bool set[64] = {false};
-  auto kern = k_gemm_b128_mid<FX, FW, EXACT, WLINE, TM, TN, WM, WN, S, U>;
+  auto kern = k_gemm_b128_mid<FX, FW, EXACT, WLINE, TM, TN, WM, WN, KS, S, U>;
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
   if (!set[dev]) {
@@ -177,11 +194,15 @@ hipError_t launch_p(const GemmB128& a, const GemmB128Plan& p, hipStream_t s) {
   // more tiles than that leaves room for at once, two steps and twice the workgroups on a CU (2048 x 4096 x
   // 4096: 51 us with four steps, 43 with two; 1024 rows 27 and 31).
   const int64_t cus = device_cu_count(), tiles = gemm_b128_tiles(a, p.tile_m, p.tile_n);
+  // Tiles of 64 that leave no CU two: twice the waves, for alternate steps each (1000 x 1000 x 4001 exact 20.0 -> 17.8
+  // us, 256 x 4096 x 4096 fp8 13.3 -> 11.6; with two tiles a CU 11.3 and 12.1).  Then codes arrive at 9.4 TB/s, and
+  // eight steps in LDS make it slower (12.7 for 11.6).
+  if (p.tile_m == 64 && tiles <= cus) return launch_t<FX, FW, EXACT, WLINE, 64, 64, 2, 2, 2, 4, 2>(a, s);
   if (p.tile_m == 64)
-    return tiles <= 2 * cus ? launch_t<FX, FW, EXACT, WLINE, 64, 64, 2, 2, 4, 2>(a, s)
-                            : launch_t<FX, FW, EXACT, WLINE, 64, 64, 2, 2, 2, 1>(a, s);
-  return tiles <= cus ? launch_t<FX, FW, EXACT, WLINE, 128, 128, 2, 4, 4, 1>(a, s)
-                      : launch_t<FX, FW, EXACT, WLINE, 128, 128, 2, 4, 2, 1>(a, s);
+    return tiles <= 2 * cus ? launch_t<FX, FW, EXACT, WLINE, 64, 64, 2, 2, 1, 4, 2>(a, s)
+                            : launch_t<FX, FW, EXACT, WLINE, 64, 64, 2, 2, 1, 2, 1>(a, s);
+  return tiles <= cus ? launch_t<FX, FW, EXACT, WLINE, 128, 128, 2, 4, 1, 4, 1>(a, s)
+                      : launch_t<FX, FW, EXACT, WLINE, 128, 128, 2, 4, 1, 2, 1>(a, s);
 }
 
 template <int FX, int FW>

@@ -206,6 +206,16 @@ def tiled(M, N, K, accum, lines, out, fx="e4m3", fw="e4m3"):
 
 @pytest.mark.parametrize("lines", [False, True])
 @pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("M,N,K", [(1000, 1000, 4001), (900, 1000, 640), (961, 1024, 300), (1000, 1000, 1)])
+def test_product_small_tiles_alone_on_their_cu(M, N, K, accum, lines):
+    """Tiles of 64, fewer than CUs: their waves share the blocks, an odd number of them too."""
+    assert -(-M // 64) * -(-N // 64) <= 256
+    tiled(M, N, K, accum, lines, F32)
+    tiled(M, N, K, accum, lines, BF16, "e5m2", "e4m3")
+
+
+@pytest.mark.parametrize("lines", [False, True])
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
 @pytest.mark.parametrize("tile,size", TILED)
 def test_product_tiled(tile, size, accum, lines):
     M, N, K = size
