@@ -1,6 +1,6 @@
-// gemm_b128.hpp -- what the two kernels of the product in blocks of 128 share (gemm_b128_tile.hip: 256 x 256
-// tiles; gemm_b128_rows.hip: small tiles whose waves split K): the problem, the tile that a workgroup takes,
-// the matrix instructions of one block, the epilogue's arithmetic.
+// gemm_b128.hpp -- what the kernels of the product in blocks of 128 share (gemm_b128_tile.hip: 256 x 256
+// tiles; gemm_b128_mid.hip: 128 x 128 and 64 x 64; gemm_b128_rows.hip: small tiles whose waves split K): the
+// problem, the tile that a workgroup takes, the matrix instructions of one block, the epilogue's arithmetic.
 //
 // Y[m][n] = act(alpha sum_b sx[m][b] sw[n][b] (sum_{k in b} qx[m][k] qw[n][k]) + bias[n]).  The inner sum is a
 // matrix product of codes from zero, the outer one FP32 fused multiply-adds on the vector unit, one for each
