@@ -37,9 +37,9 @@ struct Group {
 // Every wave searches for itself, 64 experts at a time: a tile count per lane, a scan over the lanes, the
 // first lane whose sum passes t.  Offsets are taken into 0 .. rows and in order, so that wrong ones cannot
 // lead outside the lines.  `scale` tiles count for each tile of lines (the tiles along the other axis), and
-// Group::tile counts those.  per_expert: every expert has this many tiles, with or without lines.
+// Group::tile counts those.
 __device__ __forceinline__ Group find_group(const int* __restrict__ offsets, int experts, int rows, int size, int scale,
-                                            int t, int per_expert = 0) {
+                                            int t) {
   const int lane = threadIdx.x & 63;
   Group g{-1, 0, 0, 0, 0, 0};
   int before = 0;
@@ -50,7 +50,7 @@ __device__ __forceinline__ Group find_group(const int* __restrict__ offsets, int
       lo = min(max(offsets[e], 0), rows);
       n = max(min(offsets[e + 1], rows), lo) - lo;
     }
-    const int mine = per_expert ? (e < experts ? per_expert : 0) : ((n + size - 1) / size) * scale;
+    const int mine = ((n + size - 1) / size) * scale;
     int sum = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -69,6 +69,41 @@ __device__ __forceinline__ Group find_group(const int* __restrict__ offsets, int
     before += __builtin_amdgcn_readlane(sum, 63);
   }
   g.total = before;
+  return g;
+}
+
+// The same for tile order(t, tiles of all experts), -1 where there are no more than t tiles.
+template <typename Order>
+__device__ __forceinline__ Group find_group_by(const int* __restrict__ offsets, int experts, int rows, int size, int scale,
+                                               int t, Order order) {
+  if (experts > 64) {
+    const Group g = find_group(offsets, experts, rows, size, scale, 0x7FFFFFFF);
+    return t >= g.total ? g : find_group(offsets, experts, rows, size, scale, order(t, g.total));
+  }
+  // one search, since the sums are there when the number of tiles is (8192 rows of 32 experts of 4096 x 2048, quantized
+  // too, 132 us by two, 129 so)
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = 0;
+  if (lane < experts) {
+    lo = min(max(offsets[lane], 0), rows);
+    n = max(min(offsets[lane + 1], rows), lo) - lo;
+  }
+  const int mine = ((n + size - 1) / size) * scale;
+  int sum = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(sum, d, 64);
+    sum += lane >= d ? o : 0;
+  }
+  Group g{-1, 0, 0, 0, 0, 0};
+  g.total = __builtin_amdgcn_readlane(sum, 63);
+  if (t >= g.total) return g;
+  const int at = order(t, g.total), l = __builtin_ctzll(__ballot(sum > at));
+  g.e = l;
+  g.row0 = __builtin_amdgcn_readlane(lo, l);
+  g.rows = __builtin_amdgcn_readlane(n, l);
+  g.tiles = __builtin_amdgcn_readlane(mine, l);
+  g.tile = at - (__builtin_amdgcn_readlane(sum, l) - g.tiles);
   return g;
 }
 #endif

@@ -52,9 +52,9 @@ __device__ __forceinline__ B128Tile b128_tile(const GemmB128& a, int wg) {
     t.y = (int64_t)tm * TM * a.ld_y;
   } else if (a.mode == kB128Rows) {
     // the grid is an upper bound: the tiles that there are come first, in XCD order where tiles share operands
-    Group g = find_group(a.offsets, a.experts, a.M, TM, tiles_n, XCD ? 0x7FFFFFFF : wg);
-    if (wg >= g.total) return t;
-    if (XCD) g = find_group(a.offsets, a.experts, a.M, TM, tiles_n, xcd_order(wg, g.total));
+    const Group g = find_group_by(a.offsets, a.experts, a.M, TM, tiles_n, wg,
+                                  [](int t, int total) { return XCD ? xcd_order(t, total) : t; });
+    if (g.e < 0) return t;
     tile_at(g.tile, g.tiles / tiles_n, tiles_n, tm, tn);
     const int64_t row = g.row0 + (int64_t)tm * TM;
     t.m = g.rows - tm * TM;

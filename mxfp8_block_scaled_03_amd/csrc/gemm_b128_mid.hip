@@ -1,10 +1,10 @@
 // gemm_b128_mid.hip -- the product in blocks of 128 by tiles of 64 x 64 and 128 x 128, where 256 x 256 would leave the
-// card empty.
+// card, or the tiles of uneven experts, half empty.
 //
 // WM x WN waves share a tile (KS = 2: twice, every other step for each half, whose sums meet in LDS); a step is one
-// block of K, and S steps' codes lie in LDS, so that the loads of a step have S - U steps to arrive.  Lines, pieces, fragments and sums as in gemm_b128_tile.hip; a step is short, so
-// rounds of U steps have one barrier: the one that says that a round's codes are there also says that nobody
-// reads the round before it any more, whose place is filled next.
+// block of K, and S steps' codes lie in LDS, so that the loads of a step have S - U steps to arrive.  Lines, pieces,
+// fragments and sums as in gemm_b128_tile.hip; a step is short, so rounds of U steps have one barrier: the one that says
+// that a round's codes are there also says that nobody reads the round before it any more, whose place is filled next.
 #include "gemm_b128.hpp"
 
 namespace mxq {

@@ -440,6 +440,37 @@ def test_expert_weight_gradients_tiled(tile, sizes, N, K, accum, out):
     assert torch.equal(mxq.moe_wgrad_b128(dc, ds, xc, xs, offsets, out=dense, accum=accum), got)
 
 
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("E", [64, 65, 130])
+def test_many_experts(E, accum):
+    """More experts than lanes: products of a few rows each and weight gradients, every expert's."""
+    sizes = [(7 * e) % 11 for e in range(E)]
+    N, K, R = 200, 140, sum(sizes) + 3
+    assert R > 3 * E
+    offsets = torch.tensor([0] + sizes).cumsum(0).int().to(DEV)
+    xc, xs = mxq.quantize_b128(wide(R, K, BF16, 31).to(DEV))
+    wc, ws = mxq.quantize_b128(wide(E * N, K, BF16, 32).to(DEV), axis="row")
+    wc, ws = wc.view(E, N, -1), ws.t().contiguous().view(-1, E, N).permute(1, 2, 0)
+    y = torch.full((R, N), 5.0, device=DEV)
+    mxq.moe_gemm_b128(xc, xs, wc, ws, offsets, K, out=y, accum=accum)
+    dc, ds = mxq.quantize_b128(wide(R, N, BF16, 33, False).to(DEV), "e5m2", "col", offsets=offsets)
+    cc, cs = mxq.quantize_b128(wide(R, K, BF16, 34, False).to(DEV), "e4m3", "col", offsets=offsets)
+    dw = mxq.moe_wgrad_b128(dc, ds, cc, cs, offsets, accum=accum)
+    xc, xs, wc, ws, dc, ds, cc, cs, y, dw = (t.cpu() for t in (xc, xs, wc, ws, dc, ds, cc, cs, y, dw))
+    first = block = 0
+    for e, n in enumerate(sizes):
+        if n:
+            want, tol = ref.product(xc[first:first + n], xs[first:first + n], "e4m3", wc[e], ws[e], "e4m3", accum)
+            ref.check(y[first:first + n], want, tol, "expert %d" % e)
+        nb = ref.blocks(n)
+        at = slice(128 * block, 128 * (block + nb))
+        want, tol = ref.product(dc[:, at], ds[:, block:block + nb], "e5m2", cc[:, at], cs[:, block:block + nb], "e4m3", accum)
+        ref.check(dw[e], want, tol, "gradient %d" % e)
+        first += n
+        block += nb
+    assert bool((y[first:] == 5.0).all())
+
+
 def test_wrong_offsets_stay_inside():
     """Offsets out of order or past the rows: unspecified results, but none outside the arrays."""
     R, N, K, E = 70, 40, 130, 4
