@@ -210,9 +210,8 @@ def prepare(case, seed):
         M, N, K = c["M"], c["N"], c["K"]
         s["dy"] = _gradients(g, (M, N))
         wt, ws = _tiles(_normal(g, (N, K), 0.02, torch.bfloat16).T, "e4m3")
-        xt, s["xts"] = _lines(_activations(g, (M, K)).T, "e4m3")
-        s["wt"], s["wts"] = wt.contiguous(), ws                     # [K][N], tiles; rows of codes, as the calls take them
-        s["xt"] = xt.contiguous()                                   # [K][M]
+        s["wt"], s["wts"] = wt, ws                                  # [K][N], tiles
+        s["xt"], s["xts"] = _lines(_activations(g, (M, K)).T, "e4m3")   # [K][M]
     elif c["op"] == "route":
         T, E = c["T"], c["E"]
         s["logits"] = (_normal(g, (T, E)) + _normal(g, (E,), 0.5)).to(WIDE[c["type"]])
@@ -373,8 +372,9 @@ def _own(s):
                              out_dtype=WIDE[s["out"]], accum=s["accum"])
     if s["op"] == "backward":
         rc, rs, cc, cs = mxq.quantize_b128_dual(s["dy"], "e5m2")
-        return {"dx": mxq.gemm_b128(rc, rs, s["wt"], s["wts"], s["N"], x_elem="e5m2", accum="fp8"),
-                "dw": mxq.gemm_b128(cc, cs, s["xt"], s["xts"], s["M"], x_elem="e5m2", out_dtype=torch.float32)}
+        wt, xt = s["wt"].contiguous(), s["xt"].contiguous()        # rows of codes, as the calls take them
+        return {"dx": mxq.gemm_b128(rc, rs, wt, s["wts"], s["N"], x_elem="e5m2", accum="fp8"),
+                "dw": mxq.gemm_b128(cc, cs, xt, s["xts"], s["M"], x_elem="e5m2", out_dtype=torch.float32)}
     if s["op"] == "route":
         r = mxq.moe_route(s["logits"], s["k"], renormalize=s["renorm"], mask=s["mask"])
         d = mxq.moe_route_grad(s["logits"], r, s["d_shares"], s["d_loss"], renormalize=s["renorm"], mask=s["mask"])
