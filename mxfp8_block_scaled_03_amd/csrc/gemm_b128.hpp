@@ -212,14 +212,15 @@ template <int FM, int FN, int REGION>
 __device__ __forceinline__ void epilogue(const GemmB128& a, const B128Tile& t, v4f (&acc)[FM][FN], int wid, int lane, int row0,
                                          int col0) {
   const bool has_bias = a.bias != nullptr;
-  const __amdgpu_buffer_rsrc_t brs = bias_rsrc(a.bias, a.N);
+  // (from the tile's first column on: offsets from the first of all pass 2^31 bytes in column 2^29)
+  const __amdgpu_buffer_rsrc_t brs = bias_rsrc(has_bias ? a.bias + t.n0 : nullptr, t.n);
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
-    const int col = t.n0 + col0 + 16 * j + 4 * (lane >> 4);
+    const int col = col0 + 16 * j + 4 * (lane >> 4);
     const v4f bq = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(brs, 4 * col, 0, 0));
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float bv = has_bias && col + r < a.N ? bq[r] : -0.0f;
+      const float bv = has_bias && col + r < t.n ? bq[r] : -0.0f;
 #pragma unroll
       for (int f = 0; f < FM; ++f) acc[f][j][r] = finish(acc[f][j][r], a.alpha, bv, a.act);
     }

@@ -620,3 +620,18 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for g in got:
         assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
+
+
+# ---------------------------------------------------------------------------------- ends of the ranges
+
+def test_product_bias_past_2_to_the_29_columns():
+    """A bias whose later columns lie 2^31 bytes and more from its first: every column gets its own.  No blocks of K, so that
+    the weights take no memory; y = fma(1, 0, bias) is the bias itself."""
+    N = 2 ** 29 + 133
+    assert mxq.mxq_gemm_b128_plan(0, 2, N, 0, 1, 128, 1, 256) == (64, 64, 0)
+    bias = torch.randn(N, device=DEV)
+    x, w = (torch.empty((n, 0), dtype=torch.uint8, device=DEV) for n in (2, N))
+    y = mxq.gemm_b128(x, torch.empty((2, 0), device=DEV), w, torch.empty((ref.blocks(N), 0), device=DEV), 0, bias=bias,
+                      out_dtype=F32)
+    for m in range(2):
+        assert torch.equal(y[m], bias)
