@@ -513,7 +513,8 @@ __global__ __launch_bounds__(256) void k_route_grad(const GradArgs a) {
 }
 
 bool small(int64_t T, int64_t E, int64_t k) { return T <= kSmallTokens && T * k <= kSmallSlots && E <= kSmallExperts; }
-int64_t groups_of(int64_t T) { return T < kGroups * kWaves ? (T + kWaves - 1) / kWaves : kGroups; }
+// At least one: without tokens its waves' runs are empty, and their counts and sums of zero are written.
+int64_t groups_of(int64_t T) { return T < 1 ? 1 : T < kGroups * kWaves ? (T + kWaves - 1) / kWaves : kGroups; }
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 template <int V>
@@ -523,9 +524,14 @@ hipError_t launch_v(RouteArgs a, hipStream_t s) {
     return hipGetLastError();
   }
   hipLaunchKernelGGL(k_route_tokens<V>, dim3(a.groups), dim3(64 * kWaves), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_route_scan, dim3(a.E / 8 + 1), dim3(1024), 0, s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  // (one workgroup at least: offsets, loss and slope are written without tokens too)
   const int64_t n = ((int64_t)a.T * a.k + 255) / 256;
-  hipLaunchKernelGGL(k_route_order, dim3((unsigned)(n < 1024 ? n : 1024)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(k_route_order, dim3((unsigned)(n < 1 ? 1 : n < 1024 ? n : 1024)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

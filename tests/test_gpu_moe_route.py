@@ -213,3 +213,20 @@ def test_route_graph_and_side_stream():
             torch.cuda.synchronize()
             for a, b in zip(outs, step()):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("E,k", [(6, 2), (257, 4), (600, 64), (1024, 1)])
+def test_route_no_tokens_writes_its_sums(E, k):
+    """Without tokens counts, offsets, loss and slope are zeros, written, however many experts there are."""
+    i32 = torch.full((2 * E + 1,), 7, dtype=torch.int32, device=DEV)
+    f32 = torch.full((E + 1,), 7.0, device=DEV)
+    need = mxq.mxq_moe_route_workspace(0, E, k)
+    work = torch.full((need + 256,), 7, dtype=torch.uint8, device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert mxq.mxq_moe_route(0, E, k, 1, None, mxq.MXQ_F32, E, None, None, None, i32.data_ptr(), i32.data_ptr() + 4 * E, None,
+                             f32.data_ptr(), f32.data_ptr() + 4, work.data_ptr() if need else None, need, stream) == 0
+    assert bool((i32 == 0).all()) and bool((f32 == 0).all()) and bool((work[need:] == 7).all())
+    z = torch.empty((0, E), device=DEV)
+    r = mxq.moe_route(z, k)
+    assert r.counts.tolist() == [0] * E and r.offsets.tolist() == [0] * (E + 1) and r.loss.item() == 0
+    assert mxq.moe_route_grad(z, r).shape == (0, E)
