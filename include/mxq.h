@@ -596,7 +596,8 @@ int mxq_gemm_b128_plan(int mode, int64_t M, int64_t N, int64_t K, int64_t E, int
  *          offsets[E] on.
  * loss, slope  FP32 [1], [E]; slope is the gradient of the loss by p[t][e] of a token that counts (f is a constant).
  * A NaN logit orders above every number and makes the token's shares and the loss NaN.  No atomics: the result does
- * not depend on how workgroups are scheduled.
+ * not depend on how workgroups are scheduled.  P_e is summed in FP32 in levels; a token's p passes at most
+ * 276 + T / 2^20 additions.
  * workspace  256-byte aligned, at least the bytes that mxq_moe_route_workspace gives (which may be 0); it holds
  *          nothing between calls.
  * Limits   1 <= k <= min(E, 64), E <= 1024, T k < 2^30.

@@ -21,6 +21,7 @@ namespace mxq {
 namespace {
 
 constexpr int kGroups = 512, kWaves = 8;      // workgroups at most, and a workgroup's runs of tokens
+constexpr int kSumRun = 256;                  // tokens whose p are added one after the other
 constexpr int kSmallTokens = 256, kSmallSlots = 4096, kSmallExperts = 256, kSmallWaves = 16;
 
 struct RouteArgs {
@@ -141,8 +142,11 @@ __device__ __forceinline__ void softmax(const RouteArgs& a, int lane, const floa
 template <int V, typename Put>
 __device__ __forceinline__ void route_unit(const RouteArgs& a, int t0, int t1, int lane, int cnt[V], float psum[V], int& live,
                                            Put put) {
+  // p is summed in two levels, or terms that hardly differ, rounded the same way each time, would drift as the run grows:
+  // 2^27 equal tokens of 5 experts, 32768 a wave, left the loss 2.6e-4 off, 3.2e-6 so (16384 x 256: 29.2 us, 29.6 so)
+  float part[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) cnt[v] = 0, psum[v] = 0.0f;
+  for (int v = 0; v < V; ++v) cnt[v] = 0, psum[v] = part[v] = 0.0f;
   live = 0;
   float next[V];
   uint32_t next_on = 0;          // (compared where it is used: a comparison here would wait for the loads)
@@ -170,7 +174,7 @@ __device__ __forceinline__ void route_unit(const RouteArgs& a, int t0, int t1, i
       int slot[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        psum[v] += ex[v] * inv;
+        part[v] += ex[v] * inv;
         slot[v] = -1;              // (experts past the last one have -inf's key, which nobody takes)
       }
       for (; taken < a.k; ++taken) {
@@ -208,6 +212,10 @@ __device__ __forceinline__ void route_unit(const RouteArgs& a, int t0, int t1, i
       a.experts[row + lane] = -1;
       a.shares[row + lane] = 0.0f;
       put(row + lane, -1, 0);
+    }
+    if (t + 1 == t1 || (t - t0) % kSumRun == kSumRun - 1) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) psum[v] += part[v], part[v] = 0.0f;
     }
   }
 }

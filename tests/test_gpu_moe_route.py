@@ -230,3 +230,16 @@ def test_route_no_tokens_writes_its_sums(E, k):
     r = mxq.moe_route(z, k)
     assert r.counts.tolist() == [0] * E and r.offsets.tolist() == [0] * (E + 1) and r.loss.item() == 0
     assert mxq.moe_route_grad(z, r).shape == (0, E)
+
+
+@pytest.mark.parametrize("T", [2 ** 25, 2 ** 25 + 4099, 2 ** 27])
+def test_route_loss_of_very_many_tokens(T):
+    """All logits equal: p = fl(1 / 5) of every token, all tokens to expert 0, so f = (1, 0, ..) and the loss is 1.  A sum of
+    equal terms one after the other rounds the same way each time (2^25 tokens, 8192 a wave: 6e-5 off); as it is taken, a term passes
+    256 additions, one for each 256 of its wave's T / 4096 tokens, and those of 8 waves, 4 groups and 7 steps,
+    2^-24 each; p, f, slope, its product and the last sums take fewer than 16 roundings more."""
+    z = torch.zeros((T, 5), device=DEV)
+    r = mxq.moe_route(z, 1)
+    assert r.counts.tolist() == [T, 0, 0, 0, 0]
+    adds = 256 + (T // 4096 + 255) // 256 + 1 + 8 + 4 + 7
+    assert abs(r.loss.item() - 1.0) <= (adds + 16) * 2.0 ** -24
