@@ -635,3 +635,87 @@ def test_product_bias_past_2_to_the_29_columns():
                       out_dtype=F32)
     for m in range(2):
         assert torch.equal(y[m], bias)
+
+
+def guarded(shape, dtype, ld=None):
+    """A view [rows][cols] at pitch ld inside a buffer of its own, 4 KiB before it and behind it, and a check that all but the view
+    is as it was."""
+    rows, cols = shape
+    ld = ld or cols
+    es = torch.empty((), dtype=dtype).element_size()
+    pad = 4096 // es
+    buf = torch.full((2 * pad + rows * ld,), 0x5A, dtype=torch.uint8, device=DEV) if dtype is torch.uint8 else \
+        torch.full((2 * pad + rows * ld,), 5.0, dtype=dtype, device=DEV)
+    view = buf[pad:pad + rows * ld].view(rows, ld)[:, :cols]
+
+    def untouched():
+        rest = buf.clone()
+        fill = buf[0].item()
+        rest[pad:pad + rows * ld].view(rows, ld)[:, :cols] = fill
+        return bool((rest == fill).all())
+    return view, untouched
+
+
+def wrong_offsets(E, R, seed):
+    """Offsets out of order, before the first row and past the last one."""
+    g = torch.Generator().manual_seed(seed)
+    o = torch.randint(-R, 3 * R, (E + 1,), generator=g)
+    o[::3] = torch.randint(0, R + 1, (len(o[::3]),), generator=g)
+    return o.int().to(DEV)
+
+
+@pytest.mark.parametrize("E", [1, 5, 64, 100])
+def test_quantize_by_wrong_offsets_stays_inside(E):
+    R, C = 700, 300
+    x = wide(R, C, BF16, 3).to(DEV)
+    nbr = (R + 127 * E) // 128
+    for seed in range(3):
+        off = wrong_offsets(E, R, seed)
+        rc, rc_ok = guarded((R, 384), torch.uint8, 400)
+        rs, rs_ok = guarded((3, R), F32, R + 5)
+        cc, cc_ok = guarded((C, 128 * nbr), torch.uint8, 128 * nbr + 16)
+        cs, cs_ok = guarded((nbr, C), F32, C + 3)
+        stream = torch.cuda.current_stream().cuda_stream
+        for row in (True, False):
+            assert mxq.mxq_quantize_b128(
+                x.data_ptr(), mxq.MXQ_BF16, R, C, C, mxq.MXQ_E4M3, mxq.MXQ_SCALE_AMAX, 0, rc.data_ptr() if row else None, 400,
+                rs.data_ptr() if row else None, R + 5, cc.data_ptr(), 128 * nbr + 16, cs.data_ptr(), C + 3, off.data_ptr(), E,
+                stream) == 0
+        assert rc_ok() and rs_ok() and cc_ok() and cs_ok()
+
+
+# plan, experts, rows, columns, K: the search for up to and for more than 64 experts, and every kernel
+WRONG_ROWS = [((16, 64, 1), 100, 250, 200, 300), ((64, 64, 0), 100, 700, 200, 300), ((64, 64, 0), 6, 511, 900, 384),
+              ((128, 128, 0), 4, 2011, 4100, 640), ((256, 256, 0), 3, 3811, 3000, 1280)]
+
+
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("tile,E,R,N,K", WRONG_ROWS)
+def test_experts_of_wrong_offsets_stay_inside(tile, E, R, N, K, accum):
+    assert mxq.mxq_gemm_b128_plan(1, R, N, K, E, 1, 0 if accum == "fp8" else 1, 256) == tile
+    xc, xs = mxq.quantize_b128(wide(R, K, BF16, 1).to(DEV))
+    wc, ws = mxq.quantize_b128(wide(E * N, K, BF16, 2).to(DEV))
+    wc, ws = wc.view(E, N, -1), ws.t().contiguous().view(-1, E, N).permute(1, 2, 0)
+    for seed in range(3):
+        y, y_ok = guarded((R, N), F32, N + 5)
+        mxq.moe_gemm_b128(xc, xs, wc, ws, wrong_offsets(E, R, seed), K, out=y, accum=accum)
+        assert y_ok()
+
+
+WRONG_GRADS = [((64, 64, 0), 4, 470, 512, 500), ((64, 64, 0), 100, 700, 100, 90), ((128, 128, 0), 10, 166, 1999, 2003),
+               ((256, 256, 0), 4, 15000, 8001, 2041)]
+
+
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("tile,E,R,N,K", WRONG_GRADS)
+def test_gradients_of_wrong_offsets_stay_inside(tile, E, R, N, K, accum):
+    nb = (R + 127 * E) // 128
+    assert mxq.mxq_gemm_b128_plan(2, N, K, 128 * nb + 127 - 127 * E, E, 1, 0 if accum == "fp8" else 1, 256) == tile
+    codes = [torch.randint(0, 120, (n, 128 * nb), dtype=torch.uint8, device=DEV) for n in (N, K)]
+    scales = [torch.ones((nb, n), device=DEV).t() for n in (N, K)]
+    for seed in range(3):
+        whole = torch.full((E + 2, N + 1, K + 3), 5.0, device=DEV)
+        mxq.moe_wgrad_b128(codes[0], scales[0], codes[1], scales[1], wrong_offsets(E, R, seed), x_elem="e4m3",
+                           out=whole[1:E + 1, :N, :K], accum=accum)
+        for rest in (whole[0], whole[E + 1], whole[:, N], whole[:, :, K:]):
+            assert bool((rest == 5.0).all())
