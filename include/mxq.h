@@ -500,18 +500,21 @@ int mxq_moe_fp4_plan(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k, int 
  *
  * Codes    E4M3 or E5M2 bytes, [lines][ld], 128 bytes per block: ld >= 128 nb, base and ld multiples of 16 bytes,
  *          ld < 2^24 where a product reads them.  The quantizer writes whole blocks, zero past K; a product
- *          multiplies whole blocks, so another producer's codes past K have to be zero for X or for W.
+ *          multiplies whole blocks, so another producer's codes past K have to be zero for X or for W, and for the
+ *          other no NaN or infinity (0 times those is NaN).
  * Scales   FP32.  Of lines: [nb][ld], ld >= lines: line l's scale of block b at [b * ld + l].  Of tiles: tile
  *          row i, block b, with strides of their own where a product reads them (so that the transposed
  *          weight takes the same array).  A product forms the product of two scales in FP32: it should lie
- *          inside FP32's normal range.  The scales of one matrix span less than 2^31 bytes.
+ *          inside FP32's normal range (past it a block whose sum is 0 gives NaN, below it bits are lost).  The scales
+ *          of one matrix span at most 2^31 bytes where a product reads them.
  * Experts  Lines sorted by expert: expert e has lines offsets[e] .. offsets[e+1] - 1, offsets int32 [E + 1] on the
  *          device, nondecreasing within 0 .. rows (others give unspecified results, but no access outside the
  *          arrays); E <= 1024.  Lines outside offsets[0] .. offsets[E] - 1 belong to nobody: nothing of theirs is
  *          read into a result, and outputs of theirs are left as they were.  Where K runs along such lines,
  *          every expert's lines begin a block: expert e's blocks follow those of the experts before it,
  *          ceil(n_e / 128) each, and a line has room for floor((rows + 127 E) / 128).
- * Sizes    lines < 2^30, K (or rows, where K runs along them) < 2^24.
+ * Sizes    lines < 2^30, K (or rows, where K runs along them) < 2^24.  The quantizer takes any of both below 2^30, and
+ *          fewer than 2^23 tiles of 128 x 128.
  */
 
 /*
@@ -574,7 +577,8 @@ int mxq_moe_wgrad_b128(int64_t M, int64_t N, int64_t rows, int64_t E, const int3
 
 /*
  * mxq_gemm_b128_plan -- how such a product would run on a device of `cus` compute units (host logic only): its
- * tile, and the waves that share one along K (0: the 256 x 256 kernel).  mode 0: mxq_gemm_b128; 1: mxq_moe_gemm_b128 (M its
+ * tile, and the waves that split K among them (1: a wave has a tile and all of K; 0: the workgroups of 64 x 64, 128 x 128
+ * and 256 x 256, whose waves share a tile's rows and columns).  mode 0: mxq_gemm_b128; 1: mxq_moe_gemm_b128 (M its
  * rows); 2: mxq_moe_wgrad_b128 (K its rows).  E as there (ignored by mode 0).
  */
 int mxq_gemm_b128_plan(int mode, int64_t M, int64_t N, int64_t K, int64_t E, int w_block, int accum, int cus, int* tile_m,
@@ -595,7 +599,7 @@ int mxq_gemm_b128_plan(int mode, int64_t M, int64_t N, int64_t K, int64_t E, int
  * order    int32 [T k]: the slots t * k + rank by expert, in order of slot within an expert; -1 from
  *          offsets[E] on.
  * loss, slope  FP32 [1], [E]; slope is the gradient of the loss by p[t][e] of a token that counts (f is a constant).
- * A NaN logit orders above every number and makes the token's shares and the loss NaN.  No atomics: the result does
+ * A NaN logit orders above every number; it and +inf make the token's shares and the loss NaN.  No atomics: the result does
  * not depend on how workgroups are scheduled.  P_e is summed in FP32 in levels; a token's p passes at most
  * 276 + T / 2^20 additions.
  * workspace  256-byte aligned, at least the bytes that mxq_moe_route_workspace gives (which may be 0); it holds

@@ -3,7 +3,11 @@
 ``_binding``; every call raises if the library is missing.
 
 Codes are uint8 [lines][128 * blocks]; scales float32 [lines][blocks] (a tile's: [tiles][blocks]),
-those of lines stored block by block (stride 1 along the lines), as the quantizer gives them."""
+those of lines stored block by block (stride 1 along the lines), as the quantizer gives them.
+
+A product forms the product of two scales in FP32, which should lie inside its normal range: past it a
+block whose sum is 0 gives NaN, below it bits are lost.  It multiplies whole blocks: codes past K that
+the quantizer did not write have to be zero for one operand and finite for the other."""
 from __future__ import annotations
 
 import functools

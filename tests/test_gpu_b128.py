@@ -719,3 +719,18 @@ def test_gradients_of_wrong_offsets_stay_inside(tile, E, R, N, K, accum):
                            out=whole[1:E + 1, :N, :K], accum=accum)
         for rest in (whole[0], whole[E + 1], whole[:, N], whole[:, :, K:]):
             assert bool((rest == 5.0).all())
+
+
+@pytest.mark.parametrize("accum", ["fp32", "fp8"])
+@pytest.mark.parametrize("M,N", [(9, 40), (700, 900), (1900, 2100)])
+def test_codes_past_k_of_another_producer(M, N, accum):
+    """Finite codes of any value behind K change nothing where the other operand has zeros there."""
+    K = 300
+    xc, xs = mxq.quantize_b128(wide(M, K, BF16, 1).to(DEV))
+    wc, ws = mxq.quantize_b128(wide(N, K, BF16, 2).to(DEV))
+    want = mxq.gemm_b128(xc, xs, wc, ws, K, accum=accum, out_dtype=F32)
+    for codes in (xc, wc):
+        kept = codes.clone()
+        codes[:, K:] = torch.randint(0, 127, (codes.shape[0], 384 - K), device=DEV).to(torch.uint8)
+        assert torch.equal(mxq.gemm_b128(xc, xs, wc, ws, K, accum=accum, out_dtype=F32), want)
+        codes.copy_(kept)

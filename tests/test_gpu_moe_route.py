@@ -243,3 +243,20 @@ def test_route_loss_of_very_many_tokens(T):
     assert r.counts.tolist() == [T, 0, 0, 0, 0]
     adds = 256 + (T // 4096 + 255) // 256 + 1 + 8 + 4 + 7
     assert abs(r.loss.item() - 1.0) <= (adds + 16) * 2.0 ** -24
+
+
+def test_route_infinite_logit():
+    """+inf is taken first (after a NaN), the lower index of two; the token's shares and gradients and the loss are NaN, and
+    other tokens keep theirs."""
+    for T in (10, 700):
+        z = logits_of(T, 20, F32, 2)
+        clean = mxq.moe_route(z.to(DEV), 3)
+        z[4, 7] = z[5, 2] = z[5, 11] = float("inf")
+        z[6, 3], z[6, 1] = float("nan"), float("inf")
+        r = mxq.moe_route(z.to(DEV), 3)
+        assert r.experts[4, 0] == 7 and r.experts[5, :2].tolist() == [2, 11] and r.experts[6, :2].tolist() == [3, 1]
+        assert bool(torch.isnan(r.shares[4:7]).all()) and bool(torch.isnan(r.loss).all())
+        keep = torch.tensor([t for t in range(T) if not 4 <= t <= 6], device=DEV)
+        assert torch.equal(r.shares[keep], clean.shares[keep])
+        d = mxq.moe_route_grad(z.to(DEV), r, torch.ones_like(r.shares), torch.ones(1, device=DEV))
+        assert bool(torch.isnan(d[4:7]).all()) and not bool(torch.isnan(d[keep]).any())
