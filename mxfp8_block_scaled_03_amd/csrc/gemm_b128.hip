@@ -30,7 +30,8 @@ GemmB128Plan gemm_b128_plan(const GemmB128& a, int cus) {
   // (an expert's last block counts whole)
   const double nb = a.mode == kB128Blocks ? (double)a.rows / (kB * a.experts) + 0.5 : a.nb;
   // Rows of experts: of E experts E (1 - (1 - 1/E)^rows) have some, if rows choose freely; their last tiles are taken
-  // to be a quarter full, since some have many more rows than others.  The weights come at 5.5 MB a us at best.
+  // to be a quarter full, since some have many more rows than others.  The weights come at 5.5 MB a us (128 rows of
+  // 64 x 4096 x 2048, some 50 experts with rows: 5.9 in 72 us, as the layer's one set of weights or six in turn).
   const double E = a.experts, active = E * (1 - pow(1 - 1 / E, (double)a.M)), mean = a.M / active;
   const bool by_rows = a.mode == kB128Rows;
   auto tiles = [&](int tm, int tn) {
@@ -45,7 +46,8 @@ GemmB128Plan gemm_b128_plan(const GemmB128& a, int cus) {
     if (us < least) least = us, best = GemmB128Plan{tm, tn, waves};
   };
   const int small[3][2] = {{16, 16}, {32, 16}, {64, 32}};
-  // (a row or two each: 128 rows of 64 x 4096 x 2048 67-71 us by 16 x 64, 74 by 64 x 64; 32 of 8 x 8192 x 5120 58 and 49)
+  // (up to three rows an expert on average, whoever has them: 128 rows of 64 x 4096 x 2048 67-71 us by 16 x 64, 74 by
+  // 64 x 64; 32 of 8 x 8192 x 5120, past it, 58 and 49)
   if (by_rows && a.M <= 3 * E) return {16, 64, 1};
   // the experts' weight gradients: each round's outputs too, which a large tile writes with nothing beside it
   const bool grads = a.mode == kB128Blocks;

@@ -145,11 +145,12 @@ __global__ __launch_bounds__(64 * waves_of(WK), 2) void k_gemm_b128_rows(const G
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = wid % WK;
   if (WN > 1) {
-    // this wave's columns (a tile of W's scales may end between two waves)
+    // this wave's columns (those of the workgroup lie in one tile of W's scales)
+    static_assert(kB % (16 * NT * WN) == 0, "a workgroup's columns end where a tile of scales does, or before");
     const int n = 16 * NT * (wid / WK);
     if (n >= t.n) return;
     t.w += n * a.ld_w;
-    t.ws += WLINE ? n : ((t.n0 + n) / kB - t.n0 / kB) * a.ws_n;
+    if (WLINE) t.ws += n;
     t.y += n;
     t.n -= n;
     t.n0 += n;

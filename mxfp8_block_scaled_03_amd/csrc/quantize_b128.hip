@@ -36,7 +36,7 @@ struct QuantArgs {
   int64_t ld_cs;
   const int* offsets;
   int experts, rule, blocks_c;   // blocks_c: blocks that a line of cc and cs has room for
-  int tiles_r, tiles_c;
+  int tiles_c;
 };
 
 // Scale and factor of a block from the bits of its maximum.
@@ -326,7 +326,6 @@ hipError_t launch_f(const QuantArgs& args, bool row, bool col, bool tile, hipStr
   const bool thin = !col && !tile && tiles * a.tiles_c < 2 * (int64_t)device_cu_count();
   const int64_t tr = thin ? (a.rows + 15) / 16 : tiles;
   if (tr * a.tiles_c > 0x7FFFFF) return hipErrorInvalidValue;
-  a.tiles_r = (int)tr;
   const dim3 grid((unsigned)(tr * a.tiles_c)), block(256);
   if (tile && col)
     hipLaunchKernelGGL((k_quant_b128<BF16, F, true, true, true, 8>), grid, block, 0, stream, a);
