@@ -5,6 +5,8 @@
 //     (with a K split of the last round's tiles when that round is at most half full)
 //   FP8 matrix cores (MXQ_ACC_FP8_MFMA), scale rows 16-byte aligned -> gemm_fp8.hip
 //   any other scale layout, either mode                            -> gemm_fallback.hip
+//   a bias of 2^29 columns or more                                 -> gemm_fallback.hip
+//     (the others read it with 32-bit byte offsets, past which a load gives 0)
 #include "internal.hpp"
 
 namespace mxq {
@@ -19,6 +21,8 @@ hipError_t launch_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* xc, int64
   auto aligned = [&](uintptr_t a) {
     return ((uintptr_t)xs % a == 0) && ((uintptr_t)ws % a == 0) && ld_xs % (int64_t)a == 0 && ld_ws % (int64_t)a == 0;
   };
+  if (ep.bias != nullptr && N >= (int64_t)1 << 29)
+    return launch_gemm_fallback(M, N, K, xc, ld_x, xs, ld_xs, x_fmt, wc, ld_w, ws, ld_ws, w_fmt, ep, exact, stream);
   if (exact) {
     if (aligned(4)) {
       // the K split of the last round needs a workspace: the caller's, or one taken from

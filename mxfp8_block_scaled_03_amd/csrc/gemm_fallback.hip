@@ -1,5 +1,5 @@
 // gemm_fallback.hip -- block-scaled FP8 GEMM for operands whose scale rows break the
-// alignment the fast kernels need (both accumulation modes).
+// alignment the fast kernels need (both accumulation modes), and for a bias too long for them.
 //
 // "Low-Precision GPU Programming", "Scale ownership and the GEMM dataflow": Y = X W; with
 // 32-element blocks along K the product of the X-block and W-block scales stays inside

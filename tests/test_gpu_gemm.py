@@ -313,3 +313,18 @@ def test_exact_mode_nan_scale_gives_nan():
     keep = torch.ones(M, dtype=torch.bool)
     keep[5] = False
     assert torch.isfinite(y[keep]).all()
+
+
+@pytest.mark.parametrize("accum", ACCS)
+def test_gemm_bias_past_2_to_the_29_columns(accum):
+    """A bias whose later columns lie 2^31 bytes and more from its first: every column gets its own.  K = 0, so that the
+    weights take no memory; y = fma(1, 0, bias) is the bias itself."""
+    N = 2 ** 29 + 133
+    bias = torch.randn(N, device=DEV)
+    y = torch.empty((2, N), device=DEV)
+    acc = mxq.MXQ_ACC_FP32 if accum == "fp32" else mxq.MXQ_ACC_FP8_MFMA
+    assert mxq.mxq_gemm_ex(2, N, 0, None, 0, None, 0, mxq.MXQ_E4M3, None, 0, None, 0, mxq.MXQ_E4M3, 1.0, bias.data_ptr(),
+                           mxq.MXQ_ACT_NONE, y.data_ptr(), mxq.MXQ_F32, N, mxq.MXQ_E4M3, None, 0, None, 0, acc,
+                           torch.cuda.current_stream().cuda_stream) == 0
+    for m in range(2):
+        assert torch.equal(y[m], bias)
