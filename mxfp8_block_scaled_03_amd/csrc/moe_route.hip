@@ -13,7 +13,7 @@
 // those of experts l, 64 + l, ...) number the slots of an expert in order, and sums over the waves' and
 // workgroups' counts give every slot its place: no atomics, and nothing depends on how workgroups are scheduled.
 // Up to 256 tokens take one workgroup and one launch, more take three (tokens; sums over the groups; places and
-// loss).
+// loss): 64 tokens of 64 experts, k 8, 10.5 us by one; 257 of 256 experts 15 by three, but 256 of 256 63 by one.
 #include "codec.hpp"
 #include "internal.hpp"
 
